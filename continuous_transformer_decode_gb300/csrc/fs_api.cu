@@ -903,6 +903,13 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
 
 }  // namespace
 
+void fsk::set_null_error(const char* msg) noexcept {
+  try {
+    g_create_error = msg;
+  } catch (...) {  // out of memory for a message: the code still says what happened
+  }
+}
+
 extern "C" {
 
 int fs_create(const fs_model_desc* desc, const fs_weights* weights, fs_handle** out) {

@@ -223,6 +223,17 @@ struct KV {
   int max_pages = 0;
 };
 
+// 8-bit paged KV cache (fs_kv_q8 of include/fs.h): a row is one token's key or
+// value of one KV head, hd codes (byte = code + 128) and one f32 scale.
+struct KvQ8 {
+  uint8_t* k = nullptr;  // [n_pages][Hkv][page_size][hd]
+  uint8_t* v = nullptr;
+  float* ks = nullptr;   // [n_pages][Hkv][page_size]
+  float* vs = nullptr;
+  const int32_t* page_table = nullptr;  // [n_lanes][max_pages]
+  int n_pages = 0, Hkv = 0, page_size = 0, hd = 0, n_lanes = 0, max_pages = 0;
+};
+
 // RoPE of one rotate-half pair (x0 = element i, x1 = element i + hd/2) with
 // cos c and sin s: (x0 c - x1 s, x1 c + x0 s), every product and sum rounded
 // on its own (no contraction into fused multiply-adds). Every kernel that
@@ -464,6 +475,59 @@ int launch_attention_tma(const CUtensorMap& tmK, const CUtensorMap& tmV, const A
                          int B, int x_type, cudaStream_t s);
 int launch_attention_mma(const AttnParams& a, int B, int x_type, cudaStream_t s);
 int launch_attention_tiled(const AttnParams& a, int B, int x_type, cudaStream_t s);
+
+// The message fs_last_error(NULL) returns on this thread.
+void set_null_error(const char* msg) noexcept;
+
+// ---- operators on an 8-bit paged KV cache (k_kv_q8.cu, k_attn_q8.cu)
+bool kv_q8_supports(int hd);
+// n rows of k and v (x_type, row strides in elements) into the slots of
+// (lanes[i], positions[i]); rc / rs rotate the keys (null: as they are).
+int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
+                        int64_t v_stride, int x_type, const int32_t* lanes,
+                        const int32_t* positions, int n, const float* rc, const float* rs,
+                        int rope_len, cudaStream_t s);
+// The values of the same slots into k_out / v_out (either may be null).
+int launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
+                      void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, int x_type,
+                      cudaStream_t s);
+struct AttnQ8 {
+  KvQ8 kv;
+  const void* q;      // [n] rows of [H][hd], q_stride elements apart
+  int64_t q_stride;
+  const int32_t* lanes;
+  const int32_t* lens;
+  int n, H, max_len;
+  float scale;
+  const float* rc;    // rotation of q at lens[i] - 1 (null: q as it is)
+  const float* rs;
+  void* out;          // [n] rows of [H][hd], out_stride elements apart
+  int64_t out_stride;
+  int split_len, n_splits;
+  float* part_acc;    // [n][n_splits][H][hd] when n_splits > 1
+  float* part_ml;     // [n][n_splits][H][2]
+};
+// Positions per split of one call (a multiple of 64).
+int attn_q8_split_len(int n, int Hkv, int max_len, int sms);
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s);
+
+// Verification of drafted tokens (k_verify.cu).
+struct VerifyArgs {
+  const float* logits;
+  int64_t ld_logits;
+  int n_rows, V;
+  const int32_t* row_start;
+  int n_seqs;
+  const int32_t* draft;
+  const float* probs;
+  int64_t ld_probs;
+  const float* temps;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* n_accepted;
+  int32_t* next_token;
+};
+int launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 int launch_sample(const float* logits, int B, int V, const float* temps,
                   const uint64_t* seeds, const uint64_t* counters,

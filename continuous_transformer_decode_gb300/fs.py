@@ -83,6 +83,14 @@ class fs_sched_stats(C.Structure):
                 ("jobs_cancelled", C.c_int64)]
 
 
+class fs_kv_q8(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("page_table", C.c_void_p),
+                ("n_pages", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("page_size", C.c_int32), ("head_dim", C.c_int32),
+                ("n_lanes", C.c_int32), ("max_pages", C.c_int32)]
+
+
 LIB_PATH = _build.LIB
 _lib = None
 
@@ -97,6 +105,7 @@ def lib():
                           "(run __graft_entry__.build())")
     L = C.CDLL(LIB_PATH)
     p, i32, i64, u64 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64
+    f32, kv8 = C.c_float, C.POINTER(fs_kv_q8)
     sig = {
         "fs_create": (C.c_int, [C.POINTER(fs_model_desc),
                                 C.POINTER(fs_weights), C.POINTER(p)]),
@@ -144,6 +153,12 @@ def lib():
         "fs_sched_last_batch": (C.c_int, [p, p, i32, p]),
         "fs_sched_last_error": (C.c_char_p, [p]),
         "fs_sched_model_free_fail_resets": (C.c_int, [p, i32]),
+        "fs_kv_q8_append": (C.c_int, [kv8, p, p, i64, i64, i32, p, p, i32, p, p, i32, p]),
+        "fs_kv_q8_read": (C.c_int, [kv8, p, p, i32, p, p, i64, i64, i32, p]),
+        "fs_kv_q8_attention_workspace": (i64, [kv8, i32, i32, i32, i32]),
+        "fs_kv_q8_attention": (C.c_int, [kv8, p, i64, p, p, i32, i32, i32, f32, p, p, i32, p, i64,
+                                         i32, i32, p, i64, p]),
+        "fs_verify_draft": (C.c_int, [p, i64, i32, i32, p, i32, p, p, i64, p, p, p, p, p, p]),
         "fs_gemm_bf16": (C.c_int, [p, i32, i32, p, i32, p, i32, i32, p]),
         "fs_gemm_bf16_width": (C.c_int, [p, i32, i32, p, i32, p, i32, p]),
         "fs_gemm_bf16_time": (C.c_int, [p, i32, i32, p, i32, p, i32, i32, p, p]),
@@ -164,6 +179,8 @@ def exported_symbols() -> list:
             "fs_lane_import_kv", "fs_lane_fill_random_kv", "fs_quantize_q8_0",
             "fs_kernel_launches", "fs_gemm_path", "fs_gemm_plan", "fs_lane_capacity", "fs_attention_path", "fs_sample_device",
             "fs_profile_enable", "fs_profile_read", "fs_device_error",
+            "fs_kv_q8_append", "fs_kv_q8_read", "fs_kv_q8_attention_workspace",
+            "fs_kv_q8_attention", "fs_verify_draft",
             "fs_gemm_bf16", "fs_gemm_bf16_width", "fs_gemm_bf16_time", "fs_copy_logits", "fs_gemm_bf16_noalloc",
             "fs_sched_create", "fs_sched_create_model_free", "fs_sched_destroy",
             "fs_sched_submit", "fs_sched_step", "fs_sched_run", "fs_sched_take",
@@ -501,6 +518,170 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
                                     splits, raw)
     if rc != FS_OK:
         raise FsError(rc, "fs_gemm_bf16_noalloc failed")
+
+
+# ------------------------------------------------------- 8-bit paged KV cache
+_ROW_DTYPES = {"torch.float32": FS_DTYPE_F32, "torch.bfloat16": FS_DTYPE_BF16}
+
+
+def _refuse(why: str):
+    raise FsError(CODES["FS_ERR_ARG"], why)
+
+
+def _op_check(rc: int) -> None:
+    if rc != FS_OK:
+        raise FsError(rc, fs_last_error(None))
+
+
+def _vec(x, n: int, dtype: str, what: str):
+    """Address of a contiguous CUDA vector of n entries (None: NULL)."""
+    if x.numel() != n or str(x.dtype) != dtype or not x.is_cuda or not x.is_contiguous():
+        _refuse(f"{what}: a contiguous CUDA tensor of {n} {dtype} values is needed")
+    return x.data_ptr()
+
+
+def _rows(x, n: int, heads: int, hd: int, what: str):
+    """(address, row stride, dtype) of n rows [heads, hd], each contiguous."""
+    dt = _ROW_DTYPES.get(str(x.dtype))
+    if dt is None or not x.is_cuda or tuple(x.shape) != (n, heads, hd) or \
+            (x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != hd))):
+        _refuse(f"{what}: a CUDA tensor [{n}, {heads}, {hd}] of f32 or bf16 whose rows are "
+                "contiguous is needed")
+    return x.data_ptr(), (x.stride(0) if n > 1 else heads * hd), dt
+
+
+def _rope_args(rope, hd: int):
+    if rope is None:
+        return None, None, 0
+    cos, sin = rope
+    n = cos.shape[0]
+    return (_vec(cos, n * (hd // 2), "torch.float32", "rope cos"),
+            _vec(sin, n * (hd // 2), "torch.float32", "rope sin"), n)
+
+
+def fs_kv_q8_view(k, v, k_scale, v_scale, page_table) -> fs_kv_q8:
+    """The 8-bit paged cache in the caller's CUDA tensors: codes k, v uint8
+    [n_pages, Hkv, page_size, hd], scales f32 [n_pages, Hkv, page_size],
+    page_table int32 [n_lanes, max_pages], all contiguous. The view keeps them
+    alive; page-table entries may change between calls."""
+    if k.dim() != 4 or page_table.dim() != 2:
+        _refuse("codes are [n_pages, Hkv, page_size, hd], the page table [n_lanes, max_pages]")
+    n_pages, Hkv, ps, hd = k.shape
+    n_lanes, max_pages = page_table.shape
+    rows = n_pages * Hkv * ps
+    c = fs_kv_q8(_vec(k, rows * hd, "torch.uint8", "k codes"),
+                 _vec(v, rows * hd, "torch.uint8", "v codes"),
+                 _vec(k_scale, rows, "torch.float32", "k scales"),
+                 _vec(v_scale, rows, "torch.float32", "v scales"),
+                 _vec(page_table, n_lanes * max_pages, "torch.int32", "page table"),
+                 n_pages, Hkv, ps, hd, n_lanes, max_pages)
+    c.tensors = (k, v, k_scale, v_scale, page_table)
+    return c
+
+
+def fs_kv_q8_append(cache: fs_kv_q8, k, v, lanes, positions, rope=None, stream=None) -> None:
+    """Quantises rows k, v [n, Hkv, hd] (f32 or bf16, any row stride) into
+    tokens positions[i] of lanes lanes[i] (int32 CUDA vectors); rope: (cos, sin)
+    f32 [rope_len, hd / 2] that rotate the keys."""
+    n = lanes.numel()
+    hd = cache.head_dim
+    kp, ks, dt = _rows(k, n, cache.n_kv_heads, hd, "k")
+    vp, vs, dv = _rows(v, n, cache.n_kv_heads, hd, "v")
+    if dt != dv:
+        _refuse("k and v have different types")
+    rc, rs, rl = _rope_args(rope, hd)
+    _op_check(lib().fs_kv_q8_append(C.byref(cache), kp, vp, ks, vs, dt,
+                                    _vec(lanes, n, "torch.int32", "lanes"),
+                                    _vec(positions, n, "torch.int32", "positions"), n, rc, rs, rl,
+                                    getattr(stream, "cuda_stream", stream)))
+
+
+def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, stream=None) -> None:
+    """Reads tokens back into k_out, v_out [n, Hkv, hd] (f32 or bf16; either
+    may be None)."""
+    n = lanes.numel()
+    kp, ks, dt = (None, 0, None) if k_out is None else \
+        _rows(k_out, n, cache.n_kv_heads, cache.head_dim, "k_out")
+    vp, vs, dv = (None, 0, None) if v_out is None else \
+        _rows(v_out, n, cache.n_kv_heads, cache.head_dim, "v_out")
+    if dt is not None and dv is not None and dt != dv:
+        _refuse("k_out and v_out have different types")
+    if dt is None:
+        dt = FS_DTYPE_F32 if dv is None else dv
+    _op_check(lib().fs_kv_q8_read(C.byref(cache), _vec(lanes, n, "torch.int32", "lanes"),
+                                  _vec(positions, n, "torch.int32", "positions"), n, kp, vp, ks,
+                                  vs, dt, getattr(stream, "cuda_stream", stream)))
+
+
+def fs_kv_q8_attention_workspace(cache: fs_kv_q8, n: int, n_heads: int, max_len: int = 0,
+                                 split_len: int = 0) -> int:
+    """Bytes of workspace fs_kv_q8_attention needs for the same arguments."""
+    b = lib().fs_kv_q8_attention_workspace(C.byref(cache), n, n_heads, max_len, split_len)
+    if b < 0:
+        _op_check(int(b))
+    return b
+
+
+def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0,
+                       scale: float | None = None, rope=None, split_len: int = 0,
+                       workspace=None, stream=None) -> None:
+    """out[i] = attention of q[i] (both [n, H, hd], f32 or bf16) over tokens
+    0 .. lengths[i] - 1 of lane lanes[i]. max_len: an upper bound of the lengths;
+    scale: 1 / sqrt(hd) by default; rope: (cos, sin) that rotate q by
+    lengths[i] - 1; workspace: a CUDA tensor of at least
+    fs_kv_q8_attention_workspace bytes, not shared with a call that may run at
+    the same time."""
+    n = lanes.numel()
+    hd = cache.head_dim
+    H = q.shape[1] if q.dim() == 3 else 0
+    qp, qs, dt = _rows(q, n, H, hd, "q")
+    op, os_, do = _rows(out, n, H, hd, "out")
+    if dt != do:
+        _refuse("q and out have different types")
+    rc, rs, rl = _rope_args(rope, hd)
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            _refuse("workspace: a contiguous CUDA tensor is needed")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _op_check(lib().fs_kv_q8_attention(
+        C.byref(cache), qp, qs, _vec(lanes, n, "torch.int32", "lanes"),
+        _vec(lengths, n, "torch.int32", "lengths"), n, H, max_len,
+        hd ** -0.5 if scale is None else scale, rc, rs, rl, op, os_, dt, split_len, wp, wb,
+        getattr(stream, "cuda_stream", stream)))
+
+
+# --------------------------------------------------------- draft verification
+def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sample, n_accepted,
+                    next_token, stream=None) -> None:
+    """Speculative sampling's accept / resample rule (see include/fs.h). logits
+    f32 [rows, vocab] (any row stride), row_start int32 [seqs + 1], draft int32
+    [rows], draft_probs f32 [rows, vocab] or None, temps and u_sample f32 [seqs],
+    u_accept f32 [rows]; n_accepted and next_token int32 [seqs] are written. All
+    CUDA tensors."""
+    if logits.dim() != 2 or not logits.is_cuda or str(logits.dtype) != "torch.float32":
+        _refuse("logits: a CUDA tensor [rows, vocab] of f32 is needed")
+    rows, V = logits.shape
+    if draft_probs is not None and (tuple(draft_probs.shape) != (rows, V) or
+                                    not draft_probs.is_cuda or
+                                    str(draft_probs.dtype) != "torch.float32"):
+        _refuse("draft_probs: a CUDA tensor [rows, vocab] of f32 is needed")
+    for t in (logits, draft_probs):
+        if t is not None and V > 1 and t.numel() and t.stride(1) != 1:
+            _refuse("rows of logits and draft_probs must be contiguous")
+    n = temps.numel()
+    ld = lambda t: 0 if t is None else t.stride(0) if rows > 1 else V
+    _op_check(lib().fs_verify_draft(
+        logits.data_ptr(), ld(logits), rows, V,
+        _vec(row_start, n + 1, "torch.int32", "row_start"), n,
+        _vec(draft, rows, "torch.int32", "draft"),
+        None if draft_probs is None else draft_probs.data_ptr(), ld(draft_probs),
+        _vec(temps, n, "torch.float32", "temps"),
+        _vec(u_accept, rows, "torch.float32", "u_accept"),
+        _vec(u_sample, n, "torch.float32", "u_sample"),
+        _vec(n_accepted, n, "torch.int32", "n_accepted"),
+        _vec(next_token, n, "torch.int32", "next_token"),
+        getattr(stream, "cuda_stream", stream)))
 
 
 # ------------------------------------------------------------------ scheduler

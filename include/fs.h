@@ -131,8 +131,9 @@ int fs_create(const fs_model_desc* desc, const fs_weights* weights,
 /* Frees every device buffer of the handle. NULL is accepted. */
 int fs_destroy(fs_handle* h);
 
-/* Message of the last failed call on h (or of the last failed fs_create
- * when h is NULL). Valid until the next call on the same handle. */
+/* Message of the last failed call on h (or, when h is NULL, of this thread's
+ * last failed fs_create, fs_kv_q8_* or fs_verify_draft). Valid until the next
+ * call on the same handle. */
 const char* fs_last_error(const fs_handle* h);
 
 /* Kernels of h run on `stream` (a cudaStream_t) from now on. NULL selects
@@ -453,6 +454,133 @@ int fs_gemm_bf16_time(const uint16_t* W, int32_t N, int32_t K, const uint16_t* X
 int fs_gemm_bf16_noalloc(const uint16_t* W, int32_t N, int32_t K,
                          const uint16_t* X, int32_t B, float* Y,
                          int32_t splits, void* stream);
+
+/* ---- 8-bit paged KV cache: operators on the caller's device buffers -------
+ *
+ * The paged cache of the handle (pages of page_size tokens, a page table per
+ * lane) with keys and values held in 8 bits: half the bytes of a bf16 cache,
+ * which is what bounds decode attention over long contexts. A row (one token's
+ * key or value of one KV head) is head_dim codes and one f32 scale:
+ *   scale = amax / 127, code = round(x * 127 / amax), ties to even,
+ *   amax = max |x| of the row (0: scale 0 and codes 0),
+ * stored as the byte code + 128 (1 .. 255). A value stands for code * scale,
+ * off by at most scale / 2. A NaN is stored as 0, an infinity as the largest
+ * finite f32. Token t of a lane is in slot t % page_size of its page
+ * t / page_size. A lane outside [0, n_lanes), a token outside
+ * [0, max_pages * page_size) and a page-table entry outside [0, n_pages) hold
+ * nothing: they are never written, read as zeros, and get no weight.
+ *
+ * Every pointer is a DEVICE pointer on the current device, owned by the caller
+ * and used until the stream has passed the call; the struct itself is host
+ * memory, read during the call. The calls enqueue on `stream` (a cudaStream_t,
+ * NULL = default stream), allocate nothing, do not synchronise, and can be
+ * captured into a graph. Code arrays are 16-byte aligned, the others aligned
+ * to their element type.
+ * Errors of these calls, with nothing enqueued: FS_ERR_ARG (a NULL pointer, a
+ * size, a type, an alignment, memory of another device or of the host),
+ * FS_ERR_SCRATCH (workspace too small); FS_ERR_CUDA (a launch failed). */
+typedef struct fs_kv_q8 {
+  uint8_t* k;       /* codes [n_pages][n_kv_heads][page_size][head_dim]       */
+  uint8_t* v;
+  float* k_scale;   /* [n_pages][n_kv_heads][page_size]                       */
+  float* v_scale;
+  const int32_t* page_table; /* [n_lanes][max_pages]                          */
+  int32_t n_pages;
+  int32_t n_kv_heads;
+  int32_t page_size;  /* any positive number                                  */
+  int32_t head_dim;   /* 64, 128 or 256                                       */
+  int32_t n_lanes;
+  int32_t max_pages;
+} fs_kv_q8;
+
+/* Quantises n tokens' keys and values as they are written: row i (k + i *
+ * k_stride and v + i * v_stride elements, [n_kv_heads][head_dim] of dtype
+ * FS_DTYPE_F32 or _BF16) goes to token positions[i] of lane lanes[i]. With
+ * rope_cos / rope_sin (f32 [rope_len][head_dim / 2]) the key is first rotated
+ * by its position, pairs (j, j + head_dim / 2); NULL for both stores keys as
+ * they are. A row whose position is outside [0, rope_len) or outside the cache
+ * is skipped, so -1 pads a batch. Two rows of one call must not name the same
+ * token: which of them the slot then holds is not specified (it may mix the
+ * two). A code is exact: the rounding of the real quotient, also next to a
+ * border. */
+int fs_kv_q8_append(const fs_kv_q8* cache, const void* k, const void* v, int64_t k_stride,
+                    int64_t v_stride, int32_t dtype, const int32_t* lanes,
+                    const int32_t* positions, int32_t n, const float* rope_cos,
+                    const float* rope_sin, int32_t rope_len, void* stream);
+
+/* Reads n tokens back: the values of token positions[i] of lane lanes[i] into
+ * row i of k_out and v_out (either may be NULL; strides and dtype as for
+ * fs_kv_q8_append, one rounding of code * scale to f32 and one more to bf16).
+ * A token that the cache cannot hold reads as zeros. */
+int fs_kv_q8_read(const fs_kv_q8* cache, const int32_t* lanes, const int32_t* positions,
+                  int32_t n, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                  int32_t dtype, void* stream);
+
+/* Bytes of workspace fs_kv_q8_attention needs for the same n, n_heads,
+ * max_len and split_len on the current device (0 when no row is split), or a
+ * negative FS_ERR_* code. Only n_kv_heads, page_size, head_dim and max_pages
+ * of the cache are looked at. */
+int64_t fs_kv_q8_attention_workspace(const fs_kv_q8* cache, int32_t n, int32_t n_heads,
+                                     int32_t max_len, int32_t split_len);
+
+/* Attention of one new token a row: row i attends to tokens 0 .. lengths[i] - 1
+ * of lane lanes[i]. q and out are n rows of [n_heads][head_dim] of dtype
+ * (FS_DTYPE_F32 or _BF16), q_stride and out_stride elements apart; head h reads
+ * KV head h / (n_heads / n_kv_heads), at most 8 heads per KV head. scale
+ * multiplies the scores (usually 1 / sqrt(head_dim)). With rope_cos / rope_sin
+ * q is rotated by position lengths[i] - 1 (the token it belongs to). max_len is
+ * an upper bound of the lengths, which sizes the launch (0: max_pages *
+ * page_size; at most rope_len when q is rotated): a longer row attends to its
+ * first max_len tokens. A row of length 0 (or less), or whose tokens the cache
+ * does not hold, gives zeros. Several rows may name one lane (the rows of a
+ * drafted continuation, each with its own length).
+ *
+ * Long rows are cut into splits of split_len tokens (a multiple of 64), joined
+ * in ascending order; 0 chooses from n, n_kv_heads and max_len. A row's bits
+ * depend on its own inputs and split_len alone: give split_len for results
+ * that do not depend on the batch. Scores, softmax sums and outputs are held
+ * in f32; the result is rounded once. workspace (16-byte aligned) may be NULL
+ * when fs_kv_q8_attention_workspace says 0, is needed only during the call's
+ * own kernels and starts with any content; calls that may run at the same time
+ * (other streams, other captured graphs) need one each. */
+int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
+                       const int32_t* lanes, const int32_t* lengths, int32_t n,
+                       int32_t n_heads, int32_t max_len, float scale, const float* rope_cos,
+                       const float* rope_sin, int32_t rope_len, void* out, int64_t out_stride,
+                       int32_t dtype, int32_t split_len, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Verifies drafted tokens against the target's logits (the step after
+ * fs_step_batch_chunked on a drafted continuation; the rejected suffix then
+ * leaves the cache with fs_lane_evict). Sequence s owns rows row_start[s] ..
+ * row_start[s + 1] - 1 of logits (f32 [n_rows][vocab], rows logits_stride
+ * elements apart): one row per drafted token, in order, and one more for the
+ * token after them all. Row r's draft is draft[r], drawn by the draft model
+ * with the probabilities draft_probs row r (f32 [n_rows][vocab], rows
+ * probs_stride apart) or, when draft_probs is NULL, given without any (a lookup
+ * in the prompt: probability 1); the last row of a sequence has no draft, its
+ * entries are not read. With z the row's logits and p = softmax(z / T),
+ * T = temps[s], in order:
+ *   accept draft x while u_accept[r] * q(x) < p(x);
+ *   at the first that is not accepted the next token is drawn from
+ *   max(p - q, 0) (without probabilities: p with x taken out; p itself if
+ *   nothing is left); if all are, from the last row's p.
+ * The draw takes the first token whose running sum of weights reaches
+ * u_sample[s] times their total and whose weight is not zero. T = 0 (or
+ * not positive) is greedy: x is accepted when it is the row's argmax, and the
+ * next token is the argmax (lowest index on ties). Logits of -inf or NaN have
+ * no probability; equal +inf logits share all of it; a row with no token at all
+ * accepts nothing and gives token 0. A draft outside [0, vocab) is never
+ * accepted. Random numbers are in [0, 1). Weights of the draw are held to a
+ * relative 2^-40 and summed in 64 bits.
+ * Writes n_accepted[s] and next_token[s]; a sequence without rows gets 0
+ * and -1. row_start has n_seqs + 1 ascending entries in [0, n_rows] (others are
+ * clamped). Pointers, stream and errors as for fs_kv_q8_append. */
+int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,
+                    const int32_t* row_start, int32_t n_seqs, const int32_t* draft,
+                    const float* draft_probs, int64_t probs_stride, const float* temps,
+                    const float* u_accept, const float* u_sample, int32_t* n_accepted,
+                    int32_t* next_token, void* stream);
 
 #ifdef __cplusplus
 }

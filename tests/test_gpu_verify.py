@@ -1,0 +1,167 @@
+"""GPU: verification of drafted tokens (fs_verify_draft) against the rule in 64
+bits (tests/_q8_ref.py). Results are whole numbers and compared exactly: the
+weights are good to 2^-40, so a number would have to fall within about 1e-12 of
+a border to be answered otherwise."""
+import numpy as np
+import pytest
+
+from continuous_transformer_decode_gb300 import fs
+from tests import _q8_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from continuous_transformer_decode_gb300 import build
+    build.build()
+
+
+def _cuda(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def softmax(z):
+    e = np.exp(z - z.max(-1, keepdims=True))
+    return e / e.sum(-1, keepdims=True)
+
+
+def make(rng, drafts, V, probs=True, greedy=0.3, spread=2.5):
+    drafts = np.asarray(drafts)
+    start = np.concatenate([[0], np.cumsum(drafts + 1)]).astype(np.int32)
+    rows, n = int(start[-1]), len(drafts)
+    logits = (spread * rng.standard_normal((rows, V))).astype(np.float32)
+    other = logits + 0.7 * rng.standard_normal((rows, V)).astype(np.float32)
+    temps = np.where(rng.random(n) < greedy, 0, rng.uniform(0.5, 1.3, n)).astype(np.float32)
+    seq = np.repeat(np.arange(n), drafts + 1)
+    q = softmax(other / np.where(temps > 0, temps, 1)[seq][:, None]).astype(np.float32)
+    draft = np.array([rng.choice(V, p=r.astype(np.float64) / r.astype(np.float64).sum()) for r in q], np.int32)
+    draft = np.where(temps[seq] > 0, draft, other.argmax(-1)).astype(np.int32)
+    return dict(logits=logits, row_start=start, draft=draft, probs=q if probs else None, temps=temps,
+                u_accept=rng.random(rows).astype(np.float32), u_sample=rng.random(n).astype(np.float32))
+
+
+def run(c, stream=None, out=None):
+    import torch
+    n = len(c["temps"])
+    acc, nxt = out or (torch.full((n,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    fs.fs_verify_draft(_cuda(c["logits"]), _cuda(c["row_start"]), _cuda(c["draft"]),
+                       None if c["probs"] is None else _cuda(c["probs"]), _cuda(c["temps"]),
+                       _cuda(c["u_accept"]), _cuda(c["u_sample"]), acc, nxt, stream=stream)
+    torch.cuda.synchronize()
+    return acc.cpu().numpy(), nxt.cpu().numpy()
+
+
+def check(c):
+    got, want = run(c), R.verify(**c)
+    assert np.array_equal(got[0], want[0]), (got[0], want[0])
+    assert np.array_equal(got[1], want[1]), (got[1], want[1])
+    return want
+
+
+@pytest.mark.parametrize("V", [1, 2, 31, 257, 1000, 4099, 32000, 49152, 70001])
+@pytest.mark.parametrize("probs", [True, False])
+def test_rule(V, probs):
+    rng = np.random.default_rng(V)
+    big = V > 20000
+    drafts = [4, 0, 7, 1] if big else [0, 1, 2, 5, 9, 3, 3, 0, 4, 4, 6, 2]
+    check(make(rng, drafts, V, probs))
+
+
+def test_every_outcome_is_met():
+    """Acceptance of none, some and all drafted tokens, greedy and sampled."""
+    rng = np.random.default_rng(0)
+    for greedy in (0.0, 1.0):
+        c = make(rng, [3] * 200, 50, True, greedy)
+        acc, _ = check(c)
+        assert set(acc.tolist()) == {0, 1, 2, 3}
+
+
+def test_distribution_is_the_targets():
+    """The first token that comes out is distributed as the target says, whatever
+    the draft: 20000 sequences of one draft, chi-square of 8 tokens below its
+    1 - 1e-6 quantile (7 degrees of freedom: 40.5)."""
+    rng = np.random.default_rng(3)
+    n, V = 20000, 8
+    z = rng.standard_normal(V).astype(np.float32)
+    q = softmax(rng.standard_normal(V)).astype(np.float32)
+    p = softmax(z.astype(np.float64) / 0.8)
+    c = dict(logits=np.tile(z, (2 * n, 1)), row_start=np.arange(0, 2 * n + 1, 2, dtype=np.int32),
+             draft=rng.choice(V, size=2 * n, p=q / q.astype(np.float64).sum()).astype(np.int32),
+             probs=np.tile(q, (2 * n, 1)), temps=np.full(n, 0.8, np.float32),
+             u_accept=rng.random(2 * n).astype(np.float32), u_sample=rng.random(n).astype(np.float32))
+    acc, nxt = run(c)
+    first = np.where(acc > 0, c["draft"][::2], nxt)
+    count = np.bincount(first, minlength=V)
+    assert ((count - n * p) ** 2 / (n * p)).sum() < 40.5
+
+
+def test_edges():
+    rng = np.random.default_rng(1)
+    c = make(rng, [2] * 12, 300, True, 0.0)
+    z, d = c["logits"], c["draft"]
+    z[0] = -np.inf                                   # no token at all
+    z[3, :] = -np.inf
+    z[3, 17] = 2.0                                   # one token
+    z[6, 5] = z[6, 9] = np.inf                       # two tokens share everything
+    z[9, ::2] = -np.inf                              # masked halves
+    z[12, 1::2] = np.finfo(np.float32).min           # masks of the type's lowest value
+    z[15, 4] = np.nan
+    c["u_accept"][18], d[18] = 0.0, int(np.argmin(z[18]))
+    d[21], d[24] = -1, 300                           # no such tokens
+    c["u_sample"][:] = rng.random(12)
+    c["u_sample"][8], c["u_sample"][9] = 0.0, np.float32(1 - 2.0 ** -24)
+    c["probs"][27] = softmax(z[27] / c["temps"][9])  # the draft is the target
+    c["temps"][10], c["temps"][11] = 1e-3, 1e4
+    check(c)
+    c["temps"][:6] = 0
+    c["temps"][6], c["temps"][7] = -1.0, np.nan      # not positive: greedy
+    check(c)
+    c["probs"] = None
+    check(c)
+
+
+def test_sequences_without_rows_and_clamped_starts():
+    rng = np.random.default_rng(2)
+    c = make(rng, [1, 2, 0], 40)
+    c["row_start"] = np.array([0, 0, 2, 2, 5, 6, 9, -3], np.int32)  # 6 rows
+    n = 7
+    c["temps"] = np.full(n, 0.9, np.float32)
+    c["u_sample"] = rng.random(n).astype(np.float32)
+    acc, nxt = check(c)
+    assert nxt[0] == -1 and nxt[2] == -1
+
+
+def test_ties_of_greedy_go_to_the_lowest_index():
+    rng = np.random.default_rng(4)
+    c = make(rng, [1] * 40, 5000, True, 1.0)
+    c["logits"] = np.round(c["logits"])
+    check(c)
+
+
+def test_strided_rows_streams_and_graphs():
+    import torch
+    rng = np.random.default_rng(5)
+    cs = [make(rng, [3, 0, 5], 3001), make(rng, [1, 6, 1], 3001)]
+    wide = [torch.zeros(int(c["row_start"][-1]), 4000, device="cuda") for c in cs]
+    graphs = []
+    for c, w in zip(cs, wide):
+        w[:, 7:3008] = _cuda(c["logits"])
+        args = [_cuda(c[k]) for k in ("row_start", "draft", "probs", "temps", "u_accept", "u_sample")]
+        out = [torch.full((3,), -9, dtype=torch.int32, device="cuda") for _ in range(2)]
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            fs.fs_verify_draft(w[:, 7:3008], *args, *out, stream=torch.cuda.current_stream())
+        graphs.append((st, g, out, args))
+    for _ in range(10):
+        for st, g, *_ in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (_, _, out, _) in zip(cs, graphs):
+        want = R.verify(**c)
+        assert np.array_equal(out[0].cpu().numpy(), want[0])
+        assert np.array_equal(out[1].cpu().numpy(), want[1])
