@@ -1,6 +1,6 @@
 """GPU: verification of drafted tokens (fs_verify_draft) against the rule in 64
 bits (tests/_q8_ref.py). Results are whole numbers and compared exactly: the
-weights are good to 2^-40, so a number would have to fall within about 1e-12 of
+weights are good to 2^-36, so a number would have to fall within about 1e-11 of
 a border to be answered otherwise."""
 import numpy as np
 import pytest
