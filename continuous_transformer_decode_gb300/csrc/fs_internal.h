@@ -509,7 +509,7 @@ struct AttnQ8 {
 };
 // Positions per split of one call (a multiple of 64).
 int attn_q8_split_len(int n, int Hkv, int max_len, int sms);
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s);
+int launch_attention_q8(const AttnQ8& a, int x_type, cudaStream_t s);  // q and out
 
 // Verification of drafted tokens (k_verify.cu).
 struct VerifyArgs {

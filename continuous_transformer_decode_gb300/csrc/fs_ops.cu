@@ -50,6 +50,8 @@ const char* bad_cache(const fs_kv_q8* c) {
   if (c->n_kv_heads < 1 || c->page_size < 1 || c->max_pages < 1)
     return "n_kv_heads, page_size and max_pages must be positive";
   if ((int64_t)c->max_pages * c->page_size > kMaxTokens) return "a lane may hold 2^30 tokens";
+  if (c->n_pages > 0 && (int64_t)c->n_kv_heads * c->page_size > (((int64_t)1 << 32) - 2) / c->n_pages)
+    return "the cache may hold 2^32 - 2 rows";
   return nullptr;
 }
 const char* bad_buffers(const fs_kv_q8* c) {
@@ -238,7 +240,7 @@ int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
   a.split_len = p.split_len; a.n_splits = p.n_splits;
   a.part_acc = static_cast<float*>(workspace);
   a.part_ml = a.part_acc ? a.part_acc + (int64_t)n * p.n_splits * n_heads * cache->head_dim : nullptr;
-  return launched(launch_attention_q8(a, xt, xt, (cudaStream_t)stream));
+  return launched(launch_attention_q8(a, xt, (cudaStream_t)stream));
 }
 
 int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,

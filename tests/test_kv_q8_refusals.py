@@ -61,7 +61,8 @@ BAD_CACHE = [dict(head_dim=32), dict(head_dim=96), dict(head_dim=0), dict(page_s
              dict(n_kv_heads=0), dict(max_pages=0), dict(n_pages=0), dict(n_lanes=0),
              dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None),
              dict(page_table=None), dict(k=P + 8), dict(v=P + 1), dict(k_scale=P + 2),
-             dict(page_table=P + 1), dict(max_pages=1 << 27)]
+             dict(page_table=P + 1), dict(max_pages=1 << 27),
+             dict(n_pages=1 << 27)]
 
 
 @pytest.mark.parametrize("bad", BAD_CACHE)
