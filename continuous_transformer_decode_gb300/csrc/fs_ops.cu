@@ -18,6 +18,7 @@ int refuse(int code, const char* why) {
   return code;
 }
 
+constexpr int kMaxSplits = 8192;      // of a row: the join keeps a weight of each in shared memory
 constexpr int kMaxTokens = 1 << 30;  // token + split arithmetic stays in 32 bits
 
 int x_type(int32_t dtype) {
@@ -134,6 +135,7 @@ int plan_attention(const fs_kv_q8* c, int32_t n, int32_t n_heads, int32_t max_le
     p->split_len = attn_q8_split_len(n, c->n_kv_heads, p->max_len, sms);
   }
   const int64_t ns = ((int64_t)p->max_len + p->split_len - 1) / p->split_len;
+  if (ns > kMaxSplits) return refuse(FS_ERR_ARG, "split_len too small for max_len (8192 splits)");
   p->n_splits = (int)ns;
   p->bytes = ns <= 1 ? 0 : (int64_t)n * ns * n_heads * (c->head_dim + 2) * 4;
   return FS_OK;

@@ -8,22 +8,28 @@
 // cores' rate even of warp MMAs, so the kernel is bound by HBM if a code costs
 // few instructions on its way. What that comes to:
 //   * one block takes a split of one (row, KV head); each of its warps runs
-//     through slices of 32 tokens with its own ring of stages filled by
-//     cp.async, with no barrier in the loop;
+//     through slices of 32 tokens (16 at head_dim 256) with its own ring of
+//     stages filled by cp.async, with no barrier in the loop; the page of a
+//     slice is looked up one slice before its copies are issued;
 //   * a byte becomes an f16 in one byte permute and half an addition: the byte
 //     below 0x64 is 1024 + byte, less 1152 is the code, exact. (A bf16 would
 //     take four instructions for two codes instead of two.)
-//   * S = Q K^T and O += W V are m16n8k16 f16 MMAs. The order of the inner
+//   * S = Q K^T and O^T += V^T W are m16n8k16 f16 MMAs. The order of the inner
 //     index is free, so a thread's 16 bytes of a key row are its operands of four
 //     k-steps, and 16 bytes of four value rows, interleaved by byte permutes,
-//     those of sixteen n-tiles: no ldmatrix, no transpose. Rows 0..7 of A hold
-//     the high f16 part of a head's q or weights and rows 8..15 what is left
-//     (22 bits together), which costs nothing as a KV head has at most 8 heads;
+//     those of eight m-tiles: no ldmatrix, no transpose. q and the weights are two
+//     f16 parts (22 bits): of q in rows 0..7 and 8..15 of A, which costs nothing
+//     as a KV head has at most 8 heads; of the weights in two MMAs into one
+//     accumulator, half the registers of W V with its two parts in rows;
 //   * f16 is narrow, so q is brought to [2^13, 2^14) by a power of two per head,
-//     and the weights w_t = exp2(s_t - R) vs_t are kept below 2^14 by a running
-//     reference R, the maximum of s_t + log2(vs_t) less 13 (and not less than the
-//     maximum of s less 126, for exp2's range), beside the softmax's own maximum
-//     and sum. The scores are in log2 units.
+//     and the weights w_t = exp2(s_t - R) vs_t are kept in f16's range by a
+//     reference R per head: the maximum of s_t + log2(vs_t) less 13 when it was
+//     set (and not less than the maximum of s less 110, for exp2's range), set
+//     anew only when a weight would pass 2^15.9. The softmax's sum has a reference of its
+//     own, m. So most slices look at their scores with one vote, and neither
+//     shuffle a maximum nor rescale the accumulators. Scores are in log2 units;
+//     the largest weight is at least 2^13 in f16 (values below 2^-97 apart), so
+//     each is held to 2^-22 of itself or 2^-38 of the largest.
 // The warps, then the splits of a row (by a second kernel), are joined in order:
 // a row's bits depend on its own inputs and split_len alone.
 
@@ -39,22 +45,39 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
-constexpr int kT = 32 * kWarps;
 constexpr int kG = 8;    // query heads per KV head at most
-constexpr int kS = 32;   // tokens per slice
 constexpr unsigned kAll = 0xffffffffu;
-constexpr unsigned kNone = 0xffffffffu;  // no slot
+
+// Warps of a block, blocks an SM, tokens of a slice, and stages of a warp's ring
+// (one in use, the others in flight).
+template <int HD>
+struct Shape;
+template <>
+struct Shape<64> {
+  static constexpr int kWarps = 4, kBlocks = 4, kS = 32, kStages = 3;
+};
+template <>
+struct Shape<128> {
+  static constexpr int kWarps = 4, kBlocks = 3, kS = 32, kStages = 2;
+};
+template <>
+struct Shape<256> {
+  static constexpr int kWarps = 8, kBlocks = 1, kS = 16, kStages = 3;
+};
 
 template <int HD>
-struct Lay {
-  static constexpr int kStages = HD == 64 ? 4 : 3;  // slices in flight per warp, and one in use
-  static constexpr int kK = kS * HD;                // bytes of a slice's key codes
+struct Lay : Shape<HD> {
+  using Shape<HD>::kWarps;
+  using Shape<HD>::kS;
+  using Shape<HD>::kStages;
+  static constexpr int kT = 32 * kWarps;
+  static constexpr int kK = kS * HD;                 // bytes of a slice's key codes
   static constexpr int kStage = 2 * kK + 2 * kS * 4 + 16;  // codes, scales, mask of tokens
   static constexpr int kWarpBytes = kStages * kStage;
   static constexpr int kMerge = (int)sizeof(float) * (kG * HD + 2 * kG);  // a warp's (o, m, l)
+  static constexpr int kQa = HD / 16 * 32 * 16;  // q's A fragments, 16 bytes a lane and k-step
   static constexpr int kBytes =
-      kWarps * (kWarpBytes > kMerge ? kWarpBytes : kMerge) + (int)sizeof(float) * kG * (HD + 1);
+      kWarps * (kWarpBytes > kMerge ? kWarpBytes : kMerge) + kQa + (int)sizeof(float) * kG;
 };
 
 // Byte offset of (row r < 32, 16-byte chunk c) in a slice's codes. The exclusive
@@ -74,17 +97,11 @@ __device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bf
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+__device__ __forceinline__ uint2 lds64(const uint8_t* p) {
+  return *reinterpret_cast<const uint2*>(p);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -112,11 +129,27 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
 }
 __device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two m-tiles of V^T W: a0 .. a3 are the same four columns (bytes) of tokens 2 cq,
+// 2 cq + 1, 2 cq + 8, 2 cq + 9; interleaved by twos they are the A operands,
+// columns 0 and 1 rows gq and gq + 8 of the first tile, 2 and 3 of the second.
+// w: the head's weights of these tokens (hi 0 1, lo 0 1, hi 2 3, lo 2 3).
+__device__ __forceinline__ void value_tiles(float (*o)[4], const uint32_t w[4], uint32_t a0,
+                                            uint32_t a1, uint32_t a2, uint32_t a3) {
+  const uint32_t p0 = __byte_perm(a0, a1, 0x5140), p1 = __byte_perm(a0, a1, 0x7362);
+  const uint32_t p2 = __byte_perm(a2, a3, 0x5140), p3 = __byte_perm(a2, a3, 0x7362);
+  const uint32_t x[4] = {codes2(p0, 0x4140u), codes2(p0, 0x4342u), codes2(p2, 0x4140u),
+                         codes2(p2, 0x4342u)};
+  const uint32_t y[4] = {codes2(p1, 0x4140u), codes2(p1, 0x4342u), codes2(p3, 0x4140u),
+                         codes2(p3, 0x4342u)};
+  mma_f16(o[0], x, w[0], w[2]);
+  mma_f16(o[1], y, w[0], w[2]);
+  mma_f16(o[0], x, w[1], w[3]);
+  mma_f16(o[1], y, w[1], w[3]);
 }
 // Word w of a 16-byte vector (w a constant after unrolling).
 __device__ __forceinline__ uint32_t word(const uint4& v, int w) {
@@ -128,11 +161,12 @@ __device__ __forceinline__ int row_len(const AttnQ8& a, int i) {
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
+__global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ8 a) {
   using L = Lay<HD>;
+  constexpr int kWarps = L::kWarps, kT = L::kT, kS = L::kS;
   constexpr int kHalf = HD / 2;
   constexpr int kKs = HD / 16;         // k-steps of Q K^T
-  constexpr int kNt = HD / 8;          // n-tiles of W V
+  constexpr int kMt = HD / 16;         // m-tiles of V^T W
   constexpr int kRowChunks = HD / 16;  // 16-byte chunks per row
   pdl_wait();
   pdl_trigger();
@@ -149,64 +183,105 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
 
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + warp * L::kWarpBytes;
-  float* qs = reinterpret_cast<float*>(smem + L::kBytes) - kG * (HD + 1);  // [kG][HD]
-  float* qf = qs + kG * HD;                                                // [kG]
+  uint8_t* qa = smem + L::kBytes - L::kQa - (int)sizeof(float) * kG;  // [kKs][32] uint4
+  float* qf = reinterpret_cast<float*>(qa + L::kQa);                  // [kG]
 
-  // ---- the ring: slice i of this warp is tokens t0(i) .. t0(i) + 31
+  // ---- the ring: slice i of this warp is tokens t0(i) .. t0(i) + kS - 1; lane l
+  // follows token t0(i) + l, its page in the lane's table and its slot in the page
   const int n_slices = (end - start + kS - 1) / kS;
   const int mine = (n_slices - warp + kWarps - 1) / kWarps;
-  const int row_lane = a.lanes[b];
-  auto slot_of = [&](int i) -> unsigned {  // of token `lane` of slice i
-    const int t = start + (i * kWarps + warp) * kS + lane;
-    if (i >= mine || t >= end) return kNone;
-    const int64_t x = q8::slot_of(a.kv, row_lane, t, g);
-    return x < 0 ? kNone : (unsigned)x;
+  const int row_lane = a.lanes[b], ps = a.kv.page_size;
+  const bool no_lane = (unsigned)row_lane >= (unsigned)a.kv.n_lanes;
+  const int32_t* pages = a.kv.page_table + (no_lane ? 0 : (int64_t)row_lane * a.kv.max_pages);
+  constexpr int kStep = kWarps * kS;
+  const int step_page = kStep / ps, step_slot = kStep % ps;
+  int t_next = start + warp * kS + lane, p_next = t_next / ps, s_next = t_next % ps;
+  // (page as the table has it, slot) of this lane's token of the next slice; -1: no token
+  auto look_up = [&](int& page, int& slot) {
+    page = lane < kS && t_next < end && !no_lane ? pages[p_next] : -1;
+    slot = s_next;
+    t_next += kStep;
+    p_next += step_page;
+    s_next += step_slot;
+    if (s_next >= ps) {
+      s_next -= ps;
+      ++p_next;
+    }
   };
-  auto issue = [&](int i, unsigned slot) {
-    uint8_t* st = ring + (i % L::kStages) * L::kStage;
+  auto issue = [&](uint8_t* st, int page, int in_page) {
     const uint32_t kb = smem_u32(st);
+    const bool in = (unsigned)page < (unsigned)a.kv.n_pages;
+    const unsigned slot = ((unsigned)page * a.kv.Hkv + g) * ps + in_page;
+    const unsigned mask = __ballot_sync(kAll, in);
 #pragma unroll
     for (int j = 0; j < kS * kRowChunks / 32; ++j) {
       const int x = lane + 32 * j, r = x / kRowChunks, c = x % kRowChunks;
       const unsigned sl = __shfl_sync(kAll, slot, r);
-      if (sl != kNone) {
+      if (mask >> r & 1) {
         const int64_t off = (int64_t)sl * HD + c * 16;
         cp_async16(kb + at<HD>(r, c), a.kv.k + off);
         cp_async16(kb + L::kK + at<HD>(r, c), a.kv.v + off);
       }
     }
     float* sc = reinterpret_cast<float*>(st + 2 * L::kK);  // [kS] ks, [kS] vs
-    if (slot != kNone) {
+    if (in) {
       cp_async4(smem_u32(sc + lane), a.kv.ks + slot);
       cp_async4(smem_u32(sc + kS + lane), a.kv.vs + slot);
-    } else {
+    } else if (lane < kS) {
       sc[lane] = sc[kS + lane] = 0.0f;
     }
-    const unsigned mask = __ballot_sync(kAll, slot != kNone);
     if (lane == 0) *reinterpret_cast<unsigned*>(sc + 2 * kS) = mask;
     cp_commit();
   };
+  int page[L::kStages], slot[L::kStages];
 #pragma unroll
-  for (int i = 0; i < L::kStages - 1; ++i) issue(i, slot_of(i));
-  unsigned next_slot = slot_of(L::kStages - 1);
+  for (int i = 0; i < L::kStages; ++i) look_up(page[i], slot[i]);
 
-  // ---- q, rotated; warp w brings heads w, w + 4 to [2^13, 2^14)
+  // ---- q, rotated; warp w takes heads w, w + kWarps, ..
   const T* qr = static_cast<const T*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
-  for (int h = warp; h < kG; h += kWarps) {
-    float x0[kHalf / 32], x1[kHalf / 32], mx = 0.0f;
+  constexpr int kHeads = kG / kWarps, kP = kHalf / 32;
+  float x0[kHeads][kP], x1[kHeads][kP];
 #pragma unroll
-    for (int j = 0; j < kHalf / 32; ++j) {
-      const int i = lane + 32 * j;
-      x0[j] = h < G ? ld1(qr + h * HD + i) : 0.0f;
-      x1[j] = h < G ? ld1(qr + h * HD + i + kHalf) : 0.0f;
-      if (a.rc) {
-        const int64_t p = (int64_t)(len - 1) * kHalf + i;
-        float y0, y1;
-        rope_pair(x0[j], x1[j], a.rc[p], a.rs[p], y0, y1);
-        x0[j] = y0;
-        x1[j] = y1;
-      }
-      mx = fmaxf(mx, fmaxf(fabsf(x0[j]), fabsf(x1[j])));
+  for (int u = 0; u < kHeads; ++u)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      const int h = warp + u * kWarps, i = lane + 32 * j;
+      x0[u][j] = h < G ? ld1(qr + h * HD + i) : 0.0f;
+      x1[u][j] = h < G ? ld1(qr + h * HD + i + kHalf) : 0.0f;
+    }
+#pragma unroll
+  for (int i = 0; i < L::kStages - 1; ++i) issue(ring + i * L::kStage, page[i], slot[i]);
+  int next_page = page[L::kStages - 1], next_slot = slot[L::kStages - 1];
+  float rc[kP], rs[kP];
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int64_t p = (int64_t)(len - 1) * kHalf + lane + 32 * j;
+    rc[j] = a.rc ? a.rc[p] : 1.0f;
+    rs[j] = a.rc ? a.rs[p] : 0.0f;
+  }
+  // element d of head h in the A fragments: chunk d / 16 is the j-th chunk of thread
+  // column cq, and word w of it (elements 4 w .. 4 w + 3) k-step 4 j + w; the
+  // lane's 16 bytes are (hi 0 1, lo 0 1, hi 2 3, lo 2 3)
+  auto put_q = [&](int h, int d, float x) {
+    const int chunk = d / 16, w = d % 16 / 4, e = d % 4;
+    const int c = HD == 64 ? chunk : (chunk % 8) / 2;
+    const int j = HD == 64 ? 0 : chunk % 2 + chunk / 8 * 2;
+    const __half hi = __float2half_rn(x);
+    __half* f = reinterpret_cast<__half*>(qa + ((4 * j + w) * 32 + h * 4 + c) * 16) + (e & 1) + (e & 2) * 2;
+    f[0] = hi;
+    f[2] = __float2half_rn(x - __half2float(hi));
+  };
+#pragma unroll
+  for (int u = 0; u < kHeads; ++u) {
+    const int h = warp + u * kWarps;
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      float y0 = x0[u][j], y1 = x1[u][j];
+      if (a.rc) rope_pair(x0[u][j], x1[u][j], rc[j], rs[j], y0, y1);
+      x0[u][j] = y0;
+      x1[u][j] = y1;
+      mx = fmaxf(mx, fmaxf(fabsf(y0), fabsf(y1)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
@@ -215,97 +290,107 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
     e = max(-110, min(e, 127)) - 14;
     const float up = ldexpf(1.0f, -e);
 #pragma unroll
-    for (int j = 0; j < kHalf / 32; ++j) {
-      qs[h * HD + lane + 32 * j] = x0[j] * up;
-      qs[h * HD + lane + 32 * j + kHalf] = x1[j] * up;
+    for (int j = 0; j < kP; ++j) {
+      put_q(h, lane + 32 * j, x0[u][j] * up);
+      put_q(h, lane + 32 * j + kHalf, x1[u][j] * up);
     }
     if (lane == 0) qf[h] = ldexpf(a.scale * 1.4426950408889634f, e);
   }
   __syncthreads();
 
-  // A fragments: k-step 4 j + w of the thread holds elements 4 w .. 4 w + 3 of its
-  // j-th chunk of 16
   auto chunk_of = [&](int j) {
     return HD == 64 ? cq : HD == 128 ? 2 * cq + j : 2 * cq + (j & 1) + 8 * (j >> 1);
   };
-  uint32_t qa[kKs][4];
-#pragma unroll
-  for (int ks = 0; ks < kKs; ++ks) {
-    const float* q = qs + gq * HD + chunk_of(ks / 4) * 16 + (ks % 4) * 4;
-    split_f16(q[0], q[1], qa[ks][0], qa[ks][1]);
-    split_f16(q[2], q[3], qa[ks][2], qa[ks][3]);
-  }
   const float qfac = qf[gq];
-
-  float m_run = -CUDART_INF_F, z_run = -CUDART_INF_F, ref = -CUDART_INF_F, l_run = 0.0f;
-  float acc[kNt][4];
+  constexpr float kTop = 15.9f;  // a weight may reach 2^kTop before R is set anew
+  float m_ref = -CUDART_INF_F, ref = -CUDART_INF_F, l_run = 0.0f;
+  float acc[kMt][4];  // [tile][(column 0, column 1) x (head 2 cq, head 2 cq + 1)]
 #pragma unroll
-  for (int j = 0; j < kNt; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+  for (int j = 0; j < kMt; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 
+  int use = 0, fill = L::kStages - 1;  // stages: of this slice, and of the next to issue
   for (int i = 0; i < mine; ++i) {
-    // the stage that slice i - 1 was read from takes slice i + kStages - 1
-    issue(i + L::kStages - 1, next_slot);
-    next_slot = slot_of(i + L::kStages);
+    // the stage that the last slice was read from takes slice i + kStages - 1
+    issue(ring + fill * L::kStage, next_page, next_slot);
+    look_up(next_page, next_slot);
     cp_wait<L::kStages - 1>();
     __syncwarp();
-    uint8_t* st = ring + (i % L::kStages) * L::kStage;
-    const uint32_t kb = smem_u32(st), vb = kb + L::kK;
-    const float* sc = reinterpret_cast<const float*>(st + 2 * L::kK);
+    const uint8_t* kb = ring + use * L::kStage;
+    const uint8_t* vb = kb + L::kK;
+    const float* sc = reinterpret_cast<const float*>(kb + 2 * L::kK);
     const unsigned mask = *reinterpret_cast<const unsigned*>(sc + 2 * kS);
+    fill = use;
+    use = use + 1 == L::kStages ? 0 : use + 1;
     if (mask != 0) {
-      // ---- scores of the slice, 4 n-tiles of 8 tokens
-      float z[8], zs[8];
+      // ---- scores of the slice, n-tiles of 8 tokens
+      float z[kS / 4], zs[kS / 4];
       float mx = -CUDART_INF_F, zx = -CUDART_INF_F;
+      float d[kS / 8][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int nt = 0; nt < kS / 8; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kKs / 4; ++j) {
-          const uint4 kv = lds128(kb + at<HD>(8 * nt + gq, chunk_of(j)));
+      for (int j = 0; j < kKs / 4; ++j) {
+        uint4 kv[kS / 8];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t x = word(kv, w);
-            mma_f16(d, qa[4 * j + w], codes2(x, 0x4140u), codes2(x, 0x4342u));
+        for (int nt = 0; nt < kS / 8; ++nt) kv[nt] = lds128(kb + at<HD>(8 * nt + gq, chunk_of(j)));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {  // the n-tiles in turn: independent chains of MMAs
+          const uint4 q4 = lds128(qa + ((4 * j + w) * 32 + lane) * 16);
+          const uint32_t fr[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+          for (int nt = 0; nt < kS / 8; ++nt) {
+            const uint32_t x = word(kv[nt], w);
+            mma_f16(d[nt], fr, codes2(x, 0x4140u), codes2(x, 0x4342u));
           }
         }
+      }
+#pragma unroll
+      for (int nt = 0; nt < kS / 8; ++nt) {
         const float2 ks = *reinterpret_cast<const float2*>(sc + 8 * nt + 2 * cq);
         const float2 vs = *reinterpret_cast<const float2*>(sc + kS + 8 * nt + 2 * cq);
-        const bool in0 = mask >> (8 * nt + 2 * cq) & 1, in1 = mask >> (8 * nt + 2 * cq + 1) & 1;
-        z[2 * nt] = in0 ? (d[0] + d[2]) * (ks.x * qfac) : -CUDART_INF_F;
-        z[2 * nt + 1] = in1 ? (d[1] + d[3]) * (ks.y * qfac) : -CUDART_INF_F;
+        z[2 * nt] = (d[nt][0] + d[nt][2]) * (ks.x * qfac);
+        z[2 * nt + 1] = (d[nt][1] + d[nt][3]) * (ks.y * qfac);
         zs[2 * nt] = vs.x;
         zs[2 * nt + 1] = vs.y;
-        mx = fmaxf(mx, fmaxf(z[2 * nt], z[2 * nt + 1]));
-        zx = fmaxf(zx, fmaxf(z[2 * nt] + lg2(vs.x), z[2 * nt + 1] + lg2(vs.y)));
       }
-      // ---- running maximum and reference of the head (its four threads)
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-      zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-      zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 2));
-      if (__any_sync(kAll, mx > m_run || zx > z_run)) {
-        const float m_new = fmaxf(m_run, mx);
-        z_run = fmaxf(z_run, zx);
-        const float r_new = fmaxf(z_run - 13.0f, m_new - 126.0f);
-        l_run *= m_run == -CUDART_INF_F ? 0.0f : ex2(m_run - m_new);
-        const float f = ref == -CUDART_INF_F ? 0.0f : ex2(ref - r_new);
-        m_run = m_new;
-        ref = r_new;
+      if (mask != (kS == 32 ? kAll : (1u << (kS & 31)) - 1)) {  // a slice with absent tokens
 #pragma unroll
-        for (int j = 0; j < kNt; ++j) {
-          acc[j][0] *= f;
-          acc[j][1] *= f;
-          acc[j][2] *= f;
-          acc[j][3] *= f;
+        for (int e = 0; e < kS / 4; ++e)
+          if (!(mask >> (8 * (e / 2) + 2 * cq + e % 2) & 1)) z[e] = -CUDART_INF_F;
+      }
+#pragma unroll
+      for (int e = 0; e < kS / 4; ++e) {
+        mx = fmaxf(mx, z[e]);
+        zx = fmaxf(zx, z[e] + lg2(zs[e]));
+      }
+      if (__any_sync(kAll, mx > m_ref + kTop || zx > ref + kTop)) {
+        // the head's maxima (its four threads), and new references
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+        zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+        zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 2));
+        const float m_new = fmaxf(m_ref, mx);
+        const float r_new = fmaxf(ref, fmaxf(zx - 13.0f, m_new - 110.0f));
+        l_run *= m_ref == -CUDART_INF_F ? 0.0f : ex2(m_ref - m_new);
+        const float f = ref == -CUDART_INF_F ? 0.0f : ex2(ref - r_new);
+        m_ref = m_new;
+        ref = r_new;
+        const float f0 = __shfl_sync(kAll, f, 8 * cq), f1 = __shfl_sync(kAll, f, 8 * cq + 4);
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) {
+          acc[j][0] *= f0;
+          acc[j][1] *= f1;
+          acc[j][2] *= f0;
+          acc[j][3] *= f1;
         }
       }
-      // ---- weights, and O += W V in two k-steps of 16 tokens
+      // ---- weights, and O^T += V^T W in k-steps of 16 tokens
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < kS / 16; ++kk) {
         float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          l_run += ex2(z[4 * kk + e] - m_run);
+          l_run += ex2(z[4 * kk + e] - m_ref);
           w[e] = ex2(z[4 * kk + e] - ref) * zs[4 * kk + e];
         }
         uint32_t wa[4];
@@ -318,16 +403,9 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
           const uint2 v0 = lds64(vb + at<HD>(r0, c) + o), v1 = lds64(vb + at<HD>(r0 + 1, c) + o);
           const uint2 v2 = lds64(vb + at<HD>(r0 + 8, c) + o), v3 = lds64(vb + at<HD>(r0 + 9, c) + o);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t a0 = x ? v0.y : v0.x, a1 = x ? v1.y : v1.x;
-            const uint32_t a2 = x ? v2.y : v2.x, a3 = x ? v3.y : v3.x;
-            const uint32_t p0 = __byte_perm(a0, a1, 0x5140), p1 = __byte_perm(a0, a1, 0x7362);
-            const uint32_t p2 = __byte_perm(a2, a3, 0x5140), p3 = __byte_perm(a2, a3, 0x7362);
-            mma_f16(acc[4 * x], wa, codes2(p0, 0x4140u), codes2(p2, 0x4140u));
-            mma_f16(acc[4 * x + 1], wa, codes2(p0, 0x4342u), codes2(p2, 0x4342u));
-            mma_f16(acc[4 * x + 2], wa, codes2(p1, 0x4140u), codes2(p3, 0x4140u));
-            mma_f16(acc[4 * x + 3], wa, codes2(p1, 0x4342u), codes2(p3, 0x4342u));
-          }
+          for (int x = 0; x < 2; ++x)
+            value_tiles(acc + 2 * x, wa, x ? v0.y : v0.x, x ? v1.y : v1.x, x ? v2.y : v2.x,
+                        x ? v3.y : v3.x);
         } else {
 #pragma unroll
           for (int jj = 0; jj < HD / 128; ++jj) {
@@ -335,16 +413,9 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
             const uint4 v0 = lds128(vb + at<HD>(r0, c)), v1 = lds128(vb + at<HD>(r0 + 1, c));
             const uint4 v2 = lds128(vb + at<HD>(r0 + 8, c)), v3 = lds128(vb + at<HD>(r0 + 9, c));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t a0 = word(v0, x), a1 = word(v1, x), a2 = word(v2, x), a3 = word(v3, x);
-              const uint32_t p0 = __byte_perm(a0, a1, 0x5140), p1 = __byte_perm(a0, a1, 0x7362);
-              const uint32_t p2 = __byte_perm(a2, a3, 0x5140), p3 = __byte_perm(a2, a3, 0x7362);
-              float(*o)[4] = acc + 16 * jj + 4 * x;
-              mma_f16(o[0], wa, codes2(p0, 0x4140u), codes2(p2, 0x4140u));
-              mma_f16(o[1], wa, codes2(p0, 0x4342u), codes2(p2, 0x4342u));
-              mma_f16(o[2], wa, codes2(p1, 0x4140u), codes2(p3, 0x4140u));
-              mma_f16(o[3], wa, codes2(p1, 0x4342u), codes2(p3, 0x4342u));
-            }
+            for (int x = 0; x < 4; ++x)
+              value_tiles(acc + 8 * jj + 2 * x, wa, word(v0, x), word(v1, x), word(v2, x),
+                          word(v3, x));
           }
         }
       }
@@ -359,21 +430,18 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
   float* wo = reinterpret_cast<float*>(smem);  // [kWarps][kG][HD], then m and l [kWarps][kG]
   float* wm = wo + kWarps * kG * HD;
   float* wl = wm + kWarps * kG;
-  const float back = m_run == -CUDART_INF_F ? 0.0f : ex2(ref - m_run);
-  if (gq < G) {
-    float* o = wo + (warp * kG + gq) * HD;
+  const float back = m_ref == -CUDART_INF_F ? 0.0f : ex2(ref - m_ref);
+  const float back0 = __shfl_sync(kAll, back, 8 * cq), back1 = __shfl_sync(kAll, back, 8 * cq + 4);
+  float* o0 = wo + (warp * kG + 2 * cq) * HD;  // heads 2 cq and 2 cq + 1
 #pragma unroll
-    for (int j = 0; j < kNt; ++j) {
-      // n-tile j's columns 2 cq, 2 cq + 1 are chunks of those thread rows, byte j
-      const int d0 = HD == 64 ? 2 * cq * 8 + j : (2 * cq + 8 * (j / 16)) * 16 + j % 16;
-      const int d1 = d0 + (HD == 64 ? 8 : 16);
-      o[d0] = (acc[j][0] + acc[j][2]) * back;
-      o[d1] = (acc[j][1] + acc[j][3]) * back;
-    }
-    if (cq == 0) {
-      wm[warp * kG + gq] = m_run;
-      wl[warp * kG + gq] = l_run;
-    }
+  for (int j = 0; j < kMt; ++j) {  // tile j holds columns 2 j, 2 j + 1 of the thread's chunks
+    const int col = HD == 64 ? 8 * gq + 2 * j : (gq + 8 * (j / 8)) * 16 + 2 * (j % 8);
+    *reinterpret_cast<float2*>(o0 + col) = make_float2(acc[j][0] * back0, acc[j][2] * back0);
+    *reinterpret_cast<float2*>(o0 + HD + col) = make_float2(acc[j][1] * back1, acc[j][3] * back1);
+  }
+  if (cq == 0) {
+    wm[warp * kG + gq] = m_ref;
+    wl[warp * kG + gq] = l_run;
   }
   __syncthreads();
   const int64_t base = ((int64_t)b * a.n_splits + s) * H + g * G;
@@ -400,26 +468,66 @@ __global__ void __launch_bounds__(kT, HD == 256 ? 1 : 2) k_attn_q8(AttnQ8 a) {
   }
 }
 
-// Joins the splits of one (row, head) in split order.
+// Joins the splits of one (row, head): the weights of the splits first, then
+// HD / 4 columns of threads by kJ, column x taking splits x, x + kJ, .. in
+// order, and the kJ sums in order.
+constexpr int kJ = 8;
 template <typename T, int HD>
-__global__ void __launch_bounds__(HD) k_attn_q8_join(AttnQ8 a) {
+__global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
+  constexpr int kT = HD / 4 * kJ;
+  __shared__ float4 part[kJ][HD / 4];
+  __shared__ float red[2][kT / 32];
+  extern __shared__ float w[];  // [n_splits]
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int len = row_len(a, b);
   const int ns = (len + a.split_len - 1) / a.split_len;
   if (ns <= 1) return;
-  float M = -CUDART_INF_F, Lsum = 0.0f, A = 0.0f;
   const int64_t base = (int64_t)b * a.n_splits * a.H + h;
-  for (int q = 0; q < ns; ++q) M = fmaxf(M, a.part_ml[2 * (base + (int64_t)q * a.H)]);
-  for (int q = 0; q < ns; ++q) {
-    const int64_t x = base + (int64_t)q * a.H;
-    const float m = a.part_ml[2 * x], f = m == -CUDART_INF_F ? 0.0f : ex2(m - M);
-    Lsum = fmaf(a.part_ml[2 * x + 1], f, Lsum);
-    A = fmaf(a.part_acc[x * HD + d], f, A);
+  float M = -CUDART_INF_F;
+  for (int q = tid; q < ns; q += kT) {
+    w[q] = a.part_ml[2 * (base + (int64_t)q * a.H)];
+    M = fmaxf(M, w[q]);
   }
-  st1(static_cast<T*>(a.out) + b * a.out_stride + (int64_t)h * HD + d,
-      Lsum > 0.0f ? A / Lsum : 0.0f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+  if (tid % 32 == 0) red[0][tid / 32] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kT / 32; ++i) M = fmaxf(M, red[0][i]);
+  float Lsum = 0.0f;
+  for (int q = tid; q < ns; q += kT) {
+    const float f = w[q] == -CUDART_INF_F ? 0.0f : ex2(w[q] - M);
+    w[q] = f;
+    Lsum = fmaf(a.part_ml[2 * (base + (int64_t)q * a.H) + 1], f, Lsum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) Lsum += __shfl_xor_sync(kAll, Lsum, o);
+  if (tid % 32 == 0) red[1][tid / 32] = Lsum;
+  __syncthreads();
+  const int col = tid % (HD / 4), x = tid / (HD / 4);
+  float4 A = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4* src = reinterpret_cast<const float4*>(a.part_acc) + base * (HD / 4) + col;
+#pragma unroll 4
+  for (int q = x; q < ns; q += kJ) {
+    const float4 v = src[(int64_t)q * a.H * (HD / 4)];
+    A.x = fmaf(v.x, w[q], A.x);
+    A.y = fmaf(v.y, w[q], A.y);
+    A.z = fmaf(v.z, w[q], A.z);
+    A.w = fmaf(v.w, w[q], A.w);
+  }
+  part[x][col] = A;
+  __syncthreads();
+  if (tid >= HD) return;
+  Lsum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kT / 32; ++i) Lsum += red[1][i];
+  float o = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJ; ++i) o += reinterpret_cast<const float*>(part[i])[tid];
+  st1(static_cast<T*>(a.out) + b * a.out_stride + (int64_t)h * HD + tid,
+      Lsum > 0.0f ? o / Lsum : 0.0f);
 }
 
 template <typename T, int HD>
@@ -427,9 +535,9 @@ int launch_hd(const AttnQ8& a, cudaStream_t s) {
   // per device, so set on every call (a host-side store, well below a launch)
   cudaFuncSetAttribute(k_attn_q8<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        Lay<HD>::kBytes);
-  launch_k(k_attn_q8<T, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), kT, Lay<HD>::kBytes, s, a);
+  launch_k(k_attn_q8<T, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), Lay<HD>::kT, Lay<HD>::kBytes, s, a);
   if (a.n_splits == 1) return 1;
-  launch_k(k_attn_q8_join<T, HD>, dim3(a.H, a.n), HD, 0, s, a);
+  launch_k(k_attn_q8_join<T, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);
   return 2;
 }
 

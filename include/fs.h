@@ -535,8 +535,8 @@ int64_t fs_kv_q8_attention_workspace(const fs_kv_q8* cache, int32_t n, int32_t n
  * does not hold, gives zeros. Several rows may name one lane (the rows of a
  * drafted continuation, each with its own length).
  *
- * Long rows are cut into splits of split_len tokens (a multiple of 64), joined
- * in ascending order; 0 chooses from n, n_kv_heads and max_len. A row's bits
+ * Long rows are cut into splits of split_len tokens (a multiple of 64; at most
+ * 8192 splits), joined in a fixed order; 0 chooses from n, n_kv_heads and max_len. A row's bits
  * depend on its own inputs and split_len alone: give split_len for results
  * that do not depend on the batch. Scores, softmax sums and outputs are held
  * in f32; the result is rounded once. workspace (16-byte aligned) may be NULL

@@ -112,6 +112,10 @@ def test_attention_workspace():
         fs.fs_kv_q8_attention_workspace(c, 3, 5, 200, 64)
     with pytest.raises(fs.FsError):
         fs.fs_kv_q8_attention_workspace(c, 3, 4, 200, 65)
+    long = cache(max_pages=1 << 20)
+    assert fs.fs_kv_q8_attention_workspace(long, 1, 4, 8192 * 64, 64) > 0
+    with pytest.raises(fs.FsError):
+        fs.fs_kv_q8_attention_workspace(long, 1, 4, 8192 * 64 + 1, 64)
 
 
 @pytest.mark.parametrize("bad", [
