@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdlib>
 #include <utility>
 
@@ -186,6 +187,20 @@ inline cudaError_t launch_k_cluster(void (*kern)(K...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
+}
+
+// Lets `kern` use `smem` bytes of dynamic shared memory on the current device;
+// `done` (one static per kernel) remembers the devices on which it may.
+template <typename K>
+inline cudaError_t allow_smem(K kern, int smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 enum WType { W_F32 = 0, W_BF16 = 1, W_Q8 = 2 };

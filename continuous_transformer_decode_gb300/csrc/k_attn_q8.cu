@@ -532,9 +532,8 @@ __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
 
 template <typename T, int HD>
 int launch_hd(const AttnQ8& a, cudaStream_t s) {
-  // per device, so set on every call (a host-side store, well below a launch)
-  cudaFuncSetAttribute(k_attn_q8<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       Lay<HD>::kBytes);
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(k_attn_q8<T, HD>, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
   launch_k(k_attn_q8<T, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), Lay<HD>::kT, Lay<HD>::kBytes, s, a);
   if (a.n_splits == 1) return 1;
   launch_k(k_attn_q8_join<T, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);

@@ -25,9 +25,12 @@
 #include <math_constants.h>
 
 #include "fs_internal.h"
+#include "two_f32.cuh"
 
 namespace fsk {
 namespace {
+
+using namespace two;
 
 namespace cg = cooperative_groups;
 
@@ -55,29 +58,6 @@ __constant__ float2 kExp2[32] = {
     {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
     {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}};
 
-// An unevaluated sum h + l of two f32 numbers, |l| at most half a last place of h.
-struct Two {
-  float h, l;
-};
-__device__ __forceinline__ Two two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
-__device__ __forceinline__ Two fast_two_sum(float a, float b) {  // |a| >= |b|
-  const float s = __fadd_rn(a, b);
-  return {s, __fsub_rn(b, __fsub_rn(s, a))};
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-  const Two s = two_sum(a.h, b.h);
-  return fast_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-  const float p = __fmul_rn(a.h, b.h);
-  return fast_two_sum(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, __fmul_rn(a.l, b.h)));
-}
-__device__ __forceinline__ bool less(Two a, Two b) {
-  return a.h < b.h || (a.h == b.h && a.l < b.l);
-}
 __device__ __forceinline__ Two shfl_xor(Two v, int o) {
   return {__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
 }

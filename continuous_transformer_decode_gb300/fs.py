@@ -521,7 +521,17 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
 
 
 # ------------------------------------------------------- 8-bit paged KV cache
-_ROW_DTYPES = {"torch.float32": FS_DTYPE_F32, "torch.bfloat16": FS_DTYPE_BF16}
+class _Types:
+    """torch's types, once torch is there (this module does not import it)."""
+    f32 = bf16 = i32 = u8 = None
+
+
+def _types():
+    if _Types.f32 is None:
+        import torch
+        _Types.bf16, _Types.i32, _Types.u8 = torch.bfloat16, torch.int32, torch.uint8
+        _Types.f32 = torch.float32
+    return _Types
 
 
 def _refuse(why: str):
@@ -533,21 +543,22 @@ def _op_check(rc: int) -> None:
         raise FsError(rc, fs_last_error(None))
 
 
-def _vec(x, n: int, dtype: str, what: str):
-    """Address of a contiguous CUDA vector of n entries (None: NULL)."""
-    if x.numel() != n or str(x.dtype) != dtype or not x.is_cuda or not x.is_contiguous():
-        _refuse(f"{what}: a contiguous CUDA tensor of {n} {dtype} values is needed")
-    return x.data_ptr()
+def _vec(x, n: int, dtype, what: str):
+    """Address of a contiguous CUDA tensor of n values."""
+    if x.dtype is dtype and x.numel() == n and x.is_cuda and x.is_contiguous():
+        return x.data_ptr()
+    _refuse(f"{what}: a contiguous CUDA tensor of {n} {dtype} values is needed")
 
 
 def _rows(x, n: int, heads: int, hd: int, what: str):
     """(address, row stride, dtype) of n rows [heads, hd], each contiguous."""
-    dt = _ROW_DTYPES.get(str(x.dtype))
-    if dt is None or not x.is_cuda or tuple(x.shape) != (n, heads, hd) or \
-            (x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != hd))):
-        _refuse(f"{what}: a CUDA tensor [{n}, {heads}, {hd}] of f32 or bf16 whose rows are "
-                "contiguous is needed")
-    return x.data_ptr(), (x.stride(0) if n > 1 else heads * hd), dt
+    dt = FS_DTYPE_F32 if x.dtype is _Types.f32 else FS_DTYPE_BF16
+    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.is_cuda and x.shape == (n, heads, hd):
+        s0, s1, s2 = x.stride()
+        if n == 0 or (s2 == 1 and (heads == 1 or s1 == hd)):
+            return x.data_ptr(), s0 if n > 1 else heads * hd, dt
+    _refuse(f"{what}: a CUDA tensor [{n}, {heads}, {hd}] of f32 or bf16 whose rows are "
+            "contiguous is needed")
 
 
 def _rope_args(rope, hd: int):
@@ -555,8 +566,8 @@ def _rope_args(rope, hd: int):
         return None, None, 0
     cos, sin = rope
     n = cos.shape[0]
-    return (_vec(cos, n * (hd // 2), "torch.float32", "rope cos"),
-            _vec(sin, n * (hd // 2), "torch.float32", "rope sin"), n)
+    return (_vec(cos, n * (hd // 2), _Types.f32, "rope cos"),
+            _vec(sin, n * (hd // 2), _Types.f32, "rope sin"), n)
 
 
 def fs_kv_q8_view(k, v, k_scale, v_scale, page_table) -> fs_kv_q8:
@@ -566,14 +577,15 @@ def fs_kv_q8_view(k, v, k_scale, v_scale, page_table) -> fs_kv_q8:
     alive; page-table entries may change between calls."""
     if k.dim() != 4 or page_table.dim() != 2:
         _refuse("codes are [n_pages, Hkv, page_size, hd], the page table [n_lanes, max_pages]")
+    ty = _types()
     n_pages, Hkv, ps, hd = k.shape
     n_lanes, max_pages = page_table.shape
     rows = n_pages * Hkv * ps
-    c = fs_kv_q8(_vec(k, rows * hd, "torch.uint8", "k codes"),
-                 _vec(v, rows * hd, "torch.uint8", "v codes"),
-                 _vec(k_scale, rows, "torch.float32", "k scales"),
-                 _vec(v_scale, rows, "torch.float32", "v scales"),
-                 _vec(page_table, n_lanes * max_pages, "torch.int32", "page table"),
+    c = fs_kv_q8(_vec(k, rows * hd, ty.u8, "k codes"),
+                 _vec(v, rows * hd, ty.u8, "v codes"),
+                 _vec(k_scale, rows, ty.f32, "k scales"),
+                 _vec(v_scale, rows, ty.f32, "v scales"),
+                 _vec(page_table, n_lanes * max_pages, ty.i32, "page table"),
                  n_pages, Hkv, ps, hd, n_lanes, max_pages)
     c.tensors = (k, v, k_scale, v_scale, page_table)
     return c
@@ -583,6 +595,7 @@ def fs_kv_q8_append(cache: fs_kv_q8, k, v, lanes, positions, rope=None, stream=N
     """Quantises rows k, v [n, Hkv, hd] (f32 or bf16, any row stride) into
     tokens positions[i] of lanes lanes[i] (int32 CUDA vectors); rope: (cos, sin)
     f32 [rope_len, hd / 2] that rotate the keys."""
+    ty = _types()
     n = lanes.numel()
     hd = cache.head_dim
     kp, ks, dt = _rows(k, n, cache.n_kv_heads, hd, "k")
@@ -591,14 +604,15 @@ def fs_kv_q8_append(cache: fs_kv_q8, k, v, lanes, positions, rope=None, stream=N
         _refuse("k and v have different types")
     rc, rs, rl = _rope_args(rope, hd)
     _op_check(lib().fs_kv_q8_append(C.byref(cache), kp, vp, ks, vs, dt,
-                                    _vec(lanes, n, "torch.int32", "lanes"),
-                                    _vec(positions, n, "torch.int32", "positions"), n, rc, rs, rl,
+                                    _vec(lanes, n, ty.i32, "lanes"),
+                                    _vec(positions, n, ty.i32, "positions"), n, rc, rs, rl,
                                     getattr(stream, "cuda_stream", stream)))
 
 
 def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, stream=None) -> None:
     """Reads tokens back into k_out, v_out [n, Hkv, hd] (f32 or bf16; either
     may be None)."""
+    ty = _types()
     n = lanes.numel()
     kp, ks, dt = (None, 0, None) if k_out is None else \
         _rows(k_out, n, cache.n_kv_heads, cache.head_dim, "k_out")
@@ -608,8 +622,8 @@ def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, str
         _refuse("k_out and v_out have different types")
     if dt is None:
         dt = FS_DTYPE_F32 if dv is None else dv
-    _op_check(lib().fs_kv_q8_read(C.byref(cache), _vec(lanes, n, "torch.int32", "lanes"),
-                                  _vec(positions, n, "torch.int32", "positions"), n, kp, vp, ks,
+    _op_check(lib().fs_kv_q8_read(C.byref(cache), _vec(lanes, n, ty.i32, "lanes"),
+                                  _vec(positions, n, ty.i32, "positions"), n, kp, vp, ks,
                                   vs, dt, getattr(stream, "cuda_stream", stream)))
 
 
@@ -631,6 +645,7 @@ def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0
     lengths[i] - 1; workspace: a CUDA tensor of at least
     fs_kv_q8_attention_workspace bytes, not shared with a call that may run at
     the same time."""
+    ty = _types()
     n = lanes.numel()
     hd = cache.head_dim
     H = q.shape[1] if q.dim() == 3 else 0
@@ -645,8 +660,8 @@ def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0
             _refuse("workspace: a contiguous CUDA tensor is needed")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _op_check(lib().fs_kv_q8_attention(
-        C.byref(cache), qp, qs, _vec(lanes, n, "torch.int32", "lanes"),
-        _vec(lengths, n, "torch.int32", "lengths"), n, H, max_len,
+        C.byref(cache), qp, qs, _vec(lanes, n, ty.i32, "lanes"),
+        _vec(lengths, n, ty.i32, "lengths"), n, H, max_len,
         hd ** -0.5 if scale is None else scale, rc, rs, rl, op, os_, dt, split_len, wp, wb,
         getattr(stream, "cuda_stream", stream)))
 
@@ -659,12 +674,12 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
     [rows], draft_probs f32 [rows, vocab] or None, temps and u_sample f32 [seqs],
     u_accept f32 [rows]; n_accepted and next_token int32 [seqs] are written. All
     CUDA tensors."""
-    if logits.dim() != 2 or not logits.is_cuda or str(logits.dtype) != "torch.float32":
+    ty = _types()
+    if logits.dim() != 2 or not logits.is_cuda or logits.dtype is not ty.f32:
         _refuse("logits: a CUDA tensor [rows, vocab] of f32 is needed")
     rows, V = logits.shape
-    if draft_probs is not None and (tuple(draft_probs.shape) != (rows, V) or
-                                    not draft_probs.is_cuda or
-                                    str(draft_probs.dtype) != "torch.float32"):
+    if draft_probs is not None and (draft_probs.shape != (rows, V) or not draft_probs.is_cuda or
+                                    draft_probs.dtype is not ty.f32):
         _refuse("draft_probs: a CUDA tensor [rows, vocab] of f32 is needed")
     for t in (logits, draft_probs):
         if t is not None and V > 1 and t.numel() and t.stride(1) != 1:
@@ -673,14 +688,14 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
     ld = lambda t: 0 if t is None else t.stride(0) if rows > 1 else V
     _op_check(lib().fs_verify_draft(
         logits.data_ptr(), ld(logits), rows, V,
-        _vec(row_start, n + 1, "torch.int32", "row_start"), n,
-        _vec(draft, rows, "torch.int32", "draft"),
+        _vec(row_start, n + 1, ty.i32, "row_start"), n,
+        _vec(draft, rows, ty.i32, "draft"),
         None if draft_probs is None else draft_probs.data_ptr(), ld(draft_probs),
-        _vec(temps, n, "torch.float32", "temps"),
-        _vec(u_accept, rows, "torch.float32", "u_accept"),
-        _vec(u_sample, n, "torch.float32", "u_sample"),
-        _vec(n_accepted, n, "torch.int32", "n_accepted"),
-        _vec(next_token, n, "torch.int32", "next_token"),
+        _vec(temps, n, ty.f32, "temps"),
+        _vec(u_accept, rows, ty.f32, "u_accept"),
+        _vec(u_sample, n, ty.f32, "u_sample"),
+        _vec(n_accepted, n, ty.i32, "n_accepted"),
+        _vec(next_token, n, ty.i32, "next_token"),
         getattr(stream, "cuda_stream", stream)))
 
 
