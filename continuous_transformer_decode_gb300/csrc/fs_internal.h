@@ -240,6 +240,22 @@ struct KV {
 
 // 8-bit paged KV cache (fs_kv_q8 of include/fs.h): a row is one token's key or
 // value of one KV head, hd codes (byte = code + 128) and one f32 scale.
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^s >= d and
+// m = floor(2^(31 + s) / d) + 1, m d - 2^(31 + s) <= 2^s, so floor(n m / 2^(31 + s))
+// is the quotient.
+struct FastDiv {
+  uint32_t m = 0;
+  int s = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    while (((uint64_t)1 << s) < d) ++s;
+    m = (uint32_t)(((uint64_t)1 << (31 + s)) / d + 1);
+  }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> (31 + s));
+  }
+};
+
 struct KvQ8 {
   uint8_t* k = nullptr;  // [n_pages][Hkv][page_size][hd]
   uint8_t* v = nullptr;
@@ -247,6 +263,7 @@ struct KvQ8 {
   float* vs = nullptr;
   const int32_t* page_table = nullptr;  // [n_lanes][max_pages]
   int n_pages = 0, Hkv = 0, page_size = 0, hd = 0, n_lanes = 0, max_pages = 0;
+  FastDiv by_page, by_head;  // page_size and Hkv
 };
 
 // RoPE of one rotate-half pair (x0 = element i, x1 = element i + hd/2) with

@@ -77,6 +77,8 @@ KvQ8 view(const fs_kv_q8* c) {
   v.hd = c->head_dim;
   v.n_lanes = c->n_lanes;
   v.max_pages = c->max_pages;
+  v.by_page = FastDiv((uint32_t)c->page_size);
+  v.by_head = FastDiv((uint32_t)c->n_kv_heads);
   return v;
 }
 

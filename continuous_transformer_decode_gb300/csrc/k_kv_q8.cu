@@ -21,8 +21,11 @@ namespace {
 
 using namespace two;
 
-constexpr int kT = 256;
+constexpr int kT = 128;
 constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ float ld1(const float* p) { return *p; }
+__device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // Four consecutive elements; kVec: their address is aligned to all four.
 template <bool kVec>
@@ -70,74 +73,145 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float x[4]) {
 __device__ __forceinline__ float storable(float x) {
   return x != x ? 0.0f : fminf(fmaxf(x, -FLT_MAX), FLT_MAX);
 }
+// Largest magnitude of three; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max_abs(const float (&x)[8]) {
+  return max_abs(max_abs(x[0], x[1], x[2]), max_abs(x[3], x[4], x[5]), max_abs(x[6], x[7], 0.0f));
+}
 
-// Quantises one row of 8 values a lane (x[0..3] in the lower half, x[4..7] in the
-// upper) and stores it, if `slot` says where.
-//
 // A quotient in f32 is off by at most kNear of a step: the factor 127 / amax and
 // the product round by 2^-24 of at most 127 each, 1.6e-5 together; of a rotated
 // key x is off by (1 + sqrt 2) 2^-24 amax, two rounded products and their sum,
-// 1.9e-5 of a step, and amax likewise. A quotient that comes so near to the border
-// of two codes (one row of 128 in 200 for values, in 65 for rotated keys) is
-// decided by comparing 127 x with the border times amax as two-f32 numbers:
-// exactly for values that were not rotated, to 2^-44 for others (exact(j, up) is
-// element j times a power of two so). In f64 these rows alone took four fifths
-// of the kernel (65536 rows of 8 heads of 128: 473 us).
-template <int HD, bool kRot, typename Exact>
-__device__ __forceinline__ void quantise_row(const float (&x)[8], Exact exact, uint8_t* codes,
-                                             float* scales, int64_t slot, int sub) {
-  constexpr int kL = HD / 8;  // lanes of the row
-  constexpr float kNear = kRot ? 6e-5f : 2e-5f;
-  constexpr float kMagic = 12582912.0f + 128.0f;
+// 1.9e-5 of a step, and amax likewise.
+template <bool kRot>
+constexpr float kNear = kRot ? 6e-5f : 2e-5f;
+constexpr float kMagic = 12582912.0f + 128.0f;
+
+// The rows that quantise_row() leaves (of 128 values, one in 200 of f32 and one in 65
+// of rotated keys): a quotient may lie on either side of the border of two codes, the
+// row is very large or small, or not finite. One warp takes the row and decides by
+// comparing 127 x with the border times amax as two-f32 numbers: exactly for
+// values that were not rotated, to 2^-44 for others. It is kept out of line and
+// loads the row again, so that the other rows do not hold its registers (inlined
+// in f64, 65536 rows of 8 heads of 128 took 473 us; inlined so, 179 us).
+template <typename T, int HD, bool kRot>
+__device__ __noinline__ void quantise_border_row(const T* x, const float* rc, const float* rs,
+                                                 uint8_t* codes, float* scale, int lane) {
+  constexpr int kHalf = HD / 2, kP = HD / 64;  // pairs (i, i + hd / 2) of a lane
+  float a[kP], b[kP], co[kP], si[kP];
+#pragma unroll
+  for (int p = 0; p < kP; ++p) {
+    const int i = lane + 32 * p;
+    a[p] = ld1(x + i);
+    b[p] = ld1(x + i + kHalf);
+    co[p] = kRot ? rc[i] : 1.0f;
+    si[p] = kRot ? rs[i] : 0.0f;
+  }
+  // the two elements of pair p, rounded to f32; and times a power of two as two numbers
+  auto rounded = [&](int p, float& y0, float& y1) {
+    y0 = a[p], y1 = b[p];
+    if constexpr (kRot) rope_pair(a[p], b[p], co[p], si[p], y0, y1);
+    y0 = storable(y0), y1 = storable(y1);
+  };
+  auto exact = [&](int p, int half, float y, float up) -> Two {
+    if (!kRot || !(fabsf(y) < FLT_MAX)) return {y * up, 0.0f};
+    const float a0 = a[p] * up, b0 = b[p] * up;
+    const Two e = half == 0 ? add(two_prod(a0, co[p]), two_prod(b0, -si[p]))
+                            : add(two_prod(b0, co[p]), two_prod(a0, si[p]));
+    return e.h == e.h ? e : Two{y * up, 0.0f};  // NaN: storable has made it 0
+  };
   float amax = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+  for (int p = 0; p < kP; ++p) {
+    float y0, y1;
+    rounded(p, y0, y1);
+    amax = fmaxf(amax, fmaxf(fabsf(y0), fabsf(y1)));
+  }
 #pragma unroll
-  for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
   // into the range where quotients and products neither overflow nor vanish
   const float up = amax < 1e-30f ? 0x1p96f : amax > 1e30f ? 0x1p-96f : 1.0f;
   const float top = amax * up, r = top > 0.0f ? 127.0f / top : 0.0f;
-  float u[8], off = 0.0f;
+  Two y = {0.0f, 0.0f};  // the largest magnitude: of the elements that have it in f32
+#pragma unroll
+  for (int q = 0; q < 2 * kP; ++q) {
+    float v[2];
+    rounded(q >> 1, v[0], v[1]);
+    const float w = q & 1 ? v[1] : v[0];
+    if (fabsf(w) * up >= top * (1.0f - 0x1p-20f)) {
+      Two e = exact(q >> 1, q & 1, w, up);
+      if (e.h < 0.0f) e = {-e.h, -e.l};
+      if (less(y, e)) y = e;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Two e = {__shfl_xor_sync(kAll, y.h, o), __shfl_xor_sync(kAll, y.l, o)};
+    if (less(y, e)) y = e;
+  }
+#pragma unroll
+  for (int q = 0; q < 2 * kP; ++q) {
+    float v[2];
+    rounded(q >> 1, v[0], v[1]);
+    const float w = q & 1 ? v[1] : v[0], t = w * up;
+    float n = fmaf(t, r, kMagic) - kMagic;
+    const float off = fmaf(t, r, -n);
+    if (fabsf(off) > 0.5f - kNear<kRot>) {
+      // the codes below and above, and the border between them
+      const float lo = off > 0.0f ? n : n - 1.0f;
+      const Two e = mul({127.0f, 0.0f}, exact(q >> 1, q & 1, w, up));
+      const Two border = mul({lo + 0.5f, 0.0f}, y);
+      const bool even = ((int)lo & 1) == 0;
+      n = less(e, border) || (!less(border, e) && even) ? lo : lo + 1.0f;
+    }
+    codes[lane + 32 * (q >> 1) + (q & 1) * kHalf] = (uint8_t)((int)n + 128);
+  }
+  if (lane == 0) *scale = amax / 127.0f;
+}
+
+// Quantises one row of 8 values a lane (x[0..3] in the lower half, x[4..7] in the
+// upper) and stores it, if `slot` says where. True: the row has to be taken by
+// quantise_border_row (the same for every lane of the row, whatever rows share the
+// warp).
+//
+// kTies: the values are bf16 as they came. With X and A the 8-bit significands of x
+// and amax, a quotient t = 127 X 2^e / A lies on a border or at least t / (254 X),
+// 1.5e-5 t, away from it: f32, good to 1.2e-7 t, cannot mistake the side, and what it
+// finds within 4e-6 t is a tie, which goes to the even code. Ties are common in such
+// rows: x = amax / 2, 63.5 codes, is in a third of normal rows of 128.
+template <int HD, bool kRot, bool kTies>
+__device__ __forceinline__ bool quantise_row(const float (&x)[8], uint8_t* codes, float* scales,
+                                             int64_t slot, int sub) {
+  constexpr int kL = HD / 8;  // lanes of the row
+  float amax = max_abs(x);
+  bool odd = !(amax <= 1e30f);  // also NaN
+#pragma unroll
+  for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+  odd |= amax > 0.0f && amax < 1e-30f;
+  const float r = amax > 0.0f ? 127.0f / amax : 0.0f;
+  float u[8], off[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float xs = x[j] * up;
-    u[j] = fmaf(xs, r, kMagic);
-    off = fmaxf(off, fabsf(fmaf(xs, r, kMagic - u[j])));  // distance to the code
+    u[j] = fmaf(x[j], r, kMagic);
+    off[j] = fmaf(x[j], r, kMagic - u[j]);  // distance to the code
   }
-  // by row, not by warp: a row's bits do not depend on the rows beside it
-  const unsigned near = __ballot_sync(kAll, off > 0.5f - kNear);
-  const unsigned row = (kL == 32 ? kAll : (1u << (kL & 31)) - 1) << (threadIdx.x % 32 - sub);
-  if (near & row) {
-    Two y = {top, 0.0f};
-    if constexpr (kRot) {  // the largest magnitude: of the lanes that hold it in f32
-      y = {0.0f, 0.0f};
+  bool border = max_abs(off) > 0.5f - kNear<kRot>;
+  if constexpr (kTies) {
+    if (border)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (fabsf(x[j]) >= amax * (1.0f - 0x1p-20f)) {
-          Two e = exact(j, up);
-          if (e.h < 0.0f) e = {-e.h, -e.l};
-          if (less(y, e)) y = e;
-        }
-#pragma unroll
-      for (int o = kL / 2; o > 0; o >>= 1) {
-        const Two e = {__shfl_xor_sync(row, y.h, o), __shfl_xor_sync(row, y.l, o)};
-        if (less(y, e)) y = e;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float n = u[j] - kMagic, d = fmaf(x[j] * up, r, -n);
-      if (fabsf(d) > 0.5f - kNear) {
-        // the codes below and above, and the border between them
-        const float lo = d > 0.0f ? n : n - 1.0f;
-        const Two e = mul({127.0f, 0.0f}, exact(j, up)), border = mul({lo + 0.5f, 0.0f}, y);
-        const bool even = ((int)lo & 1) == 0;
-        const bool below = less(e, border) || (!less(border, e) && even);
-        u[j] = kMagic + (below ? lo : lo + 1.0f);
-      }
-    }
+        if (fabsf(off[j]) > 0.5f - 4e-6f * fabsf(x[j] * r))
+          u[j] = kMagic + 2.0f * rintf(0.5f * (x[j] * r));
+    border = false;
   }
-  if (slot < 0) return;
+  const unsigned left = __ballot_sync(kAll, odd || border);
+  const unsigned row = (kL == 32 ? kAll : (1u << (kL & 31)) - 1) << (threadIdx.x % 32 - sub);
+  if (slot < 0) return false;
+  if (left & row) return true;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t a = __byte_perm(__float_as_uint(u[4 * h]), __float_as_uint(u[4 * h + 1]), 0x0040);
@@ -145,10 +219,13 @@ __device__ __forceinline__ void quantise_row(const float (&x)[8], Exact exact, u
     *reinterpret_cast<uint32_t*>(codes + slot * HD + h * (HD / 2) + sub * 4) = __byte_perm(a, b, 0x5410);
   }
   if (sub == 0) scales[slot] = amax / 127.0f;
+  return false;
 }
 
+// Twelve blocks an SM: what a block cannot hide of the two dependent loads before a
+// row's store (position, then its rotation; lane, then its page), the others do.
 template <typename T, int HD, bool kRot, bool kVec>
-__global__ void __launch_bounds__(kT)
+__global__ void __launch_bounds__(kT, 12)
     k_kv_q8_append(KvQ8 c, const T* __restrict__ k, const T* __restrict__ v, int64_t k_stride,
                    int64_t v_stride, const int32_t* __restrict__ lanes,
                    const int32_t* __restrict__ positions, unsigned items,
@@ -159,47 +236,47 @@ __global__ void __launch_bounds__(kT)
   const int sub = threadIdx.x % kL;
   const unsigned at = (unsigned)(((uint64_t)blockIdx.x * kT + threadIdx.x) / kL);
   const unsigned item = min(at, items - 1);  // lanes past the end follow along and store nothing
-  const unsigned i = item / (unsigned)c.Hkv;
+  const unsigned i = c.by_head.div(item);
   const int g = (int)(item - i * c.Hkv);
-  const T* kr = k + i * k_stride + (int64_t)g * HD + sub * 4;
-  const T* vr = v + i * v_stride + (int64_t)g * HD + sub * 4;
-  float kx[8], vx[8];
-  load4<kVec>(kr, kx);
-  load4<kVec>(kr + kHalf, kx + 4);
-  load4<kVec>(vr, vx);
-  load4<kVec>(vr + kHalf, vx + 4);
+  const T* kr = k + i * k_stride + (int64_t)g * HD;
+  const T* vr = v + i * v_stride + (int64_t)g * HD;
+  float x[8], y[8];
+  load4<kVec>(kr + sub * 4, x);
+  load4<kVec>(kr + sub * 4 + kHalf, x + 4);
+  load4<kVec>(vr + sub * 4, y);
+  load4<kVec>(vr + sub * 4 + kHalf, y + 4);
   const int pos = positions[i];
   int64_t slot = at < items ? q8::slot_of(c, lanes[i], pos, g) : -1;
-  float y[8], co[4] = {}, si[4] = {};
+  int64_t angles = 0;
   if constexpr (kRot) {
-    const bool in = pos >= 0 && pos < rope_len;
-    if (!in) slot = -1;
-    const int64_t p = in ? (int64_t)pos * kHalf + sub * 4 : 0;
-    load4<kVec>(rc + p, co);
-    load4<kVec>(rs + p, si);
+    if (pos < 0 || pos >= rope_len)
+      slot = -1;
+    else
+      angles = (int64_t)pos * kHalf;
+    float co[4], si[4];
+    load4<kVec>(rc + angles + sub * 4, co);
+    load4<kVec>(rs + angles + sub * 4, si);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      rope_pair(kx[j], kx[j + 4], co[j], si[j], y[j], y[j + 4]);
-      y[j] = storable(y[j]);
-      y[j + 4] = storable(y[j + 4]);
+      const float x0 = x[j], x1 = x[j + 4];
+      rope_pair(x0, x1, co[j], si[j], x[j], x[j + 4]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = storable(kx[j]);
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) vx[j] = storable(vx[j]);
-  quantise_row<HD, kRot>(
-      y,
-      [&](int j, float up) -> Two {
-        if (!kRot || fabsf(y[j]) >= FLT_MAX) return {y[j] * up, 0.0f};
-        const float a0 = kx[j & 3] * up, b0 = kx[(j & 3) + 4] * up, cc = co[j & 3], ss = si[j & 3];
-        return j < 4 ? add(two_prod(a0, cc), two_prod(b0, -ss))
-                     : add(two_prod(b0, cc), two_prod(a0, ss));
-      },
-      c.k, c.ks, slot, sub);
-  quantise_row<HD, false>(
-      vx, [&](int j, float up) -> Two { return {vx[j] * up, 0.0f}; }, c.v, c.vs, slot, sub);
+  const bool k_left = quantise_row<HD, kRot, !kRot && sizeof(T) == 2>(x, c.k, c.ks, slot, sub);
+  const bool v_left = quantise_row<HD, false, sizeof(T) == 2>(y, c.v, c.vs, slot, sub);
+  // the warp takes the rows that are left one by one
+  const int lane = threadIdx.x & 31;
+  for (unsigned m = __ballot_sync(kAll, sub == 0 && (k_left || v_left)); m; m &= m - 1) {
+    const int src = __ffs(m) - 1;
+    const bool do_k = __shfl_sync(kAll, k_left, src), do_v = __shfl_sync(kAll, v_left, src);
+    const int64_t to = __shfl_sync(kAll, slot, src), an = __shfl_sync(kAll, angles, src);
+    const int64_t ko = __shfl_sync(kAll, (int64_t)(kr - k), src);
+    const int64_t vo = __shfl_sync(kAll, (int64_t)(vr - v), src);
+    if (do_k)
+      quantise_border_row<T, HD, kRot>(k + ko, rc + an, rs + an, c.k + to * HD, c.ks + to, lane);
+    if (do_v)
+      quantise_border_row<T, HD, false>(v + vo, nullptr, nullptr, c.v + to * HD, c.vs + to, lane);
+  }
 }
 
 __device__ __forceinline__ void values4(uint32_t w, float s, float x[4]) {
@@ -219,7 +296,7 @@ __global__ void __launch_bounds__(kT)
   const int sub = threadIdx.x % kL;
   const unsigned item = (unsigned)(((uint64_t)blockIdx.x * kT + threadIdx.x) / kL);
   if (item >= items) return;
-  const unsigned i = item / (unsigned)c.Hkv;
+  const unsigned i = c.by_head.div(item);
   const int g = (int)(item - i * c.Hkv);
   const int64_t slot = q8::slot_of(c, lanes[i], positions[i], g);
   // a token of no slot reads as zeros: scale 0

@@ -12,7 +12,7 @@ namespace q8 {
 // the cache: such a token holds nothing.
 __device__ __forceinline__ int64_t slot_of(const KvQ8& c, int lane, int t, int g) {
   if ((unsigned)lane >= (unsigned)c.n_lanes || t < 0) return -1;
-  const int pi = t / c.page_size;
+  const int pi = (int)c.by_page.div(t);
   if (pi >= c.max_pages) return -1;
   const int page = c.page_table[(int64_t)lane * c.max_pages + pi];
   if ((unsigned)page >= (unsigned)c.n_pages) return -1;
