@@ -559,7 +559,7 @@ struct VerifyArgs {
   int32_t* n_accepted;
   int32_t* next_token;
 };
-int launch_verify(const VerifyArgs& a, cudaStream_t s);
+int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
 
 int launch_sample(const float* logits, int B, int V, const float* temps,
                   const uint64_t* seeds, const uint64_t* counters,

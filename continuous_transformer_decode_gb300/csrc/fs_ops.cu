@@ -253,7 +253,8 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
                     const float* u_accept, const float* u_sample, int32_t* n_accepted,
                     int32_t* next_token, void* stream) {
   if (n_rows < 0 || n_seqs < 0) return refuse(FS_ERR_ARG, "negative n_rows or n_seqs");
-  if (vocab < 1) return refuse(FS_ERR_ARG, "vocab must be positive");
+  if (vocab < 1 || vocab > kMaxTokens) return refuse(FS_ERR_ARG, "vocab outside [1, 2^30]");
+  if (n_seqs > INT32_MAX / 8) return refuse(FS_ERR_ARG, "too many sequences");
   if (n_seqs == 0) return FS_OK;
   if (n_rows > 0) {
     const char* why = bad_rows(logits, logits_stride, vocab, X_F32);
@@ -276,7 +277,9 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
   a.draft = draft; a.probs = draft_probs; a.ld_probs = probs_stride;
   a.temps = temps; a.u_accept = u_accept; a.u_sample = u_sample;
   a.n_accepted = n_accepted; a.next_token = next_token;
-  return launched(launch_verify(a, (cudaStream_t)stream));
+  const int sms = device_sms();
+  if (!sms) return refuse(FS_ERR_CUDA, "no CUDA device");
+  return launched(launch_verify(a, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

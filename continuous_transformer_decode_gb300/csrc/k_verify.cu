@@ -13,13 +13,18 @@
 // taken in order and those after a rejection are never read. One thread-block
 // cluster serves a sequence: its blocks share a row's vocabulary, a warp a run
 // of consecutive tokens, and exchange (max, sum) through distributed shared
-// memory, one cluster barrier a row. The sum that decides an acceptance is in
-// f32; where the decision comes within 2^-14 of its border (f32 sums of a
-// vocabulary below a million are better than that) it is taken again from
-// weights good to 2^-36, which also make the draw: its answer depends on the
-// running sums of a whole row, and with f32 weights one draw in a few hundred
-// would be another token. These weights and sums are pairs of f32 numbers: this
-// GPU's f64 rate, 1/60 of its f32 rate, would bound the kernel.
+// memory, one cluster barrier a row.
+//
+// Whole-number answers are held to more than f32: where an acceptance or a draw
+// comes so near to its border that f32 weights and sums cannot tell, it is taken
+// again from weights good to 2^-36, as pairs of f32 numbers (this GPU's f64 rate is
+// 1/60 of its f32 rate). That is rare for an acceptance, and a few draws in a
+// hundred for a vocabulary of 49152. What bounds the kernel is the chain of one
+// sequence (about 3 us for the first row, 2 us for each further one, 5 us for the
+// draw and 9 us for one that is taken again, on eight SMs), not the bytes: 256
+// sequences of 4 drafts from a lookup, 49152 tokens, take 33 us, 61 MB of logits
+// being read; every draw in pairs took 108 us. 64 sequences of 0 to 7 drafts take
+// 34 us, one of 4 drafts 14 us.
 
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -34,9 +39,6 @@ using namespace two;
 
 namespace cg = cooperative_groups;
 
-constexpr int kC = 8;        // blocks of a sequence's cluster
-constexpr int kT = 512;      // threads of a block
-constexpr int kW = kT / 32;  // warps of a block
 constexpr unsigned kAll = 0xffffffffu;
 
 // 2^(k/32) as pairs of f32 numbers.
@@ -72,10 +74,8 @@ __device__ __forceinline__ Two log2e_over(float T) {
 // 2^-36: y = n + k/32 + f with |f| <= 1/64, 2^f = 1 + its Taylor series (the
 // method of Tang, ACM TOMS 1989). Below 2^-126 it is zero.
 __device__ __forceinline__ Two weight2(float z, float m, Two c, const float2* tab) {
-  if (z == m) return {1.0f, 0.0f};
   const Two d = two_sum(z, -m);
   const float p = __fmul_rn(d.h, c.h);
-  if (!(p > -125.5f)) return {0.0f, 0.0f};  // also -inf and NaN
   const float pe = fmaf(d.h, c.h, -p) + fmaf(d.h, c.l, __fmul_rn(d.l, c.h));
   const float kf = rintf(__fmul_rn(p, 32.0f));
   const int k = (int)kf;
@@ -94,16 +94,22 @@ __device__ __forceinline__ Two weight2(float z, float m, Two c, const float2* ta
   const Two e = fast_two_sum(t.x, w);
   const Two r = fast_two_sum(e.h, __fadd_rn(e.l, we));
   const float s = __int_as_float(((k >> 5) + 127) << 23);  // 2^n, -126 <= n <= 0
-  return {__fmul_rn(r.h, s), __fmul_rn(r.l, s)};
+  // no branches: several of these run interleaved
+  const bool one = z == m, in = p > -125.5f;  // not in: also -inf and NaN
+  return {one ? 1.0f : in ? __fmul_rn(r.h, s) : 0.0f, !one && in ? __fmul_rn(r.l, s) : 0.0f};
 }
 
 // f32 weight under m; c = log2(e) / T.
-__device__ __forceinline__ float weight1(float z, float m, float c) {
-  return z == m ? 1.0f : z > -CUDART_INF_F ? exp2f((z - m) * c) : 0.0f;
+__device__ __forceinline__ float weight1(float z, float m, Two c) {
+  if (m == CUDART_INF_F) return z == m ? 1.0f : 0.0f;
+  const float d = z - m;
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(fmaf(d, c.h, d * c.l), -200.0f)));
+  return y;  // 0 for NaN and -inf
 }
 // factor that takes sums under m to sums under M
-__device__ __forceinline__ float rescale(float m, float M, float c) {
-  return m == -CUDART_INF_F ? 0.0f : m == M ? 1.0f : exp2f((m - M) * c);
+__device__ __forceinline__ float rescale(float m, float M, Two c) {
+  return m == -CUDART_INF_F ? 0.0f : m == M ? 1.0f : weight1(m, M, c);
 }
 
 struct Stat {  // of a row's part
@@ -111,12 +117,16 @@ struct Stat {  // of a row's part
   int best;        // lowest index of max
 };
 
+template <int kC, int kW>
 struct Shared {
   float2 tab[32];
   Stat warp[kW];
-  Two wsum[kW];
+  float left[kW], scan[kW];
+  Two left2[kW], scan2[kW];
+  int at[kW], tail[kW];
   Stat part[2][kC];  // the cluster's blocks; two buffers, taken in turn: a block may
   Two psum[2][kC];   // write the next exchange while another still reads the last
+  int again;         // the f32 draw could not tell
 };
 
 __device__ __forceinline__ float4 load4(const float* z, int i, int hi, bool vec) {
@@ -129,129 +139,260 @@ __device__ __forceinline__ float4 load4(const float* z, int i, int hi, bool vec)
   return v;
 }
 
+__device__ __forceinline__ Two shfl_up(Two v, int o) {
+  return {__shfl_up_sync(kAll, v.h, o), __shfl_up_sync(kAll, v.l, o)};
+}
+__device__ __forceinline__ Two shfl(Two v, int i) {
+  return {__shfl_sync(kAll, v.h, i), __shfl_sync(kAll, v.l, i)};
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float shfl_up(float v, int o) { return __shfl_up_sync(kAll, v, o); }
+__device__ __forceinline__ float shfl(float v, int i) { return __shfl_sync(kAll, v, i); }
+__device__ __forceinline__ bool less(float a, float b) { return a < b; }
+__device__ __forceinline__ bool positive(float a) { return a > 0.0f; }
+__device__ __forceinline__ bool positive(Two a) { return a.h > 0.0f; }
+
+// Inclusive sums over the lanes.
+template <typename T>
+__device__ __forceinline__ T scan(T v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = shfl_up(v, o);
+    if (lane >= o) v = add(up, v);
+  }
+  return v;
+}
+// Of parts with the lanes' weights, the first whose running sum (after `before`)
+// reaches the target, or the last with a weight, or -1; `before` becomes the sum of
+// those ahead of it.
+template <typename T>
+__device__ __forceinline__ int pick(T weight, T target, T& before, int lane) {
+  const T upto = add(before, scan(weight, lane));
+  const unsigned has = __ballot_sync(kAll, positive(weight));
+  const unsigned hit = __ballot_sync(kAll, positive(weight) && !less(upto, target));
+  const int at = hit ? __ffs(hit) - 1 : 31 - __clz(has);
+  if (at > 0) before = shfl(upto, at - 1);
+  return at;
+}
+
+// What is left of the block's tokens for the draw, in pairs: weight e; with draft
+// probabilities max(e - q S, 0); without token `out`.
+struct Left {
+  const float* z;
+  const float* q;  // null: none
+  float M;
+  Two c, S;
+  int out;
+  const float2* tab;
+  template <bool kQ>
+  __device__ __forceinline__ Two at(int i) const {
+    const Two e = weight2(z[i], M, c, tab);
+    if constexpr (!kQ) return {i == out ? 0.0f : e.h, i == out ? 0.0f : e.l};
+    const Two p = mul({q[i], 0.0f}, S), d = add(e, {-p.h, -p.l});
+    const bool some = e.h > 0.0f && d.h > 0.0f;
+    return {some ? d.h : 0.0f, some ? d.l : 0.0f};
+  }
+  __device__ __forceinline__ Two at(int i) const { return q ? at<true>(i) : at<false>(i); }
+};
+// A lane's share of tokens lo .. hi - 1, four at a time for their latencies. Out of
+// line: it runs seldom, from several places.
+template <bool kQ>
+__device__ __noinline__ Two left_sum_of(Left w, int lo, int hi, int lane) {
+  Two s[4] = {};
+#pragma unroll 1
+  for (int i = lo + lane; i < hi; i += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = min(i + 32 * u, hi - 1);  // all four in step, those past the end unused
+      const Two e = w.at<kQ>(j);
+      const bool in = i + 32 * u < hi;
+      s[u] = add(s[u], {in ? e.h : 0.0f, in ? e.l : 0.0f});
+    }
+  }
+  return add(add(s[0], s[1]), add(s[2], s[3]));
+}
+__device__ __forceinline__ Two left_sum(const Left& w, int lo, int hi, int lane) {
+  return w.q ? left_sum_of<true>(w, lo, hi, lane) : left_sum_of<false>(w, lo, hi, lane);
+}
+
 // Every thread takes the decisions: they come from the same numbers in the same
 // order in every block, so the cluster stays together.
-__global__ void __launch_bounds__(kT) k_verify(VerifyArgs a) {
-  __shared__ Shared sh;
+//
+// held: a block's part of the row (and of the draft's probabilities) stays in
+// dynamic shared memory for the draw; else it is read again.
+template <int kC, int kT>
+__global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
+  constexpr int kW = kT / 32;
+  __shared__ Shared<kC, kW> sh;
+  extern __shared__ __align__(16) float hold[];  // [kW * run] z, then q
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  auto sync = [&] {
+    if constexpr (kC == 1) __syncthreads();
+    else cluster.sync();
+  };
+  auto remote = [&](auto* p, int r) {
+    if constexpr (kC == 1) return p;
+    else return cluster.map_shared_rank(p, r);
+  };
+  const int rank = kC == 1 ? 0 : (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < 32) sh.tab[tid] = kExp2[tid];
-  cluster.sync();  // every block has started: its shared memory can be written
+  if (tid == 0) sh.again = 0;
+  // the other blocks' shared memory can be written once they have started: arrive
+  // now, wait before the first write
+  if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto started = [&] {
+    if constexpr (kC > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / kC, V = a.V;
-  const int r0 = max(0, min(a.row_start[b], a.n_rows));
-  const int r1 = max(r0, min(a.row_start[b + 1], a.n_rows));
+  const int first = a.row_start[b], end = a.row_start[b + 1];
+  const float temp = a.temps[b], us = fminf(a.u_sample[b], 1.0f);
+  const int r0 = max(0, min(first, a.n_rows)), r1 = max(r0, min(end, a.n_rows));
   if (r0 == r1) {  // the whole cluster
     if (rank == 0 && tid == 0) {
       a.n_accepted[b] = 0;
       a.next_token[b] = -1;
     }
+    started();
     return;
   }
-  const float temp = a.temps[b];
   const bool greedy = !(temp > 0.0f);
   const Two c = log2e_over(greedy ? 1.0f : temp);
-  // this warp's run of tokens [lo, hi)
+  // this block's tokens are base .. base + count - 1, this warp's lo .. hi - 1 of them
   const int run = (V - 1) / (kC * kW * 128) * 128 + 128;
-  const int lo = (int)min((int64_t)V, (int64_t)(rank * kW + warp) * run);
-  const int hi = (int)min((int64_t)V, (int64_t)lo + run);
+  const int base = (int)min((int64_t)V, (int64_t)rank * kW * run);
+  const int count = (int)min((int64_t)V - base, (int64_t)kW * run);
+  const int lo = min(count, warp * run), hi = min(count, lo + run);
+  // What the f32 sums are held to be off by, of the row's sum S. An exponential comes
+  // out 2^-24.3 too small in the mean, and otherwise rounds independently: measured
+  // against 64 bits, target and running sum differ by at most 2^-23.9 S through the
+  // exponentials (6000 rows of 1000 to 49152 logits of deviation 0.5 to 8). The last
+  // additions round by 2^-25 S each. With draft probabilities S itself enters twice.
+  const float rough = a.probs ? 0x1p-21f : 0x1.8p-22f;
   int turn = 0;
-
-  // the sum over the cluster, block by block in sh.psum[turn ^ 1] afterwards and
-  // warp by warp in sh.wsum
+  // The warp's sum into sh.left2, the blocks' into sh.psum[turn], and on.
   auto cluster_sum = [&](Two v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
-    if (lane == 0) sh.wsum[warp] = v;
+    if (lane == 0) sh.left2[warp] = v;
     __syncthreads();
     if (warp == 0) {
-      v = lane < kW ? sh.wsum[lane] : Two{0.0f, 0.0f};
+      v = lane < kW ? sh.left2[lane] : Two{0.0f, 0.0f};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
-      if (lane < kC) *cluster.map_shared_rank(&sh.psum[turn][rank], lane) = v;
+      for (int o = kW / 2; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
+      v = shfl(v, 0);
+      if (lane < kC) *remote(&sh.psum[turn][rank], lane) = v;
     }
-    cluster.sync();
+    sync();
     v = sh.psum[turn][0];
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < kC; ++i) v = add(v, sh.psum[turn][i]);
     turn ^= 1;
     return v;
   };
 
-  for (int r = r0; r < r1; ++r) {
-    const float* z = a.logits + r * a.ld_logits;
+  // chunks of kU groups of 128 tokens, the next one on its way while one is worked
+  // on; after a row's last comes the first of the next row, which is wanted if the
+  // draft is accepted
+  constexpr int kU = 4;
+  float4 next[kU];
+  auto fetch = [&](int row, int i0) {
+    const float* z = a.logits + row * a.ld_logits + base;
     const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) next[u] = load4(z, i0 + 128 * u + 4 * lane, hi, vec);
+  };
+  fetch(r0, lo);
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    const float* z = a.logits + r * a.ld_logits + base;
     const bool last = r == r1 - 1;
+    // what decides on the draft
+    const int x = last ? -1 : a.draft[r];
+    const bool known = x >= 0 && x < V;
+    const float u_acc = known ? a.u_accept[r] : 0.0f, z_x = known ? z[x - base] : 0.0f;
+    const float q_x = known && a.probs ? a.probs[r * a.ld_probs + x] : 1.0f;
     // ---- the row's maximum, its index, and its sum
     Stat st = {-CUDART_INF_F, 0.0f, V};
-    {
-      constexpr int kU = 4;  // groups of 128 tokens in flight
-      for (int i0 = lo; i0 < hi; i0 += 128 * kU) {
-        float4 v[kU];
+#pragma unroll 1
+    for (int i0 = lo; i0 < hi; i0 += 128 * kU) {
+      float4 v[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) v[u] = load4(z, i0 + 128 * u + 4 * lane, hi, vec);
-        float mx = -CUDART_INF_F;
+      for (int u = 0; u < kU; ++u) v[u] = next[u];
+      const bool more = i0 + 128 * kU < hi;
+      if (more || !last) fetch(more ? r : r + 1, more ? i0 + 128 * kU : lo);
+      if (held)
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-          mx = fmaxf(mx, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+          if (i0 + 128 * u < lo + run)
+            *reinterpret_cast<float4*>(hold + i0 + 128 * u + 4 * lane) = v[u];
+      float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-        if (mx > st.max) st = {mx, st.sum * rescale(st.max, mx, c.h), V};
+      for (int u = 0; u < kU; ++u)
+        mx = fmaxf(mx, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+      if (mx > st.max) st = {mx, st.sum * rescale(st.max, mx, c), V};
+      if (greedy) {
+        if (mx == st.max && st.best == V) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (greedy) {
-              if (x[e] == mx && mx == st.max) st.best = min(st.best, i0 + 128 * u + 4 * lane + e);
-            } else {
-              st.sum += weight1(x[e], st.max, c.h);
-            }
+          for (int u = kU - 1; u >= 0; --u) {
+            const int i = base + i0 + 128 * u + 4 * lane;
+            if (v[u].w == mx) st.best = i + 3;
+            if (v[u].z == mx) st.best = i + 2;
+            if (v[u].y == mx) st.best = i + 1;
+            if (v[u].x == mx) st.best = i;
           }
         }
-      }
+      } else {
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        st.sum += __shfl_xor_sync(kAll, st.sum, o);
-        st.best = min(st.best, __shfl_xor_sync(kAll, st.best, o));
+        for (int u = 0; u < kU; ++u) {
+          part[0] += weight1(v[u].x, st.max, c);
+          part[1] += weight1(v[u].y, st.max, c);
+          part[2] += weight1(v[u].z, st.max, c);
+          part[3] += weight1(v[u].w, st.max, c);
+        }
+        st.sum += (part[0] + part[1]) + (part[2] + part[3]);
       }
-      // a run without a token: its -inf equal their maximum
-      if (st.max == -CUDART_INF_F) st = {-CUDART_INF_F, 0.0f, V};
     }
+    if (greedy) {
+      st.best = __reduce_min_sync(kAll, st.best);
+    } else {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) st.sum += __shfl_xor_sync(kAll, st.sum, o);
+    }
+    // a run without a token: its -inf equal their maximum
+    if (st.max == -CUDART_INF_F) st = {-CUDART_INF_F, 0.0f, V};
     if (lane == 0) sh.warp[warp] = st;
     __syncthreads();
+    if (r == r0) started();
     if (warp == 0) {  // joins the warps; lane i writes block i's copy
       st = lane < kW ? sh.warp[lane] : Stat{-CUDART_INF_F, 0.0f, V};
-      float M = st.max;
+      float m = st.max;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-      float sum = st.sum * rescale(st.max, M, c.h);
-      int best = st.max == M ? st.best : V;
+      for (int o = kW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+      m = __shfl_sync(kAll, m, 0);
+      float sum = st.sum * rescale(st.max, m, c);
+      const int best = __reduce_min_sync(kAll, st.max == m ? st.best : V);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(kAll, sum, o);
-        best = min(best, __shfl_xor_sync(kAll, best, o));
-      }
-      if (lane < kC) *cluster.map_shared_rank(&sh.part[turn][rank], lane) = {M, sum, best};
+      for (int o = kW / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      sum = __shfl_sync(kAll, sum, 0);
+      if (lane < kC) *remote(&sh.part[turn][rank], lane) = {m, sum, best};
     }
-    cluster.sync();
-    float M = -CUDART_INF_F, S = 0.0f;
-    int best = V;
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      if (sh.part[turn][i].max > M) {
-        M = sh.part[turn][i].max;
-        best = sh.part[turn][i].best;
-      }
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      S += sh.part[turn][i].sum * rescale(sh.part[turn][i].max, M, c.h);
+    sync();
+    const Stat* part = sh.part[turn];
     turn ^= 1;
+    // lane i joins part i % kC: the same in every lane and block
+    const Stat one = part[lane % kC];
+    float M = one.max;
+#pragma unroll
+    for (int o = kC / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
     // ---- greedy sequences, and rows without a token
-    const int x = last ? -1 : a.draft[r];
     if (greedy || M == -CUDART_INF_F) {
+      int best = __reduce_min_sync(kAll, one.max == M ? one.best : V);
       if (M == -CUDART_INF_F) best = 0;
       if (!last && x == best && M > -CUDART_INF_F) continue;
       if (rank == 0 && tid == 0) {
@@ -260,128 +401,197 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a) {
       }
       break;
     }
+    const float of_one = one.sum * rescale(one.max, M, c);
+    float S = of_one;
+#pragma unroll
+    for (int o = kC / 2; o > 0; o >>= 1) S += __shfl_xor_sync(kAll, S, o);
     // ---- accept?
-    Two S2 = {0.0f, 0.0f};  // the sum to 2^-36, once it is needed
-    auto precise_sum = [&]() {
-      Two s = {0.0f, 0.0f};
-      for (int i = lo + 4 * lane; i < hi; i += 128) {
-        const float4 v = load4(z, i, hi, vec);
-        s = add(s, add(add(weight2(v.x, M, c, sh.tab), weight2(v.y, M, c, sh.tab)),
-                       add(weight2(v.z, M, c, sh.tab), weight2(v.w, M, c, sh.tab))));
-      }
-      return cluster_sum(s);
-    };
-    if (!last && x >= 0 && x < V) {
-      const float u = a.u_accept[r], q = a.probs ? a.probs[r * a.ld_probs + x] : 1.0f;
-      const Two w = weight2(z[x], M, c, sh.tab);
-      const float t = u * q * S;
-      bool ok = t < w.h;
-      if (fabsf(t - w.h) <= 0x1p-14f * w.h) {
-        S2 = precise_sum();
-        ok = less(mul(mul({u, 0.0f}, {q, 0.0f}), S2), w);
+    Left left = {held ? hold : z, nullptr, M, c, {0.0f, 0.0f}, -1, sh.tab};
+    Two wx = {0.0f, 0.0f};  // the weight of the draft
+    if (known) {
+      wx = weight2(z_x, M, c, sh.tab);
+      const float t = u_acc * q_x * S;
+      bool ok = t < wx.h;
+      if (fabsf(t - wx.h) <= 2.0f * rough * wx.h) {
+        const Two S2 = cluster_sum(left_sum(left, lo, hi, lane));
+        ok = less(mul(mul({u_acc, 0.0f}, {q_x, 0.0f}), S2), wx);
       }
       if (ok) continue;
     }
-    // ---- the draw
-    const float* pr = a.probs && !last ? a.probs + r * a.ld_probs : nullptr;
-    const bool pvec = pr && (reinterpret_cast<uintptr_t>(pr) & 15) == 0;
-    if (pr && S2.h == 0.0f) S2 = precise_sum();
-    bool minus = pr != nullptr;          // the draft's probabilities are taken off
-    int out = minus || last ? -1 : x;    // the token that is taken out
-    // what is left of four tokens: weight e and draft probability q give max(e - q S, 0)
-    auto left4 = [&](int i, Two o[4]) {
-      const float4 v = load4(z, i, hi, vec);
-      float4 q4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (minus) q4 = load4(pr, i, hi, pvec);
-      const float zz[4] = {v.x, v.y, v.z, v.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
+    // ---- the draw, first in f32. Weights are e, or max(e - q S, 0), or e without x.
+    const float* pr = a.probs && !last ? a.probs + r * a.ld_probs + base : nullptr;
+    const bool takes = known && !a.probs;
+    const int gone = takes ? x - base : -1;  // the token that is taken out, if it is here
+    float* const hold_q = hold + kW * run;
+    float* const bsum = reinterpret_cast<float*>(sh.psum[turn]);  // [kC], this exchange's buffer
+    if (pr) {
+      const bool pvec = (reinterpret_cast<uintptr_t>(pr) & 15) == 0;
+      const bool zvec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
+      float s = 0.0f;
+#pragma unroll 1
+      for (int i0 = lo; i0 < hi; i0 += 128 * kU) {
+        float4 q[kU];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[j] = weight2(zz[j], M, c, sh.tab);
-        if (i + j == out) o[j] = {0.0f, 0.0f};
-        if (minus && o[j].h > 0.0f) {
-          const Two p = mul({q[j], 0.0f}, S2);
-          o[j] = add(o[j], {-p.h, -p.l});
-          if (!(o[j].h > 0.0f)) o[j] = {0.0f, 0.0f};
-        }
-      }
-    };
-    Two total;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-      Two s = {0.0f, 0.0f};
-      for (int i = lo + 4 * lane; i < hi; i += 128) {
-        Two o[4];
-        left4(i, o);
-        s = add(s, add(add(o[0], o[1]), add(o[2], o[3])));
-      }
-      total = cluster_sum(s);
-      if (total.h > 0.0f) break;
-      minus = false;  // nothing is left: from p itself
-      out = -1;
-    }
-    const Two target = mul({fminf(a.u_sample[b], 1.0f), 0.0f}, total);
-    // the first of `n` parts with a weight whose running sum reaches the target
-    // (the last with a weight, should rounding leave the target above the total)
-    auto pick = [&](const Two* part, int n, Two& before) {
-      int at = -1;
-      for (int i = 0; i < n; ++i) {
-        if (!(part[i].h > 0.0f)) continue;
-        if (at >= 0) {
-          const Two upto = add(before, part[at]);
-          if (!less(upto, target)) break;
-          before = upto;
-        }
-        at = i;
-      }
-      return at;
-    };
-    Two cum = {0.0f, 0.0f};
-    if (pick(sh.psum[turn ^ 1], kC, cum) == rank && pick(sh.wsum, kW, cum) == warp) {
-      int found = V, pos = -1;
-      for (int i0 = lo; i0 < hi && !__any_sync(kAll, found < V); i0 += 128) {
-        const int i = i0 + 4 * lane;
-        Two o[4];
-        left4(i, o);
-        const Two s = add(add(o[0], o[1]), add(o[2], o[3]));
-        Two at = s;  // inclusive scan over the lanes, then exclusive
+        for (int u = 0; u < kU; ++u) q[u] = load4(pr, i0 + 128 * u + 4 * lane, hi, pvec);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const Two up = {__shfl_up_sync(kAll, at.h, d), __shfl_up_sync(kAll, at.l, d)};
-          if (lane >= d) at = add(up, at);
-        }
-        const Two end = add(cum, {__shfl_sync(kAll, at.h, 31), __shfl_sync(kAll, at.l, 31)});
-        at = {__shfl_up_sync(kAll, at.h, 1), __shfl_up_sync(kAll, at.l, 1)};
-        at = lane ? add(cum, at) : cum;
-        cum = end;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          at = add(at, o[j]);
-          if (o[j].h > 0.0f) {
-            pos = i + j;
-            if (!less(at, target)) found = min(found, i + j);
+        for (int u = 0; u < kU; ++u) {
+          const int i = i0 + 128 * u + 4 * lane;
+          if (i >= hi) continue;  // past the end z and q are -inf
+          float4 v;
+          if (held) {
+            *reinterpret_cast<float4*>(hold_q + i) = q[u];
+            v = *reinterpret_cast<const float4*>(hold + i);
+          } else {
+            v = load4(z, i, hi, zvec);
           }
+          const float e0 = weight1(v.x, M, c), e1 = weight1(v.y, M, c);
+          const float e2 = weight1(v.z, M, c), e3 = weight1(v.w, M, c);
+          s += (e0 > 0.0f ? fmaxf(fmaf(-q[u].x, S, e0), 0.0f) : 0.0f) +
+               (e1 > 0.0f ? fmaxf(fmaf(-q[u].y, S, e1), 0.0f) : 0.0f) +
+               ((e2 > 0.0f ? fmaxf(fmaf(-q[u].z, S, e2), 0.0f) : 0.0f) +
+                (e3 > 0.0f ? fmaxf(fmaf(-q[u].w, S, e3), 0.0f) : 0.0f));
         }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        found = min(found, __shfl_xor_sync(kAll, found, o));
-        pos = max(pos, __shfl_xor_sync(kAll, pos, o));
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+      if (lane == 0) sh.left[warp] = s;
+      __syncthreads();
+      if (warp == 0) {
+        s = lane < kW ? sh.left[lane] : 0.0f;
+#pragma unroll
+        for (int o = kW / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        s = __shfl_sync(kAll, s, 0);
+        if (lane < kC) *remote(bsum + rank, lane) = s;
       }
-      if (lane == 0) {
+      sync();
+      turn ^= 1;
+    }
+    // the blocks' weights, and this block's warps': without draft probabilities they
+    // are known from the row's sum
+    float of_block = 0.0f, of_warp = 0.0f;
+    if (lane < kC)
+      of_block = pr ? bsum[lane] : of_one - (takes && x / (kW * run) == lane ? wx.h : 0.0f);
+    if (lane < kW)
+      of_warp = pr ? sh.left[lane]
+                   : sh.warp[lane].sum * rescale(sh.warp[lane].max, M, c) -
+                         (gone >= 0 && gone < count && gone / run == lane ? wx.h : 0.0f);
+    const float* zs = held ? hold : z;
+    const float* qs = !pr ? nullptr : held ? hold_q : pr;
+    float total = of_block, before = 0.0f;
+#pragma unroll
+    for (int o = kC / 2; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    total = __shfl_sync(kAll, total, 0);
+    const float target = us * total, off = rough * S;
+    if (pick(of_block, target, before, lane) == rank) {
+      const int w = pick(of_warp, target, before, lane);
+      const int end_w = min(count, (w + 1) * run);
+      bool hit = false;  // a token whose borders the target is clear of
+#pragma unroll 1
+      for (int i0 = w * run; i0 < end_w && w >= 0; i0 += kT) {  // a token a thread
+        const int i = i0 + tid;
+        float e = i < end_w && i != gone ? weight1(zs[i], M, c) : 0.0f;
+        if (qs && e > 0.0f) e = fmaxf(fmaf(-qs[i], S, e), 0.0f);
+        const float inc = scan(e, lane);
+        if (lane == 31) sh.scan[warp] = inc;
+        __syncthreads();
+        const float in_warps = scan(lane < kW ? sh.scan[lane] : 0.0f, lane);
+        const float ahead = warp ? __shfl_sync(kAll, in_warps, warp - 1) : 0.0f;
+        const float at = before + ahead + (inc - e), then = before + ahead + inc;
+        const bool mine = at + off < target && target <= then - off;
+        if (mine) {
+          a.n_accepted[b] = r - r0;
+          a.next_token[b] = base + i;
+        }
+        before += __shfl_sync(kAll, in_warps, 31);
+        hit = __syncthreads_or(mine);
+        if (hit || before >= target + off) break;
+      }
+      if (!hit && tid < kC) *remote(&sh.again, tid) = 1;
+    }
+    // a total of nothing, or of NaN: no block is picked, every block sees it
+    if (!(total > 0.0f) && tid == 0) sh.again = 1;
+    sync();  // also: no block leaves while another may still write to it
+    if (!sh.again) return;
+    // ---- the draw again, in pairs
+    if (pr) {
+      left.S = cluster_sum(left_sum(left, lo, hi, lane));
+      left.q = qs;
+    }
+    left.out = gone;
+    Two sum = cluster_sum(left_sum(left, lo, hi, lane));
+    if (!(sum.h > 0.0f)) {  // nothing is left: from p itself
+      left.q = nullptr;
+      left.out = -1;
+      sum = cluster_sum(left_sum(left, lo, hi, lane));
+    }
+    const Two goal = mul({us, 0.0f}, sum);
+    Two cum = {0.0f, 0.0f};
+    const Two none = {0.0f, 0.0f};
+    if (pick(lane < kC ? sh.psum[turn ^ 1][lane] : none, goal, cum, lane) == rank) {
+      const int w = pick(lane < kW ? sh.left2[lane] : none, goal, cum, lane);
+      const int end_w = min(count, (w + 1) * run);
+      int found = -1, tail = -1;
+#pragma unroll 1
+      for (int i0 = w * run; i0 < end_w && found < 0; i0 += kT) {
+        const int i = i0 + tid;
+        const Two e = i < end_w ? left.at(i) : none;
+        Two at = scan(e, lane);
+        if (lane == 31) sh.scan2[warp] = at;
+        __syncthreads();
+        const Two in_warps = scan(lane < kW ? sh.scan2[lane] : none, lane);
+        if (warp) at = add(shfl(in_warps, warp - 1), at);
+        at = add(cum, at);
+        cum = add(cum, shfl(in_warps, 31));
+        // the lowest that reaches it; the highest with a weight in case none does
+        const bool has = e.h > 0.0f;
+        const unsigned m = __ballot_sync(kAll, has && !less(at, goal)), h = __ballot_sync(kAll, has);
+        if (lane == 0) {
+          sh.at[warp] = m ? i - lane + __ffs(m) - 1 : V;
+          sh.tail[warp] = h ? i - lane + 31 - __clz(h) : -1;
+        }
+        __syncthreads();
+        const int lowest = __reduce_min_sync(kAll, lane < kW ? sh.at[lane] : V);
+        if (lowest < V) found = lowest;
+        tail = max(tail, __reduce_max_sync(kAll, lane < kW ? sh.tail[lane] : -1));
+      }
+      if (tid == 0) {
         a.n_accepted[b] = r - r0;
-        a.next_token[b] = found < V ? found : pos;
+        a.next_token[b] = base + (found >= 0 ? found : tail);
       }
     }
     break;
   }
-  cluster.sync();  // no block leaves while another may still write to it
+  sync();  // no block leaves while another may still write to it
+}
+
+template <int kC>
+int launch_c(const VerifyArgs& a, cudaStream_t s) {
+  constexpr int kT = 256, kW = kT / 32;
+  constexpr int64_t kMost = 56 * 1024;  // shared memory of four blocks an SM
+  const int64_t run = (a.V - 1) / (kC * kW * 128) * 128 + 128;
+  int64_t smem = kW * run * 4 * (a.probs ? 2 : 1);
+  const int held = smem <= kMost;
+  if (!held) smem = 0;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(k_verify<kC, kT>, (int)kMost, done) != cudaSuccess) return 0;
+  if constexpr (kC == 1)
+    launch_k(k_verify<1, kT>, dim3((unsigned)a.n_seqs), kT, smem, s, a, held);
+  else
+    launch_k_cluster(k_verify<kC, kT>, dim3((unsigned)a.n_seqs * kC), kT, smem, s, kC, a, held);
+  return 1;
 }
 
 }  // namespace
 
-int launch_verify(const VerifyArgs& a, cudaStream_t s) {
+// Blocks of a sequence: eight while all sequences' blocks fit the SMs four at a time,
+// else four (64 sequences: 33.5 us with eight, 39.5 with four; 256: 44.3 and 32.8),
+// and no more than give every warp 128 tokens.
+int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
   if (a.n_seqs <= 0) return 0;
-  launch_k_cluster(k_verify, dim3((unsigned)a.n_seqs * kC), kT, 0, s, kC, a);
-  return 1;
+  const int want = (int64_t)a.n_seqs * 8 <= 4 * (int64_t)sms ? 8 : 4;
+  if (a.V > 4096 && want == 8) return launch_c<8>(a, s);
+  if (a.V > 2048) return launch_c<4>(a, s);
+  return a.V > 1024 ? launch_c<2>(a, s) : launch_c<1>(a, s);
 }
 
 }  // namespace fsk
