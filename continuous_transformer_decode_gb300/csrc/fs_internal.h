@@ -540,7 +540,7 @@ struct AttnQ8 {
   float* part_ml;     // [n][n_splits][H][2]
 };
 // Positions per split of one call (a multiple of 64).
-int attn_q8_split_len(int n, int Hkv, int max_len, int sms);
+int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms);
 int launch_attention_q8(const AttnQ8& a, int x_type, cudaStream_t s);  // q and out
 
 // Verification of drafted tokens (k_verify.cu).

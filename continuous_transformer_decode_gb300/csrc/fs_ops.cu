@@ -134,7 +134,10 @@ int plan_attention(const fs_kv_q8* c, int32_t n, int32_t n_heads, int32_t max_le
   if (!split_len) {
     const int sms = device_sms();
     if (!sms) return refuse(FS_ERR_CUDA, "no CUDA device");
-    p->split_len = attn_q8_split_len(n, c->n_kv_heads, p->max_len, sms);
+    p->split_len = attn_q8_split_len(n, c->n_kv_heads, c->head_dim, p->max_len, sms);
+    // a lane of more than 8192 splits: longer ones
+    const int64_t least = ((int64_t)p->max_len + kMaxSplits - 1) / kMaxSplits;
+    if (p->split_len < least) p->split_len = (int)((least + 127) / 128 * 128);
   }
   const int64_t ns = ((int64_t)p->max_len + p->split_len - 1) / p->split_len;
   if (ns > kMaxSplits) return refuse(FS_ERR_ARG, "split_len too small for max_len (8192 splits)");

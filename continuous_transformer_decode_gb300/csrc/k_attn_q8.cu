@@ -54,7 +54,7 @@ template <int HD>
 struct Shape;
 template <>
 struct Shape<64> {
-  static constexpr int kWarps = 4, kBlocks = 4, kS = 32, kStages = 3;
+  static constexpr int kWarps = 4, kBlocks = 5, kS = 32, kStages = 2;
 };
 template <>
 struct Shape<128> {
@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ
   const bool no_lane = (unsigned)row_lane >= (unsigned)a.kv.n_lanes;
   const int32_t* pages = a.kv.page_table + (no_lane ? 0 : (int64_t)row_lane * a.kv.max_pages);
   constexpr int kStep = kWarps * kS;
-  const int step_page = kStep / ps, step_slot = kStep % ps;
-  int t_next = start + warp * kS + lane, p_next = t_next / ps, s_next = t_next % ps;
+  const int step_page = (int)a.kv.by_page.div(kStep), step_slot = kStep - step_page * ps;
+  int t_next = start + warp * kS + lane;
+  int p_next = (int)a.kv.by_page.div(t_next), s_next = t_next - p_next * ps;
   // (page as the table has it, slot) of this lane's token of the next slice; -1: no token
   auto look_up = [&](int& page, int& slot) {
     page = lane < kS && t_next < end && !no_lane ? pages[p_next] : -1;
@@ -552,12 +553,19 @@ int dispatch(const AttnQ8& a, cudaStream_t s) {
 
 }  // namespace
 
-// Enough splits for about eight blocks an SM, of at least 128 positions.
-int attn_q8_split_len(int n, int Hkv, int max_len, int sms) {
-  const int64_t pairs = std::max<int64_t>(1, (int64_t)n * Hkv);
-  const int64_t want = std::max<int64_t>(1, 8 * (int64_t)sms / pairs);
-  const int64_t len = (std::max(max_len, 1) + want - 1) / want;
-  return (int)std::max<int64_t>(128, (len + 63) / 64 * 64);
+// Splits by the launch's sizes alone. A block costs about 3.4 us beside its tokens
+// (128 lanes of 128 to 4096 tokens: 111 us in splits of 4096 or 2048, 135 of 512), so
+// the blocks are to fill the SMs once: one lane of 131071 tokens and 8 KV heads takes
+// 55 us in 57 splits (456 blocks on 456 places), 70 in 64, 66 in 147. Lanes differ in
+// length and max_len is the longest, so several lanes aim at half as many again (33
+// lanes of up to 3001 tokens, 2 heads of 256: 23 us in 3 splits, 33 in 2). No split is
+// longer than 4096, so that one long lane among many is shared, or shorter than 256.
+int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
+  const int blocks = hd == 64 ? Shape<64>::kBlocks : hd == 128 ? Shape<128>::kBlocks : Shape<256>::kBlocks;
+  const int64_t places = (int64_t)sms * blocks, pairs = std::max<int64_t>(1, (int64_t)n * Hkv);
+  const int64_t splits = std::max<int64_t>(1, (n > 1 ? 3 * places / 2 : places) / pairs);
+  const int64_t len = (std::max(max_len, 1) + splits - 1) / splits;
+  return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
 
 int launch_attention_q8(const AttnQ8& a, int x_type, cudaStream_t s) {
