@@ -71,8 +71,8 @@ const fs_handle* g_trace_owner = nullptr;
 bool trace_install_all(TraceBuf* b) {
   return trace_install_misc(b) && trace_install_gemm(b) && trace_install_gemv(b) &&
          trace_install_attn(b) && trace_install_attn_mma(b) && trace_install_attn_tma(b) &&
-         trace_install_attn_warp(b) &&
-         trace_install_attn_tiled(b);
+         trace_install_attn_warp(b) && trace_install_attn_tiled(b) && trace_install_kv_q8(b) &&
+         trace_install_attn_q8(b);
 }
 
 // Uninstalls and frees the trace buffer if h owns it (the stream has been
@@ -193,6 +193,11 @@ struct fs_handle {
   float* part_ml = nullptr;
   float* part_acc = nullptr;
   int* attn_counters = nullptr;  // [max_lanes * Hkv], zero between steps
+  // kv_dtype FS_DTYPE_Q8_ROW: the arenas of all layers (kv.k and kv.v are null),
+  // kv_rows rows a layer, written and read by the fs_kv_q8 operators' kernels
+  bool kv_q8 = false;
+  KvQ8 q8;
+  int64_t kv_rows = 0;
   bool attn_tiled = false;
   bool attn_mma = false;
   bool attn_tma = false;         // KV tiles by TMA (k_attn_tma.cu)
@@ -368,8 +373,13 @@ int validate_desc(const fs_model_desc* d, std::string* why) {
   if (d->n_heads / d->n_kv_heads > 8) return bad("at most 8 query heads per KV head");
   if (d->head_dim % 2 || d->head_dim > 256) return bad("head_dim must be even and <= 256");
   if (d->weight_dtype < 0 || d->weight_dtype > 2) return bad("unknown weight_dtype");
-  if (d->kv_dtype != FS_DTYPE_F32 && d->kv_dtype != FS_DTYPE_BF16)
-    return bad("kv_dtype must be F32 or BF16");
+  if (d->kv_dtype != FS_DTYPE_F32 && d->kv_dtype != FS_DTYPE_BF16 &&
+      d->kv_dtype != FS_DTYPE_Q8_ROW)
+    return bad("kv_dtype must be F32, BF16 or Q8_ROW");
+  if (d->kv_dtype == FS_DTYPE_Q8_ROW && !kv_q8_supports(d->head_dim))
+    return bad("Q8_ROW KV needs head_dim 64, 128 or 256");
+  if (d->kv_dtype == FS_DTYPE_Q8_ROW && d->max_lanes > 65535)
+    return bad("Q8_ROW KV serves at most 65535 lanes");
   if (d->weight_dtype == FS_DTYPE_Q8_0 &&
       (d->d_model % 32 || d->d_ffn % 32 || (d->n_heads * d->head_dim) % 32))
     return bad("Q8_0 needs every input width to be a multiple of 32");
@@ -419,6 +429,12 @@ int create_impl(fs_handle* h, const fs_weights* W) {
     const char* e = getenv("FS_SPLIT_LEN");
     const int v = e ? atoi(e) : 0;
     if ((v == 128 || v == 256 || v == 512 || v == 1024) && h->split_len != 256) h->split_len = v;
+  }
+  h->kv_q8 = d.kv_dtype == FS_DTYPE_Q8_ROW;
+  if (h->kv_q8) {  // the operator's own rule for a full handle
+    h->split_len = attn_q8_split_len(d.max_lanes, d.n_kv_heads, d.head_dim, d.max_pos, h->sms);
+    if ((d.max_pos + h->split_len - 1) / h->split_len > kMaxQ8Splits || d.max_pos > (1 << 30))
+      return h->fail(FS_ERR_ARG, "max_pos too large for Q8_ROW KV");
   }
   h->max_splits = (d.max_pos + h->split_len - 1) / h->split_len;
   h->max_pages_per_lane = (d.max_pos + d.page_size - 1) / d.page_size;
@@ -520,12 +536,32 @@ int create_impl(fs_handle* h, const fs_weights* W) {
   kv.page_size = d.page_size;
   kv.max_pages = h->max_pages_per_lane;
   kv.layer_stride = (int64_t)d.n_pages * kv.Hkv * kv.page_size * kv.hd;
-  const size_t kv_bytes = (size_t)d.n_layers * kv.layer_stride * (kv.kv_f32 ? 4 : 2);
-  if (h->alloc(&kv.k, kv_bytes) != cudaSuccess || h->alloc(&kv.v, kv_bytes) != cudaSuccess)
-    return h->fail(FS_ERR_OOM, "KV arena allocation failed");
+  if (h->kv_q8) {
+    h->kv_rows = (int64_t)d.n_pages * kv.Hkv * kv.page_size;
+    if (h->kv_rows > ((int64_t)1 << 32) - 2 || (int64_t)kv.max_pages * kv.page_size > (1 << 30))
+      return h->fail(FS_ERR_ARG, "KV arena too large for Q8_ROW KV");
+    const size_t rows = (size_t)d.n_layers * h->kv_rows;
+    KvQ8& c = h->q8;
+    if (h->alloc(&c.k, rows * kv.hd) != cudaSuccess || h->alloc(&c.v, rows * kv.hd) != cudaSuccess ||
+        h->alloc(&c.ks, rows * 4) != cudaSuccess || h->alloc(&c.vs, rows * 4) != cudaSuccess)
+      return h->fail(FS_ERR_OOM, "KV arena allocation failed");
+    c.n_pages = d.n_pages;
+    c.Hkv = kv.Hkv;
+    c.page_size = kv.page_size;
+    c.hd = kv.hd;
+    c.n_lanes = d.max_lanes;
+    c.max_pages = kv.max_pages;
+    c.by_page = FastDiv((uint32_t)kv.page_size);
+    c.by_head = FastDiv((uint32_t)kv.Hkv);
+  } else {
+    const size_t kv_bytes = (size_t)d.n_layers * kv.layer_stride * (kv.kv_f32 ? 4 : 2);
+    if (h->alloc(&kv.k, kv_bytes) != cudaSuccess || h->alloc(&kv.v, kv_bytes) != cudaSuccess)
+      return h->fail(FS_ERR_OOM, "KV arena allocation failed");
+  }
   if (h->alloc(&kv.pt, (size_t)d.max_lanes * kv.max_pages * 4) != cudaSuccess)
     return h->fail(FS_ERR_OOM, "page table allocation failed");
   FS_CK(h, cudaMemset(kv.pt, 0, (size_t)d.max_lanes * kv.max_pages * 4));
+  h->q8.page_table = kv.pt;
   h->pt.assign(d.max_lanes, {});
   h->len.assign(d.max_lanes, 0);
   for (int p = 0; p < d.n_pages; ++p) h->free_pages.insert(p);
@@ -585,6 +621,7 @@ int create_impl(fs_handle* h, const fs_weights* W) {
     const char* e = getenv("FS_ATTN");
     const bool force_mma = e && std::string(e) == "mma";
     const bool force_warp = e && std::string(e) == "warp";
+    if (!h->kv_q8) {
     h->attn_mma = attn_mma_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, h->split_len,
                                     h->max_splits);
     // the TMA kernel's producer warp and barrier set-up pay off on long
@@ -613,6 +650,7 @@ int create_impl(fs_handle* h, const fs_weights* W) {
       return h->fail(FS_ERR_ARG,
                      "no attention kernel for this shape: head_dim must be 16, 32, 64, 128 or "
                      "256, and page_size 16, 32 or 64 for f32 KV or head_dim < 64");
+    }
   }
   FS_CK(h, cudaMemset(h->hpanel, 0, (size_t)(1 + h->act_split) * B * h->Kp_d * xs));
   FS_CK(h, cudaMemset(h->opanel, 0, (size_t)(1 + h->act_split) * B * h->Kp_q * xs));
@@ -760,6 +798,26 @@ void take_pages(fs_handle* h, int k, int n_tokens_after) {
   }
 }
 
+// Rows [q_begin, q_end) of a lane moved between page tables, in every layer (see
+// launch_kv_relocate); the number of kernels.
+int relocate(fs_handle* h, const int32_t* src_pt, const int32_t* dst_pt, int q_begin, int q_end,
+             int a, int delta) {
+  if (h->kv_q8)
+    return launch_kv_q8_relocate(h->q8, h->d.n_layers, h->kv_rows, src_pt, dst_pt, q_begin, q_end, a,
+                                 delta, h->rope_cos, h->rope_sin, h->stream);
+  return launch_kv_relocate(h->kv, h->d.n_layers, src_pt, dst_pt, q_begin, q_end, a, delta,
+                            h->rope_cos, h->rope_sin, h->stream);
+}
+
+// What the kernels that copy n tokens of a lane take: its page indices, or for an
+// 8-bit cache the rows' lanes and positions.
+std::vector<int32_t> kv_index(const fs_handle* h, int lane, int n) {
+  if (!h->kv_q8) return h->pt[lane];
+  std::vector<int32_t> v((size_t)2 * n, lane);
+  for (int t = 0; t < n; ++t) v[(size_t)n + t] = t;
+  return v;
+}
+
 int seed_lane_pages(fs_handle* h, int lane, int n) {
   if (lane < 0 || lane >= h->d.max_lanes) return h->fail(FS_ERR_LANE, "lane out of range");
   if (n < 0) return h->fail(FS_ERR_ARG, "negative token count");
@@ -775,6 +833,21 @@ int seed_lane_pages(fs_handle* h, int lane, int n) {
   return FS_OK;
 }
 
+// Bytes of one stored K or V element (8-bit rows: a code and its share of the scale).
+double kv_elem_bytes(const fs_handle* h) {
+  return h->kv_q8 ? 1.0 + 4.0 / h->kv.hd : h->kv.kv_f32 ? 4.0 : 2.0;
+}
+
+// The 8-bit cache of one layer.
+KvQ8 q8_layer(const fs_handle* h, int l) {
+  KvQ8 c = h->q8;
+  c.k += (size_t)l * h->kv_rows * c.hd;
+  c.v += (size_t)l * h->kv_rows * c.hd;
+  c.ks += (size_t)l * h->kv_rows;
+  c.vs += (size_t)l * h->kv_rows;
+  return c;
+}
+
 // Enqueues every kernel of one step for the n panel rows on h->stream (the
 // per-step arguments are read from device memory, so the sequence can be
 // captured once per n and replayed).
@@ -784,7 +857,7 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
   cudaStream_t s = h->stream;
   const StepArgs& args = h->args;
   const double xs = h->xtype == X_F32 ? 4.0 : 2.0;
-  const double kvs = h->kv.kv_f32 ? 4.0 : 2.0;
+  const double kvs = kv_elem_bytes(h);
   auto wbytes = [&](const Mat& m) {
     double b = (double)m.N * m.K * (m.wtype == W_F32 ? 4 : (m.wtype == W_BF16 ? 2 : 1));
     if (m.wtype == W_Q8) b += (double)m.N * (m.K / 32) * 2;
@@ -842,6 +915,26 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
                               h->xtype, h->Kp_d, h->lo_h, s);
       });
     gemm(W.qkv, W.qkv_tc, h->hpanel, h->lo_h, EPI_STORE, h->qkv, nullptr, h->Nqkv, h->Nqkv);
+    if (h->kv_q8) {  // every row's k, v are quantised into the cache, then attended to
+      const KvQ8 c = q8_layer(h, l);
+      const float* k = h->qkv + h->Nq;
+      h->launch(FS_PROF_OTHER, (double)n * 2.0 * h->Nkv * (4.0 + kvs), [&] {
+        return launch_kv_q8_append(c, k, k + h->Nkv, h->Nqkv, h->Nqkv, X_F32, args.lane, args.pos,
+                                   n, h->rope_cos, h->rope_sin, d.max_pos, s);
+      });
+      AttnQ8 a{};
+      a.kv = c;
+      a.q = h->qkv; a.q_stride = h->Nqkv;
+      a.lanes = args.lane; a.lens = args.pos; a.len_add = 1;
+      a.n = n; a.H = d.n_heads; a.max_len = d.max_pos;
+      a.scale = 1.0f / std::sqrt((float)d.head_dim);
+      a.rc = h->rope_cos; a.rs = h->rope_sin;
+      a.out = h->opanel; a.out_stride = h->Kp_q; a.out_lo = h->lo_o;
+      a.split_len = h->split_len; a.n_splits = h->max_splits;
+      a.part_acc = h->part_acc; a.part_ml = h->part_ml;
+      h->launch(FS_PROF_ATTN, kv_read + (double)n * h->Nq * (4.0 + xs),
+                [&] { return launch_attention_q8(a, X_F32, h->xtype, s); });
+    } else {
     // a chunked step first appends every row's k, v (rows of one lane at
     // consecutive positions see each other's keys); the MMA attention kernels
     // then only read, the other kernels give way to the three-kernel path
@@ -869,6 +962,7 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
                   return h->attn_mma ? launch_attention_mma(ap, n, h->xtype, s)
                                      : launch_attention_tiled(ap, n, h->xtype, s);
                 });
+    }
     }
     gemm(W.o, W.o_tc, h->opanel, h->lo_o, EPI_STORE, h->y, nullptr, d.d_model,
          d.d_model);
@@ -983,9 +1077,7 @@ int fs_lane_clone(fs_handle* h, int32_t src, int32_t dst) {
     int32_t* dst_row = h->kv.pt + (size_t)dst * h->kv.max_pages;
     FS_CK(h, cudaMemcpyAsync(dst_row, t.data(), t.size() * 4, cudaMemcpyHostToDevice, h->stream));
     if (partial) {
-      h->launches += launch_kv_relocate(h->kv, h->d.n_layers,
-                                        h->kv.pt + (size_t)src * h->kv.max_pages, dst_row,
-                                        full * ps, n, n, 0, h->rope_cos, h->rope_sin, h->stream);
+      h->launches += relocate(h, h->kv.pt + (size_t)src * h->kv.max_pages, dst_row, full * ps, n, n, 0);
       FS_CK(h, cudaGetLastError());
     }
   }
@@ -1024,8 +1116,7 @@ int fs_lane_evict(fs_handle* h, int32_t lane, int32_t start, int32_t end) {
                              h->stream));
     cudaError_t e = cudaMemcpyAsync(row, t.data(), t.size() * 4, cudaMemcpyHostToDevice, h->stream);
     if (e == cudaSuccess) {
-      h->launches += launch_kv_relocate(h->kv, h->d.n_layers, h->d_reloc_pt, row, q_begin, nl,
-                                        start, delta, h->rope_cos, h->rope_sin, h->stream);
+      h->launches += relocate(h, h->d_reloc_pt, row, q_begin, nl, start, delta);
       e = cudaGetLastError();
     }
     if (e != cudaSuccess) {  // put the lane's device row back (best effort)
@@ -1102,7 +1193,7 @@ int run_step(fs_handle* h, const int32_t* lanes, int32_t* positions, const int32
   // ---- the step: one graph replay, or the kernels one by one
   double kv_read = 0.0;  // K and V bytes attention reads per layer
   for (int i = 0; i < n; ++i)
-    kv_read += (double)(positions[i] + 1) * h->Nkv * 2.0 * (h->kv.kv_f32 ? 4.0 : 2.0);
+    kv_read += (double)(positions[i] + 1) * h->Nkv * 2.0 * kv_elem_bytes(h);
   float* out = logits_out ? logits_out : h->logits;
   int32_t* greedy = greedy_out ? h->d_greedy : nullptr;
   if (!logits_out && !h->prof_on && h->graphs_on) {
@@ -1352,14 +1443,17 @@ int fs_lane_export_kv(fs_handle* h, int32_t lane, int32_t layer, float* k_out, f
   int32_t* dp = nullptr;
   float *dk = nullptr, *dv = nullptr;
   int rc = FS_OK;
-  if (cudaMalloc(&dp, h->pt[lane].size() * 4) != cudaSuccess ||
+  const std::vector<int32_t> idx = kv_index(h, lane, n);
+  if (cudaMalloc(&dp, idx.size() * 4) != cudaSuccess ||
       cudaMalloc(&dk, cnt * 4) != cudaSuccess || cudaMalloc(&dv, cnt * 4) != cudaSuccess) {
     rc = h->fail(FS_ERR_OOM, "export buffers");
   } else {
-    cudaError_t e = cudaMemcpyAsync(dp, h->pt[lane].data(), h->pt[lane].size() * 4,
-                                    cudaMemcpyHostToDevice, h->stream);
+    cudaError_t e = cudaMemcpyAsync(dp, idx.data(), idx.size() * 4, cudaMemcpyHostToDevice,
+                                    h->stream);
     if (e == cudaSuccess) {
-      h->launches += launch_export_kv(h->kv, layer, dp, n, dk, dv, h->stream);
+      h->launches += h->kv_q8 ? launch_kv_q8_read(q8_layer(h, layer), dp, dp + n, n, dk, dv, h->Nkv,
+                                                  h->Nkv, X_F32, h->stream)
+                              : launch_export_kv(h->kv, layer, dp, n, dk, dv, h->stream);
       e = cudaGetLastError();
     }
     if (e == cudaSuccess) e = cudaMemcpyAsync(k_out, dk, cnt * 4, cudaMemcpyDeviceToHost, h->stream);
@@ -1381,18 +1475,22 @@ int fs_lane_import_kv(fs_handle* h, int32_t lane, const float* k, const float* v
   const size_t cnt = (size_t)n * h->kv.Hkv * h->kv.hd;
   int32_t* dp = nullptr;
   float *dk = nullptr, *dv = nullptr;
-  if (cudaMalloc(&dp, h->pt[lane].size() * 4) != cudaSuccess ||
+  const std::vector<int32_t> idx = kv_index(h, lane, n);
+  if (cudaMalloc(&dp, idx.size() * 4) != cudaSuccess ||
       cudaMalloc(&dk, cnt * 4) != cudaSuccess || cudaMalloc(&dv, cnt * 4) != cudaSuccess) {
     rc = h->fail(FS_ERR_OOM, "import buffers");
   } else {
-    cudaError_t e = cudaMemcpyAsync(dp, h->pt[lane].data(), h->pt[lane].size() * 4,
-                                    cudaMemcpyHostToDevice, h->stream);
+    cudaError_t e = cudaMemcpyAsync(dp, idx.data(), idx.size() * 4, cudaMemcpyHostToDevice,
+                                    h->stream);
     for (int l = 0; l < h->d.n_layers && e == cudaSuccess; ++l) {
       e = cudaMemcpyAsync(dk, k + (size_t)l * cnt, cnt * 4, cudaMemcpyHostToDevice, h->stream);
       if (e == cudaSuccess)
         e = cudaMemcpyAsync(dv, v + (size_t)l * cnt, cnt * 4, cudaMemcpyHostToDevice, h->stream);
       if (e == cudaSuccess) {
-        h->launches += launch_import_kv(h->kv, l, dp, n, dk, dv, h->stream);
+        h->launches += h->kv_q8
+                           ? launch_kv_q8_append(q8_layer(h, l), dk, dv, h->Nkv, h->Nkv, X_F32, dp,
+                                                 dp + n, n, nullptr, nullptr, 0, h->stream)
+                           : launch_import_kv(h->kv, l, dp, n, dk, dv, h->stream);
         e = cudaGetLastError();
       }
     }
@@ -1414,7 +1512,9 @@ int fs_lane_fill_random_kv(fs_handle* h, int32_t lane, int32_t n, uint64_t seed)
   if (cudaMalloc(&dp, np * 4) != cudaSuccess) return h->fail(FS_ERR_OOM, "fill buffers");
   cudaError_t e = cudaMemcpyAsync(dp, h->pt[lane].data(), np * 4, cudaMemcpyHostToDevice, h->stream);
   if (e == cudaSuccess) {
-    h->launches += launch_fill_random_kv(h->kv, h->d.n_layers, dp, (int)np, seed, h->stream);
+    h->launches += h->kv_q8 ? launch_fill_random_kv_q8(h->q8, h->d.n_layers, h->kv_rows, dp, (int)np,
+                                                       seed, h->stream)
+                            : launch_fill_random_kv(h->kv, h->d.n_layers, dp, (int)np, seed, h->stream);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(h->stream);
@@ -1517,6 +1617,7 @@ int fs_gemm_plan(int64_t n_rows, int64_t k_inputs, int max_lanes, int n, int sms
 
 const char* fs_attention_path(const fs_handle* h) {
   if (!h) return "";
+  if (h->kv_q8) return "q8-mma";
   if (h->attn_warp) return "warp-mma";
   if (h->attn_tma) return "tma-mma";
   if (h->attn_mma) return "cp.async-mma";

@@ -55,8 +55,9 @@ enum TraceTag {
   TR_EMBED = 1, TR_RMSNORM = 2, TR_SAMPLE = 3, TR_ARGMAX = 4,
   TR_ATTN_MMA = 5, TR_ATTN_TMA = 6, TR_ATTN_TILED = 7, TR_ATTN_WARP = 8,
   TR_ROPE_APPEND = 9, TR_GEMV = 10, TR_ATTN_PARTIAL = 11, TR_ATTN_COMBINE = 12,
-  TR_GEMV_SWIGLU = 13,
-  TR_GEMM = 16  // + the epilogue kind (Epi)
+  TR_GEMV_SWIGLU = 13, TR_KV_Q8_APPEND = 14, TR_ATTN_Q8 = 15,
+  TR_GEMM = 16,  // + the epilogue kind (Epi)
+  TR_ATTN_Q8_JOIN = 20
 };
 
 __device__ __forceinline__ unsigned long long gtime() {
@@ -150,6 +151,8 @@ int trace_install_attn_mma(TraceBuf* p);
 int trace_install_attn_warp(TraceBuf* p);
 int trace_install_attn_tma(TraceBuf* p);
 int trace_install_attn_tiled(TraceBuf* p);
+int trace_install_kv_q8(TraceBuf* p);
+int trace_install_attn_q8(TraceBuf* p);
 
 // Kernel launch with the programmatic-stream-serialization attribute.
 template <typename... K, typename... A>
@@ -529,19 +532,31 @@ struct AttnQ8 {
   int64_t q_stride;
   const int32_t* lanes;
   const int32_t* lens;
+  int len_add;        // added to lens[i] (1: they are the positions of new tokens)
   int n, H, max_len;
   float scale;
   const float* rc;    // rotation of q at lens[i] - 1 (null: q as it is)
   const float* rs;
   void* out;          // [n] rows of [H][hd], out_stride elements apart
   int64_t out_stride;
+  int64_t out_lo;     // bf16 out: remainders bf16(v - hi) at out + out_lo (0: none)
   int split_len, n_splits;
   float* part_acc;    // [n][n_splits][H][hd] when n_splits > 1
   float* part_ml;     // [n][n_splits][H][2]
 };
+constexpr int kMaxQ8Splits = 8192;  // of a row: the join keeps a weight of each in shared memory
 // Positions per split of one call (a multiple of 64).
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms);
-int launch_attention_q8(const AttnQ8& a, int x_type, cudaStream_t s);  // q and out
+// q and out of one type, or f32 q and bf16 out.
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s);
+// fs_kv_q8 counterparts of launch_fill_random_kv and launch_kv_relocate, over the
+// layers of an arena (layer_rows rows each); a key that is turned back is quantised
+// anew (f32 quotients).
+int launch_fill_random_kv_q8(const KvQ8& c, int L, int64_t layer_rows, const int32_t* pages,
+                             int n_pages, uint64_t seed, cudaStream_t s);
+int launch_kv_q8_relocate(const KvQ8& c, int L, int64_t layer_rows, const int32_t* src_pt,
+                          const int32_t* dst_pt, int q_begin, int q_end, int a, int delta,
+                          const float* rc, const float* rs, cudaStream_t s);
 
 // Verification of drafted tokens (k_verify.cu).
 struct VerifyArgs {

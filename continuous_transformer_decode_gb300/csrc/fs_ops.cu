@@ -18,7 +18,6 @@ int refuse(int code, const char* why) {
   return code;
 }
 
-constexpr int kMaxSplits = 8192;      // of a row: the join keeps a weight of each in shared memory
 constexpr int kMaxTokens = 1 << 30;  // token + split arithmetic stays in 32 bits
 
 int x_type(int32_t dtype) {
@@ -136,11 +135,11 @@ int plan_attention(const fs_kv_q8* c, int32_t n, int32_t n_heads, int32_t max_le
     if (!sms) return refuse(FS_ERR_CUDA, "no CUDA device");
     p->split_len = attn_q8_split_len(n, c->n_kv_heads, c->head_dim, p->max_len, sms);
     // a lane of more than 8192 splits: longer ones
-    const int64_t least = ((int64_t)p->max_len + kMaxSplits - 1) / kMaxSplits;
+    const int64_t least = ((int64_t)p->max_len + kMaxQ8Splits - 1) / kMaxQ8Splits;
     if (p->split_len < least) p->split_len = (int)((least + 127) / 128 * 128);
   }
   const int64_t ns = ((int64_t)p->max_len + p->split_len - 1) / p->split_len;
-  if (ns > kMaxSplits) return refuse(FS_ERR_ARG, "split_len too small for max_len (8192 splits)");
+  if (ns > kMaxQ8Splits) return refuse(FS_ERR_ARG, "split_len too small for max_len (8192 splits)");
   p->n_splits = (int)ns;
   p->bytes = ns <= 1 ? 0 : (int64_t)n * ns * n_heads * (c->head_dim + 2) * 4;
   return FS_OK;
@@ -247,7 +246,7 @@ int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
   a.split_len = p.split_len; a.n_splits = p.n_splits;
   a.part_acc = static_cast<float*>(workspace);
   a.part_ml = a.part_acc ? a.part_acc + (int64_t)n * p.n_splits * n_heads * cache->head_dim : nullptr;
-  return launched(launch_attention_q8(a, xt, (cudaStream_t)stream));
+  return launched(launch_attention_q8(a, xt, xt, (cudaStream_t)stream));
 }
 
 int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,

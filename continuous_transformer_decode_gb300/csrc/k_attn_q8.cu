@@ -41,6 +41,7 @@
 #include "kv_q8.cuh"
 
 namespace fsk {
+FS_TRACE_TU(attn_q8)
 namespace {
 
 using namespace attn;
@@ -91,9 +92,6 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
 
 __device__ __forceinline__ float ld1(const float* p) { return *p; }
 __device__ __forceinline__ float ld1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -157,28 +155,26 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int w) {
 }
 
 __device__ __forceinline__ int row_len(const AttnQ8& a, int i) {
-  return min(min(max(a.lens[i], 0), a.max_len), a.kv.max_pages * a.kv.page_size);
+  return min(max(a.lens[i], 0), a.max_len - a.len_add) + a.len_add;
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ8 a) {
+template <typename QT, typename OT, int HD>
+__device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   using L = Lay<HD>;
   constexpr int kWarps = L::kWarps, kT = L::kT, kS = L::kS;
   constexpr int kHalf = HD / 2;
   constexpr int kKs = HD / 16;         // k-steps of Q K^T
   constexpr int kMt = HD / 16;         // m-tiles of V^T W
   constexpr int kRowChunks = HD / 16;  // 16-byte chunks per row
-  pdl_wait();
-  pdl_trigger();
   const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int H = a.H, G = H / a.kv.Hkv;
   const int len = row_len(a, b);
   const int start = s * a.split_len, end = min(len, start + a.split_len);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, cq = lane & 3;
-  T* orow = static_cast<T*>(a.out) + b * a.out_stride + (int64_t)g * G * HD;
+  OT* orow = static_cast<OT*>(a.out) + b * a.out_stride + (int64_t)g * G * HD;
   if (len == 0 && s == 0)
-    for (int i = tid; i < G * HD; i += kT) st1(orow + i, 0.0f);
+    for (int i = tid; i < G * HD; i += kT) st_out(orow + i, 0.0f, a.out_lo);
   if (start >= end) return;
 
   extern __shared__ __align__(128) uint8_t smem[];
@@ -239,7 +235,7 @@ __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ
   for (int i = 0; i < L::kStages; ++i) look_up(page[i], slot[i]);
 
   // ---- q, rotated; warp w takes heads w, w + kWarps, ..
-  const T* qr = static_cast<const T*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
+  const QT* qr = static_cast<const QT*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
   constexpr int kHeads = kG / kWarps, kP = kHalf / 32;
   float x0[kHeads][kP], x1[kHeads][kP];
 #pragma unroll
@@ -458,7 +454,7 @@ __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ
       A = fmaf(wo[(w * kG + h) * HD + d], f, A);
     }
     if (len <= a.split_len) {
-      st1(orow + i, Lsum > 0.0f ? A / Lsum : 0.0f);
+      st_out(orow + i, Lsum > 0.0f ? A / Lsum : 0.0f, a.out_lo);
     } else {
       a.part_acc[base * HD + i] = A;
       if (d == 0) {
@@ -469,17 +465,30 @@ __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ
   }
 }
 
+template <typename QT, typename OT, int HD>
+__global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ8 a) {
+  __shared__ unsigned long long s_tr[4];
+  TraceSmem::begin(s_tr, g_trace);
+  pdl_wait();
+  TraceSmem::ready(s_tr);
+  pdl_trigger();
+  attn_q8_body<QT, OT, HD>(a);
+  TraceSmem::end(s_tr, TR_ATTN_Q8);
+}
+
 // Joins the splits of one (row, head): the weights of the splits first, then
 // HD / 4 columns of threads by kJ, column x taking splits x, x + kJ, .. in
 // order, and the kJ sums in order.
 constexpr int kJ = 8;
-template <typename T, int HD>
+template <typename OT, int HD>
 __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
+  TraceScope tr(g_trace, TR_ATTN_Q8_JOIN);
   constexpr int kT = HD / 4 * kJ;
   __shared__ float4 part[kJ][HD / 4];
   __shared__ float red[2][kT / 32];
   extern __shared__ float w[];  // [n_splits]
   pdl_wait();
+  tr.ready();
   pdl_trigger();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int len = row_len(a, b);
@@ -527,26 +536,27 @@ __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
   float o = 0.0f;
 #pragma unroll
   for (int i = 0; i < kJ; ++i) o += reinterpret_cast<const float*>(part[i])[tid];
-  st1(static_cast<T*>(a.out) + b * a.out_stride + (int64_t)h * HD + tid,
-      Lsum > 0.0f ? o / Lsum : 0.0f);
+  st_out(static_cast<OT*>(a.out) + b * a.out_stride + (int64_t)h * HD + tid,
+         Lsum > 0.0f ? o / Lsum : 0.0f, a.out_lo);
 }
 
-template <typename T, int HD>
+template <typename QT, typename OT, int HD>
 int launch_hd(const AttnQ8& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  if (allow_smem(k_attn_q8<T, HD>, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
-  launch_k(k_attn_q8<T, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), Lay<HD>::kT, Lay<HD>::kBytes, s, a);
+  if (allow_smem(k_attn_q8<QT, OT, HD>, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
+  launch_k(k_attn_q8<QT, OT, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), Lay<HD>::kT, Lay<HD>::kBytes, s,
+           a);
   if (a.n_splits == 1) return 1;
-  launch_k(k_attn_q8_join<T, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);
+  launch_k(k_attn_q8_join<OT, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);
   return 2;
 }
 
-template <typename T>
+template <typename QT, typename OT>
 int dispatch(const AttnQ8& a, cudaStream_t s) {
   switch (a.kv.hd) {
-    case 64: return launch_hd<T, 64>(a, s);
-    case 128: return launch_hd<T, 128>(a, s);
-    case 256: return launch_hd<T, 256>(a, s);
+    case 64: return launch_hd<QT, OT, 64>(a, s);
+    case 128: return launch_hd<QT, OT, 128>(a, s);
+    case 256: return launch_hd<QT, OT, 256>(a, s);
     default: return 0;
   }
 }
@@ -568,9 +578,10 @@ int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
   return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
 
-int launch_attention_q8(const AttnQ8& a, int x_type, cudaStream_t s) {
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s) {
   if (a.n <= 0) return 0;
-  return x_type == X_BF16 ? dispatch<__nv_bfloat16>(a, s) : dispatch<float>(a, s);
+  if (q_type == X_BF16) return dispatch<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return out_type == X_BF16 ? dispatch<float, __nv_bfloat16>(a, s) : dispatch<float, float>(a, s);
 }
 
 }  // namespace fsk

@@ -17,6 +17,7 @@
 #include "two_f32.cuh"
 
 namespace fsk {
+FS_TRACE_TU(kv_q8)
 namespace {
 
 using namespace two;
@@ -231,7 +232,10 @@ __global__ void __launch_bounds__(kT, 12)
                    const int32_t* __restrict__ positions, unsigned items,
                    const float* __restrict__ rc, const float* __restrict__ rs, int rope_len) {
   constexpr int kL = HD / 8, kHalf = HD / 2;
+  __shared__ unsigned long long s_tr[4];
+  TraceSmem::begin(s_tr, g_trace);
   pdl_wait();
+  TraceSmem::ready(s_tr);
   pdl_trigger();
   const int sub = threadIdx.x % kL;
   const unsigned at = (unsigned)(((uint64_t)blockIdx.x * kT + threadIdx.x) / kL);
@@ -277,6 +281,7 @@ __global__ void __launch_bounds__(kT, 12)
     if (do_v)
       quantise_border_row<T, HD, false>(v + vo, nullptr, nullptr, c.v + to * HD, c.vs + to, lane);
   }
+  TraceSmem::end(s_tr, TR_KV_Q8_APPEND);
 }
 
 __device__ __forceinline__ void values4(uint32_t w, float s, float x[4]) {
@@ -326,6 +331,105 @@ __global__ void __launch_bounds__(kT)
       values4(vw[h], vs, x);
       store4<kVec>(v_out + i * v_stride + (int64_t)g * HD + sub * 4 + h * kHalf, x);
     }
+  }
+}
+
+__device__ __forceinline__ uint64_t mix64(uint64_t z) {  // splitmix64 finaliser
+  z += 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+
+// Fills whole pages of every layer, K and V, with codes uniform in -127 .. 127 under
+// scales sqrt(3) / 127 (unit variance), from (seed, word index).
+__global__ void k_fill_random_kv_q8(KvQ8 c, int L, int64_t layer_rows,
+                                    const int32_t* __restrict__ pages, int n_pages, uint64_t seed) {
+  const int64_t page_rows = (int64_t)c.Hkv * c.page_size, row_words = c.hd / 4;
+  const int64_t per_layer = n_pages * page_rows * row_words;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < L * per_layer;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t l = i / per_layer, rest = i - l * per_layer;
+    const int64_t r = rest / row_words, w = rest - r * row_words;
+    const int64_t row = l * layer_rows + pages[r / page_rows] * page_rows + r % page_rows;
+    const int64_t word = row * row_words + w;
+    uint32_t out[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = (uint32_t)(mix64(seed ^ (uint64_t)(8 * word + j)) >> 40);  // 24 bits
+      out[j / 4] |= (1u + (uint32_t)(((uint64_t)u * 255u) >> 24)) << (8 * (j % 4));
+    }
+    reinterpret_cast<uint32_t*>(c.k)[word] = out[0];
+    reinterpret_cast<uint32_t*>(c.v)[word] = out[1];
+    if (w == 0) c.ks[row] = c.vs[row] = 1.7320508f / 127.0f;
+  }
+}
+
+// k_kv_relocate (k_misc.cu) for an 8-bit cache: rows [q_begin, q_end) of one lane into
+// the pages of dst_pt, row q from row q (q < a) or q + delta of src_pt's pages. A row
+// that keeps its place, and every value row, moves as it is stored; a key that moves
+// down by delta is turned back by delta positions and quantised anew. One block per
+// (layer, KV head, K|V) walks its rows in ascending batches, a warp a row; a batch is
+// read whole before any of it is written.
+constexpr int kRelocWarps = 8;
+template <int HD>
+__global__ void __launch_bounds__(32 * kRelocWarps)
+    k_kv_q8_relocate(KvQ8 c, int64_t layer_rows, const int32_t* __restrict__ src_pt,
+                     const int32_t* __restrict__ dst_pt, int q_begin, int q_end, int a, int delta,
+                     const float* __restrict__ rc, const float* __restrict__ rs) {
+  constexpr int kHalf = HD / 2, kP = HD / 64;
+  const bool values = blockIdx.x & 1;
+  const int g = (int)(blockIdx.x >> 1) % c.Hkv;
+  const int64_t base = (int64_t)((blockIdx.x >> 1) / c.Hkv) * layer_rows;
+  uint8_t* codes = values ? c.v : c.k;
+  float* scales = values ? c.vs : c.ks;
+  auto row_of = [&](const int32_t* pt, int t) {
+    const int pi = (int)c.by_page.div(t);
+    return base + ((int64_t)pt[pi] * c.Hkv + g) * c.page_size + (t - pi * c.page_size);
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r0 = q_begin; r0 < q_end; r0 += kRelocWarps) {
+    const int q = r0 + warp;
+    uint8_t lo[kP] = {}, hi[kP] = {};
+    float s = 0.0f;
+    if (q < q_end) {
+      const int64_t from = row_of(src_pt, q < a ? q : q + delta);
+      s = scales[from];
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        lo[p] = codes[from * HD + lane + 32 * p];
+        hi[p] = codes[from * HD + kHalf + lane + 32 * p];
+      }
+      if (!values && q >= a && delta > 0) {  // the same for every lane of the warp
+        float y0[kP], y1[kP], amax = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          const int64_t at = (int64_t)delta * kHalf + lane + 32 * p;
+          rope_pair((float)((int)lo[p] - 128) * s, (float)((int)hi[p] - 128) * s, rc[at], -rs[at],
+                    y0[p], y1[p]);
+          amax = fmaxf(amax, fmaxf(fabsf(y0[p]), fabsf(y1[p])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          lo[p] = (uint8_t)(128 + (amax > 0.0f ? (int)rintf(y0[p] / amax * 127.0f) : 0));
+          hi[p] = (uint8_t)(128 + (amax > 0.0f ? (int)rintf(y1[p] / amax * 127.0f) : 0));
+        }
+        s = amax / 127.0f;
+      }
+    }
+    __syncthreads();
+    if (q < q_end) {
+      const int64_t to = row_of(dst_pt, q);
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        codes[to * HD + lane + 32 * p] = lo[p];
+        codes[to * HD + kHalf + lane + 32 * p] = hi[p];
+      }
+      if (lane == 0) scales[to] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -394,6 +498,25 @@ int launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positi
                       cudaStream_t s) {
   if (n <= 0) return 0;
   FS_Q8_DISPATCH(read_hd, c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s)
+}
+
+int launch_fill_random_kv_q8(const KvQ8& c, int L, int64_t layer_rows, const int32_t* pages,
+                             int n_pages, uint64_t seed, cudaStream_t s) {
+  if (n_pages <= 0) return 0;
+  k_fill_random_kv_q8<<<1216, 256, 0, s>>>(c, L, layer_rows, pages, n_pages, seed);
+  return 1;
+}
+
+int launch_kv_q8_relocate(const KvQ8& c, int L, int64_t layer_rows, const int32_t* src_pt,
+                          const int32_t* dst_pt, int q_begin, int q_end, int a, int delta,
+                          const float* rc, const float* rs, cudaStream_t s) {
+  if (q_end <= q_begin) return 0;
+  auto kern = c.hd == 64    ? k_kv_q8_relocate<64>
+              : c.hd == 128 ? k_kv_q8_relocate<128>
+                            : k_kv_q8_relocate<256>;
+  kern<<<(unsigned)L * c.Hkv * 2, 32 * kRelocWarps, 0, s>>>(c, layer_rows, src_pt, dst_pt, q_begin,
+                                                            q_end, a, delta, rc, rs);
+  return 1;
 }
 
 }  // namespace fsk

@@ -21,7 +21,7 @@ ERRORS = {-1: "FS_ERR_ARG", -2: "FS_ERR_LANE", -3: "FS_ERR_DUP_LANE",
           -10: "FS_ERR_DEVICE", -11: "FS_ERR_SCRATCH", -12: "FS_ERR_QUEUE_FULL",
           -13: "FS_ERR_KV_BUDGET"}
 CODES = {v: k for k, v in ERRORS.items()}
-FS_DTYPE_F32, FS_DTYPE_BF16, FS_DTYPE_Q8_0 = 0, 1, 2
+FS_DTYPE_F32, FS_DTYPE_BF16, FS_DTYPE_Q8_0, FS_DTYPE_Q8_ROW = 0, 1, 2, 3
 
 
 class FsError(RuntimeError):
@@ -264,9 +264,9 @@ def fs_lane_reset(h, lane: int) -> None:
 TRACE_TAGS = {1: "embed", 2: "rmsnorm", 3: "sample", 4: "argmax_tiles",
               5: "attn_mma", 6: "attn_tma", 7: "attn_tiled", 8: "attn_warp",
               9: "rope_append", 10: "gemv", 11: "attn_partial", 12: "attn_combine",
-              13: "gemv_swiglu",
+              13: "gemv_swiglu", 14: "kv_q8_append", 15: "attn_q8",
               16: "gemm_store", 17: "gemm_resid",
-              18: "gemm_swiglu", 19: "gemm_argmax"}
+              18: "gemm_swiglu", 19: "gemm_argmax", 20: "attn_q8_join"}
 
 
 def fs_trace_enable(h, capacity: int) -> None:

@@ -68,6 +68,8 @@ extern "C" {
                             A [rows, cols] matrix is rows*cols/32 blocks in
                             row-major order (cols must be a multiple of 32).  */
 
+#define FS_DTYPE_Q8_ROW 3 /* KV only: 8-bit rows, see fs_kv_q8                   */
+
 /* Model and arena description. */
 typedef struct fs_model_desc {
   int32_t n_layers;        /* L                                              */
@@ -81,7 +83,9 @@ typedef struct fs_model_desc {
   double rope_theta;       /* RoPE base                                      */
   int32_t tied_embeddings; /* 1: LM head is the embedding matrix             */
   int32_t weight_dtype;    /* FS_DTYPE_F32 / _BF16 / _Q8_0 for all matrices  */
-  int32_t kv_dtype;        /* FS_DTYPE_F32 or FS_DTYPE_BF16                  */
+  int32_t kv_dtype;        /* FS_DTYPE_F32, _BF16, or _Q8_ROW (keys and values
+                              quantised as they are appended, see fs_kv_q8;
+                              head_dim 64, 128 or 256)                       */
   int32_t max_lanes;       /* lanes addressable by fs_decode_step_batch      */
   int32_t page_size;       /* tokens per KV page (e.g. 16)                   */
   int32_t n_pages;         /* pages in the shared arena                      */
@@ -167,7 +171,8 @@ int fs_lane_clone(fs_handle* h, int32_t src, int32_t dst);
  * span was present). end == length drops a suffix and moves nothing. Pages
  * the lane writes (from the one holding `start` on) that another lane still
  * holds are first replaced by private copies (lowest free index); pages
- * past the new end are let go. Enqueued on the handle's stream.
+ * past the new end are let go. An 8-bit key that is rotated back is quantised
+ * anew, one more rounding of half a code. Enqueued on the handle's stream.
  * Errors: FS_ERR_LANE, FS_ERR_ARG (not 0 <= start <= end <= length),
  * FS_ERR_KV_FULL (too few free pages for the copies); nothing changes on
  * error. */
@@ -284,7 +289,8 @@ int fs_lane_capacity(const fs_handle* h, int32_t* tokens_out);
  * embed, 2 RMSNorm, 3 sampler, 4 tile argmax, 5 attention (cp.async), 6
  * attention (TMA), 7 attention (tiled), 8 attention (fused), 9 RoPE +
  * KV append, 10 GEMV, 11 / 12 split attention partials / combine (the
- * three-kernel path), 13 GEMV with the SwiGLU epilogue, 16 + epilogue
+ * three-kernel path), 13 GEMV with the SwiGLU epilogue, 14 quantised KV
+ * append, 15 / 20 attention over an 8-bit cache / its join, 16 + epilogue
  * kind for the tensor-core GEMM: 16
  * store, 17 residual, 18 SwiGLU, 19 argmax); words 1-3 = %globaltimer ns
  * at the block's entry, after its wait for the preceding kernel, and at its
@@ -374,8 +380,8 @@ int fs_gemm_plan(int64_t n_rows, int64_t k_inputs, int max_lanes, int n, int sms
 /* Name of the decode-attention kernel serving the handle: "tma-mma" (KV
  * tiles by TMA, warp MMAs; bf16 KV, page_size a multiple of 8 that divides
  * or is a multiple of 64), "cp.async-mma" (KV tiles by cp.async, warp MMAs;
- * bf16 KV), "tiled", "fused" or "three-kernel" (the f32-KV and odd-shape
- * paths). The environment variable FS_ATTN=mma|tiled|fused, read by
+ * bf16 KV), "q8-mma" (8-bit KV), "tiled", "fused" or "three-kernel" (the
+ * f32-KV and odd-shape paths). The environment variable FS_ATTN=mma|tiled|fused, read by
  * fs_create, selects a slower kernel (a comparison point). */
 const char* fs_attention_path(const fs_handle* h);
 
