@@ -11,20 +11,20 @@
 //
 // The bytes are the rows of logits, each wanted once. A sequence's rows are
 // taken in order and those after a rejection are never read. One thread-block
-// cluster serves a sequence: its blocks share a row's vocabulary, a warp a run
-// of consecutive tokens, and exchange (max, sum) through distributed shared
-// memory, one cluster barrier a row.
+// cluster serves a sequence: its warps share a row's vocabulary in runs of
+// consecutive tokens, and each writes its (max, sum) into every block's shared
+// memory: one cluster barrier a row, and one more for a draw.
 //
 // Whole-number answers are held to more than f32: where an acceptance or a draw
 // comes so near to its border that f32 weights and sums cannot tell, it is taken
 // again from weights good to 2^-36, as pairs of f32 numbers (this GPU's f64 rate is
 // 1/60 of its f32 rate). That is rare for an acceptance, and a few draws in a
 // hundred for a vocabulary of 49152. What bounds the kernel is the chain of one
-// sequence (about 3 us for the first row, 2 us for each further one, 5 us for the
-// draw and 9 us for one that is taken again, on eight SMs), not the bytes: 256
-// sequences of 4 drafts from a lookup, 49152 tokens, take 33 us, 61 MB of logits
-// being read; every draw in pairs took 108 us. 64 sequences of 0 to 7 drafts take
-// 34 us, one of 4 drafts 14 us.
+// sequence on eight SMs (2 to 3 us a row: a row's loads, its maximum and sum, the
+// barrier; 5 us for the draw and 9 us for one that is taken again), not the bytes:
+// 256 sequences of 4 drafts from a lookup, 49152 tokens, take 31 us, 61 MB of logits
+// being read (every draw in pairs: 108 us); 64 sequences of 0 to 7 drafts 33 us; one
+// of 4 drafts 11 us.
 
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -117,16 +117,17 @@ struct Stat {  // of a row's part
   int best;        // lowest index of max
 };
 
+// Every warp of the cluster writes what it found to all blocks; two buffers, taken in
+// turn: a block may write the next exchange while another still reads the last.
 template <int kC, int kW>
 struct Shared {
   float2 tab[32];
-  Stat warp[kW];
-  float left[kW], scan[kW];
-  Two left2[kW], scan2[kW];
+  Stat stat[2][kC * kW];
+  Two sum[2][kC * kW];
+  float scan[kW];
+  Two scan2[kW];
   int at[kW], tail[kW];
-  Stat part[2][kC];  // the cluster's blocks; two buffers, taken in turn: a block may
-  Two psum[2][kC];   // write the next exchange while another still reads the last
-  int again;         // the f32 draw could not tell
+  int again;  // the f32 draw could not tell
 };
 
 __device__ __forceinline__ float4 load4(const float* z, int i, int hi, bool vec) {
@@ -162,17 +163,23 @@ __device__ __forceinline__ T scan(T v, int lane) {
   }
   return v;
 }
-// Of parts with the lanes' weights, the first whose running sum (after `before`)
-// reaches the target, or the last with a weight, or -1; `before` becomes the sum of
-// those ahead of it.
+// Of parts with weights, two a lane, the first whose running sum reaches the target, or
+// the last with a weight, or -1; `before` becomes the sum of those ahead of it.
 template <typename T>
-__device__ __forceinline__ int pick(T weight, T target, T& before, int lane) {
-  const T upto = add(before, scan(weight, lane));
-  const unsigned has = __ballot_sync(kAll, positive(weight));
-  const unsigned hit = __ballot_sync(kAll, positive(weight) && !less(upto, target));
+__device__ __forceinline__ int pick(T w0, T w1, T target, T& before, int lane) {
+  const T upto = scan(add(w0, w1), lane);
+  const bool some = positive(w0) || positive(w1);
+  const unsigned has = __ballot_sync(kAll, some);
+  const unsigned hit = __ballot_sync(kAll, some && !less(upto, target));
+  if (!has) return -1;
   const int at = hit ? __ffs(hit) - 1 : 31 - __clz(has);
   if (at > 0) before = shfl(upto, at - 1);
-  return at;
+  w0 = shfl(w0, at);
+  w1 = shfl(w1, at);
+  const T half = add(before, w0);
+  if (positive(w0) && (!positive(w1) || (hit && !less(half, target)))) return 2 * at;
+  before = half;
+  return 2 * at + 1;
 }
 
 // What is left of the block's tokens for the draw, in pairs: weight e; with draft
@@ -272,24 +279,22 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
   // additions round by 2^-25 S each. With draft probabilities S itself enters twice.
   const float rough = a.probs ? 0x1p-21f : 0x1.8p-22f;
   int turn = 0;
-  // The warp's sum into sh.left2, the blocks' into sh.psum[turn], and on.
+  constexpr int kN = kC * kW;  // warps of the cluster, two a lane in what follows
+  static_assert(kN <= 64, "two warps a lane");
+  const int e0 = 2 * lane, e1 = 2 * lane + 1;
+  // the sum of the lanes' v over the cluster; the warps' sums are in w0 and w1
+  Two w0, w1;
   auto cluster_sum = [&](Two v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
-    if (lane == 0) sh.left2[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      v = lane < kW ? sh.left2[lane] : Two{0.0f, 0.0f};
-#pragma unroll
-      for (int o = kW / 2; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
-      v = shfl(v, 0);
-      if (lane < kC) *remote(&sh.psum[turn][rank], lane) = v;
-    }
+    if (lane < kC) *remote(&sh.sum[turn][rank * kW + warp], lane) = v;
     sync();
-    v = sh.psum[turn][0];
-#pragma unroll 1
-    for (int i = 1; i < kC; ++i) v = add(v, sh.psum[turn][i]);
+    w0 = e0 < kN ? sh.sum[turn][e0] : Two{0.0f, 0.0f};
+    w1 = e1 < kN ? sh.sum[turn][e1] : Two{0.0f, 0.0f};
     turn ^= 1;
+    v = add(w0, w1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add(v, shfl_xor(v, o));
     return v;
   };
 
@@ -366,33 +371,18 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     }
     // a run without a token: its -inf equal their maximum
     if (st.max == -CUDART_INF_F) st = {-CUDART_INF_F, 0.0f, V};
-    if (lane == 0) sh.warp[warp] = st;
-    __syncthreads();
     if (r == r0) started();
-    if (warp == 0) {  // joins the warps; lane i writes block i's copy
-      st = lane < kW ? sh.warp[lane] : Stat{-CUDART_INF_F, 0.0f, V};
-      float m = st.max;
-#pragma unroll
-      for (int o = kW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-      m = __shfl_sync(kAll, m, 0);
-      float sum = st.sum * rescale(st.max, m, c);
-      const int best = __reduce_min_sync(kAll, st.max == m ? st.best : V);
-#pragma unroll
-      for (int o = kW / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      sum = __shfl_sync(kAll, sum, 0);
-      if (lane < kC) *remote(&sh.part[turn][rank], lane) = {m, sum, best};
-    }
+    if (lane < kC) *remote(&sh.stat[turn][rank * kW + warp], lane) = st;
     sync();
-    const Stat* part = sh.part[turn];
+    const Stat none = {-CUDART_INF_F, 0.0f, V};
+    const Stat s0 = e0 < kN ? sh.stat[turn][e0] : none, s1 = e1 < kN ? sh.stat[turn][e1] : none;
     turn ^= 1;
-    // lane i joins part i % kC: the same in every lane and block
-    const Stat one = part[lane % kC];
-    float M = one.max;
+    float M = fmaxf(s0.max, s1.max);
 #pragma unroll
-    for (int o = kC / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
     // ---- greedy sequences, and rows without a token
     if (greedy || M == -CUDART_INF_F) {
-      int best = __reduce_min_sync(kAll, one.max == M ? one.best : V);
+      int best = __reduce_min_sync(kAll, s0.max == M ? s0.best : s1.max == M ? s1.best : V);
       if (M == -CUDART_INF_F) best = 0;
       if (!last && x == best && M > -CUDART_INF_F) continue;
       if (rank == 0 && tid == 0) {
@@ -401,20 +391,20 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
       }
       break;
     }
-    const float of_one = one.sum * rescale(one.max, M, c);
-    float S = of_one;
+    // the warps' sums under M, and the row's
+    float f0 = s0.sum * rescale(s0.max, M, c), f1 = s1.sum * rescale(s1.max, M, c), S = f0 + f1;
 #pragma unroll
-    for (int o = kC / 2; o > 0; o >>= 1) S += __shfl_xor_sync(kAll, S, o);
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(kAll, S, o);
     // ---- accept?
     Left left = {held ? hold : z, nullptr, M, c, {0.0f, 0.0f}, -1, sh.tab};
-    Two wx = {0.0f, 0.0f};  // the weight of the draft
+    float wx = 0.0f;  // the weight of the draft
     if (known) {
-      wx = weight2(z_x, M, c, sh.tab);
+      wx = weight1(z_x, M, c);
       const float t = u_acc * q_x * S;
-      bool ok = t < wx.h;
-      if (fabsf(t - wx.h) <= 2.0f * rough * wx.h) {
+      bool ok = t < wx;
+      if (fabsf(t - wx) <= 2.0f * rough * wx) {
         const Two S2 = cluster_sum(left_sum(left, lo, hi, lane));
-        ok = less(mul(mul({u_acc, 0.0f}, {q_x, 0.0f}), S2), wx);
+        ok = less(mul(mul({u_acc, 0.0f}, {q_x, 0.0f}), S2), weight2(z_x, M, c, sh.tab));
       }
       if (ok) continue;
     }
@@ -423,7 +413,6 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     const bool takes = known && !a.probs;
     const int gone = takes ? x - base : -1;  // the token that is taken out, if it is here
     float* const hold_q = hold + kW * run;
-    float* const bsum = reinterpret_cast<float*>(sh.psum[turn]);  // [kC], this exchange's buffer
     if (pr) {
       const bool pvec = (reinterpret_cast<uintptr_t>(pr) & 15) == 0;
       const bool zvec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
@@ -454,40 +443,29 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-      if (lane == 0) sh.left[warp] = s;
-      __syncthreads();
-      if (warp == 0) {
-        s = lane < kW ? sh.left[lane] : 0.0f;
-#pragma unroll
-        for (int o = kW / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-        s = __shfl_sync(kAll, s, 0);
-        if (lane < kC) *remote(bsum + rank, lane) = s;
-      }
+      float* const sums = reinterpret_cast<float*>(sh.sum[turn]);
+      if (lane < kC) *remote(sums + rank * kW + warp, lane) = s;
       sync();
+      f0 = e0 < kN ? sums[e0] : 0.0f;
+      f1 = e1 < kN ? sums[e1] : 0.0f;
       turn ^= 1;
+    } else if (takes) {  // the warps' weights are known from the row's sum
+      if (x / run == e0) f0 -= wx;
+      if (x / run == e1) f1 -= wx;
     }
-    // the blocks' weights, and this block's warps': without draft probabilities they
-    // are known from the row's sum
-    float of_block = 0.0f, of_warp = 0.0f;
-    if (lane < kC)
-      of_block = pr ? bsum[lane] : of_one - (takes && x / (kW * run) == lane ? wx.h : 0.0f);
-    if (lane < kW)
-      of_warp = pr ? sh.left[lane]
-                   : sh.warp[lane].sum * rescale(sh.warp[lane].max, M, c) -
-                         (gone >= 0 && gone < count && gone / run == lane ? wx.h : 0.0f);
     const float* zs = held ? hold : z;
     const float* qs = !pr ? nullptr : held ? hold_q : pr;
-    float total = of_block, before = 0.0f;
+    float total = f0 + f1, before = 0.0f;
 #pragma unroll
-    for (int o = kC / 2; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    total = __shfl_sync(kAll, total, 0);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
     const float target = us * total, off = rough * S;
-    if (pick(of_block, target, before, lane) == rank) {
-      const int w = pick(of_warp, target, before, lane);
+    const int chosen = pick(f0, f1, target, before, lane);
+    if (chosen >= 0 && chosen / kW == rank) {
+      const int w = chosen % kW;
       const int end_w = min(count, (w + 1) * run);
       bool hit = false;  // a token whose borders the target is clear of
 #pragma unroll 1
-      for (int i0 = w * run; i0 < end_w && w >= 0; i0 += kT) {  // a token a thread
+      for (int i0 = w * run; i0 < end_w; i0 += kT) {  // a token a thread
         const int i = i0 + tid;
         float e = i < end_w && i != gone ? weight1(zs[i], M, c) : 0.0f;
         if (qs && e > 0.0f) e = fmaxf(fmaf(-qs[i], S, e), 0.0f);
@@ -508,8 +486,8 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
       }
       if (!hit && tid < kC) *remote(&sh.again, tid) = 1;
     }
-    // a total of nothing, or of NaN: no block is picked, every block sees it
-    if (!(total > 0.0f) && tid == 0) sh.again = 1;
+    // a total of nothing, or of NaN: every block sees it
+    if (!(total > 0.0f && chosen >= 0) && tid == 0) sh.again = 1;
     sync();  // also: no block leaves while another may still write to it
     if (!sh.again) return;
     // ---- the draw again, in pairs
@@ -526,9 +504,10 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     }
     const Two goal = mul({us, 0.0f}, sum);
     Two cum = {0.0f, 0.0f};
-    const Two none = {0.0f, 0.0f};
-    if (pick(lane < kC ? sh.psum[turn ^ 1][lane] : none, goal, cum, lane) == rank) {
-      const int w = pick(lane < kW ? sh.left2[lane] : none, goal, cum, lane);
+    const int taken = pick(w0, w1, goal, cum, lane);
+    if (taken >= 0 && taken / kW == rank) {
+      const Two none = {0.0f, 0.0f};
+      const int w = taken % kW;
       const int end_w = min(count, (w + 1) * run);
       int found = -1, tail = -1;
 #pragma unroll 1
@@ -584,8 +563,8 @@ int launch_c(const VerifyArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Blocks of a sequence: eight while all sequences' blocks fit the SMs four at a time,
-// else four (64 sequences: 33.5 us with eight, 39.5 with four; 256: 44.3 and 32.8),
-// and no more than give every warp 128 tokens.
+// else four (64 sequences: 33 us with eight, 40 with four; 256: 44 and 33), and no more
+// than give every warp 128 tokens.
 int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
   if (a.n_seqs <= 0) return 0;
   const int want = (int64_t)a.n_seqs * 8 <= 4 * (int64_t)sms ? 8 : 4;

@@ -539,8 +539,12 @@ def _refuse(why: str):
 
 
 def _op_check(rc: int) -> None:
-    if rc != FS_OK:
+    if rc:
         raise FsError(rc, fs_last_error(None))
+
+
+def _raw(stream):
+    return None if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _vec(x, n: int, dtype, what: str):
@@ -565,7 +569,7 @@ def _rope_args(rope, hd: int):
     if rope is None:
         return None, None, 0
     cos, sin = rope
-    n = cos.shape[0]
+    n = cos.numel() // (hd // 2)
     return (_vec(cos, n * (hd // 2), _Types.f32, "rope cos"),
             _vec(sin, n * (hd // 2), _Types.f32, "rope sin"), n)
 
@@ -606,7 +610,7 @@ def fs_kv_q8_append(cache: fs_kv_q8, k, v, lanes, positions, rope=None, stream=N
     _op_check(lib().fs_kv_q8_append(C.byref(cache), kp, vp, ks, vs, dt,
                                     _vec(lanes, n, ty.i32, "lanes"),
                                     _vec(positions, n, ty.i32, "positions"), n, rc, rs, rl,
-                                    getattr(stream, "cuda_stream", stream)))
+                                    _raw(stream)))
 
 
 def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, stream=None) -> None:
@@ -624,7 +628,7 @@ def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, str
         dt = FS_DTYPE_F32 if dv is None else dv
     _op_check(lib().fs_kv_q8_read(C.byref(cache), _vec(lanes, n, ty.i32, "lanes"),
                                   _vec(positions, n, ty.i32, "positions"), n, kp, vp, ks,
-                                  vs, dt, getattr(stream, "cuda_stream", stream)))
+                                  vs, dt, _raw(stream)))
 
 
 def fs_kv_q8_attention_workspace(cache: fs_kv_q8, n: int, n_heads: int, max_len: int = 0,
@@ -663,7 +667,7 @@ def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0
         C.byref(cache), qp, qs, _vec(lanes, n, ty.i32, "lanes"),
         _vec(lengths, n, ty.i32, "lengths"), n, H, max_len,
         hd ** -0.5 if scale is None else scale, rc, rs, rl, op, os_, dt, split_len, wp, wb,
-        getattr(stream, "cuda_stream", stream)))
+        _raw(stream)))
 
 
 # --------------------------------------------------------- draft verification
@@ -696,7 +700,7 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
         _vec(u_sample, n, ty.f32, "u_sample"),
         _vec(n_accepted, n, ty.i32, "n_accepted"),
         _vec(next_token, n, ty.i32, "next_token"),
-        getattr(stream, "cuda_stream", stream)))
+        _raw(stream)))
 
 
 # ------------------------------------------------------------------ scheduler
