@@ -548,8 +548,9 @@ def _raw(stream):
 
 
 def _vec(x, n: int, dtype, what: str):
-    """Address of a contiguous CUDA tensor of n values."""
-    if x.dtype is dtype and x.numel() == n and x.is_cuda and x.is_contiguous():
+    """Address of a contiguous tensor of n values (that it is the current
+    device's memory the C call checks)."""
+    if x.dtype is dtype and x.numel() == n and x.is_contiguous():
         return x.data_ptr()
     _refuse(f"{what}: a contiguous CUDA tensor of {n} {dtype} values is needed")
 
@@ -557,7 +558,7 @@ def _vec(x, n: int, dtype, what: str):
 def _rows(x, n: int, heads: int, hd: int, what: str):
     """(address, row stride, dtype) of n rows [heads, hd], each contiguous."""
     dt = FS_DTYPE_F32 if x.dtype is _Types.f32 else FS_DTYPE_BF16
-    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.is_cuda and x.shape == (n, heads, hd):
+    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.shape == (n, heads, hd):
         s0, s1, s2 = x.stride()
         if n == 0 or (s2 == 1 and (heads == 1 or s1 == hd)):
             return x.data_ptr(), s0 if n > 1 else heads * hd, dt
@@ -581,6 +582,8 @@ def fs_kv_q8_view(k, v, k_scale, v_scale, page_table) -> fs_kv_q8:
     alive; page-table entries may change between calls."""
     if k.dim() != 4 or page_table.dim() != 2:
         _refuse("codes are [n_pages, Hkv, page_size, hd], the page table [n_lanes, max_pages]")
+    if not all(t.is_cuda for t in (k, v, k_scale, v_scale, page_table)):
+        _refuse("a cache in CUDA tensors is needed")
     ty = _types()
     n_pages, Hkv, ps, hd = k.shape
     n_lanes, max_pages = page_table.shape
@@ -660,7 +663,7 @@ def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0
     rc, rs, rl = _rope_args(rope, hd)
     wp, wb = None, 0
     if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
+        if not workspace.is_contiguous():
             _refuse("workspace: a contiguous CUDA tensor is needed")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _op_check(lib().fs_kv_q8_attention(
@@ -679,10 +682,10 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
     u_accept f32 [rows]; n_accepted and next_token int32 [seqs] are written. All
     CUDA tensors."""
     ty = _types()
-    if logits.dim() != 2 or not logits.is_cuda or logits.dtype is not ty.f32:
+    if logits.dim() != 2 or logits.dtype is not ty.f32:
         _refuse("logits: a CUDA tensor [rows, vocab] of f32 is needed")
     rows, V = logits.shape
-    if draft_probs is not None and (draft_probs.shape != (rows, V) or not draft_probs.is_cuda or
+    if draft_probs is not None and (draft_probs.shape != (rows, V) or
                                     draft_probs.dtype is not ty.f32):
         _refuse("draft_probs: a CUDA tensor [rows, vocab] of f32 is needed")
     for t in (logits, draft_probs):
