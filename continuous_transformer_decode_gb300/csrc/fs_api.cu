@@ -919,8 +919,8 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
       const KvQ8 c = q8_layer(h, l);
       const float* k = h->qkv + h->Nq;
       h->launch(FS_PROF_OTHER, (double)n * 2.0 * h->Nkv * (4.0 + kvs), [&] {
-        return launch_kv_q8_append(c, k, k + h->Nkv, h->Nqkv, h->Nqkv, X_F32, args.lane, args.pos,
-                                   n, h->rope_cos, h->rope_sin, d.max_pos, s);
+        return launch_kv_q8_append(c, k, k + h->Nkv, h->Nqkv, h->Nqkv, X_F32, true, args.lane,
+                                   args.pos, n, h->rope_cos, h->rope_sin, d.max_pos, s);
       });
       AttnQ8 a{};
       a.kv = c;
@@ -933,7 +933,7 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
       a.split_len = h->split_len; a.n_splits = h->max_splits;
       a.part_acc = h->part_acc; a.part_ml = h->part_ml;
       h->launch(FS_PROF_ATTN, kv_read + (double)n * h->Nq * (4.0 + xs),
-                [&] { return launch_attention_q8(a, X_F32, h->xtype, s); });
+                [&] { return launch_attention_q8(a, X_F32, h->xtype, true, s); });
     } else {
     // a chunked step first appends every row's k, v (rows of one lane at
     // consecutive positions see each other's keys); the MMA attention kernels
@@ -1488,8 +1488,8 @@ int fs_lane_import_kv(fs_handle* h, int32_t lane, const float* k, const float* v
         e = cudaMemcpyAsync(dv, v + (size_t)l * cnt, cnt * 4, cudaMemcpyHostToDevice, h->stream);
       if (e == cudaSuccess) {
         h->launches += h->kv_q8
-                           ? launch_kv_q8_append(q8_layer(h, l), dk, dv, h->Nkv, h->Nkv, X_F32, dp,
-                                                 dp + n, n, nullptr, nullptr, 0, h->stream)
+                           ? launch_kv_q8_append(q8_layer(h, l), dk, dv, h->Nkv, h->Nkv, X_F32, false,
+                                                 dp, dp + n, n, nullptr, nullptr, 0, h->stream)
                            : launch_import_kv(h->kv, l, dp, n, dk, dv, h->stream);
         e = cudaGetLastError();
       }

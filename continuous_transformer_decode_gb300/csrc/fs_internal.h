@@ -517,9 +517,10 @@ void set_null_error(const char* msg) noexcept;
 // ---- operators on an 8-bit paged KV cache (k_kv_q8.cu, k_attn_q8.cu)
 bool kv_q8_supports(int hd);
 // n rows of k and v (x_type, row strides in elements) into the slots of
-// (lanes[i], positions[i]); rc / rs rotate the keys (null: as they are).
+// (lanes[i], positions[i]); rc / rs rotate the keys (null: as they are). traced: with
+// the trace marks of the step's kernels (f32 rows).
 int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
-                        int64_t v_stride, int x_type, const int32_t* lanes,
+                        int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
                         const int32_t* positions, int n, const float* rc, const float* rs,
                         int rope_len, cudaStream_t s);
 // The values of the same slots into k_out / v_out (either may be null).
@@ -547,8 +548,8 @@ struct AttnQ8 {
 constexpr int kMaxQ8Splits = 8192;  // of a row: the join keeps a weight of each in shared memory
 // Positions per split of one call (a multiple of 64).
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms);
-// q and out of one type, or f32 q and bf16 out.
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s);
+// q and out of one type; traced: f32 q, out of either type.
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, cudaStream_t s);
 // fs_kv_q8 counterparts of launch_fill_random_kv and launch_kv_relocate, over the
 // layers of an arena (layer_rows rows each); a key that is turned back is quantised
 // anew (f32 quotients).

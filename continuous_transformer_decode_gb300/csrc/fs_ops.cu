@@ -170,8 +170,8 @@ int fs_kv_q8_append(const fs_kv_q8* cache, const void* k, const void* v, int64_t
   if ((why = not_here({cache->k, cache->v, cache->k_scale, cache->v_scale, cache->page_table, k, v,
                        lanes, positions, rope_cos, rope_sin})))
     return refuse(FS_ERR_ARG, why);
-  return launched(launch_kv_q8_append(view(cache), k, v, k_stride, v_stride, xt, lanes, positions,
-                                      n, rope_cos, rope_sin, rope_len, (cudaStream_t)stream));
+  return launched(launch_kv_q8_append(view(cache), k, v, k_stride, v_stride, xt, false, lanes,
+                                      positions, n, rope_cos, rope_sin, rope_len, (cudaStream_t)stream));
 }
 
 int fs_kv_q8_read(const fs_kv_q8* cache, const int32_t* lanes, const int32_t* positions,
@@ -246,7 +246,7 @@ int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
   a.split_len = p.split_len; a.n_splits = p.n_splits;
   a.part_acc = static_cast<float*>(workspace);
   a.part_ml = a.part_acc ? a.part_acc + (int64_t)n * p.n_splits * n_heads * cache->head_dim : nullptr;
-  return launched(launch_attention_q8(a, xt, xt, (cudaStream_t)stream));
+  return launched(launch_attention_q8(a, xt, xt, false, (cudaStream_t)stream));
 }
 
 int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,

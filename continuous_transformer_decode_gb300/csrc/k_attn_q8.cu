@@ -166,7 +166,7 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   constexpr int kKs = HD / 16;         // k-steps of Q K^T
   constexpr int kMt = HD / 16;         // m-tiles of V^T W
   constexpr int kRowChunks = HD / 16;  // 16-byte chunks per row
-  const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int g = blockIdx.x, b = blockIdx.y, s = blockIdx.z;
   const int H = a.H, G = H / a.kv.Hkv;
   const int len = row_len(a, b);
   const int start = s * a.split_len, end = min(len, start + a.split_len);
@@ -465,15 +465,15 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   }
 }
 
-template <typename QT, typename OT, int HD>
+template <typename QT, typename OT, int HD, bool kTrace>
 __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ8 a) {
-  __shared__ unsigned long long s_tr[4];
-  TraceSmem::begin(s_tr, g_trace);
+  __shared__ unsigned long long s_tr[kTrace ? 4 : 1];
+  if constexpr (kTrace) TraceSmem::begin(s_tr, g_trace);
   pdl_wait();
-  TraceSmem::ready(s_tr);
+  if constexpr (kTrace) TraceSmem::ready(s_tr);
   pdl_trigger();
   attn_q8_body<QT, OT, HD>(a);
-  TraceSmem::end(s_tr, TR_ATTN_Q8);
+  if constexpr (kTrace) TraceSmem::end(s_tr, TR_ATTN_Q8);
 }
 
 // Joins the splits of one (row, head): the weights of the splits first, then
@@ -540,23 +540,23 @@ __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
          Lsum > 0.0f ? o / Lsum : 0.0f, a.out_lo);
 }
 
-template <typename QT, typename OT, int HD>
+template <typename QT, typename OT, int HD, bool kTrace>
 int launch_hd(const AttnQ8& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  if (allow_smem(k_attn_q8<QT, OT, HD>, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
-  launch_k(k_attn_q8<QT, OT, HD>, dim3(a.n_splits, a.kv.Hkv, a.n), Lay<HD>::kT, Lay<HD>::kBytes, s,
-           a);
+  auto kern = k_attn_q8<QT, OT, HD, kTrace>;
+  if (allow_smem(kern, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
+  launch_k(kern, dim3(a.kv.Hkv, a.n, a.n_splits), Lay<HD>::kT, Lay<HD>::kBytes, s, a);
   if (a.n_splits == 1) return 1;
   launch_k(k_attn_q8_join<OT, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);
   return 2;
 }
 
-template <typename QT, typename OT>
+template <typename QT, typename OT, bool kTrace>
 int dispatch(const AttnQ8& a, cudaStream_t s) {
   switch (a.kv.hd) {
-    case 64: return launch_hd<QT, OT, 64>(a, s);
-    case 128: return launch_hd<QT, OT, 128>(a, s);
-    case 256: return launch_hd<QT, OT, 256>(a, s);
+    case 64: return launch_hd<QT, OT, 64, kTrace>(a, s);
+    case 128: return launch_hd<QT, OT, 128, kTrace>(a, s);
+    case 256: return launch_hd<QT, OT, 256, kTrace>(a, s);
     default: return 0;
   }
 }
@@ -564,9 +564,9 @@ int dispatch(const AttnQ8& a, cudaStream_t s) {
 }  // namespace
 
 // Splits by the launch's sizes alone. A block costs about 3.4 us beside its tokens
-// (128 lanes of 128 to 4096 tokens: 111 us in splits of 4096 or 2048, 135 of 512), so
+// (128 lanes of 128 to 4096 tokens: 108 us in splits of 4096, 117 of 1024, 138 of 512), so
 // the blocks are to fill the SMs once: one lane of 131071 tokens and 8 KV heads takes
-// 55 us in 57 splits (456 blocks on 456 places), 70 in 64, 66 in 147. Lanes differ in
+// 55 us in 57 splits (456 blocks on 456 places), 69 in 64, 68 in 256. Lanes differ in
 // length and max_len is the longest, so several lanes aim at half as many again (33
 // lanes of up to 3001 tokens, 2 heads of 256: 23 us in 3 splits, 33 in 2). No split is
 // longer than 4096, so that one long lane among many is shared, or shorter than 256.
@@ -578,10 +578,13 @@ int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
   return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
 
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, cudaStream_t s) {
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, cudaStream_t s) {
   if (a.n <= 0) return 0;
-  if (q_type == X_BF16) return dispatch<__nv_bfloat16, __nv_bfloat16>(a, s);
-  return out_type == X_BF16 ? dispatch<float, __nv_bfloat16>(a, s) : dispatch<float, float>(a, s);
+  if (traced)
+    return out_type == X_BF16 ? dispatch<float, __nv_bfloat16, true>(a, s)
+                              : dispatch<float, float, true>(a, s);
+  return out_type == X_BF16 ? dispatch<__nv_bfloat16, __nv_bfloat16, false>(a, s)
+                            : dispatch<float, float, false>(a, s);
 }
 
 }  // namespace fsk

@@ -13,6 +13,8 @@
 
 #include <float.h>
 
+#include <type_traits>
+
 #include "kv_q8.cuh"
 #include "two_f32.cuh"
 
@@ -225,17 +227,18 @@ __device__ __forceinline__ bool quantise_row(const float (&x)[8], uint8_t* codes
 
 // Twelve blocks an SM: what a block cannot hide of the two dependent loads before a
 // row's store (position, then its rotation; lane, then its page), the others do.
-template <typename T, int HD, bool kRot, bool kVec>
+// kTrace: with the step kernels' trace marks (0.4 us of a small call's 2.4).
+template <typename T, int HD, bool kRot, bool kVec, bool kTrace>
 __global__ void __launch_bounds__(kT, 12)
     k_kv_q8_append(KvQ8 c, const T* __restrict__ k, const T* __restrict__ v, int64_t k_stride,
                    int64_t v_stride, const int32_t* __restrict__ lanes,
                    const int32_t* __restrict__ positions, unsigned items,
                    const float* __restrict__ rc, const float* __restrict__ rs, int rope_len) {
   constexpr int kL = HD / 8, kHalf = HD / 2;
-  __shared__ unsigned long long s_tr[4];
-  TraceSmem::begin(s_tr, g_trace);
+  __shared__ unsigned long long s_tr[kTrace ? 4 : 1];
+  if constexpr (kTrace) TraceSmem::begin(s_tr, g_trace);
   pdl_wait();
-  TraceSmem::ready(s_tr);
+  if constexpr (kTrace) TraceSmem::ready(s_tr);
   pdl_trigger();
   const int sub = threadIdx.x % kL;
   const unsigned at = (unsigned)(((uint64_t)blockIdx.x * kT + threadIdx.x) / kL);
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kT, 12)
     if (do_v)
       quantise_border_row<T, HD, false>(v + vo, nullptr, nullptr, c.v + to * HD, c.vs + to, lane);
   }
-  TraceSmem::end(s_tr, TR_KV_Q8_APPEND);
+  if constexpr (kTrace) TraceSmem::end(s_tr, TR_KV_Q8_APPEND);
 }
 
 __device__ __forceinline__ void values4(uint32_t w, float s, float x[4]) {
@@ -442,17 +445,27 @@ bool rows_aligned(const void* p, int64_t stride, size_t es) {
   return reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && stride % 4 == 0;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool kTrace>
 void append_hd(const KvQ8& c, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                const int32_t* lanes, const int32_t* positions, int n, const float* rc,
                const float* rs, int rope_len, cudaStream_t s) {
   const unsigned items = (unsigned)((int64_t)n * c.Hkv);
   const bool vec = rows_aligned(k, k_stride, sizeof(T)) && rows_aligned(v, v_stride, sizeof(T)) &&
                    rows_aligned(rc, 4, 4) && rows_aligned(rs, 4, 4);
-  auto kern = rc ? (vec ? k_kv_q8_append<T, HD, true, true> : k_kv_q8_append<T, HD, true, false>)
-                 : (vec ? k_kv_q8_append<T, HD, false, true> : k_kv_q8_append<T, HD, false, false>);
+  auto kern = rc ? (vec ? k_kv_q8_append<T, HD, true, true, kTrace>
+                        : k_kv_q8_append<T, HD, true, false, kTrace>)
+                 : (vec ? k_kv_q8_append<T, HD, false, true, kTrace>
+                        : k_kv_q8_append<T, HD, false, false, kTrace>);
   launch_k(kern, dim3(blocks(items, HD)), kT, 0, s, c, static_cast<const T*>(k),
            static_cast<const T*>(v), k_stride, v_stride, lanes, positions, items, rc, rs, rope_len);
+}
+
+template <int HD, typename... A>
+int append_types(const KvQ8& c, int x_type, bool traced, A... a) {
+  if (x_type == X_BF16) append_hd<__nv_bfloat16, HD, false>(c, a...);
+  else if (traced) append_hd<float, HD, true>(c, a...);
+  else append_hd<float, HD, false>(c, a...);
+  return 1;
 }
 
 template <typename T, int HD>
@@ -470,34 +483,37 @@ void read_hd(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int 
 
 bool kv_q8_supports(int hd) { return hd == 64 || hd == 128 || hd == 256; }
 
-#define FS_Q8_DISPATCH(fn, ...)                                                             \
-  switch (c.hd) {                                                                           \
-    case 64:                                                                                \
-      x_type == X_BF16 ? fn<__nv_bfloat16, 64>(__VA_ARGS__) : fn<float, 64>(__VA_ARGS__);   \
-      return 1;                                                                             \
-    case 128:                                                                               \
-      x_type == X_BF16 ? fn<__nv_bfloat16, 128>(__VA_ARGS__) : fn<float, 128>(__VA_ARGS__); \
-      return 1;                                                                             \
-    case 256:                                                                               \
-      x_type == X_BF16 ? fn<__nv_bfloat16, 256>(__VA_ARGS__) : fn<float, 256>(__VA_ARGS__); \
-      return 1;                                                                             \
-    default:                                                                                \
-      return 0;                                                                             \
-  }
-
 int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
-                        int64_t v_stride, int x_type, const int32_t* lanes,
+                        int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
                         const int32_t* positions, int n, const float* rc, const float* rs,
                         int rope_len, cudaStream_t s) {
   if (n <= 0) return 0;
-  FS_Q8_DISPATCH(append_hd, c, k, v, k_stride, v_stride, lanes, positions, n, rc, rs, rope_len, s)
+  auto go = [&](auto hd) {
+    return append_types<decltype(hd)::value>(c, x_type, traced, k, v, k_stride, v_stride, lanes,
+                                             positions, n, rc, rs, rope_len, s);
+  };
+  return c.hd == 64    ? go(std::integral_constant<int, 64>())
+         : c.hd == 128 ? go(std::integral_constant<int, 128>())
+         : c.hd == 256 ? go(std::integral_constant<int, 256>())
+                       : 0;
 }
 
 int launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
                       void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, int x_type,
                       cudaStream_t s) {
   if (n <= 0) return 0;
-  FS_Q8_DISPATCH(read_hd, c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s)
+  auto go = [&](auto hd) {
+    constexpr int HD = decltype(hd)::value;
+    if (x_type == X_BF16)
+      read_hd<__nv_bfloat16, HD>(c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s);
+    else
+      read_hd<float, HD>(c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s);
+    return 1;
+  };
+  return c.hd == 64    ? go(std::integral_constant<int, 64>())
+         : c.hd == 128 ? go(std::integral_constant<int, 128>())
+         : c.hd == 256 ? go(std::integral_constant<int, 256>())
+                       : 0;
 }
 
 int launch_fill_random_kv_q8(const KvQ8& c, int L, int64_t layer_rows, const int32_t* pages,

@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     return;
   }
   const bool greedy = !(temp > 0.0f);
-  const Two c = log2e_over(greedy ? 1.0f : temp);
+  // outside this range only the largest logits count, or all alike
+  const Two c = log2e_over(greedy ? 1.0f : fminf(fmaxf(temp, 1e-30f), 1e30f));
   // this block's tokens are base .. base + count - 1, this warp's lo .. hi - 1 of them
   const int run = (V - 1) / (kC * kW * 128) * 128 + 128;
   const int base = (int)min((int64_t)V, (int64_t)rank * kW * run);

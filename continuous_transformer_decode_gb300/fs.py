@@ -582,6 +582,8 @@ def fs_kv_q8_view(k, v, k_scale, v_scale, page_table) -> fs_kv_q8:
     alive; page-table entries may change between calls."""
     if k.dim() != 4 or page_table.dim() != 2:
         _refuse("codes are [n_pages, Hkv, page_size, hd], the page table [n_lanes, max_pages]")
+    if v.shape != k.shape or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3]:
+        _refuse("v has the shape of k, the scales all but its last dimension")
     if not all(t.is_cuda for t in (k, v, k_scale, v_scale, page_table)):
         _refuse("a cache in CUDA tensors is needed")
     ty = _types()

@@ -122,6 +122,14 @@ def test_edges():
     check(c)
 
 
+@pytest.mark.parametrize("probs", [True, False])
+def test_extreme_temperatures(probs):
+    rng = np.random.default_rng(11)
+    c = make(rng, [3] * 8, 700, probs, 0.0)
+    c["temps"] = np.float32([np.inf, 3e38, 1e30, 1e5, 1e-5, 1e-30, 1e-38, 1e-45])
+    check(c)
+
+
 def test_sequences_without_rows_and_clamped_starts():
     rng = np.random.default_rng(2)
     c = make(rng, [1, 2, 0], 40)

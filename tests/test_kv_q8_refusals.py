@@ -146,6 +146,8 @@ def test_binding_refuses_tensors_it_cannot_use():
     codes, scale = z(2, 1, 16, 64, dtype=torch.uint8), z(2, 1, 16)
     with pytest.raises(fs.FsError):  # host tensors
         fs.fs_kv_q8_view(codes, codes, scale, scale, z(1, 1, dtype=torch.int32))
+    with pytest.raises(fs.FsError):  # codes and scales of different shapes
+        fs.fs_kv_q8_view(codes, codes, scale, z(2, 16, 1), z(1, 1, dtype=torch.int32))
     one = z(1, dtype=torch.int32)
     with pytest.raises(fs.FsError):
         fs.fs_kv_q8_append(cache(), z(1, 2, 64), z(1, 2, 64), one, one)
