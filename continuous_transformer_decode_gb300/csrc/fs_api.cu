@@ -933,7 +933,7 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
       a.split_len = h->split_len; a.n_splits = h->max_splits;
       a.part_acc = h->part_acc; a.part_ml = h->part_ml;
       h->launch(FS_PROF_ATTN, kv_read + (double)n * h->Nq * (4.0 + xs),
-                [&] { return launch_attention_q8(a, X_F32, h->xtype, true, s); });
+                [&] { return launch_attention_q8(a, X_F32, h->xtype, true, h->sms, s); });
     } else {
     // a chunked step first appends every row's k, v (rows of one lane at
     // consecutive positions see each other's keys); the MMA attention kernels

@@ -544,12 +544,14 @@ struct AttnQ8 {
   int split_len, n_splits;
   float* part_acc;    // [n][n_splits][H][hd] when n_splits > 1
   float* part_ml;     // [n][n_splits][H][2]
+  int by_len;         // set by the launcher: blocks take the rows by length
 };
 constexpr int kMaxQ8Splits = 8192;  // of a row: the join keeps a weight of each in shared memory
 // Positions per split of one call (a multiple of 64).
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms);
 // q and out of one type; traced: f32 q, out of either type.
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, cudaStream_t s);
+int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, int sms,
+                        cudaStream_t s);
 // fs_kv_q8 counterparts of launch_fill_random_kv and launch_kv_relocate, over the
 // layers of an arena (layer_rows rows each); a key that is turned back is quantised
 // anew (f32 quotients).

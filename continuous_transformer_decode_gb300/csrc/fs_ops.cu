@@ -246,7 +246,9 @@ int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
   a.split_len = p.split_len; a.n_splits = p.n_splits;
   a.part_acc = static_cast<float*>(workspace);
   a.part_ml = a.part_acc ? a.part_acc + (int64_t)n * p.n_splits * n_heads * cache->head_dim : nullptr;
-  return launched(launch_attention_q8(a, xt, xt, false, (cudaStream_t)stream));
+  const int sms = device_sms();
+  if (!sms) return refuse(FS_ERR_CUDA, "no CUDA device");
+  return launched(launch_attention_q8(a, xt, xt, false, sms, (cudaStream_t)stream));
 }
 
 int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, int32_t vocab,

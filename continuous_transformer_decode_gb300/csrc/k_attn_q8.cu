@@ -158,6 +158,39 @@ __device__ __forceinline__ int row_len(const AttnQ8& a, int i) {
   return min(max(a.lens[i], 0), a.max_len - a.len_add) + a.len_add;
 }
 
+// The row whose length is the rank-th largest (ties: the lower row first), found by
+// every block for itself: blocks start in about the order of their indexes, so the
+// long rows start first and the SMs finish together: 128 lanes of 128 to 4096 tokens
+// take 92 us instead of 108. It costs a block one to three microseconds, so it is for
+// launches of at least two blocks a place whose blocks may be long (256 lanes of up
+// to 512 tokens would take 19 us instead of 13).
+constexpr int kRankRows = 256;  // most rows that this is done for
+template <int kT>
+__device__ __forceinline__ int row_of_rank(const AttnQ8& a, int rank, uint8_t* smem) {
+  // keys that differ: the length (up to 2^22), then the row
+  int* key = reinterpret_cast<int*>(smem);
+  const int4* key4 = reinterpret_cast<const int4*>(smem);
+  __shared__ int row;
+  for (int i = threadIdx.x; i < (a.n + 3) / 4 * 4; i += kT)
+    key[i] = i < a.n ? min(max(a.lens[i], 0), 1 << 22) * kRankRows + (kRankRows - 1 - i) : -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n; i += kT) {
+    const int mine = key[i];
+    int ahead[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int j = 0; j < (a.n + 3) / 4; ++j) {
+      const int4 v = key4[j];
+      ahead[0] += v.x > mine;
+      ahead[1] += v.y > mine;
+      ahead[2] += v.z > mine;
+      ahead[3] += v.w > mine;
+    }
+    if (ahead[0] + ahead[1] + ahead[2] + ahead[3] == rank) row = i;
+  }
+  __syncthreads();
+  return row;
+}
+
 template <typename QT, typename OT, int HD>
 __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   using L = Lay<HD>;
@@ -166,7 +199,9 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   constexpr int kKs = HD / 16;         // k-steps of Q K^T
   constexpr int kMt = HD / 16;         // m-tiles of V^T W
   constexpr int kRowChunks = HD / 16;  // 16-byte chunks per row
-  const int g = blockIdx.x, b = blockIdx.y, s = blockIdx.z;
+  const int g = blockIdx.x, s = blockIdx.z;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int b = a.by_len ? row_of_rank<kT>(a, blockIdx.y, smem) : blockIdx.y;
   const int H = a.H, G = H / a.kv.Hkv;
   const int len = row_len(a, b);
   const int start = s * a.split_len, end = min(len, start + a.split_len);
@@ -177,7 +212,6 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
     for (int i = tid; i < G * HD; i += kT) st_out(orow + i, 0.0f, a.out_lo);
   if (start >= end) return;
 
-  extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem + warp * L::kWarpBytes;
   uint8_t* qa = smem + L::kBytes - L::kQa - (int)sizeof(float) * kG;  // [kKs][32] uint4
   float* qf = reinterpret_cast<float*>(qa + L::kQa);                  // [kG]
@@ -236,7 +270,7 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
 
   // ---- q, rotated; warp w takes heads w, w + kWarps, ..
   const QT* qr = static_cast<const QT*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
-  constexpr int kHeads = kG / kWarps, kP = kHalf / 32;
+  constexpr int kHeads = (kG + kWarps - 1) / kWarps, kP = kHalf / 32;
   float x0[kHeads][kP], x1[kHeads][kP];
 #pragma unroll
   for (int u = 0; u < kHeads; ++u)
@@ -271,6 +305,7 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
 #pragma unroll
   for (int u = 0; u < kHeads; ++u) {
     const int h = warp + u * kWarps;
+    if (h >= kG) break;
     float mx = 0.0f;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
@@ -563,6 +598,13 @@ int dispatch(const AttnQ8& a, cudaStream_t s) {
 
 }  // namespace
 
+// Blocks that the SMs hold at a time.
+static int64_t places(int hd, int sms) {
+  return (int64_t)sms * (hd == 64    ? Shape<64>::kBlocks
+                         : hd == 128 ? Shape<128>::kBlocks
+                                     : Shape<256>::kBlocks);
+}
+
 // Splits by the launch's sizes alone. A block costs about 3.4 us beside its tokens
 // (128 lanes of 128 to 4096 tokens: 108 us in splits of 4096, 117 of 1024, 138 of 512), so
 // the blocks are to fill the SMs once: one lane of 131071 tokens and 8 KV heads takes
@@ -571,15 +613,18 @@ int dispatch(const AttnQ8& a, cudaStream_t s) {
 // lanes of up to 3001 tokens, 2 heads of 256: 23 us in 3 splits, 33 in 2). No split is
 // longer than 4096, so that one long lane among many is shared, or shorter than 256.
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
-  const int blocks = hd == 64 ? Shape<64>::kBlocks : hd == 128 ? Shape<128>::kBlocks : Shape<256>::kBlocks;
-  const int64_t places = (int64_t)sms * blocks, pairs = std::max<int64_t>(1, (int64_t)n * Hkv);
-  const int64_t splits = std::max<int64_t>(1, (n > 1 ? 3 * places / 2 : places) / pairs);
+  const int64_t room = places(hd, sms), pairs = std::max<int64_t>(1, (int64_t)n * Hkv);
+  const int64_t splits = std::max<int64_t>(1, (n > 1 ? 3 * room / 2 : room) / pairs);
   const int64_t len = (std::max(max_len, 1) + splits - 1) / splits;
   return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
 
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, cudaStream_t s) {
-  if (a.n <= 0) return 0;
+int launch_attention_q8(const AttnQ8& args, int q_type, int out_type, bool traced, int sms,
+                        cudaStream_t s) {
+  if (args.n <= 0) return 0;
+  AttnQ8 a = args;
+  a.by_len = a.n <= kRankRows && a.max_len >= 2048 && a.split_len >= 2048 &&
+             (int64_t)a.n * a.kv.Hkv >= 2 * places(a.kv.hd, sms);
   if (traced)
     return out_type == X_BF16 ? dispatch<float, __nv_bfloat16, true>(a, s)
                               : dispatch<float, float, true>(a, s);
