@@ -111,6 +111,12 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// NaN if one of them is: a head whose q is not a number gives no number.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 // Two codes (bytes lo and hi of w, chosen by the selector) as an f16 pair.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
   const uint32_t x = __byte_perm(w, 0x64646464u, sel);
@@ -392,16 +398,16 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
       }
 #pragma unroll
       for (int e = 0; e < kS / 4; ++e) {
-        mx = fmaxf(mx, z[e]);
+        mx = max_nan(mx, z[e]);
         zx = fmaxf(zx, z[e] + lg2(zs[e]));
       }
-      if (__any_sync(kAll, mx > m_ref + kTop || zx > ref + kTop)) {
+      if (__any_sync(kAll, !(mx <= m_ref + kTop) || zx > ref + kTop)) {
         // the head's maxima (its four threads), and new references
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+        mx = max_nan(mx, __shfl_xor_sync(kAll, mx, 1));
         zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+        mx = max_nan(mx, __shfl_xor_sync(kAll, mx, 2));
         zx = fmaxf(zx, __shfl_xor_sync(kAll, zx, 2));
-        const float m_new = fmaxf(m_ref, mx);
+        const float m_new = max_nan(m_ref, mx);
         const float r_new = fmaxf(ref, fmaxf(zx - 13.0f, m_new - 110.0f));
         l_run *= m_ref == -CUDART_INF_F ? 0.0f : ex2(m_ref - m_new);
         const float f = ref == -CUDART_INF_F ? 0.0f : ex2(ref - r_new);
@@ -489,7 +495,7 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
       A = fmaf(wo[(w * kG + h) * HD + d], f, A);
     }
     if (len <= a.split_len) {
-      st_out(orow + i, Lsum > 0.0f ? A / Lsum : 0.0f, a.out_lo);
+      st_out(orow + i, Lsum == 0.0f ? 0.0f : A / Lsum, a.out_lo);
     } else {
       a.part_acc[base * HD + i] = A;
       if (d == 0) {
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
 #pragma unroll
   for (int i = 0; i < kJ; ++i) o += reinterpret_cast<const float*>(part[i])[tid];
   st_out(static_cast<OT*>(a.out) + b * a.out_stride + (int64_t)h * HD + tid,
-         Lsum > 0.0f ? o / Lsum : 0.0f, a.out_lo);
+         Lsum == 0.0f ? 0.0f : o / Lsum, a.out_lo);
 }
 
 template <typename QT, typename OT, int HD, bool kTrace>

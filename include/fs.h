@@ -545,7 +545,8 @@ int64_t fs_kv_q8_attention_workspace(const fs_kv_q8* cache, int32_t n, int32_t n
  * 8192 splits), joined in a fixed order; 0 chooses from n, n_kv_heads and max_len. A row's bits
  * depend on its own inputs and split_len alone: give split_len for results
  * that do not depend on the batch. Scores, softmax sums and outputs are held
- * in f32; the result is rounded once. workspace (16-byte aligned) may be NULL
+ * in f32; the result is rounded once. A head whose q is not finite gives NaN and
+ * leaves the others alone. workspace (16-byte aligned) may be NULL
  * when fs_kv_q8_attention_workspace says 0, is needed only during the call's
  * own kernels and starts with any content; calls that may run at the same time
  * (other streams, other captured graphs) need one each. */

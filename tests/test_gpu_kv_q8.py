@@ -283,6 +283,43 @@ def test_attention_large_scores_and_scales(hd):
         _check_attention(got, ref, tol)
 
 
+@pytest.mark.parametrize("split", [64, 4096])
+def test_a_query_that_is_no_number_stays_in_its_head(split):
+    import torch
+    rng = np.random.default_rng(12)
+    lens = [300, 40]
+    pg = Pages(rng, lens, 2, 64, 16)
+    q = rng.standard_normal((2, 8, 64)).astype(np.float32)
+    ref, tol = R.attention(pg.ref(), q, [0, 1], lens, 0.125)
+    q[0, 2, 5], q[0, 7, 0], q[1, 4, 63] = np.nan, np.inf, -np.inf
+    got = _attend(pg, _cuda(q), [0, 1], lens, split_len=split)
+    bad = torch.zeros(2, 8, dtype=torch.bool)
+    bad[0, 2] = bad[0, 7] = bad[1, 4] = True
+    assert torch.isnan(got.cpu()[bad]).all()
+    # not the same bits: the heads of a KV head set their references together
+    _check_attention(got.cpu()[~bad], ref[~bad.numpy()], tol[~bad.numpy()])
+
+
+def test_attention_takes_rows_by_length():
+    """A launch of many long ragged rows: the blocks take them by length; every row
+    comes out as in a call of its own. Equal lengths, empty rows and rows past
+    max_len among them."""
+    import torch
+    rng = np.random.default_rng(13)
+    n, Hkv = 150, 8
+    lens = np.where(rng.random(n) < 0.2, 0, rng.integers(1, 2300, n))
+    lens[5:9] = 2100
+    pg = Pages(rng, lens.tolist(), Hkv, 128, 16)
+    q = _cuda(rng.standard_normal((n, Hkv, 128)).astype(np.float32))
+    got = _attend(pg, q, range(n), lens, max_len=2200, split_len=2048)
+    for i in list(range(12)) + [n - 1, int(lens.argmax()), int(lens.argmin())]:
+        one = _attend(pg, q[i:i + 1], [i], lens[i:i + 1], max_len=2200, split_len=2048)
+        assert torch.equal(one[0], got[i]), i
+    pick = [0, 5, 77, n - 1]
+    ref, tol = R.attention(pg.ref(), q.cpu().numpy()[pick], pick, np.minimum(lens[pick], 2200), 128 ** -0.5)
+    _check_attention(got[pick], ref, tol)
+
+
 def test_attention_long_offsets():
     """A cache of more than 2^31 code bytes: rows at both ends of it."""
     import torch
