@@ -209,9 +209,23 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int b = a.by_len ? row_of_rank<kT>(a, blockIdx.y, smem) : blockIdx.y;
   const int H = a.H, G = H / a.kv.Hkv;
+  // a block's loads depend on one another three deep: (length, lane, q), then (pages,
+  // rotation), then codes; each level is asked for together
+  const int row_lane = a.lanes[b];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const QT* qr = static_cast<const QT*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
+  constexpr int kHeads = (kG + kWarps - 1) / kWarps, kP = kHalf / 32;
+  float x0[kHeads][kP], x1[kHeads][kP];  // warp w takes heads w, w + kWarps, ..
+#pragma unroll
+  for (int u = 0; u < kHeads; ++u)
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      const int h = warp + u * kWarps, i = lane + 32 * j;
+      x0[u][j] = h < G ? ld1(qr + h * HD + i) : 0.0f;
+      x1[u][j] = h < G ? ld1(qr + h * HD + i + kHalf) : 0.0f;
+    }
   const int len = row_len(a, b);
   const int start = s * a.split_len, end = min(len, start + a.split_len);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, cq = lane & 3;
   OT* orow = static_cast<OT*>(a.out) + b * a.out_stride + (int64_t)g * G * HD;
   if (len == 0 && s == 0)
@@ -226,7 +240,7 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
   // follows token t0(i) + l, its page in the lane's table and its slot in the page
   const int n_slices = (end - start + kS - 1) / kS;
   const int mine = (n_slices - warp + kWarps - 1) / kWarps;
-  const int row_lane = a.lanes[b], ps = a.kv.page_size;
+  const int ps = a.kv.page_size;
   const bool no_lane = (unsigned)row_lane >= (unsigned)a.kv.n_lanes;
   const int32_t* pages = a.kv.page_table + (no_lane ? 0 : (int64_t)row_lane * a.kv.max_pages);
   constexpr int kStep = kWarps * kS;
@@ -274,21 +288,6 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
 #pragma unroll
   for (int i = 0; i < L::kStages; ++i) look_up(page[i], slot[i]);
 
-  // ---- q, rotated; warp w takes heads w, w + kWarps, ..
-  const QT* qr = static_cast<const QT*>(a.q) + b * a.q_stride + (int64_t)g * G * HD;
-  constexpr int kHeads = (kG + kWarps - 1) / kWarps, kP = kHalf / 32;
-  float x0[kHeads][kP], x1[kHeads][kP];
-#pragma unroll
-  for (int u = 0; u < kHeads; ++u)
-#pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      const int h = warp + u * kWarps, i = lane + 32 * j;
-      x0[u][j] = h < G ? ld1(qr + h * HD + i) : 0.0f;
-      x1[u][j] = h < G ? ld1(qr + h * HD + i + kHalf) : 0.0f;
-    }
-#pragma unroll
-  for (int i = 0; i < L::kStages - 1; ++i) issue(ring + i * L::kStage, page[i], slot[i]);
-  int next_page = page[L::kStages - 1], next_slot = slot[L::kStages - 1];
   float rc[kP], rs[kP];
 #pragma unroll
   for (int j = 0; j < kP; ++j) {
@@ -296,6 +295,11 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
     rc[j] = a.rc ? a.rc[p] : 1.0f;
     rs[j] = a.rc ? a.rs[p] : 0.0f;
   }
+#pragma unroll
+  for (int i = 0; i < L::kStages - 1; ++i) issue(ring + i * L::kStage, page[i], slot[i]);
+  int next_page = page[L::kStages - 1], next_slot = slot[L::kStages - 1];
+
+  // ---- q, rotated, into A fragments
   // element d of head h in the A fragments: chunk d / 16 is the j-th chunk of thread
   // column cq, and word w of it (elements 4 w .. 4 w + 3) k-step 4 j + w; the
   // lane's 16 bytes are (hi 0 1, lo 0 1, hi 2 3, lo 2 3)
@@ -323,16 +327,16 @@ __device__ __forceinline__ void attn_q8_body(const AttnQ8& a) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-    int e = 0;
-    if (mx > 0.0f) frexpf(mx, &e);  // mx in [2^(e-1), 2^e)
-    e = max(-110, min(e, 127)) - 14;
-    const float up = ldexpf(1.0f, -e);
+    // mx in [2^(e + 13), 2^(e + 14)), by its exponent; -124 <= e <= 114
+    const int e = max((int)(__float_as_uint(mx) >> 23) - 127, -111) - 13;
+    const float up = __uint_as_float((unsigned)(127 - e) << 23);  // 2^-e
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
       put_q(h, lane + 32 * j, x0[u][j] * up);
       put_q(h, lane + 32 * j + kHalf, x1[u][j] * up);
     }
-    if (lane == 0) qf[h] = ldexpf(a.scale * 1.4426950408889634f, e);
+    if (lane == 0)
+      qf[h] = a.scale * 1.4426950408889634f * __uint_as_float((unsigned)(127 + e) << 23);
   }
   __syncthreads();
 
@@ -611,16 +615,18 @@ static int64_t places(int hd, int sms) {
                                      : Shape<256>::kBlocks);
 }
 
-// Splits by the launch's sizes alone. A block costs about 3.4 us beside its tokens
-// (128 lanes of 128 to 4096 tokens: 108 us in splits of 4096, 117 of 1024, 138 of 512), so
-// the blocks are to fill the SMs once: one lane of 131071 tokens and 8 KV heads takes
-// 55 us in 57 splits (456 blocks on 456 places), 69 in 64, 68 in 256. Lanes differ in
-// length and max_len is the longest, so several lanes aim at half as many again (33
-// lanes of up to 3001 tokens, 2 heads of 256: 23 us in 3 splits, 33 in 2). No split is
-// longer than 4096, so that one long lane among many is shared, or shorter than 256.
+// Splits by the launch's sizes alone. A block costs about 3 us beside its tokens (128
+// lanes of 128 to 4096 tokens, in row order: 108 us in splits of 4096, 117 of 1024, 138
+// of 512), so the blocks of one lane are to fill two thirds of the places once: 131071
+// tokens and 8 KV heads take 52 us in 38 splits (304 blocks, two an SM), 56 in 57 (456
+// blocks on 456 places), 69 in 64, 68 in 256. Lanes differ in length and max_len is the
+// longest, so several lanes aim at one and a half times the places (33 lanes of up to
+// 3001 tokens, 2 heads of 256: 23 us in 3 splits, 33 in 2). No split is longer than 4096,
+// so that one long lane among many is shared, or shorter than 256.
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
   const int64_t room = places(hd, sms), pairs = std::max<int64_t>(1, (int64_t)n * Hkv);
-  const int64_t splits = std::max<int64_t>(1, (n > 1 ? 3 * room / 2 : room) / pairs);
+  const int64_t want = n > 1 ? 3 * room / 2 : std::max<int64_t>(sms, 2 * room / 3);
+  const int64_t splits = std::max<int64_t>(1, want / pairs);
   const int64_t len = (std::max(max_len, 1) + splits - 1) / splits;
   return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
