@@ -76,6 +76,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float x[4]) {
 __device__ __forceinline__ float storable(float x) {
   return x != x ? 0.0f : fminf(fmaxf(x, -FLT_MAX), FLT_MAX);
 }
+// The largest scale: the f32 below FLT_MAX / 127 rounded, which is above the quotient, so
+// that 127 of it would be infinite. Within 2^-23 of the quotient.
+constexpr float kMaxScale = 0x1.020406p+121f;
 // Largest magnitude of three; NaN if one is.
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
   float y;
@@ -173,7 +176,7 @@ __device__ __noinline__ void quantise_border_row(const T* x, const float* rc, co
     }
     codes[lane + 32 * (q >> 1) + (q & 1) * kHalf] = (uint8_t)((int)n + 128);
   }
-  if (lane == 0) *scale = amax / 127.0f;
+  if (lane == 0) *scale = fminf(amax / 127.0f, kMaxScale);
 }
 
 // Quantises one row of 8 values a lane (x[0..3] in the lower half, x[4..7] in the

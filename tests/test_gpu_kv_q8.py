@@ -177,6 +177,30 @@ def test_append_not_finite():
     assert np.allclose(pg.dev[2].cpu().numpy()[pg.table[0, 0], 0], scale[:, 0], rtol=2.0 ** -22)
 
 
+@pytest.mark.parametrize("hd", [64, 256])
+def test_infinities_read_back_finite(hd):
+    """An infinity is stored as the largest finite f32, and so is read back finite:
+    the scale's rounding does not take 127 of it past the range."""
+    import torch
+    rng = np.random.default_rng(7)
+    pg = Pages(rng, [3], 2, hd, 4)
+    big = float(np.finfo(np.float32).max)
+    x = rng.standard_normal((3, 2, hd)).astype(np.float32)
+    x[0, 0, 3], x[1, 1, hd - 1], x[2, 0, 0], x[2, 1, 1] = np.inf, -np.inf, big, -3.4e38
+    xx, out = _cuda(x), [torch.zeros(3, 2, hd, device="cuda") for _ in range(2)]
+    at = _cuda(np.zeros(3, np.int32)), _cuda(np.arange(3, dtype=np.int32))
+    fs.fs_kv_q8_append(pg.view, xx, xx, *at)
+    fs.fs_kv_q8_read(pg.view, *at, *out)
+    torch.cuda.synchronize()
+    codes, scale = R.quantise(x)
+    for o in out:
+        got = o.cpu().numpy().astype(np.float64)
+        assert np.isfinite(got).all()
+        want = codes * scale[..., None]
+        # the scale within 2^-23 of the quotient, one product rounded
+        assert (np.abs(got - want) <= 2.0 ** -22 * np.abs(want)).all()
+
+
 def test_rows_outside_the_cache():
     """Padding rows (-1), lanes and positions outside, positions past the
     rotation tables, page-table entries of no page: nothing is written, zeros are
