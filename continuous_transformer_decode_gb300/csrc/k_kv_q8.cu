@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(32 * kRelocWarps)
           const int64_t at = (int64_t)delta * kHalf + lane + 32 * p;
           rope_pair((float)((int)lo[p] - 128) * s, (float)((int)hi[p] - 128) * s, rc[at], -rs[at],
                     y0[p], y1[p]);
+          y0[p] = storable(y0[p]), y1[p] = storable(y1[p]);
           amax = fmaxf(amax, fmaxf(fabsf(y0[p]), fabsf(y1[p])));
         }
 #pragma unroll
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(32 * kRelocWarps)
           lo[p] = (uint8_t)(128 + (amax > 0.0f ? (int)rintf(y0[p] / amax * 127.0f) : 0));
           hi[p] = (uint8_t)(128 + (amax > 0.0f ? (int)rintf(y1[p] / amax * 127.0f) : 0));
         }
-        s = amax / 127.0f;
+        s = fminf(amax / 127.0f, kMaxScale);
       }
     }
     __syncthreads();

@@ -152,6 +152,34 @@ def test_import_export_clone_and_evict():
         fs.fs_destroy(h)
 
 
+def test_evict_of_keys_near_the_largest_value():
+    """A key turned back past the largest f32 is stored as an infinity is by the
+    append: as the largest value, in a row with a finite scale."""
+    cfg, n, cut, end = SMALL, 24, 3, 9
+    h = U.make_gpu(cfg, synth.make_weights(cfg, seed=1, fmt="f32"), fs.FS_DTYPE_F32, Q8,
+                   max_lanes=1, max_pos=64, page_size=16)
+    rng = np.random.default_rng(12)
+    shape = (cfg["L"], n, cfg["Hkv"], cfg["hd"])
+    K = (3.2e38 * rng.choice([-1.0, 1.0], shape)).astype(np.float32)
+    V = rng.standard_normal(shape).astype(np.float32)
+    big = float(np.finfo(np.float32).max)
+    cos, sin = R.rope_tables(end, cfg["hd"])
+    try:
+        fs.fs_lane_import_kv(h, 0, K, V)
+        old = [fs.fs_lane_export_kv(h, 0, l, cfg["Hkv"], cfg["hd"])[0] for l in range(cfg["L"])]
+        fs.fs_lane_evict(h, 0, cut, end)
+        for l in range(cfg["L"]):
+            k = fs.fs_lane_export_kv(h, 0, l, cfg["Hkv"], cfg["hd"])[0].astype(np.float64)
+            moved = R.rotate(old[l][end:], cos[[end - cut]], -sin[[end - cut]]).astype(np.float64)
+            assert (np.abs(moved) > big).any()
+            moved = np.clip(moved, -big, big)
+            amax = np.abs(moved).max(-1, keepdims=True)
+            assert np.isfinite(k).all()
+            assert (np.abs(k[cut:] - moved) <= amax * (0.5 / 127 + 2.0 ** -18)).all()
+    finally:
+        fs.fs_destroy(h)
+
+
 def test_speculative_step_end_to_end():
     """Three lanes, drafts of 4, 2 and 0 tokens: one chunked step scores them, the
     verification accepts a prefix, the rejected suffix leaves the cache; the lane
