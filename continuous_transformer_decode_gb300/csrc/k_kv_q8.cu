@@ -9,8 +9,8 @@
 // rotation pairs), so that the loads and stores of a warp are whole sectors of
 // consecutive rows, and every lane has its key and its value row in flight
 // together. 65536 rows of 8 heads of 128 in bf16 are read back in 73 us, 5.6 TB/s, and
-// written in 111 us, 3.7 TB/s: 404 instructions for a warp's two rows of keys and two of
-// values bound that (0.78 of the issue slots). Rounding to a code is one fused multiply-add: x * r + 1.5 * 2^23 + 128
+// written in 104 us, 3.9 TB/s: 381 instructions for a warp's two rows of keys and two of
+// values bound that (0.79 of the issue slots). Rounding to a code is one fused multiply-add: x * r + 1.5 * 2^23 + 128
 // has the byte code + 128 in its last bits.
 
 #include <float.h>
@@ -188,9 +188,13 @@ __device__ __noinline__ void quantise_border_row(const T* x, const float* rc, co
 //
 // kTies: the values are bf16 as they came. With X and A the 8-bit significands of x
 // and amax, a quotient t = 127 X 2^e / A lies on a border or at least t / (254 X),
-// 1.5e-5 t, away from it: f32, good to 1.2e-7 t, cannot mistake the side, and what it
-// finds within 4e-6 t is a tie, which goes to the even code. Ties are common in such
-// rows: x = amax / 2, 63.5 codes, is in a third of normal rows of 128.
+// 1.5e-5 t, away from it. So t is rounded to a grid of its own size before its code
+// is: p = 64 t, q = p - t rounded, p - q. The difference is exact and differs from t by
+// q's rounding alone, at most half of a step of q, 2^-24 64 t = 3.8e-6 t; the borders
+// (k + 1/2, k < 127) are on q's grid, and the f32 quotient of one, within 1.2e-7 t,
+// goes to it (half a step is at least 1.9e-6 t), so that the sum with kMagic sees
+// the tie. Ties are common in such rows: x = amax / 2, 63.5 codes, is in a third of
+// normal rows of 128. Found by a comparison and a branch they took 11 us of 111.
 template <int HD, bool kRot, bool kTies>
 __device__ __forceinline__ bool quantise_row(const float (&x)[8], uint8_t* codes, float* scales,
                                              int64_t slot, int sub) {
@@ -201,20 +205,23 @@ __device__ __forceinline__ bool quantise_row(const float (&x)[8], uint8_t* codes
   for (int o = kL / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
   odd |= amax > 0.0f && amax < 1e-30f;
   const float r = amax > 0.0f ? 127.0f / amax : 0.0f;
-  float u[8], off[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    u[j] = fmaf(x[j], r, kMagic);
-    off[j] = fmaf(x[j], r, kMagic - u[j]);  // distance to the code
-  }
-  bool border = max_abs(off) > 0.5f - kNear<kRot>;
+  float u[8];
+  bool border = false;
   if constexpr (kTies) {
-    if (border)
+    const float r64 = r * 64.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (fabsf(off[j]) > 0.5f - 4e-6f * fabsf(x[j] * r))
-          u[j] = kMagic + 2.0f * rintf(0.5f * (x[j] * r));
-    border = false;
+    for (int j = 0; j < 8; ++j) {
+      const float p = __fmul_rn(x[j], r64), q = fmaf(-x[j], r, p);
+      u[j] = __fadd_rn(__fsub_rn(p, q), kMagic);
+    }
+  } else {
+    float off[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u[j] = fmaf(x[j], r, kMagic);
+      off[j] = fmaf(x[j], r, kMagic - u[j]);  // distance to the code
+    }
+    border = max_abs(off) > 0.5f - kNear<kRot>;
   }
   const unsigned left = __ballot_sync(kAll, odd || border);
   const unsigned row = (kL == 32 ? kAll : (1u << (kL & 31)) - 1) << (threadIdx.x % 32 - sub);

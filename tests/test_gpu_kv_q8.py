@@ -177,6 +177,34 @@ def test_append_not_finite():
     assert np.allclose(pg.dev[2].cpu().numpy()[pg.table[0, 0], 0], scale[:, 0], rtol=2.0 ** -22)
 
 
+@pytest.mark.parametrize("base", [-97, 0, 92])
+def test_codes_of_every_bf16_quotient(base):
+    """Rows of bf16 as they came: every significand over every largest one, a
+    quotient of up to 127 down to a quarter of a code, both signs. Exact codes: a
+    quotient is a tie or 1.5e-5 of itself away from one, which 64 bits tell apart."""
+    import torch
+    A, X = np.arange(128, 256), np.arange(128, 256)
+    rows = []
+    for e in range(11):
+        x = np.where((X[None] <= A[:, None]) | (e > 0), X[None] * 2.0 ** -e, 0.0)
+        row = np.concatenate([x, -x], 1)
+        row[:, 127] = A  # the largest magnitude
+        rows.append(row)
+    x = (np.concatenate(rows) * 2.0 ** base).astype(np.float32)[:, None]
+    assert np.array_equal(R.bf16(x), x)
+    n = len(x)
+    pg = Pages(np.random.default_rng(3), [n], 1, 256, 64)
+    v = _cuda(x).to(torch.bfloat16)
+    at = _cuda(np.zeros(n, np.int32)), _cuda(np.arange(n, dtype=np.int32))
+    fs.fs_kv_q8_append(pg.view, v, -v, *at)
+    torch.cuda.synchronize()
+    codes, _ = R.quantise(x)
+    t = np.arange(n)
+    for which, want in ((0, codes), (1, -codes)):
+        got = pg.dev[which].cpu().numpy()[pg.table[0, t // 64], :, t % 64].astype(np.int64) - 128
+        assert np.array_equal(got, want), np.argwhere(got != want)[:5]
+
+
 @pytest.mark.parametrize("hd", [64, 256])
 def test_infinities_read_back_finite(hd):
     """An infinity is stored as the largest finite f32, and so is read back finite:
