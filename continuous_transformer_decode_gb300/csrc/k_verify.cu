@@ -70,9 +70,12 @@ __device__ __forceinline__ Two log2e_over(float T) {
   return {q, (fmaf(-q, T, lh) + ll) / T};
 }
 
-// exp((z - m) / T) as 2^y, y = (z - m) * c with c = log2(e) / T, to a relative
-// 2^-36: y = n + k/32 + f with |f| <= 1/64, 2^f = 1 + its Taylor series (the
-// method of Tang, ACM TOMS 1989). Below 2^-126 it is zero.
+// 2^60 exp((z - m) / T) as 2^(60 + y), y = (z - m) * c with c = log2(e) / T, to a
+// relative 2^-36: y = n + k/32 + f with |f| <= 1/64, 2^f = 1 + its Taylor series (the
+// method of Tang, ACM TOMS 1989). Below y = -125.5 it is zero. The factor, which every
+// weight and sum in pairs has, keeps the second halves of the smallest (2^-150 of the
+// largest) in f32's range, and the largest sum, 2^30 of them, as well.
+constexpr float kUp = 0x1p60f;
 __device__ __forceinline__ Two weight2(float z, float m, Two c, const float2* tab) {
   const Two d = two_sum(z, -m);
   const float p = __fmul_rn(d.h, c.h);
@@ -93,10 +96,10 @@ __device__ __forceinline__ Two weight2(float z, float m, Two c, const float2* ta
   const float we = fmaf(t.x, u.h, -w) + fmaf(t.x, u.l, fmaf(t.y, u.h, t.y));
   const Two e = fast_two_sum(t.x, w);
   const Two r = fast_two_sum(e.h, __fadd_rn(e.l, we));
-  const float s = __int_as_float(((k >> 5) + 127) << 23);  // 2^n, -126 <= n <= 0
+  const float s = __int_as_float(((k >> 5) + 127 + 60) << 23);  // 2^60 2^n, -126 <= n <= 0
   // no branches: several of these run interleaved
   const bool one = z == m, in = p > -125.5f;  // not in: also -inf and NaN
-  return {one ? 1.0f : in ? __fmul_rn(r.h, s) : 0.0f, !one && in ? __fmul_rn(r.l, s) : 0.0f};
+  return {one ? kUp : in ? __fmul_rn(r.h, s) : 0.0f, !one && in ? __fmul_rn(r.l, s) : 0.0f};
 }
 
 // f32 weight under m; c = log2(e) / T.

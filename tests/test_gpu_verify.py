@@ -173,3 +173,36 @@ def test_strided_rows_streams_and_graphs():
         want = R.verify(**c)
         assert np.array_equal(out[0].cpu().numpy(), want[0])
         assert np.array_equal(out[1].cpu().numpy(), want[1])
+
+
+def test_draw_among_the_smallest_weights():
+    """All that is left are weights of 2^-124.9 to 2^-118 of the largest: they are held
+    to 2^-36 too, though the second half of such a pair is below f32's range."""
+    rng = np.random.default_rng(21)
+    n, V = 300, 60
+    z = np.empty((2 * n, V), np.float32)
+    q = np.zeros((2 * n, V), np.float32)
+    us = []
+    temps = rng.uniform(0.5, 1.5, n).astype(np.float32)
+    for s in range(n):
+        row = -(rng.uniform(118.0, 124.8, V) * np.log(2.0) * float(temps[s])).astype(np.float32)
+        row[0] = 0.0
+        z[2 * s:2 * s + 2] = row
+        q[2 * s:2 * s + 2, 0] = 1.0   # takes all of the largest
+        q[2 * s:2 * s + 2, 5] = 1.0   # the draft
+        w = np.exp(row.astype(np.float64) / float(temps[s]))
+        w[[0, 5]] = 0.0
+        cum = np.cumsum(w)
+        i = rng.integers(1, 4)
+        for step in (0, 1, -1):
+            u = np.float32(cum[i] / cum[-1])
+            u = (u.view(np.int32) + np.int32(step)).view(np.float32)
+            # a running sum of weights good to 2^-36, its own roundings, and the total
+            if abs(float(u) * cum[-1] - cum[i]) > 2.0 ** -33 * cum[i]:
+                break
+        us.append(u)
+    c = dict(logits=z, row_start=np.arange(0, 2 * n + 1, 2, dtype=np.int32),
+             draft=np.full(2 * n, 5, np.int32), probs=q, temps=temps,
+             u_accept=np.full(2 * n, 0.5, np.float32), u_sample=np.float32(us))
+    acc, _ = check(c)
+    assert (acc == 0).all()
