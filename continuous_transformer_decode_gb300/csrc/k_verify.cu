@@ -102,7 +102,9 @@ __device__ __forceinline__ Two weight2(float z, float m, Two c, const float2* ta
   return {one ? kUp : in ? __fmul_rn(r.h, s) : 0.0f, !one && in ? __fmul_rn(r.l, s) : 0.0f};
 }
 
-// f32 weight under m; c = log2(e) / T.
+// f32 weight under m; c = log2(e) / T. Good to a relative (4 + 1.4 |y|) 2^-24 with y
+// its logarithm to the base 2: ex2.approx is good to 2^-22, and z - m and then y are
+// rounded, 2^-24 |y| each, times ln 2. Zero below y = -126.
 __device__ __forceinline__ float weight1(float z, float m, Two c) {
   if (m == CUDART_INF_F) return z == m ? 1.0f : 0.0f;
   const float d = z - m;
@@ -143,6 +145,11 @@ __device__ __forceinline__ float4 load4(const float* z, int i, int hi, bool vec)
   return v;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ Two shfl_up(Two v, int o) {
   return {__shfl_up_sync(kAll, v.h, o), __shfl_up_sync(kAll, v.l, o)};
 }
@@ -282,6 +289,16 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
   // exponentials (6000 rows of 1000 to 49152 logits of deviation 0.5 to 8). The last
   // additions round by 2^-25 S each. With draft probabilities S itself enters twice.
   const float rough = a.probs ? 0x1p-21f : 0x1.8p-22f;
+  // How far f32 may be off, in units of 2^-24. A weight: 4 + 1.4 |y| (weight1). A lane
+  // sums sixteen weights of a chunk in five additions that round, and chunk by chunk
+  // takes its sum to a new maximum (a product by a weight, 5 + 1.4 |y|) and adds, 6 a
+  // chunk; five more sum the lanes, one product takes a warp's sum to the row's maximum
+  // and six additions sum the warps. The |y| of a token's weight and of the factors
+  // that it meets add up to its |y| under the row's maximum, and the mean of that over
+  // the row is log2(V / S) at most, as -sum p log2 p <= log2 V. So S is off by
+  // 25 + 6 chunks + 1.4 log2(V / S).
+  const float chunks = (float)((run + 511) / 512), log_v = lg2((float)V);
+  constexpr float kUnit = 0x1p-24f;
   int turn = 0;
   constexpr int kN = kC * kW;  // warps of the cluster, two a lane in what follows
   static_assert(kN <= 64, "two warps a lane");
@@ -404,11 +421,15 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     float wx = 0.0f;  // the weight of the draft
     if (known) {
       wx = weight1(z_x, M, c);
-      const float t = u_acc * q_x * S;
+      const float t = u_acc * S * q_x;
       bool ok = t < wx;
-      if (fabsf(t - wx) <= 2.0f * rough * wx) {
+      // t is off by S's error and two products, wx by a weight's, and two units are for
+      // the products of errors. Below 2^-100 t's products may leave f32's range.
+      const float deep = z_x == M ? 0.0f : fabsf(z_x - M) * c.h;
+      const float unsure = 33.0f + 6.0f * chunks + 1.4f * (log_v - lg2(S) + deep);
+      if (wx > 0.0f && (wx < 0x1p-100f || fabsf(t - wx) <= unsure * kUnit * wx)) {
         const Two S2 = cluster_sum(left_sum(left, lo, hi, lane));
-        ok = less(mul(mul({u_acc, 0.0f}, {q_x, 0.0f}), S2), weight2(z_x, M, c, sh.tab));
+        ok = less(mul(mul({u_acc, 0.0f}, S2), {q_x, 0.0f}), weight2(z_x, M, c, sh.tab));
       }
       if (ok) continue;
     }

@@ -206,3 +206,42 @@ def test_draw_among_the_smallest_weights():
              u_accept=np.full(2 * n, 0.5, np.float32), u_sample=np.float32(us))
     acc, _ = check(c)
     assert (acc == 0).all()
+
+
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("V,depths", [(2, 300), (1500, 20), (5000, 3), (5000, 16), (60000, 2)])
+def test_acceptance_next_to_its_border(V, depths, probs):
+    """Drafts of 5 to 86 nats below the largest logit (a third of the probability in
+    equal logits, whose roundings are alike), u * q(x) a few f32 steps to either side
+    of p(x): nearer than an f32 weight is good to, further than one of 2^-36 (cases
+    within 2^-33 are left out)."""
+    rng = np.random.default_rng(V + depths)
+    rows, q, ua, temps = [], [], [], []
+    for d in rng.uniform(5.0, 86.0, depths):
+        T, M = np.float32(rng.uniform(0.3, 2.0)), np.float32(5 * rng.standard_normal())
+        z = np.empty(V, np.float32)
+        z[:] = M - T * np.float32(np.log(2.0 * max(V - 2, 1)) + rng.uniform(-0.2, 0.2))
+        z[0], z[V - 1] = M, M - np.float32(d) * T
+        e = np.exp((z.astype(np.float64) - float(M)) / float(T))
+        p = e[V - 1] / e.sum()
+        for k in (-64, -32, -16, -11, -8, -5, -4, -3, -2, -1, 0, 1, 2, 3, 4, 5, 8, 11, 16, 32, 64):
+            u = np.float32(rng.uniform(0.25, 1.0)) if probs else np.float32(p)
+            near = np.float32(p / float(u)) if probs else u
+            near = (np.float32(near).view(np.int32) + np.int32(k)).view(np.float32)
+            u, x = (u, near) if probs else (near, np.float32(1.0))
+            if abs(float(u) * float(x) - p) <= 2.0 ** -33 * p:
+                continue
+            rows += [z, z]
+            one = np.zeros(V, np.float32)
+            one[V - 1] = x
+            q += [one, one]
+            ua += [u, u]
+            temps.append(T)
+    n = len(temps)
+    assert n > 15 * depths
+    c = dict(logits=np.stack(rows), row_start=np.arange(0, 2 * n + 1, 2, dtype=np.int32),
+             draft=np.full(2 * n, V - 1, np.int32), probs=np.stack(q) if probs else None,
+             temps=np.float32(temps), u_accept=np.float32(ua),
+             u_sample=rng.uniform(0.1, 0.5, n).astype(np.float32))
+    acc, _ = check(c)
+    assert 0 < acc.sum() < n  # both sides are met
