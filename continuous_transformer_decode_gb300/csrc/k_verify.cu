@@ -18,13 +18,14 @@
 // Whole-number answers are held to more than f32: where an acceptance or a draw
 // comes so near to its border that f32 weights and sums cannot tell, it is taken
 // again from weights good to 2^-36, as pairs of f32 numbers (this GPU's f64 rate is
-// 1/60 of its f32 rate). That is rare for an acceptance, and a few draws in a
-// hundred for a vocabulary of 49152. What bounds the kernel is the chain of one
+// 1/60 of its f32 rate). What f32 may be off by is derived, not measured (in the kernel,
+// below). That is rare for an acceptance, and 10 to 13 draws in a hundred for normal
+// logits over a vocabulary of 32000 to 49152. What bounds the kernel is the chain of one
 // sequence on eight SMs (2 to 3 us a row: a row's loads, its maximum and sum, the
-// barrier; 5 us for the draw and 9 us for one that is taken again), not the bytes:
-// 256 sequences of 4 drafts from a lookup, 49152 tokens, take 31 us, 61 MB of logits
-// being read (every draw in pairs: 108 us); 64 sequences of 0 to 7 drafts 33 us; one
-// of 4 drafts 11 us.
+// barrier; and 9 us for a draw that is taken again with draft probabilities), not the
+// bytes. Means over many inputs: 256 sequences of 4 drafts from a lookup, 49152 tokens,
+// 37 us, 61 to 77 MB of logits being read (every draw taken again: 61 us); 64 sequences
+// of 0 to 7 drafts 35 us (45 us); one of 4 drafts 11 us (19 us).
 
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -236,9 +237,10 @@ __device__ __forceinline__ Two left_sum(const Left& w, int lo, int hi, int lane)
 // order in every block, so the cluster stays together.
 //
 // held: a block's part of the row (and of the draft's probabilities) stays in
-// dynamic shared memory for the draw; else it is read again.
+// dynamic shared memory for the draw; else it is read again. Three blocks an SM, which is
+// 80 registers (left to itself the compiler takes up to 93, and 256 sequences 12 % longer).
 template <int kC, int kT>
-__global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
+__global__ void __launch_bounds__(kT, 3) k_verify(VerifyArgs a, int held) {
   constexpr int kW = kT / 32;
   __shared__ Shared<kC, kW> sh;
   extern __shared__ __align__(16) float hold[];  // [kW * run] z, then q
@@ -283,12 +285,6 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
   const int base = (int)min((int64_t)V, (int64_t)rank * kW * run);
   const int count = (int)min((int64_t)V - base, (int64_t)kW * run);
   const int lo = min(count, warp * run), hi = min(count, lo + run);
-  // What the f32 sums are held to be off by, of the row's sum S. An exponential comes
-  // out 2^-24.3 too small in the mean, and otherwise rounds independently: measured
-  // against 64 bits, target and running sum differ by at most 2^-23.9 S through the
-  // exponentials (6000 rows of 1000 to 49152 logits of deviation 0.5 to 8). The last
-  // additions round by 2^-25 S each. With draft probabilities S itself enters twice.
-  const float rough = a.probs ? 0x1p-21f : 0x1.8p-22f;
   // How far f32 may be off, in units of 2^-24. A weight: 4 + 1.4 |y| (weight1). A lane
   // sums sixteen weights of a chunk in five additions that round, and chunk by chunk
   // takes its sum to a new maximum (a product by a weight, 5 + 1.4 |y|) and adds, 6 a
@@ -297,6 +293,19 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
   // that it meets add up to its |y| under the row's maximum, and the mean of that over
   // the row is log2(V / S) at most, as -sum p log2 p <= log2 V. So S is off by
   // 25 + 6 chunks + 1.4 log2(V / S).
+  //
+  // In a draw, an error that a running sum P and the total share moves P - u total by
+  // max(u, 1 - u) of itself at most. So, of S: the warps' sums, 19 + 6 chunks +
+  // 1.4 log2(V / S); the additions that give the total and the running sum, and the
+  // product by u, 15; 6 of a weight of 1 for the draft's, taken out (5 + 1.4 |y| of it).
+  // The chosen warp's tokens are summed anew: their weights, with a mean |y| of
+  // log2(run / own) if own is their sum, and additions of numbers up to own, ten of the
+  // scans, four for the place and two a chunk. With draft probabilities a weight
+  // max(e - q S, 0) is off by e (5 + 1.4 |y|) and, where it is not zero, S's error times e,
+  // and they are summed in 7 + 4 chunks additions. (Weights of equal logits err alike, so
+  // nothing is taken to cancel: what suffices where roundings are independent, 6 or 8 of
+  // S in all, gave wrong tokens in rows of 262144.)
+  const float log_run = lg2((float)run);
   const float chunks = (float)((run + 511) / 512), log_v = lg2((float)V);
   constexpr float kUnit = 0x1p-24f;
   int turn = 0;
@@ -483,11 +492,19 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     float total = f0 + f1, before = 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    const float target = us * total, off = rough * S;
+    const float target = us * total;
     const int chosen = pick(f0, f1, target, before, lane);
     if (chosen >= 0 && chosen / kW == rank) {
       const int w = chosen % kW;
       const int end_w = min(count, (w + 1) * run);
+      // what the running sum is ahead of the target, and what that may be off by
+      float place = before - target;
+      const float own = fmaxf(__shfl_sync(kAll, chosen & 1 ? f1 : f0, chosen / 2), 0x1p-100f);
+      const float log_row = log_v - lg2(S);
+      const float row = pr ? 52.0f + 10.0f * chunks + 2.8f * log_row
+                           : 34.0f + 6.0f * chunks + 1.4f * log_row;
+      const float off = kUnit * (row * S + 6.0f +
+                                 (18.0f + 2.0f * chunks + 1.4f * (log_run - lg2(own))) * own);
       bool hit = false;  // a token whose borders the target is clear of
 #pragma unroll 1
       for (int i0 = w * run; i0 < end_w; i0 += kT) {  // a token a thread
@@ -499,15 +516,15 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
         __syncthreads();
         const float in_warps = scan(lane < kW ? sh.scan[lane] : 0.0f, lane);
         const float ahead = warp ? __shfl_sync(kAll, in_warps, warp - 1) : 0.0f;
-        const float at = before + ahead + (inc - e), then = before + ahead + inc;
-        const bool mine = at + off < target && target <= then - off;
+        const float at = place + ahead + (inc - e), then = place + ahead + inc;
+        const bool mine = at + off < 0.0f && 0.0f <= then - off;
         if (mine) {
           a.n_accepted[b] = r - r0;
           a.next_token[b] = base + i;
         }
-        before += __shfl_sync(kAll, in_warps, 31);
+        place += __shfl_sync(kAll, in_warps, 31);
         hit = __syncthreads_or(mine);
-        if (hit || before >= target + off) break;
+        if (hit || place >= off) break;
       }
       if (!hit && tid < kC) *remote(&sh.again, tid) = 1;
     }
@@ -531,36 +548,50 @@ __global__ void __launch_bounds__(kT) k_verify(VerifyArgs a, int held) {
     Two cum = {0.0f, 0.0f};
     const int taken = pick(w0, w1, goal, cum, lane);
     if (taken >= 0 && taken / kW == rank) {
-      const Two none = {0.0f, 0.0f};
-      const int w = taken % kW;
-      const int end_w = min(count, (w + 1) * run);
-      int found = -1, tail = -1;
-#pragma unroll 1
-      for (int i0 = w * run; i0 < end_w && found < 0; i0 += kT) {
-        const int i = i0 + tid;
-        const Two e = i < end_w ? left.at(i) : none;
-        Two at = scan(e, lane);
-        if (lane == 31) sh.scan2[warp] = at;
-        __syncthreads();
-        const Two in_warps = scan(lane < kW ? sh.scan2[lane] : none, lane);
-        if (warp) at = add(shfl(in_warps, warp - 1), at);
-        at = add(cum, at);
-        cum = add(cum, shfl(in_warps, 31));
-        // the lowest that reaches it; the highest with a weight in case none does
-        const bool has = e.h > 0.0f;
-        const unsigned m = __ballot_sync(kAll, has && !less(at, goal)), h = __ballot_sync(kAll, has);
-        if (lane == 0) {
-          sh.at[warp] = m ? i - lane + __ffs(m) - 1 : V;
-          sh.tail[warp] = h ? i - lane + 31 - __clz(h) : -1;
-        }
-        __syncthreads();
-        const int lowest = __reduce_min_sync(kAll, lane < kW ? sh.at[lane] : V);
-        if (lowest < V) found = lowest;
-        tail = max(tail, __reduce_max_sync(kAll, lane < kW ? sh.tail[lane] : -1));
+      // its run in the warps' lanes, `each` consecutive tokens a lane
+      const int from = taken % kW * run, upto = min(count, from + run);
+      const int each = (run + kT - 1) / kT, mine = from + tid * each;
+      Two e = {0.0f, 0.0f};
+      int tail = -1;
+#pragma unroll 4
+      for (int i = mine; i < min(upto, mine + each); ++i) {
+        const Two v = left.at(i);
+        if (v.h > 0.0f) tail = i;
+        e = add(e, v);
       }
+      Two at = scan(e, lane);
+      if (lane == 31) sh.scan2[warp] = at;
+      __syncthreads();
+      const Two in_warps = scan(lane < kW ? sh.scan2[lane] : Two{0.0f, 0.0f}, lane);
+      if (warp) cum = add(cum, shfl(in_warps, warp - 1));
+      // the first lane that reaches the goal looks for its first token that does; the
+      // run's last token with a weight is taken if none does
+      const unsigned m = __ballot_sync(kAll, e.h > 0.0f && !less(add(cum, at), goal));
+      tail = __reduce_max_sync(kAll, tail);
+      if (lane == 0) sh.at[warp] = V, sh.tail[warp] = tail;
+      __syncwarp();
+      if (m) {
+        const int who = __ffs(m) - 1, start = mine + (who - lane) * each;
+        if (who) cum = add(cum, shfl(at, who - 1));
+        int found = -1, last_in = -1;
+        for (int i0 = start; i0 < min(upto, start + each) && found < 0; i0 += 32) {
+          const int i = i0 + lane;
+          const Two v = i < min(upto, start + each) ? left.at(i) : Two{0.0f, 0.0f};
+          const Two s = add(cum, scan(v, lane));
+          const unsigned h = __ballot_sync(kAll, v.h > 0.0f);
+          const unsigned r = __ballot_sync(kAll, v.h > 0.0f && !less(s, goal));
+          cum = shfl(s, 31);
+          if (r) found = i0 + __ffs(r) - 1;
+          if (h) last_in = i0 + 31 - __clz(h);
+        }
+        if (lane == 0) sh.at[warp] = found >= 0 ? found : last_in;
+      }
+      __syncthreads();
+      const int lowest = __reduce_min_sync(kAll, lane < kW ? sh.at[lane] : V);
+      const int highest = __reduce_max_sync(kAll, lane < kW ? sh.tail[lane] : -1);
       if (tid == 0) {
         a.n_accepted[b] = r - r0;
-        a.next_token[b] = base + (found >= 0 ? found : tail);
+        a.next_token[b] = base + (lowest < V ? lowest : highest);
       }
     }
     break;
@@ -588,7 +619,7 @@ int launch_c(const VerifyArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Blocks of a sequence: eight while all sequences' blocks fit the SMs four at a time,
-// else four (64 sequences: 33 us with eight, 40 with four; 256: 44 and 33), and no more
+// else four (64 sequences: 35 us with eight, 58 with four; 256: 47 and 37), and no more
 // than give every warp 128 tokens.
 int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
   if (a.n_seqs <= 0) return 0;

@@ -245,3 +245,80 @@ def test_acceptance_next_to_its_border(V, depths, probs):
              u_sample=rng.uniform(0.1, 0.5, n).astype(np.float32))
     acc, _ = check(c)
     assert 0 < acc.sum() < n  # both sides are met
+
+
+def _next_to_borders(rng, cum, n, steps=24):
+    """n numbers of u_sample, each a few f32 steps from the place of a running sum of
+    cum, none within 2^-33 of one: what weights good to 2^-36 and their sums tell."""
+    out = []
+    for _ in range(100 * n):
+        i = rng.integers(0, len(cum) - 1)
+        u = np.float32(cum[i] / cum[-1])
+        u = (u.view(np.int32) + np.int32(rng.integers(-steps, steps + 1))).view(np.float32)
+        j = np.searchsorted(cum, float(u) * cum[-1])
+        near = min(abs(cum[k] - float(u) * cum[-1]) for k in (max(j - 1, 0), min(j, len(cum) - 1)))
+        if 0 <= u < 1 and near > 2.0 ** -33 * cum[-1]:
+            out.append(u)
+        if len(out) == n:
+            return np.float32(out)
+    raise AssertionError("no such numbers")
+
+
+def _draws(z, T, us):
+    """next_token of sequences of one row each, all of them the row z."""
+    n = len(us)
+    c = dict(logits=np.tile(z, (n, 1)), row_start=np.arange(n + 1, dtype=np.int32),
+             draft=np.full(n, -1, np.int32), probs=None, temps=np.full(n, T, np.float32),
+             u_accept=np.zeros(n, np.float32), u_sample=us)
+    acc, nxt = run(c)
+    assert (acc == 0).all()
+    return nxt
+
+
+def _equal_groups(rng, V):
+    """One largest logit and two groups of equal ones of about its probability each,
+    in runs or mixed: every weight of a group is rounded alike."""
+    T, M = np.float32(rng.uniform(0.4, 1.5)), np.float32(4 * rng.standard_normal())
+    below = [T * np.float32(np.log(V / 2.0) + rng.uniform(-0.3, 0.3)) for _ in range(2)]
+    z = np.full(V, M - below[0], np.float32)
+    z[V // 2:] = M - below[1]
+    if rng.random() < 0.5:
+        rng.shuffle(z)
+    z[rng.integers(0, V)] = M
+    return z, T
+
+
+@pytest.mark.parametrize("V,n,rows", [(2000, 100, 3), (9000, 40, 3), (49152, 40, 4), (131072, 40, 4),
+                                      (262144, 40, 6), (262144, 100, 6), (1 << 20, 80, 2)])
+def test_draw_next_to_borders_among_equal_logits(V, n, rows):
+    rng = np.random.default_rng(V + n)
+    for r in range(rows):
+        z, T = _equal_groups(rng, V)
+        if r == 0 and V == 262144:  # 1e-6 too large and too small in f32
+            T, z[:] = np.float32(0.7341579), np.float32(-5.716526)
+            z[V // 2:], z[0] = np.float32(-5.7151575), np.float32(2.3561673)
+        e = np.exp((z.astype(np.float64) - float(z.max())) / float(T))
+        cum = np.cumsum(e)
+        us = _next_to_borders(rng, cum, n)
+        want = np.searchsorted(cum, us.astype(np.float64) * cum[-1])
+        assert np.array_equal(_draws(z, T, us), want)
+
+
+@pytest.mark.parametrize("V,n", [(9000, 30), (49152, 30), (262144, 8), (49152, 100)])
+def test_residual_draw_next_to_borders(V, n):
+    """The same of max(p - q, 0), after a draft of no probability, q in equal runs."""
+    rng = np.random.default_rng(V + 7 * n)
+    z, T = _equal_groups(rng, V)
+    x = int(rng.integers(1, V - 1))
+    z[x] = -np.inf
+    e = np.exp((z.astype(np.float64) - float(z.max())) / float(T))
+    p = e / e.sum()
+    q = (p * np.where(np.arange(V) // 37 % 3 == 0, 1.5, rng.uniform(0.1, 0.9))).astype(np.float32)
+    q[x] = 0.1
+    cum = np.cumsum(np.maximum(p - q, 0.0))
+    c = dict(logits=np.tile(z, (2 * n, 1)), row_start=np.arange(0, 2 * n + 1, 2, dtype=np.int32),
+             draft=np.full(2 * n, x, np.int32), probs=np.tile(q, (2 * n, 1)),
+             temps=np.full(n, T, np.float32), u_accept=np.full(2 * n, 0.5, np.float32),
+             u_sample=_next_to_borders(rng, cum, n))
+    acc, _ = check(c)
+    assert (acc == 0).all()
