@@ -521,14 +521,19 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
 
 
 # ------------------------------------------------------- 8-bit paged KV cache
+# The calls of this section and the next take CUDA tensors and a stream (a
+# torch.cuda.Stream or an address; None: torch's current stream) and return once
+# their work is enqueued there. As with any kernel on a stream of the caller's,
+# tensors that were made or are freed on another stream are the caller's to order.
 class _Types:
-    """torch's types, once torch is there (this module does not import it)."""
-    f32 = bf16 = i32 = u8 = None
+    """torch and its types, once torch is there (this module does not import it)."""
+    torch = f32 = bf16 = i32 = u8 = None
 
 
 def _types():
     if _Types.f32 is None:
         import torch
+        _Types.torch = torch
         _Types.bf16, _Types.i32, _Types.u8 = torch.bfloat16, torch.int32, torch.uint8
         _Types.f32 = torch.float32
     return _Types
@@ -543,8 +548,14 @@ def _op_check(rc: int) -> None:
         raise FsError(rc, fs_last_error(None))
 
 
-def _raw(stream):
-    return None if stream is None else getattr(stream, "cuda_stream", stream)
+def _raw(stream, x):
+    """Address of the stream: without one, torch's current stream of x's device, as
+    torch's own calls take it."""
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    if not x.is_cuda:  # refused by the C call
+        return None
+    return _types().torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
 def _vec(x, n: int, dtype, what: str):
@@ -615,7 +626,7 @@ def fs_kv_q8_append(cache: fs_kv_q8, k, v, lanes, positions, rope=None, stream=N
     _op_check(lib().fs_kv_q8_append(C.byref(cache), kp, vp, ks, vs, dt,
                                     _vec(lanes, n, ty.i32, "lanes"),
                                     _vec(positions, n, ty.i32, "positions"), n, rc, rs, rl,
-                                    _raw(stream)))
+                                    _raw(stream, lanes)))
 
 
 def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, stream=None) -> None:
@@ -633,7 +644,7 @@ def fs_kv_q8_read(cache: fs_kv_q8, lanes, positions, k_out=None, v_out=None, str
         dt = FS_DTYPE_F32 if dv is None else dv
     _op_check(lib().fs_kv_q8_read(C.byref(cache), _vec(lanes, n, ty.i32, "lanes"),
                                   _vec(positions, n, ty.i32, "positions"), n, kp, vp, ks,
-                                  vs, dt, _raw(stream)))
+                                  vs, dt, _raw(stream, lanes)))
 
 
 def fs_kv_q8_attention_workspace(cache: fs_kv_q8, n: int, n_heads: int, max_len: int = 0,
@@ -672,7 +683,7 @@ def fs_kv_q8_attention(cache: fs_kv_q8, q, lanes, lengths, out, max_len: int = 0
         C.byref(cache), qp, qs, _vec(lanes, n, ty.i32, "lanes"),
         _vec(lengths, n, ty.i32, "lengths"), n, H, max_len,
         hd ** -0.5 if scale is None else scale, rc, rs, rl, op, os_, dt, split_len, wp, wb,
-        _raw(stream)))
+        _raw(stream, lanes)))
 
 
 # --------------------------------------------------------- draft verification
@@ -705,7 +716,7 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
         _vec(u_sample, n, ty.f32, "u_sample"),
         _vec(n_accepted, n, ty.i32, "n_accepted"),
         _vec(next_token, n, ty.i32, "next_token"),
-        _raw(stream)))
+        _raw(stream, temps)))
 
 
 # ------------------------------------------------------------------ scheduler

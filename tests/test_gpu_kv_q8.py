@@ -501,3 +501,56 @@ def test_host_tensors_of_the_c_interface_are_refused():
     rc = fs.lib().fs_kv_q8_append(C.byref(pg.view), host.ctypes.data, host.ctypes.data, 64, 64, 0,
                                   one.data_ptr(), one.data_ptr(), 1, None, None, 0, None)
     assert rc == fs.CODES["FS_ERR_ARG"]
+
+
+def test_calls_without_a_stream_run_on_torchs_current_one():
+    """Inputs made on a side stream by slow work, the operators called without a
+    stream inside it, and the same captured into a graph."""
+    import torch
+    rng = np.random.default_rng(16)
+    pg = Pages(rng, [200, 200], 2, 64, 16)
+    kv = rng.standard_normal((2, 2, 2, 64)).astype(np.float32)
+    q = rng.standard_normal((2, 4, 64)).astype(np.float32)
+    z = rng.standard_normal((2, 300)).astype(np.float32)
+    src = {k: _cuda(v) for k, v in dict(
+        k=kv[0], v=kv[1], lanes=np.int32([0, 1]), pos=np.int32([150, 20]), lens=np.int32([151, 21]),
+        q=q, z=z, start=np.int32([0, 1, 2]), temps=np.float32([0, 0]), u=np.float32([0.5, 0.5])).items()}
+    dst = {k: torch.zeros_like(v) for k, v in src.items()}
+    ws = torch.zeros(fs.fs_kv_q8_attention_workspace(pg.view, 2, 4, 200, 64), dtype=torch.uint8,
+                     device="cuda")
+    out, k_out = torch.zeros(2, 4, 64, device="cuda"), torch.zeros(2, 2, 64, device="cuda")
+    acc, nxt = (torch.full((2,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    slow = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+
+    def step():
+        d = dst
+        fs.fs_kv_q8_append(pg.view, d["k"], d["v"], d["lanes"], d["pos"])
+        fs.fs_kv_q8_read(pg.view, d["lanes"], d["pos"], k_out)
+        fs.fs_kv_q8_attention(pg.view, d["q"], d["lanes"], d["lens"], out, max_len=200, split_len=64,
+                              workspace=ws)
+        fs.fs_verify_draft(d["z"], d["start"], d["lanes"], None, d["temps"], d["u"], d["u"], acc, nxt)
+
+    def look():
+        torch.cuda.synchronize()
+        codes, scale = R.quantise(kv[0])
+        assert np.allclose(k_out.cpu().numpy(), codes * scale[..., None], rtol=2.0 ** -22, atol=0)
+        ref, tol = R.attention(pg.now(), q, [0, 1], [151, 21], 0.125)
+        _check_attention(out, ref, tol)
+        assert np.array_equal(nxt.cpu().numpy(), z.argmax(-1))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            slow = slow @ slow * 1e-3
+        for k in src:
+            dst[k].copy_(src[k])
+        step()
+    look()
+    out.zero_(), k_out.zero_(), nxt.fill_(-9)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    g.replay()
+    look()

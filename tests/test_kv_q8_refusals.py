@@ -153,3 +153,44 @@ def test_binding_refuses_tensors_it_cannot_use():
         fs.fs_kv_q8_append(cache(), z(1, 2, 64), z(1, 2, 64), one, one)
     with pytest.raises(fs.FsError):
         fs.fs_verify_draft(z(1, 8), z(2, dtype=torch.int32), one, None, z(1), z(1), z(1), one, one)
+
+
+def test_no_stream_is_torchs_current_stream(monkeypatch):
+    """A call that is given no stream goes to the current stream of its tensors' device,
+    one that is given a stream to that."""
+    import torch
+
+    class OnDevice(torch.Tensor):  # a host tensor that says it is on device 0
+        __torch_function__ = torch._C._disabled_torch_function_impl
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+        @property
+        def device(self):
+            return torch.device("cuda", 0)
+
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype).as_subclass(OnDevice)
+    i32 = lambda *s: z(*s, dtype=torch.int32)
+    got = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: got.append((name, a[-1])) or 0
+
+    monkeypatch.setattr(fs, "lib", lambda: Lib())
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 4242 + d, raising=False)
+
+    class Stream:
+        cuda_stream = 77
+
+    for given, want in ((None, 4242), (Stream(), 77), (55, 55)):
+        got.clear()
+        fs.fs_kv_q8_append(cache(), z(1, 2, 64), z(1, 2, 64), i32(1), i32(1), stream=given)
+        fs.fs_kv_q8_read(cache(), i32(1), i32(1), z(1, 2, 64), stream=given)
+        fs.fs_kv_q8_attention(cache(), z(1, 4, 64), i32(1), i32(1), z(1, 4, 64), stream=given)
+        fs.fs_verify_draft(z(1, 8), i32(2), i32(1), None, z(1), z(1), z(1), i32(1), i32(1),
+                           stream=given)
+        assert got == [(n, want) for n in ("fs_kv_q8_append", "fs_kv_q8_read", "fs_kv_q8_attention",
+                                           "fs_verify_draft")]
