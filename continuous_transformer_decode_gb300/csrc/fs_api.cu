@@ -278,11 +278,15 @@ struct fs_handle {
     prof_pending.push_back({cls, a, b, bytes});
   }
 
+  // A CUDA error that a call of this handle reports does not stay the thread's last
+  // error, where the next launch check, of any handle, would find it.
   int fail(int code, const std::string& msg) {
+    if (code == FS_ERR_OOM) cudaGetLastError();
     err = msg;
     return code;
   }
   int cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();
     err = std::string(what) + ": " + cudaGetErrorString(e);
     return FS_ERR_CUDA;
   }

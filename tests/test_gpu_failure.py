@@ -83,3 +83,20 @@ def test_canary_lane_is_untouched_by_other_lanes_work():
         assert fs.fs_device_error(h) == 0
     finally:
         fs.fs_destroy(h)
+
+
+def test_a_failed_create_is_not_another_handles_error():
+    """A handle of more pages than there is memory fails to be created; the next step
+    of another handle runs and is counted."""
+    cfg = synth.with_layers(synth.MODEL_S, 2)
+    W = synth.make_weights(cfg, seed=1, fmt="bf16")
+    h = U.make_gpu(cfg, W, fs.FS_DTYPE_BF16, max_lanes=2, max_pos=64)
+    try:
+        _logits(h, [0], [5], cfg["V"])
+        with pytest.raises(fs.FsError) as e:
+            U.make_gpu(cfg, W, fs.FS_DTYPE_BF16, max_lanes=2, max_pos=64, n_pages=1 << 30)
+        assert e.value.code == fs.CODES["FS_ERR_OOM"]
+        _logits(h, [0], [6], cfg["V"])
+        assert fs.fs_lane_length(h, 0) == 2
+    finally:
+        fs.fs_destroy(h)
