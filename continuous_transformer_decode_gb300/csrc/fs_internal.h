@@ -206,6 +206,19 @@ inline cudaError_t allow_smem(K kern, int smem, std::atomic<uint64_t>& done) {
   return e;
 }
 
+// What a launcher enqueued: its kernels, and the first error of its own calls (not
+// whatever an earlier call left as the thread's last one).
+struct Launched {
+  int kernels = 0;
+  cudaError_t error = cudaSuccess;
+  bool add(cudaError_t e) {  // one launch; false: it failed, and nothing may follow it
+    if (e == cudaSuccess) ++kernels;
+    else error = e;
+    return e == cudaSuccess;
+  }
+  operator int() const { return kernels; }
+};
+
 enum WType { W_F32 = 0, W_BF16 = 1, W_Q8 = 2 };
 enum XType { X_F32 = 0, X_BF16 = 1 };
 
@@ -519,14 +532,14 @@ bool kv_q8_supports(int hd);
 // n rows of k and v (x_type, row strides in elements) into the slots of
 // (lanes[i], positions[i]); rc / rs rotate the keys (null: as they are). traced: with
 // the trace marks of the step's kernels (f32 rows).
-int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
-                        int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
-                        const int32_t* positions, int n, const float* rc, const float* rs,
-                        int rope_len, cudaStream_t s);
+Launched launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
+                             int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
+                             const int32_t* positions, int n, const float* rc, const float* rs,
+                             int rope_len, cudaStream_t s);
 // The values of the same slots into k_out / v_out (either may be null).
-int launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
-                      void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, int x_type,
-                      cudaStream_t s);
+Launched launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
+                           void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                           int x_type, cudaStream_t s);
 struct AttnQ8 {
   KvQ8 kv;
   const void* q;      // [n] rows of [H][hd], q_stride elements apart
@@ -550,8 +563,8 @@ constexpr int kMaxQ8Splits = 8192;  // of a row: the join keeps a weight of each
 // Positions per split of one call (a multiple of 64).
 int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms);
 // q and out of one type; traced: f32 q, out of either type.
-int launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, int sms,
-                        cudaStream_t s);
+Launched launch_attention_q8(const AttnQ8& a, int q_type, int out_type, bool traced, int sms,
+                             cudaStream_t s);
 // fs_kv_q8 counterparts of launch_fill_random_kv and launch_kv_relocate, over the
 // layers of an arena (layer_rows rows each); a key that is turned back is quantised
 // anew (f32 quotients).
@@ -577,7 +590,7 @@ struct VerifyArgs {
   int32_t* n_accepted;
   int32_t* next_token;
 };
-int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
+Launched launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
 
 int launch_sample(const float* logits, int B, int V, const float* temps,
                   const uint64_t* seeds, const uint64_t* counters,

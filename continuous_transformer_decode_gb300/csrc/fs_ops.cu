@@ -97,10 +97,12 @@ const char* bad_rope(const float* c, const float* s, int32_t len) {
 // Blocks a grid may have along x is 2^31 - 1; rows and KV heads share it.
 bool grid_fits(int64_t n, int64_t heads) { return n * heads <= (int64_t)INT32_MAX; }
 
-int launched(int kernels) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return refuse(FS_ERR_CUDA, cudaGetErrorString(e));
-  return kernels > 0 ? FS_OK : refuse(FS_ERR_CUDA, "no kernel for this shape");
+int launched(const Launched& l) {
+  if (l.error != cudaSuccess) {
+    cudaGetLastError();  // reported here
+    return refuse(FS_ERR_CUDA, cudaGetErrorString(l.error));
+  }
+  return l.kernels > 0 ? FS_OK : refuse(FS_ERR_CUDA, "no kernel for this shape");
 }
 
 int device_sms() {

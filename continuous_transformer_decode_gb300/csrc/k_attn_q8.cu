@@ -586,23 +586,26 @@ __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
 }
 
 template <typename QT, typename OT, int HD, bool kTrace>
-int launch_hd(const AttnQ8& a, cudaStream_t s) {
+Launched launch_hd(const AttnQ8& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   auto kern = k_attn_q8<QT, OT, HD, kTrace>;
-  if (allow_smem(kern, Lay<HD>::kBytes, done) != cudaSuccess) return 0;
-  launch_k(kern, dim3(a.kv.Hkv, a.n, a.n_splits), Lay<HD>::kT, Lay<HD>::kBytes, s, a);
-  if (a.n_splits == 1) return 1;
-  launch_k(k_attn_q8_join<OT, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float), s, a);
-  return 2;
+  Launched l;
+  l.error = allow_smem(kern, Lay<HD>::kBytes, done);
+  if (l.error == cudaSuccess &&
+      l.add(launch_k(kern, dim3(a.kv.Hkv, a.n, a.n_splits), Lay<HD>::kT, Lay<HD>::kBytes, s, a)) &&
+      a.n_splits > 1)
+    l.add(launch_k(k_attn_q8_join<OT, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float),
+                   s, a));
+  return l;
 }
 
 template <typename QT, typename OT, bool kTrace>
-int dispatch(const AttnQ8& a, cudaStream_t s) {
+Launched dispatch(const AttnQ8& a, cudaStream_t s) {
   switch (a.kv.hd) {
     case 64: return launch_hd<QT, OT, 64, kTrace>(a, s);
     case 128: return launch_hd<QT, OT, 128, kTrace>(a, s);
     case 256: return launch_hd<QT, OT, 256, kTrace>(a, s);
-    default: return 0;
+    default: return {};
   }
 }
 
@@ -631,9 +634,9 @@ int attn_q8_split_len(int n, int Hkv, int hd, int max_len, int sms) {
   return (int)std::min<int64_t>(4096, std::max<int64_t>(256, (len + 127) / 128 * 128));
 }
 
-int launch_attention_q8(const AttnQ8& args, int q_type, int out_type, bool traced, int sms,
-                        cudaStream_t s) {
-  if (args.n <= 0) return 0;
+Launched launch_attention_q8(const AttnQ8& args, int q_type, int out_type, bool traced, int sms,
+                             cudaStream_t s) {
+  if (args.n <= 0) return {};
   AttnQ8 a = args;
   a.by_len = a.n <= kRankRows && a.max_len >= 2048 && a.split_len >= 2048 &&
              (int64_t)a.n * a.kv.Hkv >= 2 * places(a.kv.hd, sms);

@@ -459,9 +459,9 @@ bool rows_aligned(const void* p, int64_t stride, size_t es) {
 }
 
 template <typename T, int HD, bool kTrace>
-void append_hd(const KvQ8& c, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
-               const int32_t* lanes, const int32_t* positions, int n, const float* rc,
-               const float* rs, int rope_len, cudaStream_t s) {
+Launched append_hd(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
+                   int64_t v_stride, const int32_t* lanes, const int32_t* positions, int n,
+                   const float* rc, const float* rs, int rope_len, cudaStream_t s) {
   const unsigned items = (unsigned)((int64_t)n * c.Hkv);
   const bool vec = rows_aligned(k, k_stride, sizeof(T)) && rows_aligned(v, v_stride, sizeof(T)) &&
                    rows_aligned(rc, 4, 4) && rows_aligned(rs, 4, 4);
@@ -469,38 +469,41 @@ void append_hd(const KvQ8& c, const void* k, const void* v, int64_t k_stride, in
                         : k_kv_q8_append<T, HD, true, false, kTrace>)
                  : (vec ? k_kv_q8_append<T, HD, false, true, kTrace>
                         : k_kv_q8_append<T, HD, false, false, kTrace>);
-  launch_k(kern, dim3(blocks(items, HD)), kT, 0, s, c, static_cast<const T*>(k),
-           static_cast<const T*>(v), k_stride, v_stride, lanes, positions, items, rc, rs, rope_len);
+  Launched l;
+  l.add(launch_k(kern, dim3(blocks(items, HD)), kT, 0, s, c, static_cast<const T*>(k),
+                 static_cast<const T*>(v), k_stride, v_stride, lanes, positions, items, rc, rs,
+                 rope_len));
+  return l;
 }
 
 template <int HD, typename... A>
-int append_types(const KvQ8& c, int x_type, bool traced, A... a) {
-  if (x_type == X_BF16) append_hd<__nv_bfloat16, HD, false>(c, a...);
-  else if (traced) append_hd<float, HD, true>(c, a...);
-  else append_hd<float, HD, false>(c, a...);
-  return 1;
+Launched append_types(const KvQ8& c, int x_type, bool traced, A... a) {
+  if (x_type == X_BF16) return append_hd<__nv_bfloat16, HD, false>(c, a...);
+  return traced ? append_hd<float, HD, true>(c, a...) : append_hd<float, HD, false>(c, a...);
 }
 
 template <typename T, int HD>
-void read_hd(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n, void* k_out,
-             void* v_out, int64_t k_stride, int64_t v_stride, cudaStream_t s) {
+Launched read_hd(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n, void* k_out,
+                 void* v_out, int64_t k_stride, int64_t v_stride, cudaStream_t s) {
   const unsigned items = (unsigned)((int64_t)n * c.Hkv);
   const bool vec = (!k_out || rows_aligned(k_out, k_stride, sizeof(T))) &&
                    (!v_out || rows_aligned(v_out, v_stride, sizeof(T)));
   auto kern = vec ? k_kv_q8_read<T, HD, true> : k_kv_q8_read<T, HD, false>;
-  launch_k(kern, dim3(blocks(items, HD)), kT, 0, s, c, lanes, positions, items,
-           static_cast<T*>(k_out), static_cast<T*>(v_out), k_stride, v_stride);
+  Launched l;
+  l.add(launch_k(kern, dim3(blocks(items, HD)), kT, 0, s, c, lanes, positions, items,
+                 static_cast<T*>(k_out), static_cast<T*>(v_out), k_stride, v_stride));
+  return l;
 }
 
 }  // namespace
 
 bool kv_q8_supports(int hd) { return hd == 64 || hd == 128 || hd == 256; }
 
-int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
-                        int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
-                        const int32_t* positions, int n, const float* rc, const float* rs,
-                        int rope_len, cudaStream_t s) {
-  if (n <= 0) return 0;
+Launched launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_stride,
+                             int64_t v_stride, int x_type, bool traced, const int32_t* lanes,
+                             const int32_t* positions, int n, const float* rc, const float* rs,
+                             int rope_len, cudaStream_t s) {
+  if (n <= 0) return {};
   auto go = [&](auto hd) {
     return append_types<decltype(hd)::value>(c, x_type, traced, k, v, k_stride, v_stride, lanes,
                                              positions, n, rc, rs, rope_len, s);
@@ -508,25 +511,24 @@ int launch_kv_q8_append(const KvQ8& c, const void* k, const void* v, int64_t k_s
   return c.hd == 64    ? go(std::integral_constant<int, 64>())
          : c.hd == 128 ? go(std::integral_constant<int, 128>())
          : c.hd == 256 ? go(std::integral_constant<int, 256>())
-                       : 0;
+                       : Launched{};
 }
 
-int launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
-                      void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, int x_type,
-                      cudaStream_t s) {
-  if (n <= 0) return 0;
+Launched launch_kv_q8_read(const KvQ8& c, const int32_t* lanes, const int32_t* positions, int n,
+                           void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                           int x_type, cudaStream_t s) {
+  if (n <= 0) return {};
   auto go = [&](auto hd) {
     constexpr int HD = decltype(hd)::value;
-    if (x_type == X_BF16)
-      read_hd<__nv_bfloat16, HD>(c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s);
-    else
-      read_hd<float, HD>(c, lanes, positions, n, k_out, v_out, k_stride, v_stride, s);
-    return 1;
+    return x_type == X_BF16 ? read_hd<__nv_bfloat16, HD>(c, lanes, positions, n, k_out, v_out,
+                                                         k_stride, v_stride, s)
+                            : read_hd<float, HD>(c, lanes, positions, n, k_out, v_out, k_stride,
+                                                 v_stride, s);
   };
   return c.hd == 64    ? go(std::integral_constant<int, 64>())
          : c.hd == 128 ? go(std::integral_constant<int, 128>())
          : c.hd == 256 ? go(std::integral_constant<int, 256>())
-                       : 0;
+                       : Launched{};
 }
 
 int launch_fill_random_kv_q8(const KvQ8& c, int L, int64_t layer_rows, const int32_t* pages,

@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kT, 3) k_verify(VerifyArgs a, int held) {
 }
 
 template <int kC>
-int launch_c(const VerifyArgs& a, cudaStream_t s) {
+Launched launch_c(const VerifyArgs& a, cudaStream_t s) {
   constexpr int kT = 256, kW = kT / 32;
   constexpr int64_t kMost = 56 * 1024;  // shared memory of four blocks an SM
   const int64_t run = (a.V - 1) / (kC * kW * 128) * 128 + 128;
@@ -608,12 +608,14 @@ int launch_c(const VerifyArgs& a, cudaStream_t s) {
   const int held = smem <= kMost;
   if (!held) smem = 0;
   static std::atomic<uint64_t> done{0};
-  if (allow_smem(k_verify<kC, kT>, (int)kMost, done) != cudaSuccess) return 0;
+  Launched l;
+  l.error = allow_smem(k_verify<kC, kT>, (int)kMost, done);
+  if (l.error != cudaSuccess) return l;
   if constexpr (kC == 1)
-    launch_k(k_verify<1, kT>, dim3((unsigned)a.n_seqs), kT, smem, s, a, held);
+    l.add(launch_k(k_verify<1, kT>, dim3((unsigned)a.n_seqs), kT, smem, s, a, held));
   else
-    launch_k_cluster(k_verify<kC, kT>, dim3((unsigned)a.n_seqs * kC), kT, smem, s, kC, a, held);
-  return 1;
+    l.add(launch_k_cluster(k_verify<kC, kT>, dim3((unsigned)a.n_seqs * kC), kT, smem, s, kC, a, held));
+  return l;
 }
 
 }  // namespace
@@ -621,8 +623,8 @@ int launch_c(const VerifyArgs& a, cudaStream_t s) {
 // Blocks of a sequence: eight while all sequences' blocks fit the SMs four at a time,
 // else four (64 sequences: 35 us with eight, 58 with four; 256: 47 and 37), and no more
 // than give every warp 128 tokens.
-int launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
-  if (a.n_seqs <= 0) return 0;
+Launched launch_verify(const VerifyArgs& a, int sms, cudaStream_t s) {
+  if (a.n_seqs <= 0) return {};
   const int want = (int64_t)a.n_seqs * 8 <= 4 * (int64_t)sms ? 8 : 4;
   if (a.V > 4096 && want == 8) return launch_c<8>(a, s);
   if (a.V > 2048) return launch_c<4>(a, s);

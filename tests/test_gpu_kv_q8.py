@@ -554,3 +554,32 @@ def test_calls_without_a_stream_run_on_torchs_current_one():
         step()
     g.replay()
     look()
+
+
+def test_a_failure_of_another_call_is_not_reported_as_this_ones():
+    """An allocation that failed before (a handle of more pages than there is
+    memory) leaves CUDA's last error set: the operators report their own launches."""
+    import torch
+    from continuous_transformer_decode_gb300 import synth
+    from tests import _gpu_util as U
+    cfg = dict(name="stale", L=1, d=64, H=1, Hkv=1, hd=64, F=64, V=64, rms_eps=1e-5, rope_theta=1e4,
+               tied=True)
+    W = synth.make_weights(cfg, seed=1, fmt="f32")
+    rng = np.random.default_rng(14)
+    pg = Pages(rng, [200], 1, 64, 16)
+    x = _cuda(rng.standard_normal((1, 1, 64)).astype(np.float32))
+    at = _cuda(np.int32([0])), _cuda(np.int32([7]))
+    out = torch.zeros_like(x)
+    z, one = torch.zeros(1, 8, device="cuda"), torch.zeros(1, device="cuda")
+    acc, nxt = (torch.full((1,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    calls = [
+        lambda: fs.fs_kv_q8_append(pg.view, x, x, *at),
+        lambda: fs.fs_kv_q8_read(pg.view, *at, out),
+        lambda: _attend(pg, x, [0], [200], split_len=64),
+        lambda: fs.fs_verify_draft(z, _cuda(np.int32([0, 1])), at[0], None, one, one, one, acc, nxt)]
+    for call in calls:
+        with pytest.raises(fs.FsError) as e:
+            U.make_gpu(cfg, W, fs.FS_DTYPE_F32, max_lanes=1, n_pages=1 << 30)  # 2 TB a side
+        assert e.value.code == fs.CODES["FS_ERR_OOM"]
+        call()
+    torch.cuda.synchronize()
