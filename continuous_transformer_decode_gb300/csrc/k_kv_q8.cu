@@ -62,15 +62,22 @@ __device__ __forceinline__ void store4(float* p, const float x[4]) {
     for (int j = 0; j < 4; ++j) p[j] = x[j];
   }
 }
+// Two values as bf16, those past its range as its largest: the largest f32, which
+// stands for a stored infinity, is past it.
+__device__ __forceinline__ uint32_t finite_bf16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
 template <bool kVec>
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float x[4]) {
+  const uint32_t a = finite_bf16x2(x[0], x[1]), b = finite_bf16x2(x[2], x[3]);
   if constexpr (kVec) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
+    *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = __float2bfloat16_rn(x[j]);
+    for (int j = 0; j < 4; ++j)
+      p[j] = __ushort_as_bfloat16((unsigned short)((j < 2 ? a : b) >> (16 * (j & 1))));
   }
 }
 

@@ -516,7 +516,8 @@ int fs_kv_q8_append(const fs_kv_q8* cache, const void* k, const void* v, int64_t
 
 /* Reads n tokens back: the values of token positions[i] of lane lanes[i] into
  * row i of k_out and v_out (either may be NULL; strides and dtype as for
- * fs_kv_q8_append, one rounding of code * scale to f32 and one more to bf16).
+ * fs_kv_q8_append, one rounding of code * scale to f32 and one more to the
+ * nearest finite bf16: a stored infinity reads as the type's largest value).
  * A token that the cache cannot hold reads as zeros. */
 int fs_kv_q8_read(const fs_kv_q8* cache, const int32_t* lanes, const int32_t* positions,
                   int32_t n, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,

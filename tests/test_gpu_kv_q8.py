@@ -583,3 +583,27 @@ def test_a_failure_of_another_call_is_not_reported_as_this_ones():
         assert e.value.code == fs.CODES["FS_ERR_OOM"]
         call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_infinities_read_back_finite_in_bf16(odd):
+    """A bf16 read rounds to the nearest finite bf16: a stored infinity (the largest
+    f32) does not come back infinite. Rows at odd addresses take the scalar stores."""
+    import torch
+    rng = np.random.default_rng(7)
+    pg = Pages(rng, [4], 2, 64, 4)
+    x = rng.standard_normal((4, 2, 64)).astype(np.float32)
+    x[0, 0, 3], x[1, 1, 63], x[2, 0, 0], x[2, 1, 1] = np.inf, -np.inf, 3.4e38, -3.39e38
+    at = _cuda(np.zeros(4, np.int32)), _cuda(np.arange(4, dtype=np.int32))
+    fs.fs_kv_q8_append(pg.view, _cuda(x), -_cuda(x), *at)
+    big = float(torch.finfo(torch.bfloat16).max)
+    outs = [torch.zeros(4, 2 * 64 + 1, dtype=torch.bfloat16, device="cuda")[:, odd:odd + 128]
+            .unflatten(1, (2, 64)) for _ in range(2)]
+    fs.fs_kv_q8_read(pg.view, *at, *outs)
+    full = [torch.zeros(4, 2, 64, device="cuda") for _ in range(2)]
+    fs.fs_kv_q8_read(pg.view, *at, *full)
+    torch.cuda.synchronize()
+    for o, f in zip(outs, full):
+        want = np.clip(R.bf16(np.clip(f.cpu().numpy(), -big, big)), -big, big)
+        assert np.array_equal(o.float().cpu().numpy(), want)
+        assert (np.abs(want) == big).sum() == 4
