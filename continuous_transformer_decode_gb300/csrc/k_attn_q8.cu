@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(Lay<HD>::kT, Lay<HD>::kBlocks) k_attn_q8(AttnQ
 // HD / 4 columns of threads by kJ, column x taking splits x, x + kJ, .. in
 // order, and the kJ sums in order.
 constexpr int kJ = 8;
-template <typename OT, int HD>
+template <typename OT, int HD, bool kTrace>
 __global__ void __launch_bounds__(HD / 4 * kJ) k_attn_q8_join(AttnQ8 a) {
-  TraceScope tr(g_trace, TR_ATTN_Q8_JOIN);
+  TraceScope tr(kTrace ? g_trace : nullptr, TR_ATTN_Q8_JOIN);
   constexpr int kT = HD / 4 * kJ;
   __shared__ float4 part[kJ][HD / 4];
   __shared__ float red[2][kT / 32];
@@ -594,7 +594,7 @@ Launched launch_hd(const AttnQ8& a, cudaStream_t s) {
   if (l.error == cudaSuccess &&
       l.add(launch_k(kern, dim3(a.kv.Hkv, a.n, a.n_splits), Lay<HD>::kT, Lay<HD>::kBytes, s, a)) &&
       a.n_splits > 1)
-    l.add(launch_k(k_attn_q8_join<OT, HD>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float),
+    l.add(launch_k(k_attn_q8_join<OT, HD, kTrace>, dim3(a.H, a.n), HD / 4 * kJ, a.n_splits * sizeof(float),
                    s, a));
   return l;
 }

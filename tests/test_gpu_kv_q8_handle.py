@@ -268,3 +268,21 @@ def test_refused_shapes():
     W = synth.make_weights(cfg, seed=1, fmt="f32")
     with pytest.raises(fs.FsError):
         U.make_gpu(cfg, W, fs.FS_DTYPE_F32, Q8, max_lanes=2, max_pos=64)
+
+
+def test_operators_leave_no_marks_in_a_handles_trace():
+    """The trace holds the handle's steps: a call on the caller's own cache, whatever
+    its stream, neither fills it nor holds its buffer."""
+    from tests.test_gpu_kv_q8 import Pages, _attend, _cuda
+    h = U.make_gpu(SMALL, synth.make_weights(SMALL, seed=1, fmt="f32"), fs.FS_DTYPE_F32, Q8,
+                   max_lanes=2, max_pos=64)
+    rng = np.random.default_rng(13)
+    pg = Pages(rng, [300], 2, 64, 16)
+    q = rng.standard_normal((1, 4, 64)).astype(np.float32)
+    try:
+        fs.fs_trace_enable(h, 1 << 12)
+        _attend(pg, _cuda(q), [0], [300], split_len=64)   # split, so joined too
+        recs, n = fs.fs_trace_read(h)
+        assert n == 0 and len(recs) == 0
+    finally:
+        fs.fs_destroy(h)
