@@ -581,7 +581,9 @@ def _rope_args(rope, hd: int):
     if rope is None:
         return None, None, 0
     cos, sin = rope
-    n = cos.numel() // (hd // 2)
+    n = cos.shape[0] if cos.dim() == 2 else 0
+    if cos.shape != (n, hd // 2) or sin.shape != cos.shape:
+        _refuse(f"rope: two tables [rope_len, {hd // 2}] are needed")
     return (_vec(cos, n * (hd // 2), _Types.f32, "rope cos"),
             _vec(sin, n * (hd // 2), _Types.f32, "rope sin"), n)
 

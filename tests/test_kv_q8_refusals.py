@@ -194,3 +194,17 @@ def test_no_stream_is_torchs_current_stream(monkeypatch):
                            stream=given)
         assert got == [(n, want) for n in ("fs_kv_q8_append", "fs_kv_q8_read", "fs_kv_q8_attention",
                                            "fs_verify_draft")]
+
+
+@pytest.mark.parametrize("shape", [(10, 64), (5, 64), (10, 16), (320,), (1, 10, 32)])
+def test_rotation_tables_of_another_shape(shape):
+    """Tables are [rope_len, head_dim / 2]: ones of the whole head_dim would be read as
+    twice as many positions of the wrong angles."""
+    import torch
+    t = torch.zeros(shape)
+    one = torch.zeros(1, dtype=torch.int32)
+    x = torch.zeros(1, 2, 64)
+    for call in (lambda: fs.fs_kv_q8_append(cache(), x, x, one, one, rope=(t, t)),
+                 lambda: fs.fs_kv_q8_attention(cache(), x, one, one, x, rope=(t, t))):
+        with pytest.raises(fs.FsError, match="rope"):
+            call()
