@@ -254,8 +254,6 @@ struct KV {
   int max_pages = 0;
 };
 
-// 8-bit paged KV cache (fs_kv_q8 of include/fs.h): a row is one token's key or
-// value of one KV head, hd codes (byte = code + 128) and one f32 scale.
 // n / d for 0 <= n < 2^31 by a multiplication: with 2^s >= d and
 // m = floor(2^(31 + s) / d) + 1, m d - 2^(31 + s) <= 2^s, so floor(n m / 2^(31 + s))
 // is the quotient.
@@ -272,6 +270,8 @@ struct FastDiv {
   }
 };
 
+// 8-bit paged KV cache (fs_kv_q8 of include/fs.h): a row is one token's key or
+// value of one KV head, hd codes (byte = code + 128) and one f32 scale.
 struct KvQ8 {
   uint8_t* k = nullptr;  // [n_pages][Hkv][page_size][hd]
   uint8_t* v = nullptr;

@@ -172,7 +172,8 @@ int fs_lane_clone(fs_handle* h, int32_t src, int32_t dst);
  * the lane writes (from the one holding `start` on) that another lane still
  * holds are first replaced by private copies (lowest free index); pages
  * past the new end are let go. An 8-bit key that is rotated back is quantised
- * anew, one more rounding of half a code. Enqueued on the handle's stream.
+ * anew, one more rounding of half a code; this quotient is f32, so within 1e-4
+ * of the border of two codes it may take either. Enqueued on the handle's stream.
  * Errors: FS_ERR_LANE, FS_ERR_ARG (not 0 <= start <= end <= length),
  * FS_ERR_KV_FULL (too few free pages for the copies); nothing changes on
  * error. */
@@ -508,7 +509,8 @@ typedef struct fs_kv_q8 {
  * is skipped, so -1 pads a batch. Two rows of one call must not name the same
  * token: which of them the slot then holds is not specified (it may mix the
  * two). A code is exact: the rounding of the real quotient, also next to a
- * border. */
+ * border. The scale is one rounding of amax / 127; a rotated key's amax is that
+ * of its f32 values, three roundings each. */
 int fs_kv_q8_append(const fs_kv_q8* cache, const void* k, const void* v, int64_t k_stride,
                     int64_t v_stride, int32_t dtype, const int32_t* lanes,
                     const int32_t* positions, int32_t n, const float* rope_cos,
@@ -537,17 +539,20 @@ int64_t fs_kv_q8_attention_workspace(const fs_kv_q8* cache, int32_t n, int32_t n
  * multiplies the scores (usually 1 / sqrt(head_dim)). With rope_cos / rope_sin
  * q is rotated by position lengths[i] - 1 (the token it belongs to). max_len is
  * an upper bound of the lengths, which sizes the launch (0: max_pages *
- * page_size; at most rope_len when q is rotated): a longer row attends to its
- * first max_len tokens. A row of length 0 (or less), or whose tokens the cache
- * does not hold, gives zeros. Several rows may name one lane (the rows of a
- * drafted continuation, each with its own length).
+ * page_size; at most rope_len when q is rotated): a longer row is taken as one of
+ * max_len tokens, in what it attends to and in the rotation of its q. A row of
+ * length 0 (or less), or whose tokens the cache does not hold, gives zeros.
+ * Several rows may name one lane (the rows of a drafted continuation, each with
+ * its own length).
  *
  * Long rows are cut into splits of split_len tokens (a multiple of 64; at most
- * 8192 splits), joined in a fixed order; 0 chooses from n, n_kv_heads and max_len. A row's bits
- * depend on its own inputs and split_len alone: give split_len for results
- * that do not depend on the batch. Scores, softmax sums and outputs are held
- * in f32; the result is rounded once. A head whose q is not finite gives NaN and
- * leaves the others alone. workspace (16-byte aligned) may be NULL
+ * 8192 splits), joined in a fixed order; 0 chooses from n, n_kv_heads, head_dim,
+ * max_len and the device. A row's bits depend on its own inputs and split_len
+ * alone: give split_len for results that do not depend on the batch. Scores,
+ * softmax sums, partial results and outputs are held in f32; q and the weights
+ * enter the products as two f16 parts each, 22 bits (weights to fewer where the
+ * scales of all values are below 2^-97); the result is rounded once. A head
+ * whose q is not finite gives NaN and leaves the others alone. workspace (16-byte aligned) may be NULL
  * when fs_kv_q8_attention_workspace says 0, is needed only during the call's
  * own kernels and starts with any content; calls that may run at the same time
  * (other streams, other captured graphs) need one each. */

@@ -607,3 +607,17 @@ def test_infinities_read_back_finite_in_bf16(odd):
         want = np.clip(R.bf16(np.clip(f.cpu().numpy(), -big, big)), -big, big)
         assert np.array_equal(o.float().cpu().numpy(), want)
         assert (np.abs(want) == big).sum() == 4
+
+
+@pytest.mark.parametrize("split", [64, 4096])
+def test_a_row_longer_than_max_len_is_a_row_of_max_len(split):
+    """Its tokens and the position that rotates its q."""
+    import torch
+    rng = np.random.default_rng(15)
+    pg = Pages(rng, [300], 2, 128, 16)
+    q = _cuda(rng.standard_normal((3, 4, 128)).astype(np.float32))
+    tables = R.rope_tables(400, 128)
+    rope = tuple(_cuda(a) for a in tables)
+    got = _attend(pg, q, [0] * 3, [150, 299, 10000], rope=rope, max_len=150, split_len=split)
+    ref, tol = R.attention(pg.ref(), q.cpu().numpy(), [0] * 3, [150] * 3, 128 ** -0.5, tables)
+    _check_attention(got, ref, tol)
