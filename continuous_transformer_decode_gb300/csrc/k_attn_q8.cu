@@ -167,10 +167,13 @@ __device__ __forceinline__ int row_len(const AttnQ8& a, int i) {
 // The row whose length is the rank-th largest (ties: the lower row first), found by
 // every block for itself: blocks start in about the order of their indexes, so the
 // long rows start first and the SMs finish together: 128 lanes of 128 to 4096 tokens
-// take 92 us instead of 108. It costs a block one to three microseconds, so it is for
-// launches of at least two blocks a place whose blocks may be long (256 lanes of up
-// to 512 tokens would take 19 us instead of 13).
-constexpr int kRankRows = 256;  // most rows that this is done for
+// take 94 us instead of 108, 192 lanes 142 instead of 144. Comparing all rows costs a
+// block one to three microseconds and more with more rows (256 lanes would take 190
+// instead of 185), so it is for at most 192 rows, in launches of at least two blocks a
+// place whose blocks may be long (256 lanes of up to 512 tokens would take 19 us instead
+// of 13). max_len stands for the lengths, which the host does not know: 128 rows of 200
+// tokens under a max_len of 4096 pay for nothing, 27 us instead of 23.
+constexpr int kRankRows = 192;  // most rows that this is done for
 template <int kT>
 __device__ __forceinline__ int row_of_rank(const AttnQ8& a, int rank, uint8_t* smem) {
   // keys that differ: the length (up to 2^22), then the row
