@@ -626,34 +626,34 @@ int create_impl(fs_handle* h, const fs_weights* W) {
     const bool force_mma = e && std::string(e) == "mma";
     const bool force_warp = e && std::string(e) == "warp";
     if (!h->kv_q8) {
-    h->attn_mma = attn_mma_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, h->split_len,
-                                    h->max_splits);
-    // the TMA kernel's producer warp and barrier set-up pay off on long
-    // contexts; a handle whose lanes stay short keeps the cp.async kernel
-    h->attn_tma = !force_mma && d.max_pos > 256 &&
-                  attn_tma_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, d.page_size,
-                                    h->split_len, h->max_splits);
-    if (h->attn_tma) {
-      const int64_t rows = (int64_t)d.n_layers * (h->kv.layer_stride / d.head_dim);
-      if (attn_tma_make_map(h->kv.k, rows, d.head_dim, d.page_size, &h->tm_kv_k) ||
-          attn_tma_make_map(h->kv.v, rows, d.head_dim, d.page_size, &h->tm_kv_v))
-        h->attn_tma = false;  // arena too large for 32-bit rows: the cp.async kernel serves
-    }
-    // lanes of at most 64 positions: one warp per (lane, KV head), the
-    // cp.async kernel's bits. It holds ten pairs an SM against the cp.async
-    // kernel's six of four warps each, so it pays once a call fills the SMs
-    // ten times over (SmolLM2 shape: 8.0 vs 5.8 us per layer at 256 lanes,
-    // faster at 960); smaller calls keep the cp.async kernel.
-    h->attn_warp = !force_mma && h->attn_mma &&
-                   attn_warp_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, d.max_pos);
-    h->attn_warp_rows = force_warp ? 0 : (10 * h->sms + d.n_kv_heads - 1) / d.n_kv_heads;
-    // f32 KV and head dims below 64: the tiled kernel
-    h->attn_tiled = !h->attn_tma && !h->attn_mma &&
-                    attn_tiled_supports(d.head_dim, h->G, d.page_size, h->split_len);
-    if (!h->attn_tma && !h->attn_mma && !h->attn_tiled)
-      return h->fail(FS_ERR_ARG,
-                     "no attention kernel for this shape: head_dim must be 16, 32, 64, 128 or "
-                     "256, and page_size 16, 32 or 64 for f32 KV or head_dim < 64");
+      h->attn_mma = attn_mma_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, h->split_len,
+                                      h->max_splits);
+      // the TMA kernel's producer warp and barrier set-up pay off on long
+      // contexts; a handle whose lanes stay short keeps the cp.async kernel
+      h->attn_tma = !force_mma && d.max_pos > 256 &&
+                    attn_tma_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, d.page_size,
+                                      h->split_len, h->max_splits);
+      if (h->attn_tma) {
+        const int64_t rows = (int64_t)d.n_layers * (h->kv.layer_stride / d.head_dim);
+        if (attn_tma_make_map(h->kv.k, rows, d.head_dim, d.page_size, &h->tm_kv_k) ||
+            attn_tma_make_map(h->kv.v, rows, d.head_dim, d.page_size, &h->tm_kv_v))
+          h->attn_tma = false;  // arena too large for 32-bit rows: the cp.async kernel serves
+      }
+      // lanes of at most 64 positions: one warp per (lane, KV head), the
+      // cp.async kernel's bits. It holds ten pairs an SM against the cp.async
+      // kernel's six of four warps each, so it pays once a call fills the SMs
+      // ten times over (SmolLM2 shape: 8.0 vs 5.8 us per layer at 256 lanes,
+      // faster at 960); smaller calls keep the cp.async kernel.
+      h->attn_warp = !force_mma && h->attn_mma &&
+                     attn_warp_supports(d.head_dim, h->G, d.kv_dtype == FS_DTYPE_F32, d.max_pos);
+      h->attn_warp_rows = force_warp ? 0 : (10 * h->sms + d.n_kv_heads - 1) / d.n_kv_heads;
+      // f32 KV and head dims below 64: the tiled kernel
+      h->attn_tiled = !h->attn_tma && !h->attn_mma &&
+                      attn_tiled_supports(d.head_dim, h->G, d.page_size, h->split_len);
+      if (!h->attn_tma && !h->attn_mma && !h->attn_tiled)
+        return h->fail(FS_ERR_ARG,
+                       "no attention kernel for this shape: head_dim must be 16, 32, 64, 128 or "
+                       "256, and page_size 16, 32 or 64 for f32 KV or head_dim < 64");
     }
   }
   FS_CK(h, cudaMemset(h->hpanel, 0, (size_t)(1 + h->act_split) * B * h->Kp_d * xs));
@@ -939,34 +939,34 @@ void enqueue_step(fs_handle* h, int n, float* out, double kv_read, bool chunked,
       h->launch(FS_PROF_ATTN, kv_read + (double)n * h->Nq * (4.0 + xs),
                 [&] { return launch_attention_q8(a, X_F32, h->xtype, true, h->sms, s); });
     } else {
-    // a chunked step first appends every row's k, v (rows of one lane at
-    // consecutive positions see each other's keys); the MMA attention kernels
-    // then only read, the other kernels give way to the three-kernel path
-    if (chunked)
-      h->launch(FS_PROF_OTHER, (double)n * (h->Nqkv * 4.0 + h->Nq * 4.0 + 2.0 * h->Nkv * kvs),
-                [&] {
-                  return launch_rope_append(h->qkv, n, d.n_heads, d.n_kv_heads, d.head_dim,
-                                            h->rope_cos, h->rope_sin, args, h->kv, l, h->q, s);
-                });
-    {
-      AttnParams ap{};
-      ap.kv_written = chunked ? 1 : 0;
-      ap.qkv = h->qkv; ap.H = d.n_heads; ap.rc = h->rope_cos; ap.rs = h->rope_sin;
-      ap.args = args; ap.kv = h->kv; ap.layer = l; ap.split_len = h->split_len;
-      ap.max_splits = h->max_splits; ap.part_ml = h->part_ml; ap.part_acc = h->part_acc;
-      ap.counters = h->attn_counters; ap.o = h->opanel; ap.ld_o = h->Kp_q; ap.err = h->d_err_flag;
-      ap.o_lo = h->lo_o;
-      h->launch(FS_PROF_ATTN,
-                kv_read + (double)n * (h->Nqkv * 4.0 + h->Nq * xs + 2.0 * h->Nkv * kvs),
-                [&] {
-                  if (h->attn_warp && n >= h->attn_warp_rows)
-                    return launch_attention_warp(ap, n, h->xtype, s);
-                  if (h->attn_tma)
-                    return launch_attention_tma(h->tm_kv_k, h->tm_kv_v, ap, n, h->xtype, s);
-                  return h->attn_mma ? launch_attention_mma(ap, n, h->xtype, s)
-                                     : launch_attention_tiled(ap, n, h->xtype, s);
-                });
-    }
+      // a chunked step first appends every row's k, v (rows of one lane at
+      // consecutive positions see each other's keys); the MMA attention kernels
+      // then only read, the other kernels give way to the three-kernel path
+      if (chunked)
+        h->launch(FS_PROF_OTHER, (double)n * (h->Nqkv * 4.0 + h->Nq * 4.0 + 2.0 * h->Nkv * kvs),
+                  [&] {
+                    return launch_rope_append(h->qkv, n, d.n_heads, d.n_kv_heads, d.head_dim,
+                                              h->rope_cos, h->rope_sin, args, h->kv, l, h->q, s);
+                  });
+      {
+        AttnParams ap{};
+        ap.kv_written = chunked ? 1 : 0;
+        ap.qkv = h->qkv; ap.H = d.n_heads; ap.rc = h->rope_cos; ap.rs = h->rope_sin;
+        ap.args = args; ap.kv = h->kv; ap.layer = l; ap.split_len = h->split_len;
+        ap.max_splits = h->max_splits; ap.part_ml = h->part_ml; ap.part_acc = h->part_acc;
+        ap.counters = h->attn_counters; ap.o = h->opanel; ap.ld_o = h->Kp_q; ap.err = h->d_err_flag;
+        ap.o_lo = h->lo_o;
+        h->launch(FS_PROF_ATTN,
+                  kv_read + (double)n * (h->Nqkv * 4.0 + h->Nq * xs + 2.0 * h->Nkv * kvs),
+                  [&] {
+                    if (h->attn_warp && n >= h->attn_warp_rows)
+                      return launch_attention_warp(ap, n, h->xtype, s);
+                    if (h->attn_tma)
+                      return launch_attention_tma(h->tm_kv_k, h->tm_kv_v, ap, n, h->xtype, s);
+                    return h->attn_mma ? launch_attention_mma(ap, n, h->xtype, s)
+                                       : launch_attention_tiled(ap, n, h->xtype, s);
+                  });
+      }
     }
     gemm(W.o, W.o_tc, h->opanel, h->lo_o, EPI_STORE, h->y, nullptr, d.d_model,
          d.d_model);
