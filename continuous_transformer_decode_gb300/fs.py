@@ -582,7 +582,7 @@ def _rope_args(rope, hd: int):
         return None, None, 0
     cos, sin = rope
     n = cos.shape[0] if cos.dim() == 2 else 0
-    if cos.shape != (n, hd // 2) or sin.shape != cos.shape:
+    if n < 1 or cos.shape != (n, hd // 2) or sin.shape != cos.shape:
         _refuse(f"rope: two tables [rope_len, {hd // 2}] are needed")
     return (_vec(cos, n * (hd // 2), _Types.f32, "rope cos"),
             _vec(sin, n * (hd // 2), _Types.f32, "rope sin"), n)

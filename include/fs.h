@@ -471,8 +471,8 @@ int fs_gemm_bf16_noalloc(const uint16_t* W, int32_t N, int32_t K,
  *   scale = amax / 127, code = round(x * 127 / amax), ties to even,
  *   amax = max |x| of the row (0: scale 0 and codes 0),
  * stored as the byte code + 128 (1 .. 255). A value stands for code * scale,
- * off by at most scale / 2. A NaN is stored as 0, an infinity as the largest
- * finite f32. Token t of a lane is in slot t % page_size of its page
+ * off by at most scale / 2 and its share of the scale's own rounding (2^-24, more
+ * in rows below 2^-119). A NaN is stored as 0, an infinity as the largest finite f32. Token t of a lane is in slot t % page_size of its page
  * t / page_size. A lane outside [0, n_lanes), a token outside
  * [0, max_pages * page_size) and a page-table entry outside [0, n_pages) hold
  * nothing: they are never written, read as zeros, and get no weight.

@@ -196,10 +196,11 @@ def test_no_stream_is_torchs_current_stream(monkeypatch):
                                            "fs_verify_draft")]
 
 
-@pytest.mark.parametrize("shape", [(10, 64), (5, 64), (10, 16), (320,), (1, 10, 32)])
+@pytest.mark.parametrize("shape", [(10, 64), (5, 64), (10, 16), (320,), (1, 10, 32), (0, 32)])
 def test_rotation_tables_of_another_shape(shape):
     """Tables are [rope_len, head_dim / 2]: ones of the whole head_dim would be read as
-    twice as many positions of the wrong angles."""
+    twice as many positions of the wrong angles, empty ones (which have no address) as
+    no rotation."""
     import torch
     t = torch.zeros(shape)
     one = torch.zeros(1, dtype=torch.int32)
