@@ -485,7 +485,8 @@ int fs_gemm_bf16_noalloc(const uint16_t* W, int32_t N, int32_t K,
  * to their element type.
  * Errors of these calls, with nothing enqueued: FS_ERR_ARG (a NULL pointer, a
  * size, a type, an alignment, memory of another device or of the host),
- * FS_ERR_SCRATCH (workspace too small); FS_ERR_CUDA (a launch failed). */
+ * FS_ERR_SCRATCH (workspace too small); FS_ERR_CUDA (a launch failed: of an
+ * attention over splits the first of two may have run, on its workspace). */
 typedef struct fs_kv_q8 {
   uint8_t* k;       /* codes [n_pages][n_kv_heads][page_size][head_dim]       */
   uint8_t* v;
