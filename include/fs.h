@@ -588,7 +588,7 @@ int fs_kv_q8_attention(const fs_kv_q8* cache, const void* q, int64_t q_stride,
  * accepted. Random numbers are in [0, 1); T is held in [1e-30, 1e30]. What is
  * decided in f32 is clear of its border by more than f32 may be off; the rest is
  * decided from weights held to a relative 2^-36 and summed in pairs of f32
- * numbers. Weights below 2^-125 of the largest are 0.
+ * numbers. A weight below 2^-126 of the largest is 0, one below 2^-125 may be.
  * Writes n_accepted[s] and next_token[s]; a sequence without rows gets 0
  * and -1. row_start has n_seqs + 1 ascending entries in [0, n_rows] (others are
  * clamped). Pointers, stream and errors as for fs_kv_q8_append. */
