@@ -592,6 +592,74 @@ struct VerifyArgs {
 };
 Launched launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
 
+// ---- what differs from request to request (k_pages.cu, k_rope.cu, k_lora.cu,
+// k_sample_filtered.cu); arguments as in include/fs.h
+constexpr int kMaxPageLanes = 16384;  // their sums lie in shared memory
+struct PagesArgs {
+  int32_t* holders;
+  int32_t* table;
+  int32_t* lengths;
+  const int32_t* keep;  // null: all
+  const int32_t* grow;
+  int n_pages, n_lanes, max_pages, page_size;
+  FastDiv by_page;
+  int32_t* row_start;
+  int32_t* row_lane;
+  int32_t* row_position;
+  int32_t* row_length;
+  int64_t* row_slot;
+  int max_rows;
+  int32_t* status;
+  int code_full, code_rows;
+};
+Launched launch_pages(const PagesArgs& a, cudaStream_t s);
+
+constexpr int kMaxRotary = 512;
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, qo_stride, ko_stride;
+  const int32_t* positions;
+  int n, H, Hkv, hd, rot;
+  float factor;
+  bool inverse;
+  int units, per, groups;      // set by the launcher
+  uint64_t F[kMaxRotary / 2];  // 2^64ths of a turn a position
+};
+Launched launch_rope(const RopeArgs& a, int x_type, bool near, cudaStream_t s);
+
+struct LoraArgs {
+  const void* x;
+  int64_t x_stride;
+  const int32_t* adapter;
+  int n, K, N;
+  const __nv_bfloat16* A;
+  const __nv_bfloat16* B;
+  const float* scale;
+  int n_adapters, rank;
+  const void* base;  // null: 0
+  int64_t base_stride;
+  void* out;
+  int64_t out_stride;
+};
+Launched launch_lora(const LoraArgs& a, int x_type, int y_type, int sms, cudaStream_t s);
+
+struct FilteredArgs {
+  const float* logits;
+  int64_t ld;
+  int n, V;
+  const float* temps;
+  const int32_t* top_k;  // null: all
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int32_t* tokens;
+  int32_t* kept;         // null: not wanted
+};
+Launched launch_sample_filtered(const FilteredArgs& a, int sms, cudaStream_t s);
+
 int launch_sample(const float* logits, int B, int V, const float* temps,
                   const uint64_t* seeds, const uint64_t* counters,
                   int32_t* out, cudaStream_t s);

@@ -1,0 +1,171 @@
+// Rotary positions of queries and keys (fs_rope): pair (x, y) of a head turned by the
+// angle a = position * frequency, to factor * (x cos a - y sin a, y cos a + x sin a).
+//
+// Angles. A frequency is held as a 64-bit fraction of a turn a position, F = f / (2 pi) *
+// 2^64; position * F modulo 2^64 is the angle's fraction of a turn, exact but for F's
+// rounding (position * 2^-65 turns), whatever the position: whole turns drop out of the
+// integer product. (f64 would cost more than the rows' bytes do: its rate here is 1/60 of
+// f32's.) The signed top 24 bits give sine and cosine by sincospi, the next 24 turn them
+// by a first-order step, as their angle is below 2^-22.
+//
+// One pass over the bytes: a thread has one vector of pairs of a row, computes their sines
+// and cosines once and takes several heads by them.
+#include "fs_internal.h"
+
+namespace fsk {
+namespace {
+
+template <int kBytes>
+struct VecOf;
+template <>
+struct VecOf<16> { using T = uint4; };
+template <>
+struct VecOf<4> { using T = uint32_t; };
+template <>
+struct VecOf<2> { using T = uint16_t; };
+
+// kN consecutive values of T in vectors of kBytes.
+template <typename T, int kN, int kBytes>
+struct Vals {
+  using V = typename VecOf<kBytes>::T;
+  static constexpr int kV = kN * (int)sizeof(T) / kBytes;
+  V v[kV];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = reinterpret_cast<const V*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) reinterpret_cast<V*>(p)[i] = v[i];
+  }
+  __device__ __forceinline__ float get(int i) const {
+    const T x = reinterpret_cast<const T*>(v)[i];
+    if constexpr (sizeof(T) == 4) return x;
+    else return __bfloat162float(x);
+  }
+  __device__ __forceinline__ void set(int i, float x) {
+    T* p = reinterpret_cast<T*>(v);
+    if constexpr (sizeof(T) == 4) p[i] = x;
+    else p[i] = __float2bfloat16_rn(x);
+  }
+};
+
+// (cos, sin) of pos * F turns, times m.
+__device__ __forceinline__ float2 turn(uint32_t pos, uint64_t F, float m, bool inverse) {
+  const uint64_t r = (uint64_t)pos * F;
+  const int top = (int)(r >> 32) >> 8;               // of 2^-24 turns, signed
+  const float rest = (float)((uint32_t)(r >> 16) & 0xffffffu);  // of 2^-48 turns
+  float s, c;
+  sincospif((float)top * 0x1p-23f, &s, &c);
+  const float d = rest * (6.2831855f * 0x1p-48f);
+  const float s1 = fmaf(c, d, s), c1 = fmaf(-s, d, c);
+  return make_float2(c1 * m, (inverse ? -s1 : s1) * m);
+}
+
+// kNear: pairs of neighbours, else of halves. A unit is kP pairs of a head, or 2 kP
+// values behind the turned ones, which are copied.
+template <typename T, int kBytes, bool kNear>
+__global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
+  constexpr int kP = kNear ? (kBytes / (2 * (int)sizeof(T)) > 0 ? kBytes / (2 * (int)sizeof(T)) : 1)
+                           : kBytes / (int)sizeof(T);
+  pdl_wait();
+  pdl_trigger();
+  const int half = a.rot / 2, turned = half / kP;
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t item = t / a.units;  // (row, group of heads)
+  const int unit = (int)(t - item * a.units);
+  const int row = (int)(item / a.groups), group = (int)(item - (int64_t)row * a.groups);
+  if (row >= a.n) return;
+  const int pos = a.positions[row];
+  if (pos < 0) return;
+  const int H = a.H + a.Hkv;
+  const int h0 = group * a.per, h1 = min(H, h0 + a.per);
+  auto in = [&](int h) {
+    return h < a.H ? static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)h * a.hd
+                   : static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)(h - a.H) * a.hd;
+  };
+  auto out = [&](int h) {
+    return h < a.H ? static_cast<T*>(a.q_out) + row * a.qo_stride + (int64_t)h * a.hd
+                   : static_cast<T*>(a.k_out) + row * a.ko_stride + (int64_t)(h - a.H) * a.hd;
+  };
+  if (unit >= turned) {  // behind the turned values (out of place)
+    const int at = a.rot + (unit - turned) * (kBytes / (int)sizeof(T));
+    for (int h = h0; h < h1; ++h) {
+      Vals<T, kBytes / (int)sizeof(T), kBytes> x;
+      x.load(in(h) + at);
+      x.store(out(h) + at);
+    }
+    return;
+  }
+  float2 cs[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) cs[i] = turn((uint32_t)pos, a.F[unit * kP + i], a.factor, a.inverse);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const T* p = in(h);
+    T* o = out(h);
+    if constexpr (kNear) {
+      Vals<T, 2 * kP, kBytes> x;
+      x.load(p + unit * 2 * kP);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float u = x.get(2 * i), v = x.get(2 * i + 1);
+        x.set(2 * i, fmaf(u, cs[i].x, -v * cs[i].y));
+        x.set(2 * i + 1, fmaf(v, cs[i].x, u * cs[i].y));
+      }
+      x.store(o + unit * 2 * kP);
+    } else {
+      Vals<T, kP, kBytes> x, y;
+      x.load(p + unit * kP);
+      y.load(p + half + unit * kP);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float u = x.get(i), v = y.get(i);
+        x.set(i, fmaf(u, cs[i].x, -v * cs[i].y));
+        y.set(i, fmaf(v, cs[i].x, u * cs[i].y));
+      }
+      x.store(o + unit * kP);
+      y.store(o + half + unit * kP);
+    }
+  }
+}
+
+template <typename T, int kBytes>
+Launched launch_t(RopeArgs a, bool near, cudaStream_t s) {
+  constexpr int kE = kBytes / (int)sizeof(T);
+  const int p = near ? std::max(1, kE / 2) : kE;
+  const bool copies = a.q_out != a.q || (a.Hkv > 0 && a.k_out != a.k);
+  a.units = a.rot / 2 / p + (copies ? (a.hd - a.rot) / kE : 0);
+  a.per = a.H + a.Hkv;
+  a.groups = 1;
+  const int64_t threads = (int64_t)a.n * a.groups * a.units;
+  Launched l;
+  l.add(launch_k(near ? k_rope<T, kBytes, true> : k_rope<T, kBytes, false>,
+                 dim3((unsigned)((threads + 255) / 256)), 256, 0, s, a));
+  return l;
+}
+
+// The widest vectors that every row, head, half and the copied rest start and end on.
+template <typename T>
+Launched launch_x(const RopeArgs& a, bool near, cudaStream_t s) {
+  const int64_t e = sizeof(T);
+  int64_t all = (int64_t)reinterpret_cast<uintptr_t>(a.q) | (int64_t)reinterpret_cast<uintptr_t>(a.q_out) |
+                a.hd * e | a.rot * e | (near ? 0 : a.rot / 2 * e);
+  if (a.n > 1) all |= a.q_stride * e | a.qo_stride * e;
+  if (a.Hkv) {
+    all |= (int64_t)reinterpret_cast<uintptr_t>(a.k) | (int64_t)reinterpret_cast<uintptr_t>(a.k_out);
+    if (a.n > 1) all |= a.k_stride * e | a.ko_stride * e;
+  }
+  if (all % 16 == 0) return launch_t<T, 16>(a, near, s);
+  if (sizeof(T) == 4 || all % 4 == 0) return launch_t<T, 4>(a, near, s);
+  if constexpr (sizeof(T) == 2) return launch_t<T, 2>(a, near, s);
+  return {};
+}
+
+}  // namespace
+
+Launched launch_rope(const RopeArgs& a, int x_type, bool near, cudaStream_t s) {
+  return x_type == X_F32 ? launch_x<float>(a, near, s) : launch_x<__nv_bfloat16>(a, near, s);
+}
+
+}  // namespace fsk

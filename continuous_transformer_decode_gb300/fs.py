@@ -91,6 +91,11 @@ class fs_kv_q8(C.Structure):
                 ("n_lanes", C.c_int32), ("max_pages", C.c_int32)]
 
 
+class fs_rope_scaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("original", C.c_int32), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double)]
+
+
 LIB_PATH = _build.LIB
 _lib = None
 
@@ -159,6 +164,13 @@ def lib():
         "fs_kv_q8_attention": (C.c_int, [kv8, p, i64, p, p, i32, i32, i32, f32, p, p, i32, p, i64,
                                          i32, i32, p, i64, p]),
         "fs_verify_draft": (C.c_int, [p, i64, i32, i32, p, i32, p, p, i64, p, p, p, p, p, p]),
+        "fs_pages_update": (C.c_int, [p, i32, p, p, i32, i32, i32, p, p, p, p, p, p, p, i32, p, p]),
+        "fs_rope_frequencies": (C.c_int, [i32, C.c_double, C.POINTER(fs_rope_scaling), p, p]),
+        "fs_rope": (C.c_int, [p, i64, i32, p, i64, i32, i32, i32, i32, p, p, i32, C.c_double, i32, p,
+                              i64, p, i64, p]),
+        "fs_lora_add": (C.c_int, [p, i64, i32, p, i32, i32, i32, p, p, p, i32, i32, p, i64, p, i64,
+                                  i32, p]),
+        "fs_sample_filtered": (C.c_int, [p, i64, i32, i32, p, p, p, p, p, p, p, p]),
         "fs_gemm_bf16": (C.c_int, [p, i32, i32, p, i32, p, i32, i32, p]),
         "fs_gemm_bf16_width": (C.c_int, [p, i32, i32, p, i32, p, i32, p]),
         "fs_gemm_bf16_time": (C.c_int, [p, i32, i32, p, i32, p, i32, i32, p, p]),
@@ -181,6 +193,8 @@ def exported_symbols() -> list:
             "fs_profile_enable", "fs_profile_read", "fs_device_error",
             "fs_kv_q8_append", "fs_kv_q8_read", "fs_kv_q8_attention_workspace",
             "fs_kv_q8_attention", "fs_verify_draft",
+            "fs_pages_update", "fs_rope_frequencies", "fs_rope", "fs_lora_add",
+            "fs_sample_filtered",
             "fs_gemm_bf16", "fs_gemm_bf16_width", "fs_gemm_bf16_time", "fs_copy_logits", "fs_gemm_bf16_noalloc",
             "fs_sched_create", "fs_sched_create_model_free", "fs_sched_destroy",
             "fs_sched_submit", "fs_sched_step", "fs_sched_run", "fs_sched_take",
@@ -527,7 +541,7 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
 # tensors that were made or are freed on another stream are the caller's to order.
 class _Types:
     """torch and its types, once torch is there (this module does not import it)."""
-    torch = f32 = bf16 = i32 = u8 = None
+    torch = f32 = bf16 = i32 = i64 = u8 = None
 
 
 def _types():
@@ -535,6 +549,7 @@ def _types():
         import torch
         _Types.torch = torch
         _Types.bf16, _Types.i32, _Types.u8 = torch.bfloat16, torch.int32, torch.uint8
+        _Types.i64 = torch.int64
         _Types.f32 = torch.float32
     return _Types
 
@@ -719,6 +734,148 @@ def fs_verify_draft(logits, row_start, draft, draft_probs, temps, u_accept, u_sa
         _vec(n_accepted, n, ty.i32, "n_accepted"),
         _vec(next_token, n, ty.i32, "next_token"),
         _raw(stream, temps)))
+
+
+# ------------------------------------ what differs from request to request
+def _or_none(x, n: int, dtype, what: str):
+    return None if x is None else _vec(x, n, dtype, what)
+
+
+def fs_pages_update(holders, page_table, lengths, grow, page_size: int, status, keep=None,
+                    row_start=None, row_lane=None, row_position=None, row_length=None,
+                    row_slot=None, max_rows: int | None = None, stream=None) -> None:
+    """Lanes keep keep[l] tokens (all without it) and take grow[l] new ones; pages are
+    let go and taken, and each new token gets its row (see include/fs.h). int32 CUDA
+    tensors, contiguous: holders [n_pages], page_table [n_lanes, max_pages], lengths,
+    keep, grow [n_lanes], row_start [n_lanes + 1], status [4]; row_lane, row_position,
+    row_length int32 and row_slot int64 [max_rows], each or None. max_rows: the rows'
+    length where none of the four is given."""
+    ty = _types()
+    if page_table.dim() != 2:
+        _refuse("the page table is [n_lanes, max_pages]")
+    n, wide = page_table.shape
+    if row_start is None:
+        _refuse(f"row_start: a contiguous CUDA tensor of {n + 1} values is needed")
+    rows = [t.numel() for t in (row_lane, row_position, row_length, row_slot) if t is not None]
+    m = max_rows if max_rows is not None else rows[0] if rows else 0
+    n_pages = holders.numel()
+    _op_check(lib().fs_pages_update(
+        _vec(holders, n_pages, ty.i32, "holders"), n_pages,
+        _vec(page_table, n * wide, ty.i32, "page table"), _vec(lengths, n, ty.i32, "lengths"), n,
+        wide, page_size, _or_none(keep, n, ty.i32, "keep"), _vec(grow, n, ty.i32, "grow"),
+        _vec(row_start, n + 1, ty.i32, "row_start"), _or_none(row_lane, m, ty.i32, "row_lane"),
+        _or_none(row_position, m, ty.i32, "row_position"),
+        _or_none(row_length, m, ty.i32, "row_length"), _or_none(row_slot, m, ty.i64, "row_slot"),
+        m, _vec(status, 4, ty.i32, "status"), _raw(stream, lengths)))
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
+
+
+def fs_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: dict | None = None):
+    """(angles a position of the rotary_dim / 2 pairs as f64, factor of the turned values)
+    for fs_rope. scaling: {"kind": "linear" | "base", "factor"}, {"kind": "ramp", "factor",
+    "original", "beta_fast" (32), "beta_slow" (1)} or {"kind": "bands", "factor",
+    "original", "low" (1), "high" (4)}; see include/fs.h."""
+    c = None
+    if scaling is not None:
+        s = dict(scaling)
+        kind = s.pop("kind", None)
+        if kind not in ROPE_SCALINGS:
+            _refuse(f"scaling: kind is one of {', '.join(ROPE_SCALINGS)}")
+        c = fs_rope_scaling(ROPE_SCALINGS[kind], 0, float(s.pop("factor", 1.0)), 0.0, 0.0)
+        if kind in ("ramp", "bands"):
+            c.original = int(s.pop("original", 0))
+            names = ("beta_slow", "beta_fast", 1.0, 32.0) if kind == "ramp" else ("low", "high", 1.0, 4.0)
+            c.low, c.high = float(s.pop(names[0], names[2])), float(s.pop(names[1], names[3]))
+        if s:
+            _refuse(f"scaling: {kind} has no {', '.join(s)}")
+    f = np.empty(max(0, rotary_dim // 2), np.float64)
+    m = C.c_double()
+    _op_check(lib().fs_rope_frequencies(rotary_dim, theta, None if c is None else C.byref(c),
+                                        f.ctypes.data, C.byref(m)))
+    return f, m.value
+
+
+def fs_rope(q, positions, inv_freq, k=None, q_out=None, k_out=None, interleaved: bool = False,
+            factor: float = 1.0, inverse: bool = False, stream=None) -> None:
+    """Turns the first 2 * len(inv_freq) values of each head of q [n, H, hd] and k
+    [n, Hkv, hd] (f32 or bf16 CUDA tensors, any row stride) by positions (int32 [n]; a
+    negative one skips its row). inv_freq and factor from fs_rope_frequencies (inv_freq: a
+    host array of f64). Without q_out / k_out in place."""
+    ty = _types()
+    n = positions.numel()
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        _refuse("q and k are [n, heads, head_dim]")
+    H, hd = q.shape[1:]
+    qp, qs, dt = _rows(q, n, H, hd, "q")
+    op, os_, do = (qp, qs, dt) if q_out is None else _rows(q_out, n, H, hd, "q_out")
+    kp, ks, dk, Hkv, okp, oks, dko = None, 0, dt, 0, None, 0, dt
+    if k is not None:
+        Hkv = k.shape[1]
+        kp, ks, dk = _rows(k, n, Hkv, hd, "k")
+        okp, oks, dko = (kp, ks, dk) if k_out is None else _rows(k_out, n, Hkv, hd, "k_out")
+    elif k_out is not None:
+        _refuse("k_out without k")
+    if not dt == do == dk == dko:
+        _refuse("q, k and their outputs have different types")
+    f = np.ascontiguousarray(inv_freq, np.float64)
+    if f.ndim != 1:
+        _refuse("inv_freq: a vector of f64 is needed")
+    _op_check(lib().fs_rope(qp, qs, H, kp, ks, Hkv, n, hd, dt, _vec(positions, n, ty.i32, "positions"),
+                            f.ctypes.data, 2 * f.size, factor, bool(interleaved) | bool(inverse) << 1,
+                            op, os_, okp, oks, _raw(stream, positions)))
+
+
+def _panel(x, n: int, width: int, what: str):
+    """(address, row stride, dtype) of n contiguous rows of `width` f32 or bf16 values."""
+    dt = FS_DTYPE_F32 if x.dtype is _Types.f32 else FS_DTYPE_BF16
+    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.shape == (n, width) and (
+            width == 1 or n == 0 or x.stride(1) == 1):
+        return x.data_ptr(), x.stride(0) if n > 1 else width, dt
+    _refuse(f"{what}: a CUDA tensor [{n}, {width}] of f32 or bf16 whose rows are contiguous is needed")
+
+
+def fs_lora_add(x, adapter, A, B, scale, out, base=None, stream=None) -> None:
+    """out[i] = base[i] + scale[a] * B[a] (A[a] x[i]) with a = adapter[i] (int32 [n];
+    outside [0, adapters): out[i] = base[i]). x [n, K], base and out [n, N] (f32 or bf16,
+    any row stride; base may be out, None is 0), A bf16 [adapters, rank, K], B bf16
+    [adapters, N, rank], contiguous, scale f32 [adapters]. All CUDA tensors."""
+    ty = _types()
+    if A.dim() != 3 or B.dim() != 3:
+        _refuse("A is [adapters, rank, K], B [adapters, N, rank]")
+    n, (ad, r, K), N = adapter.numel(), A.shape, B.shape[1]
+    if B.shape != (ad, N, r):
+        _refuse(f"B: [{ad}, N, {r}] is needed")
+    xp, xs, dx = _panel(x, n, K, "x")
+    op, os_, do = _panel(out, n, N, "out")
+    bp, bs, db = (None, 0, do) if base is None else _panel(base, n, N, "base")
+    if db != do:
+        _refuse("base and out have different types")
+    _op_check(lib().fs_lora_add(xp, xs, dx, _vec(adapter, n, ty.i32, "adapter"), n, K, N,
+                                _vec(A, ad * r * K, ty.bf16, "A"), _vec(B, ad * N * r, ty.bf16, "B"),
+                                _vec(scale, ad, ty.f32, "scale"), ad, r, bp, bs, op, os_, do,
+                                _raw(stream, adapter)))
+
+
+def fs_sample_filtered(logits, temps, u, tokens, top_k=None, top_p=None, min_p=None, kept=None,
+                       stream=None) -> None:
+    """One token a row of logits f32 [n, vocab] (any row stride) with the row's temps,
+    top_p, min_p (f32 [n]), top_k (int32 [n]) and random number u (f32 [n]): see
+    include/fs.h. tokens int32 [n] is written, and kept int32 [n] (how many tokens
+    stayed) if given. top_k, top_p, min_p: None for all tokens. All CUDA tensors."""
+    ty = _types()
+    n = temps.numel()
+    if logits.dim() != 2 or logits.dtype is not ty.f32 or logits.shape[0] != n:
+        _refuse(f"logits: a CUDA tensor [{n}, vocab] of f32 is needed")
+    V = logits.shape[1]
+    if V > 1 and n and logits.stride(1) != 1:
+        _refuse("rows of logits must be contiguous")
+    _op_check(lib().fs_sample_filtered(
+        logits.data_ptr(), logits.stride(0) if n > 1 else V, n, V, _vec(temps, n, ty.f32, "temps"),
+        _or_none(top_k, n, ty.i32, "top_k"), _or_none(top_p, n, ty.f32, "top_p"),
+        _or_none(min_p, n, ty.f32, "min_p"), _vec(u, n, ty.f32, "u"),
+        _vec(tokens, n, ty.i32, "tokens"), _or_none(kept, n, ty.i32, "kept"), _raw(stream, temps)))
 
 
 # ------------------------------------------------------------------ scheduler

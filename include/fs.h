@@ -136,8 +136,8 @@ int fs_create(const fs_model_desc* desc, const fs_weights* weights,
 int fs_destroy(fs_handle* h);
 
 /* Message of the last failed call on h (or, when h is NULL, of this thread's
- * last failed fs_create, fs_kv_q8_* or fs_verify_draft). Valid until the next
- * call on the same handle. */
+ * last failed fs_create or operator on the caller's buffers). Valid until the
+ * next call on the same handle. */
 const char* fs_last_error(const fs_handle* h);
 
 /* Kernels of h run on `stream` (a cudaStream_t) from now on. NULL selects
@@ -597,6 +597,144 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
                     const float* draft_probs, int64_t probs_stride, const float* temps,
                     const float* u_accept, const float* u_sample, int32_t* n_accepted,
                     int32_t* next_token, void* stream);
+
+/* ---- what differs from request to request in a step: operators on the
+ * caller's device buffers -----------------------------------------------------
+ *
+ * Pages and slots of the new tokens (fs_pages_update), their rotary positions
+ * (fs_rope), each request's low-rank adapter beside a shared projection
+ * (fs_lora_add) and its sampling settings (fs_sample_filtered). Pointers are
+ * DEVICE pointers on the current device, owned by the caller and used until the
+ * stream has passed the call, unless they are said to be HOST pointers. The calls
+ * enqueue on `stream` (a cudaStream_t, NULL = default stream), allocate nothing,
+ * need no workspace, do not synchronise, and can be captured into a graph. Arrays
+ * are aligned to their element type.
+ * Errors, with nothing enqueued: FS_ERR_ARG (a NULL pointer, a size, a type, an
+ * alignment, overlapping buffers, memory of another device or of the host);
+ * FS_ERR_CUDA (a launch failed). */
+
+/* Page tables and slot maps, kept on the GPU: one call lets lanes give up tokens
+ * and take new ones. The pool is holders[n_pages] (how many lanes hold a page, 0:
+ * free), a lane's pages are page_table[lane][0 .. ceil(length / page_size)) of
+ * [n_lanes][max_pages], lengths[lane] its tokens: the page table of fs_kv_q8.
+ *   1. lane l keeps its first min(lengths[l], keep[l]) tokens (keep NULL: all).
+ *      Pages past their end lose a holder and their table entries become -1: a
+ *      rejected draft's suffix, or (keep 0) a finished request.
+ *   2. lane l takes grow[l] more tokens. The pages that needs are the lowest free
+ *      ones, ascending, lanes in order, and get one holder; pages let go by 1. are
+ *      free already. All lanes grow or none does.
+ *   3. each new token is a row, lanes in order and tokens ascending: lane l's rows
+ *      are row_start[l] .. row_start[l + 1] - 1 (n_lanes + 1 entries), and a row's
+ *      row_lane, row_position (the token's place in its lane), row_length (that
+ *      plus 1) and row_slot (page * page_size + place in the page) are what
+ *      fs_kv_q8_append, fs_rope and fs_kv_q8_attention take. Rows up to max_rows
+ *      behind the last get lane, position and slot -1 and length 0, which pad a
+ *      batch there. The five row arrays may each be NULL (max_rows limits the rows
+ *      all the same).
+ * status (int32 [4]): FS_OK or why no lane grew, rows wanted, pages wanted, pages
+ * that were free for them (counts past 2^31 - 1 as that). FS_ERR_KV_FULL: too few
+ * free pages, or a lane past max_pages * page_size tokens; FS_ERR_SCRATCH: more than
+ * max_rows rows. 1. has happened then too, row_start is all 0 and every row padding.
+ * Lengths are taken as in [0, max_pages * page_size], negative keep and grow as 0. A
+ * let go entry outside [0, n_pages) is only cleared, and a page that nobody holds
+ * stays free. A page that several lanes hold is one that no lane will write: a lane
+ * that shares its last, partial page must be given a copy before it grows. At most
+ * 16384 lanes; max_pages * page_size at most 2^30. One call at a time on one pool. */
+int fs_pages_update(int32_t* holders, int32_t n_pages, int32_t* page_table, int32_t* lengths,
+                    int32_t n_lanes, int32_t max_pages, int32_t page_size, const int32_t* keep,
+                    const int32_t* grow, int32_t* row_start, int32_t* row_lane,
+                    int32_t* row_position, int32_t* row_length, int64_t* row_slot,
+                    int32_t max_rows, int32_t* status, void* stream);
+
+/* How a model's frequencies are scaled for contexts longer than it was trained on. */
+#define FS_ROPE_SCALING_NONE 0
+#define FS_ROPE_SCALING_LINEAR 1 /* f / factor (position interpolation)           */
+#define FS_ROPE_SCALING_BASE 2   /* theta * factor^(r / (r - 2)), r = rotary_dim (a
+                                    factor of factor * len / original - (factor - 1)
+                                    is its dynamic form)                         */
+#define FS_ROPE_SCALING_RAMP 3   /* pairs below `lo` keep f, above `hi` take f /
+                                    factor, between a linear mix; lo and hi are where
+                                    a pair turns `high` and `low` times over
+                                    `original` tokens, rounded outwards to [0, r - 1]
+                                    ("YaRN", Peng et al. 2023); turned values are
+                                    multiplied by 0.1 ln(factor) + 1 (factor > 1) */
+#define FS_ROPE_SCALING_BANDS 4  /* pairs that turn at least `high` times over
+                                    `original` tokens keep f, at most `low` times
+                                    take f / factor, between a mix linear in turns */
+typedef struct fs_rope_scaling {
+  int32_t kind;
+  int32_t original; /* tokens of the trained context (RAMP, BANDS)                */
+  double factor;    /* > 0                                                        */
+  double low;       /* RAMP: usually 1; BANDS: usually 1. 0 < low < high          */
+  double high;      /* RAMP: usually 32; BANDS: usually 4                         */
+} fs_rope_scaling;
+
+/* Frequencies for fs_rope: inv_freq[j] (HOST, rotary_dim / 2 entries) = the angle a
+ * position turns pair j by, theta^(-2 j / rotary_dim) scaled, and *factor_out (HOST)
+ * the factor of the turned values (1 but for RAMP). Host arithmetic in 64 bits, no
+ * device needed; scaling NULL is NONE. Errors: FS_ERR_ARG. */
+int fs_rope_frequencies(int32_t rotary_dim, double theta, const fs_rope_scaling* scaling,
+                        double* inv_freq, double* factor_out);
+
+#define FS_ROPE_INTERLEAVED 1 /* pairs (2 j, 2 j + 1); else (j, j + rotary_dim / 2) */
+#define FS_ROPE_INVERSE 2     /* turns by minus the angle                          */
+
+/* Rotary positions of n rows of queries [n_heads][head_dim] and keys
+ * [n_kv_heads][head_dim] (k NULL: queries alone), rows *_stride elements apart, of
+ * dtype FS_DTYPE_F32 or _BF16: with a = positions[i] * inv_freq[j], pair j (x, y) of the
+ * first rotary_dim values of each head becomes factor * (x cos a - y sin a, y cos a + x
+ * sin a); the other values are copied. q_out may be q (in place, same stride), and k_out
+ * k; buffers must not overlap otherwise. A negative position skips its row, which is
+ * neither read nor written: -1 pads a batch. inv_freq is a HOST array of rotary_dim / 2
+ * numbers within 2^20, read during the call. Angles are reduced exactly (as 64-bit fractions of
+ * a turn: off by at most position * 2^-65 turns), sines and cosines are f32, and a result
+ * is rounded once to dtype. head_dim at most 1024, rotary_dim even, at most 512. */
+int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int64_t k_stride,
+            int32_t n_kv_heads, int32_t n, int32_t head_dim, int32_t dtype,
+            const int32_t* positions, const double* inv_freq, int32_t rotary_dim, double factor,
+            int32_t flags, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+            void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection: for rows i < n with
+ * a = adapter[i] in [0, n_adapters),
+ *   out[i] = base[i] + scale[a] * B[a] (A[a] x[i]),
+ * other rows give out[i] = base[i]. x is n rows of K (x_dtype), base and out n rows of N
+ * (y_dtype; FS_DTYPE_F32 or _BF16 each), strides in elements. base is what the projection
+ * gave; it may be out (in place, same stride: rows without an adapter are then not
+ * touched), or NULL for 0; buffers must not overlap otherwise. A [n_adapters][rank][K] and
+ * B [n_adapters][N][rank] are bf16, 16-byte aligned; rank is a multiple of 8, at most 128
+ * (smaller ones padded with zeros), K a multiple of 8. scale is f32 [n_adapters]. Rows may
+ * come in any order and mix; rows of one adapter within a block of rows share its reads.
+ * Products are exact, sums f32; A x is kept to 24 bits for f32 out and 16 for bf16; the
+ * result is rounded once. A row's bits depend on its own inputs alone, not on the
+ * batch. */
+int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t* adapter,
+                int32_t n, int32_t K, int32_t N, const uint16_t* A, const uint16_t* B,
+                const float* scale, int32_t n_adapters, int32_t rank, const void* base,
+                int64_t base_stride, void* out, int64_t out_stride, int32_t y_dtype,
+                void* stream);
+
+/* One token a row from given random numbers, with each row's own settings. logits are
+ * n rows of f32 [vocab], logits_stride apart (what fs_decode_step_batch writes). Tokens
+ * rank by their logits, the larger first, and of equal ones the lower index. With w =
+ * exp((z - max z) / temps[i]):
+ *   top-k: the first top_k[i] tokens stay (0 or less: all);
+ *   top-p: of those, the tokens ahead of which less than top_p[i] of their sum lies
+ *          (1 or more: all; the first always stays);
+ *   min-p: of those, the tokens with w >= min_p[i], and the first (0 or less: all).
+ * The token is the first by index whose running sum of the kept weights reaches u[i]
+ * (in [0, 1)) times their total and whose weight is not 0. temps[i] = 0 (or not
+ * positive) takes the first in rank. kept[i] (kept may be NULL) is how many stay: 1 for
+ * temps[i] = 0. top_k, top_p and min_p may each be NULL: all stay. Logits of -inf or NaN never stay; equal +inf
+ * logits share all of the weight; a row without a token gives token 0 and kept 0. temps is
+ * held in [1e-30, 1e30]; a NaN in top_p or min_p turns it off. Weights are good to a
+ * relative 2^-36 and summed in pairs of f32 numbers, so that a cut or a draw is that of
+ * the real numbers but next to a border. A weight below 2^-125 of the largest is 0. vocab
+ * is at most 2^20. */
+int fs_sample_filtered(const float* logits, int64_t logits_stride, int32_t n, int32_t vocab,
+                       const float* temps, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const float* u, int32_t* tokens, int32_t* kept,
+                       void* stream);
 
 #ifdef __cplusplus
 }
