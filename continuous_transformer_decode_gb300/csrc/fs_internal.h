@@ -594,7 +594,7 @@ Launched launch_verify(const VerifyArgs& a, int sms, cudaStream_t s);
 
 // ---- what differs from request to request (k_pages.cu, k_rope.cu, k_lora.cu,
 // k_sample_filtered.cu); arguments as in include/fs.h
-constexpr int kMaxPageLanes = 16384;  // their sums lie in shared memory
+constexpr int kMaxPageLanes = 8192;  // their sums lie in shared memory
 struct PagesArgs {
   int32_t* holders;
   int32_t* table;
@@ -628,7 +628,7 @@ struct RopeArgs {
   int units, per, groups;      // set by the launcher
   uint64_t F[kMaxRotary / 2];  // 2^64ths of a turn a position
 };
-Launched launch_rope(const RopeArgs& a, int x_type, bool near, cudaStream_t s);
+Launched launch_rope(const RopeArgs& a, int x_type, bool near, int sms, cudaStream_t s);
 
 struct LoraArgs {
   const void* x;

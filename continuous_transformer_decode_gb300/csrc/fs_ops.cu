@@ -318,7 +318,7 @@ int fs_pages_update(int32_t* holders, int32_t n_pages, int32_t* page_table, int3
   if (n_pages < 1 || max_pages < 1 || page_size < 1)
     return refuse(FS_ERR_ARG, "n_pages, max_pages and page_size must be positive");
   if ((int64_t)max_pages * page_size > kMaxTokens) return refuse(FS_ERR_ARG, "a lane may hold 2^30 tokens");
-  if (n_lanes < 1 || n_lanes > kMaxPageLanes) return refuse(FS_ERR_ARG, "n_lanes outside [1, 16384]");
+  if (n_lanes < 1 || n_lanes > kMaxPageLanes) return refuse(FS_ERR_ARG, "n_lanes outside [1, 8192]");
   if (max_rows < 0) return refuse(FS_ERR_ARG, "negative max_rows");
   if (!holders || !page_table || !lengths || !grow || !row_start || !status)
     return refuse(FS_ERR_ARG, "NULL argument array");
@@ -446,12 +446,14 @@ int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int
     const double f = inv_freq[j], p = f * ih, pe = std::fma(f, ih, -p) + f * il;
     double whole;
     const double part = std::modf(p, &whole);  // exact
-    // 53 bits at a time: the top 32 of the fraction, then what is left of it and pe
-    const double top = std::floor(std::ldexp(part, 32));
-    const double rest = std::ldexp(std::ldexp(part, 32) - top, 32) + std::ldexp(pe, 64);
+    // the top 32 bits of the fraction, then what is left of it and pe
+    const double top = std::floor(part * 0x1p32);
+    const double rest = (part * 0x1p32 - top) * 0x1p32 + pe * 0x1p64;
     a.F[j] = ((uint64_t)(int64_t)top << 32) + (uint64_t)(int64_t)std::llrint(rest);
   }
-  return launched(launch_rope(a, xt, (flags & FS_ROPE_INTERLEAVED) != 0, (cudaStream_t)stream));
+  const int sms = device_sms();
+  if (!sms) return refuse(FS_ERR_CUDA, "no CUDA device");
+  return launched(launch_rope(a, xt, (flags & FS_ROPE_INTERLEAVED) != 0, sms, (cudaStream_t)stream));
 }
 
 int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t* adapter,

@@ -1,66 +1,472 @@
 // Low-rank adapters of many requests (fs_lora_add): out = base + scale B (A x) with the
 // row's own A [rank][K] and B [N][rank].
+//
+// The bytes bound it: base and out once, x once, an adapter once for all its rows. One
+// launch does both products. A cluster of eight blocks takes up to kR rows of one adapter
+// out of a window of 256 rows (rows of any order are gathered by a hash of their adapters
+// in shared memory, in each block alike); its blocks share K, exchange their parts of A x
+// through distributed shared memory, and then share N.
+//
+// Both products run on bf16 warp MMAs (m16n8k16, rows of x as M): a decode step has one to
+// a few rows an adapter, so that most of a 128-row tcgen05 tile would be empty, and a
+// prompt's products are a few percent of the bytes' time. Fragments come straight from
+// global memory, 16 bytes a lane: the order of the summed index is free as long as both
+// operands have the same, so a lane's 8 values of 32 feed two MMAs.
+//
+// A x is held in f32 and enters the second product as two bf16 parts (16 bits) for bf16
+// results and three (24 bits) for f32 ones; an f32 x enters the first as three. Products of
+// parts are exact, sums f32. Sums run over the same pieces in the same order whatever kR:
+// K in eight blocks' shares, each in eight pieces, so that a row's bits depend on the row
+// alone.
+
+#include <cooperative_groups.h>
+
+#include "attn_mma.cuh"
 #include "fs_internal.h"
 
 namespace fsk {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float val(const T* p, int64_t i) {
-  if constexpr (sizeof(T) == 4) return p[i];
-  else return __bfloat162float(p[i]);
+namespace cg = cooperative_groups;
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kC = 8, kT = 256, kW = kT / 32;  // blocks of a cluster, threads, warps
+constexpr int kWindow = kT;                    // rows that are gathered, one a thread
+constexpr int kSlots = 2 * kWindow;
+
+// Three bf16 parts of f32 values that hold their 24 bits (two: 16). A value past bf16's
+// range is its largest, and the rest; infinities and NaN are in the first part alone.
+template <int kParts>
+__device__ __forceinline__ void split(float x, __nv_bfloat16 (&p)[kParts]) {
+  __nv_bfloat16 h = __float2bfloat16_rn(x);
+  float f = __bfloat162float(h);
+  if (fabsf(f) > 3.3895314e38f) {  // inf or NaN
+    if (fabsf(x) <= 3.4028235e38f) {
+      h = __ushort_as_bfloat16(x < 0 ? 0xff7f : 0x7f7f);
+      f = __bfloat162float(h);
+    } else {
+      f = x = 0.0f;
+    }
+  }
+  p[0] = h;
+  float rest = x - f;
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) {
+    p[i] = __float2bfloat16_rn(rest);
+    rest -= __bfloat162float(p[i]);
+  }
 }
 
-constexpr int kT = 256;
+// 8 consecutive values as bf16 parts.
+template <typename T>
+struct Eight {
+  static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+  uint4 p[kParts];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) p[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const T* x, bool vec) {
+    if constexpr (sizeof(T) == 2) {
+      if (vec) {
+        p[0] = *reinterpret_cast<const uint4*>(x);
+      } else {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(x);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&p[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)u[2 * i] | ((uint32_t)u[2 * i + 1] << 16);
+      }
+    } else {
+      float v[8];
+      if (vec) {
+        const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i];
+      }
+      __nv_bfloat16* out[3] = {reinterpret_cast<__nv_bfloat16*>(&p[0]), reinterpret_cast<__nv_bfloat16*>(&p[1]),
+                               reinterpret_cast<__nv_bfloat16*>(&p[2])};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        __nv_bfloat16 s[3];
+        split(v[i], s);
+        out[0][i] = s[0], out[1][i] = s[1], out[2][i] = s[2];
+      }
+    }
+  }
+};
 
-// A block a row and part of the columns.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(kT) k_lora(const LoraArgs a) {
-  __shared__ float low[128];
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// d += a b over 32 values of the summed index: rows g (lo) and g + 8 (hi) of a, column g
+// of b, a lane's 8 values each.
+__device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint4& hi, const uint4& b) {
+  const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+  attn::mma16816(d, a0, b.x, b.y);
+  attn::mma16816(d, a1, b.z, b.w);
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, int n, float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(&u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(h[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = i < n ? p[i] : 0.0f;
+      else v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, int n, const float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint4 u;
+      u.x = attn::pack_bf16(v[0], v[1]), u.y = attn::pack_bf16(v[2], v[3]);
+      u.z = attn::pack_bf16(v[4], v[5]), u.w = attn::pack_bf16(v[6], v[7]);
+      *reinterpret_cast<uint4*>(p) = u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) p[i] = v[i];
+        else p[i] = __float2bfloat16_rn(v[i]);
+      }
+  }
+}
+
+struct Gather {
+  int key[kSlots];
+  uint16_t count[kW][kSlots];  // rows of a warp
+  int id[kWindow];
+  int16_t nth[kWindow];   // of its adapter's rows in the window
+  int16_t lead[kWindow];  // first rows of the items
+  int row[64];            // of an item
+  int firsts[kW], bare[kW];
+};
+
+// Shared memory behind Gather: the parts of A x, [part][row] of `pitch` values, and f32
+// sums: a tile a warp and a tile a block of the cluster (kMT 1), or the block's own.
+struct Sizes {
+  int pitch;
+  int64_t low, sums, bytes;
+  __host__ __device__ Sizes(int mt, int parts, int rank) {
+    const int blocks = (rank + 31) / 32;
+    pitch = 32 * blocks + (blocks % 2 ? 0 : 32);  // rows 64 bytes apart modulo 128: no conflicts
+    low = (int64_t)parts * mt * 16 * pitch * 2;
+    sums = (int64_t)(mt == 1 ? kW + kC : 1) * mt * 16 * rank * 4;
+    bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + sums;
+  }
+};
+
+template <typename TX, typename TY, int kMT>
+__global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
+  constexpr int kR = 16 * kMT;                  // rows of an item
+  constexpr int kMP = kMT == 1 ? 1 : 2;         // row tiles that share a load of B
+  constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
+  extern __shared__ __align__(16) unsigned char dyn[];
+  Gather& sh = *reinterpret_cast<Gather*>(dyn);
+  const Sizes sz(kMT, kParts, a.rank);
+  __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
+  float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int c = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  // the other blocks' shared memory can be written once they have started
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  for (int i = tid; i < kSlots; i += kT) sh.key[i] = -1;
+  for (int i = tid; i < kW * kSlots / 8; i += kT) reinterpret_cast<uint4*>(sh.count)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   pdl_trigger();
-  const int which = a.adapter[row];
-  const bool has = which >= 0 && which < a.n_adapters;
-  if (has) {
-    const TX* x = static_cast<const TX*>(a.x) + row * a.x_stride;
-    for (int r = warp; r < a.rank; r += kT / 32) {
-      const __nv_bfloat16* A = a.A + ((int64_t)which * a.rank + r) * a.K;
-      float s = 0.0f;
-      for (int k = lane; k < a.K; k += 32) s = fmaf(val(x, k), __bfloat162float(A[k]), s);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) low[r] = s * a.scale[which];
-    }
-  } else if (a.base == a.out) {
-    return;
-  }
+  const int item0 = blockIdx.x / kC % per_window;
+  const int first = (int)(blockIdx.x / kC / per_window) * kWindow;
+  // ---- the window's rows by adapter
+  const int my_row = first + tid;
+  const int my_id = my_row < a.n ? a.adapter[my_row] : -1;
+  const bool has = my_id >= 0 && my_id < a.n_adapters;
   __syncthreads();
-  const TY* base = static_cast<const TY*>(a.base) + row * a.base_stride;
-  TY* out = static_cast<TY*>(a.out) + row * a.out_stride;
-  for (int j = blockIdx.y * kT + tid; j < a.N; j += gridDim.y * kT) {
-    float s = a.base ? val(base, j) : 0.0f;
-    if (has) {
-      float d = 0.0f;
-      const __nv_bfloat16* B = a.B + ((int64_t)which * a.N + j) * a.rank;
-      for (int r = 0; r < a.rank; ++r) d = fmaf(low[r], __bfloat162float(B[r]), d);
-      s += d;
+  int slot = 0;
+  if (has) {
+    slot = (int)((uint32_t)my_id * 2654435761u >> 23);
+    static_assert(kSlots == 512, "nine bits");
+    while (true) {
+      const int old = atomicCAS(&sh.key[slot], -1, my_id);
+      if (old == -1 || old == my_id) break;
+      slot = (slot + 1) % kSlots;
     }
-    if constexpr (sizeof(TY) == 4) out[j] = s;
-    else out[j] = __float2bfloat16_rn(s);
   }
+  const unsigned same = __match_any_sync(kAll, has ? my_id : -1);
+  const unsigned below = (1u << lane) - 1;
+  if (has && (same & below) == 0) sh.count[warp][slot] = (uint16_t)__popc(same);
+  sh.id[tid] = has ? my_id : -1;
+  __syncthreads();
+  int nth = __popc(same & below);
+  if (has)
+    for (int w = 0; w < warp; ++w) nth += sh.count[w][slot];
+  sh.nth[tid] = (int16_t)nth;
+  const unsigned leads = __ballot_sync(kAll, has && nth % kR == 0);
+  const unsigned bare = __ballot_sync(kAll, !has && my_row < a.n);
+  if (lane == 0) sh.firsts[warp] = __popc(leads), sh.bare[warp] = __popc(bare);
+  __syncthreads();
+  int items = 0, bares = 0, at = 0, bare_at = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w == warp) at = items, bare_at = bares;
+    items += sh.firsts[w];
+    bares += sh.bare[w];
+  }
+  if (has && nth % kR == 0) sh.lead[at + __popc(leads & below)] = (int16_t)tid;
+
+  // this block's columns, in chunks of 32
+  const int chunks = (a.N + 31) / 32, per = (chunks + kC - 1) / kC;
+  const int chunk0 = min(chunks, c * per), chunk1 = min(chunks, chunk0 + per);
+  const TX* const x = static_cast<const TX*>(a.x);
+  const TY* const base = static_cast<const TY*>(a.base);
+  TY* const out = static_cast<TY*>(a.out);
+  const bool x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && a.x_stride * sizeof(TX) % 16 == 0;
+  const bool y_vec = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
+                     (a.base_stride | a.out_stride) * sizeof(TY) % 16 == 0;
+  // ---- rows without an adapter, shared by the window's clusters
+  if (a.base != a.out && bares) {
+    unsigned m = bare;
+    for (int i = bare_at; m; ++i, m &= m - 1) {  // a warp its own rows
+      if (i % per_window != item0) continue;
+      const int64_t row = first + warp * 32 + __ffs(m) - 1;
+      for (int j = 32 * chunk0 + 8 * lane; j < min(a.N, 32 * chunk1); j += 256) {
+        float v[8] = {};
+        if (base) load8(base + row * a.base_stride + j, y_vec, a.N - j, v);
+        store8(out + row * a.out_stride + j, y_vec, a.N - j, v);
+      }
+    }
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // ---- this block's part of K, in blocks of 32
+  const int kbs = (a.K + 31) / 32;
+  const int kb0 = (int)((int64_t)kbs * c / kC), kb1 = (int)((int64_t)kbs * (c + 1) / kC);
+  const int tiles = a.rank / 8, rblocks = (a.rank + 31) / 32;
+  auto piece = [&](int s) { return kb0 + (kb1 - kb0) * s / kW; };  // the s-th of eight starts here
+
+  for (int item = item0; item < items; item += per_window) {
+    __syncthreads();  // also: sh.lead
+    const int lead = sh.lead[item], id = sh.id[lead], part = sh.nth[lead] / kR;
+    const bool mine = has && my_id == id && nth / kR == part;
+    if (mine) sh.row[nth % kR] = my_row;
+    const int rows = __syncthreads_count(mine);
+    const float scale = a.scale[id];
+    const __nv_bfloat16* const A = a.A + (int64_t)id * a.rank * a.K;
+    const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
+    auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
+    if (kMT == 1 && item != item0) cluster.sync();  // the last item's sums have been read
+
+    // sums += x A^T of row tile mt and rank tiles nt0 .. nt0 + 3 over blocks b0 .. b1 - 1
+    auto shrink = [&](int mt, int nt0, int b0, int b1, float (&d)[4][4]) {
+      const int64_t r0 = row_of(16 * mt + g), r1 = row_of(16 * mt + g + 8);
+#pragma unroll 2
+      for (int b = b0; b < b1; ++b) {
+        const int k = 32 * b + 8 * tig;
+        const bool in = k < a.K;
+        Eight<TX> lo, hi;
+        lo.clear(), hi.clear();
+        if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
+        if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
+                                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(d[j], lo.p[p], hi.p[p], w[j]);
+      }
+    };
+    auto put = [&](float* to, int mt, int nt0, const float (&d)[4][4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (nt0 + j < tiles) {
+          float* p = to + (16 * mt + g) * a.rank + 8 * (nt0 + j) + 2 * tig;
+          *reinterpret_cast<float2*>(p) = make_float2(d[j][0], d[j][1]);
+          *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[j][2], d[j][3]);
+        }
+    };
+    const int tile = 16 * a.rank;
+    if constexpr (kMT == 1) {
+      for (int nt0 = 0; nt0 < tiles; nt0 += 4) {
+        float d[4][4] = {};
+        shrink(0, nt0, piece(warp), piece(warp + 1), d);
+        put(sums + warp * tile, 0, nt0, d);
+      }
+      __syncthreads();
+      for (int i = tid; i < tile; i += kT) {
+        float s = sums[i];
+#pragma unroll
+        for (int w = 1; w < kW; ++w) s += sums[w * tile + i];
+        for (int r = 0; r < kC; ++r) *cluster.map_shared_rank(sums + (kW + c) * tile + i, r) = s;
+      }
+      cluster.sync();
+      for (int i = tid; i < 16 * sz.pitch; i += kT) {
+        const int m = i / sz.pitch, r = i - m * sz.pitch;
+        float s = 0.0f;
+        if (r < a.rank) {
+          const float* p = sums + kW * tile + m * a.rank + r;
+          s = p[0];
+#pragma unroll
+          for (int b = 1; b < kC; ++b) s += p[b * tile];
+          s *= scale;
+        }
+        __nv_bfloat16 v[kParts];
+        split(s, v);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = v[p];
+      }
+      __syncthreads();
+    } else {
+      static_assert(kMT == 4, "eight warps are four row tiles and two halves of the ranks");
+      const int mt = warp & 3;
+      for (int nt0 = 4 * (warp >> 2); nt0 < tiles; nt0 += 8) {
+        float d[4][4] = {};
+        if (16 * mt < rows)
+          for (int s = 0; s < kW; ++s) {
+            float e[4][4] = {};
+            shrink(mt, nt0, piece(s), piece(s + 1), e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) d[j][q] = s == 0 ? e[j][q] : d[j][q] + e[j][q];
+          }
+        put(sums, mt, nt0, d);
+      }
+      cluster.sync();
+      // this block adds up kR / kC of the rows and gives them to all
+      constexpr int kOwn = kR / kC;
+      for (int i = tid; i < kOwn * sz.pitch / 2; i += kT) {
+        const int m = i / (sz.pitch / 2), r = 2 * (i - m * (sz.pitch / 2));
+        float2 s = make_float2(0.0f, 0.0f);
+        if (r < a.rank) {
+          const int o = (c * kOwn + m) * a.rank + r;
+          s = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sums + o, 0));
+#pragma unroll
+          for (int b = 1; b < kC; ++b) {
+            const float2 t = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sums + o, b));
+            s.x += t.x, s.y += t.y;
+          }
+          s.x *= scale, s.y *= scale;
+        }
+        __nv_bfloat16 u[kParts], v[kParts];
+        split(s.x, u);
+        split(s.y, v);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          const uint32_t w = (uint32_t)__bfloat16_as_ushort(u[p]) | ((uint32_t)__bfloat16_as_ushort(v[p]) << 16);
+          uint32_t* to = reinterpret_cast<uint32_t*>(low + (p * kR + c * kOwn + m) * sz.pitch + r);
+          for (int b = 0; b < kC; ++b) *cluster.map_shared_rank(to, b) = w;
+        }
+      }
+      cluster.sync();
+    }
+
+    // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles
+    for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW) {
+      const int col = 32 * chunk + 8 * tig, left = a.N - col;
+#pragma unroll 1
+      for (int m0 = 0; m0 < kMT; m0 += kMP) {
+        if (16 * m0 >= rows) break;
+        float y[kMP][2][8];
+#pragma unroll
+        for (int m = 0; m < kMP; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t r = row_of(16 * (m0 + m) + g + 8 * h);
+            if (base && r >= 0) {
+              load8(base + r * a.base_stride + col, y_vec, left, y[m][h]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[m][h][i] = 0.0f;
+            }
+          }
+        float d[kMP][4][4] = {};
+#pragma unroll 1
+        for (int b = 0; b < rblocks; ++b) {
+          const int r = 32 * b + 8 * tig;
+          uint4 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // tile j's column g
+            const int n = 32 * chunk + 8 * (g >> 1) + 2 * j + (g & 1);
+            w[j] = r < a.rank && n < a.N ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.rank + r)
+                                         : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int m = 0; m < kMP; ++m)
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+              const __nv_bfloat16* t = low + (p * kR + 16 * (m0 + m) + g) * sz.pitch + r;
+              const uint4 lo = *reinterpret_cast<const uint4*>(t), hi = *reinterpret_cast<const uint4*>(t + 8 * sz.pitch);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma32(d[m][j], lo, hi, w[j]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kMP; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t r = row_of(16 * (m0 + m) + g + 8 * h);
+            if (r < 0 || left <= 0) continue;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[2 * j] = y[m][h][2 * j] + d[m][j][2 * h];
+              v[2 * j + 1] = y[m][h][2 * j + 1] + d[m][j][2 * h + 1];
+            }
+            store8(out + r * a.out_stride + col, y_vec, left, v);
+          }
+      }
+    }
+  }
+}
+
+template <typename TX, typename TY, int kMT>
+Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
+  constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
+  static std::atomic<uint64_t> done{0};
+  Launched l;
+  l.error = allow_smem(k_lora<TX, TY, kMT>, (int)Sizes(kMT, kParts, 128).bytes, done);
+  if (l.error != cudaSuccess) return l;
+  const int64_t windows = (a.n + kWindow - 1) / kWindow;
+  l.add(launch_k_cluster(k_lora<TX, TY, kMT>, dim3((unsigned)(windows * per_window * kC)), kT,
+                         (size_t)Sizes(kMT, kParts, a.rank).bytes, s, kC, a, per_window));
+  return l;
+}
+template <typename TX, typename TY>
+Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
+  const int64_t windows = (a.n + kWindow - 1) / kWindow;
+  const bool wide = a.n > 1024;
+  // clusters a window: what fits the SMs at once (two blocks each), a row each at most
+  const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
+  if (wide) return launch_t<TX, TY, 4>(a, (int)std::min<int64_t>(4, std::max<int64_t>(2, fit)), s);
+  return launch_t<TX, TY, 1>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 
 }  // namespace
 
 Launched launch_lora(const LoraArgs& a, int x_type, int y_type, int sms, cudaStream_t s) {
-  const dim3 grid((unsigned)a.n, (unsigned)std::max(1, std::min((a.N + kT - 1) / kT, 4 * sms / a.n)));
-  auto k = x_type == X_F32 ? (y_type == X_F32 ? k_lora<float, float> : k_lora<float, __nv_bfloat16>)
-                           : (y_type == X_F32 ? k_lora<__nv_bfloat16, float>
-                                              : k_lora<__nv_bfloat16, __nv_bfloat16>);
-  Launched l;
-  l.add(launch_k(k, grid, kT, 0, s, a));
-  return l;
+  if (x_type == X_F32)
+    return y_type == X_F32 ? launch_xy<float, float>(a, sms, s) : launch_xy<float, __nv_bfloat16>(a, sms, s);
+  return y_type == X_F32 ? launch_xy<__nv_bfloat16, float>(a, sms, s)
+                         : launch_xy<__nv_bfloat16, __nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace fsk

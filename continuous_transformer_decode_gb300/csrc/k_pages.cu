@@ -2,41 +2,62 @@
 //
 // Which pages a lane takes follows from two running sums: of the pages that the lanes
 // want, in lane order, and of the free pages, in page order; the j-th wanted page is the
-// j-th free one. Every block has the lanes' sums in shared memory (each forms them from
-// the lanes' numbers, which are few) and a part of the pages; a thread finds the lane of a
-// wanted page, of a page to let go or of a row by bisection there.
+// j-th free one. The lanes' sums are formed by every block for itself, in its shared
+// memory, from the lanes' numbers, which are few; the pages and the rows are shared among
+// the blocks of one cluster, which exchange their counts of free pages. A page's or a
+// row's lane is found by bisection in the running sums.
+#include <cooperative_groups.h>
+
 #include "fs_internal.h"
 
 namespace fsk {
 namespace {
 
-constexpr int kT = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kT = 1024, kW = kT / 32;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Exclusive running sums over the block's threads of v; total becomes the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t s = v;
+struct Three {
+  int64_t a, b, c;
+};
+__device__ __forceinline__ Three operator+(Three x, Three y) { return {x.a + y.a, x.b + y.b, x.c + y.c}; }
+__device__ __forceinline__ Three up(Three v, int o) {
+  return {__shfl_up_sync(kAll, v.a, o), __shfl_up_sync(kAll, v.b, o), __shfl_up_sync(kAll, v.c, o)};
+}
+__device__ __forceinline__ Three at(Three v, int i) {
+  return {__shfl_sync(kAll, v.a, i), __shfl_sync(kAll, v.b, i), __shfl_sync(kAll, v.c, i)};
+}
+__device__ __forceinline__ int up(int v, int o) { return __shfl_up_sync(kAll, v, o); }
+__device__ __forceinline__ int at(int v, int i) { return __shfl_sync(kAll, v, i); }
+// Inclusive running sums over the lanes of a warp.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(kAll, s, o);
-    if (lane >= o) s += up;
+    const T u = up(v, o);
+    if (lane >= o) v = v + u;
   }
-  if (lane == 31) tmp[warp] = s;
-  __syncthreads();
-  int64_t w = tmp[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(kAll, w, o);
-    if (lane >= o) w += up;
-  }
-  total = __shfl_sync(kAll, w, 31);
-  const int64_t before = warp ? __shfl_sync(kAll, w, warp - 1) : 0;
-  __syncthreads();
-  return before + s - v;
+  return v;
 }
 
-// The last i < n with first[i] <= x (first[0] = 0 <= x; equal entries: the last).
+// Exclusive running sums over the block's threads; total becomes the sum.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* tmp, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T s = warp_scan(v, lane);
+  if (lane == 31) tmp[warp] = s;
+  __syncthreads();
+  const T w = warp_scan(tmp[lane], lane);
+  total = at(w, 31);
+  T before = at(w, max(warp - 1, 0));
+  if (warp == 0) before = T{};
+  T ahead = up(s, 1);
+  if (lane == 0) ahead = T{};
+  return before + ahead;
+}
+
+// The last i < n with first[i] <= x (first[0] = 0 <= x).
 __device__ __forceinline__ int owner(const int* first, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
@@ -47,106 +68,158 @@ __device__ __forceinline__ int owner(const int* first, int n, int x) {
   return lo;
 }
 
+template <int kC>
 __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   extern __shared__ int sh[];
-  __shared__ int64_t tmp[32];
-  const int n = a.n_lanes, tid = threadIdx.x;
-  int* const held = sh;          // tokens kept
-  int* const pages0 = sh + n;    // running sum of the pages wanted
-  int* const rows0 = pages0 + n; // running sum of the rows (and first of the pages let go)
+  __shared__ Three tmp3[kW];
+  __shared__ int tmp[2][kW];
+  __shared__ int free_of[8];
+  static_assert(kC <= 8, "free_of");
+  cg::cluster_group cluster = cg::this_cluster();
+  auto sync = [&] {
+    if constexpr (kC == 1) __syncthreads();
+    else cluster.sync();
+  };
+  const int c = kC == 1 ? 0 : (int)cluster.block_rank();
+  const int n = a.n_lanes, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* const held = sh;           // tokens kept
+  int* const pages0 = sh + n;     // running sum of the pages wanted
+  int* const rows0 = pages0 + n;  // of the rows
+  int* const gone0 = rows0 + n;   // of the pages let go
+  if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
   const int cap = a.max_pages * a.page_size, add = a.page_size - 1;
-  auto pages_of = [&](int64_t tokens) { return (int)a.by_page.div((uint32_t)(tokens + add)); };
+  auto pages_of = [&](int tokens) { return (int)a.by_page.div((uint32_t)(tokens + add)); };
+  // ---- the lanes' running sums
   const int each = (n + kT - 1) / kT, l0 = min(n, tid * each), l1 = min(n, l0 + each);
-  int64_t gone_n;
-  {
-    int64_t mine = 0;
-    for (int l = l0; l < l1; ++l) {
-      const int had = max(0, min(a.lengths[l], cap));
-      const int keep = a.keep ? max(0, a.keep[l]) : had;
-      held[l] = min(had, keep);
-      mine += pages_of(had) - pages_of(held[l]);
-    }
-    int64_t at = block_scan(mine, tmp, gone_n);
-    for (int l = l0; l < l1; ++l) {
-      rows0[l] = (int)at;
-      at += pages_of(max(0, min(a.lengths[l], cap))) - pages_of(held[l]);
-    }
-  }
-  __syncthreads();
-  // ---- 1. pages let go
-  for (int64_t t = tid; t < gone_n; t += kT) {
-    const int l = owner(rows0, n, (int)t);
-    int32_t* const e = a.table + (int64_t)l * a.max_pages + pages_of(held[l]) + ((int)t - rows0[l]);
-    const int p = *e;
-    *e = -1;
-    if (p >= 0 && p < a.n_pages && atomicSub(a.holders + p, 1) <= 0) atomicAdd(a.holders + p, 1);
-  }
-  __syncthreads();
-  // ---- what the lanes want
-  int64_t want_n, rows_n;
+  auto of_lane = [&](int l, int& keeps) {
+    const int had = max(0, min(a.lengths[l], cap));
+    keeps = a.keep ? min(had, max(0, a.keep[l])) : had;
+    const int64_t grow = max(0, a.grow[l]), end = keeps + grow;
+    const int first = pages_of(keeps);
+    return Three{pages_of(had) - first, end <= cap ? pages_of((int)end) - first : (end + add) / a.page_size - first, grow};
+  };
   bool past = false;
-  {
-    int64_t want = 0, rows = 0;
+  Three mine = {}, total;
+  for (int l = l0; l < l1; ++l) {
+    int keeps;
+    const Three t = of_lane(l, keeps);
+    past |= keeps + t.c > cap;
+    held[l] = keeps;
+    mine = mine + t;
+  }
+  Three run = block_scan(mine, tmp3, total);
+  if (each == 1) {
+    if (l0 < l1) gone0[l0] = (int)run.a, pages0[l0] = (int)run.b, rows0[l0] = (int)run.c;
+  } else {
     for (int l = l0; l < l1; ++l) {
-      const int64_t g = max(0, a.grow[l]), end = held[l] + g;
-      past |= end > cap;
-      rows += g;
-      if (end <= cap) want += pages_of(end) - pages_of(held[l]);
-      else want += (end + add) / a.page_size - pages_of(held[l]);
-    }
-    int64_t at = block_scan(want, tmp, want_n), row = block_scan(rows, tmp, rows_n);
-    for (int l = l0; l < l1; ++l) {
-      const int64_t g = max(0, a.grow[l]), end = held[l] + g;
-      pages0[l] = (int)at;
-      rows0[l] = (int)row;
-      at += end <= cap ? pages_of(end) - pages_of(held[l]) : 0;
-      row += g;
+      int keeps;
+      const Three t = of_lane(l, keeps);
+      gone0[l] = (int)run.a, pages0[l] = (int)run.b, rows0[l] = (int)run.c;
+      run = run + t;
     }
   }
   past = __syncthreads_or(past);
-  // ---- free pages
-  int64_t free_n = 0;
-  {
-    int64_t mine = 0;
-    for (int p = tid; p < a.n_pages; p += kT) mine += __ldcg(a.holders + p) == 0;
-    block_scan(mine, tmp, free_n);
+  if constexpr (kC > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // ---- 1. pages let go (past 2^31 of them the running sums do not count: lane by lane)
+  if (total.a > 0) {
+    auto let_go = [&](int l, int j) {
+      int32_t* const e = a.table + (int64_t)l * a.max_pages + j;
+      const int p = *e;
+      *e = -1;
+      if (p >= 0 && p < a.n_pages && atomicSub(a.holders + p, 1) <= 0) atomicAdd(a.holders + p, 1);
+    };
+    if (total.a <= INT32_MAX) {
+      for (int64_t t = c * kT + tid; t < total.a; t += kC * kT) {
+        const int l = owner(gone0, n, (int)t);
+        let_go(l, pages_of(held[l]) + ((int)t - gone0[l]));
+      }
+    } else {
+      for (int l = c; l < n; l += kC) {
+        const int end = pages_of(max(0, min(a.lengths[l], cap)));
+        for (int j = pages_of(held[l]) + tid; j < end; j += kT) let_go(l, j);
+      }
+    }
+    sync();
   }
-  const int code = past || want_n > free_n ? a.code_full : rows_n > a.max_rows ? a.code_rows : 0;
+  // ---- free pages: this block's are page0 .. page1 - 1, 32 a warp's word
+  const int words = (a.n_pages + 31) / 32;
+  const int word0 = (int)((int64_t)words * c / kC), word1 = (int)((int64_t)words * (c + 1) / kC);
+  auto free_word = [&](int w) {  // by the whole warp
+    const int p = 32 * w + lane;
+    return __ballot_sync(kAll, p < a.n_pages && __ldcg(a.holders + p) == 0);
+  };
+  // the first 1024 words, a warp 32 of them, stay with the threads
+  unsigned word = 0;
+  const int mine0 = word0 + warp * 32;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const unsigned m = mine0 + i < word1 ? free_word(mine0 + i) : 0;
+    if (i == lane) word = m;
+  }
+  int rest = 0;
+  for (int w = word0 + kT + warp; w < word1; w += kW) rest += __popc(free_word(w));  // the same in all lanes
+  int here, first_n;
+  const int rank_in = block_scan(__popc(word), tmp[0], first_n);
+  {
+    int rest_n;
+    block_scan(lane == 0 ? rest : 0, tmp[1], rest_n);
+    here = first_n + rest_n;
+  }
+  int before = 0, free_n = here;
+  if constexpr (kC > 1) {
+    if (tid < kC) *cluster.map_shared_rank(&free_of[c], tid) = here;
+    sync();
+    free_n = 0;
+    for (int b = 0; b < kC; ++b) {
+      if (b == c) before = free_n;
+      free_n += free_of[b];
+    }
+  }
+  const int code = past || total.b > free_n ? a.code_full : total.c > a.max_rows ? a.code_rows : 0;
   const bool ok = code == 0;
   // ---- 2. the j-th free page is the j-th wanted
   if (ok) {
-    int64_t rank0 = 0;
-    for (int p0 = 0; p0 < a.n_pages && rank0 < want_n; p0 += kT) {
-      const int p = p0 + tid;
-      const bool is_free = p < a.n_pages && __ldcg(a.holders + p) == 0;
-      int64_t found;
-      const int64_t rank = rank0 + block_scan(is_free, tmp, found);
-      if (is_free && rank < want_n) {
-        const int l = owner(pages0, n, (int)rank);
-        a.table[(int64_t)l * a.max_pages + pages_of(held[l]) + ((int)rank - pages0[l])] = p;
-        a.holders[p] = 1;
+    const int want = (int)total.b;
+    auto take = [&](int p, int rank) {
+      const int l = owner(pages0, n, rank);
+      a.table[(int64_t)l * a.max_pages + pages_of(held[l]) + (rank - pages0[l])] = p;
+      a.holders[p] = 1;
+    };
+    int rank = before + rank_in;
+    for (unsigned m = word; m && rank < want; m &= m - 1, ++rank) take(32 * (mine0 + lane) + __ffs(m) - 1, rank);
+    rank = before + first_n;
+    for (int w0 = word0 + kT; w0 < word1 && rank < want; w0 += kW) {
+      const int w = w0 + warp;
+      const unsigned m = w < word1 ? free_word(w) : 0;
+      int found;
+      __syncthreads();
+      const int ahead = block_scan(lane == 0 ? __popc(m) : 0, tmp[0], found);
+      const int first = rank + at(ahead, 0);
+      if ((m >> lane) & 1) {
+        const int r = first + __popc(m & ((1u << lane) - 1));
+        if (r < want) take(32 * w + lane, r);
       }
-      rank0 += found;
+      rank += found;
     }
   }
-  __syncthreads();
   // ---- 3. lanes and rows
-  for (int l = tid; l < n; l += kT) {
+  sync();
+  for (int l = c * kT + tid; l < n; l += kC * kT) {
     a.row_start[l] = ok ? rows0[l] : 0;
-    if (l == 0) a.row_start[n] = ok ? (int)rows_n : 0;
     a.lengths[l] = held[l] + (ok ? max(0, a.grow[l]) : 0);
   }
-  if (tid == 0) {
+  if (c == 0 && tid == 0) {
     const int64_t most = INT32_MAX;
+    a.row_start[n] = ok ? (int)total.c : 0;
     a.status[0] = code;
-    a.status[1] = (int)min(rows_n, most);
-    a.status[2] = (int)min(want_n, most);
-    a.status[3] = (int)free_n;
+    a.status[1] = (int)min(total.c, most);
+    a.status[2] = (int)min(total.b, most);
+    a.status[3] = free_n;
   }
-  const int rows = ok ? (int)rows_n : 0;
-  for (int64_t r64 = tid; r64 < a.max_rows; r64 += kT) {
+  const int rows = ok ? (int)total.c : 0;
+  for (int64_t r64 = c * kT + tid; r64 < a.max_rows; r64 += kC * kT) {
     const int r = (int)r64;
     int l = -1, pos = -1;
     int64_t slot = -1;
@@ -155,7 +228,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
       pos = held[l] + (r - rows0[l]);
       const int j = a.by_page.div((uint32_t)pos);
       if (a.row_slot)
-        slot = (int64_t)a.table[(int64_t)l * a.max_pages + j] * a.page_size + (pos - j * a.page_size);
+        slot = (int64_t)__ldcg(a.table + (int64_t)l * a.max_pages + j) * a.page_size + (pos - j * a.page_size);
     }
     if (a.row_lane) a.row_lane[r] = l;
     if (a.row_position) a.row_position[r] = pos;
@@ -164,15 +237,23 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   }
 }
 
-}  // namespace
-
-Launched launch_pages(const PagesArgs& a, cudaStream_t s) {
+template <int kC>
+Launched launch_c(const PagesArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_pages, kMaxPageLanes * 12, done);
+  l.error = allow_smem(k_pages<kC>, kMaxPageLanes * 16, done);
   if (l.error != cudaSuccess) return l;
-  l.add(launch_k(k_pages, dim3(1), kT, (size_t)a.n_lanes * 12, s, a));
+  const size_t smem = (size_t)a.n_lanes * 16;
+  if constexpr (kC == 1) l.add(launch_k(k_pages<1>, dim3(1), kT, smem, s, a));
+  else l.add(launch_k_cluster(k_pages<kC>, dim3(kC), kT, smem, s, kC, a));
   return l;
+}
+
+}  // namespace
+
+// One block for small pools and batches, which saves the cluster's barriers.
+Launched launch_pages(const PagesArgs& a, cudaStream_t s) {
+  return a.n_pages <= 32768 && a.max_rows <= 4096 && a.n_lanes <= 1024 ? launch_c<1>(a, s) : launch_c<8>(a, s);
 }
 
 }  // namespace fsk

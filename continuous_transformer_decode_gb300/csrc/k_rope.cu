@@ -88,56 +88,80 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
     return h < a.H ? static_cast<T*>(a.q_out) + row * a.qo_stride + (int64_t)h * a.hd
                    : static_cast<T*>(a.k_out) + row * a.ko_stride + (int64_t)(h - a.H) * a.hd;
   };
+  // kH heads at a time: their loads are asked for before the first store
+  constexpr int kH = 4;
   if (unit >= turned) {  // behind the turned values (out of place)
-    const int at = a.rot + (unit - turned) * (kBytes / (int)sizeof(T));
-    for (int h = h0; h < h1; ++h) {
-      Vals<T, kBytes / (int)sizeof(T), kBytes> x;
-      x.load(in(h) + at);
-      x.store(out(h) + at);
+    constexpr int kE = kBytes / (int)sizeof(T);
+    const int at = a.rot + (unit - turned) * kE;
+#pragma unroll 1
+    for (int h = h0; h < h1; h += kH) {
+      Vals<T, kE, kBytes> x[kH];
+#pragma unroll
+      for (int u = 0; u < kH; ++u)
+        if (h + u < h1) x[u].load(in(h + u) + at);
+#pragma unroll
+      for (int u = 0; u < kH; ++u)
+        if (h + u < h1) x[u].store(out(h + u) + at);
     }
     return;
   }
   float2 cs[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) cs[i] = turn((uint32_t)pos, a.F[unit * kP + i], a.factor, a.inverse);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const T* p = in(h);
-    T* o = out(h);
+#pragma unroll 1
+  for (int h = h0; h < h1; h += kH) {
     if constexpr (kNear) {
-      Vals<T, 2 * kP, kBytes> x;
-      x.load(p + unit * 2 * kP);
+      Vals<T, 2 * kP, kBytes> x[kH];
 #pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        const float u = x.get(2 * i), v = x.get(2 * i + 1);
-        x.set(2 * i, fmaf(u, cs[i].x, -v * cs[i].y));
-        x.set(2 * i + 1, fmaf(v, cs[i].x, u * cs[i].y));
+      for (int u = 0; u < kH; ++u)
+        if (h + u < h1) x[u].load(in(h + u) + unit * 2 * kP);
+#pragma unroll
+      for (int u = 0; u < kH; ++u) {
+        if (h + u >= h1) break;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const float v = x[u].get(2 * i), w = x[u].get(2 * i + 1);
+          x[u].set(2 * i, fmaf(v, cs[i].x, -w * cs[i].y));
+          x[u].set(2 * i + 1, fmaf(w, cs[i].x, v * cs[i].y));
+        }
+        x[u].store(out(h + u) + unit * 2 * kP);
       }
-      x.store(o + unit * 2 * kP);
     } else {
-      Vals<T, kP, kBytes> x, y;
-      x.load(p + unit * kP);
-      y.load(p + half + unit * kP);
+      Vals<T, kP, kBytes> x[kH], y[kH];
 #pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        const float u = x.get(i), v = y.get(i);
-        x.set(i, fmaf(u, cs[i].x, -v * cs[i].y));
-        y.set(i, fmaf(v, cs[i].x, u * cs[i].y));
+      for (int u = 0; u < kH; ++u)
+        if (h + u < h1) {
+          x[u].load(in(h + u) + unit * kP);
+          y[u].load(in(h + u) + half + unit * kP);
+        }
+#pragma unroll
+      for (int u = 0; u < kH; ++u) {
+        if (h + u >= h1) break;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const float v = x[u].get(i), w = y[u].get(i);
+          x[u].set(i, fmaf(v, cs[i].x, -w * cs[i].y));
+          y[u].set(i, fmaf(w, cs[i].x, v * cs[i].y));
+        }
+        x[u].store(out(h + u) + unit * kP);
+        y[u].store(out(h + u) + half + unit * kP);
       }
-      x.store(o + unit * kP);
-      y.store(o + half + unit * kP);
     }
   }
 }
 
 template <typename T, int kBytes>
-Launched launch_t(RopeArgs a, bool near, cudaStream_t s) {
+Launched launch_t(RopeArgs a, bool near, int sms, cudaStream_t s) {
   constexpr int kE = kBytes / (int)sizeof(T);
   const int p = near ? std::max(1, kE / 2) : kE;
   const bool copies = a.q_out != a.q || (a.Hkv > 0 && a.k_out != a.k);
   a.units = a.rot / 2 / p + (copies ? (a.hd - a.rot) / kE : 0);
-  a.per = a.H + a.Hkv;
-  a.groups = 1;
+  // heads a thread: all, or as few as fill the SMs' threads (latency)
+  const int heads = a.H + a.Hkv;
+  const int64_t fill = (int64_t)sms * 2048 / std::max<int64_t>(1, (int64_t)a.n * a.units);
+  a.groups = (int)std::min<int64_t>(heads, std::max<int64_t>(1, fill));
+  a.per = (heads + a.groups - 1) / a.groups;
+  a.groups = (heads + a.per - 1) / a.per;
   const int64_t threads = (int64_t)a.n * a.groups * a.units;
   Launched l;
   l.add(launch_k(near ? k_rope<T, kBytes, true> : k_rope<T, kBytes, false>,
@@ -147,7 +171,7 @@ Launched launch_t(RopeArgs a, bool near, cudaStream_t s) {
 
 // The widest vectors that every row, head, half and the copied rest start and end on.
 template <typename T>
-Launched launch_x(const RopeArgs& a, bool near, cudaStream_t s) {
+Launched launch_x(const RopeArgs& a, bool near, int sms, cudaStream_t s) {
   const int64_t e = sizeof(T);
   int64_t all = (int64_t)reinterpret_cast<uintptr_t>(a.q) | (int64_t)reinterpret_cast<uintptr_t>(a.q_out) |
                 a.hd * e | a.rot * e | (near ? 0 : a.rot / 2 * e);
@@ -156,16 +180,16 @@ Launched launch_x(const RopeArgs& a, bool near, cudaStream_t s) {
     all |= (int64_t)reinterpret_cast<uintptr_t>(a.k) | (int64_t)reinterpret_cast<uintptr_t>(a.k_out);
     if (a.n > 1) all |= a.k_stride * e | a.ko_stride * e;
   }
-  if (all % 16 == 0) return launch_t<T, 16>(a, near, s);
-  if (sizeof(T) == 4 || all % 4 == 0) return launch_t<T, 4>(a, near, s);
-  if constexpr (sizeof(T) == 2) return launch_t<T, 2>(a, near, s);
+  if (all % 16 == 0) return launch_t<T, 16>(a, near, sms, s);
+  if (sizeof(T) == 4 || all % 4 == 0) return launch_t<T, 4>(a, near, sms, s);
+  if constexpr (sizeof(T) == 2) return launch_t<T, 2>(a, near, sms, s);
   return {};
 }
 
 }  // namespace
 
-Launched launch_rope(const RopeArgs& a, int x_type, bool near, cudaStream_t s) {
-  return x_type == X_F32 ? launch_x<float>(a, near, s) : launch_x<__nv_bfloat16>(a, near, s);
+Launched launch_rope(const RopeArgs& a, int x_type, bool near, int sms, cudaStream_t s) {
+  return x_type == X_F32 ? launch_x<float>(a, near, sms, s) : launch_x<__nv_bfloat16>(a, near, sms, s);
 }
 
 }  // namespace fsk

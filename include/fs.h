@@ -639,7 +639,7 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
  * let go entry outside [0, n_pages) is only cleared, and a page that nobody holds
  * stays free. A page that several lanes hold is one that no lane will write: a lane
  * that shares its last, partial page must be given a copy before it grows. At most
- * 16384 lanes; max_pages * page_size at most 2^30. One call at a time on one pool. */
+ * 8192 lanes; max_pages * page_size at most 2^30. One call at a time on one pool. */
 int fs_pages_update(int32_t* holders, int32_t n_pages, int32_t* page_table, int32_t* lengths,
                     int32_t n_lanes, int32_t max_pages, int32_t page_size, const int32_t* keep,
                     const int32_t* grow, int32_t* row_start, int32_t* row_lane,

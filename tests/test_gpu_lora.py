@@ -120,6 +120,20 @@ def test_a_rows_bits_do_not_depend_on_the_batch(n):
     assert torch.equal(run(d), whole[order])
 
 
+@pytest.mark.parametrize("xb,yb", [(True, False), (False, True)])
+def test_a_rows_bits_are_the_same_in_large_batches(xb, yb):
+    """Batches of all sizes that are taken in tiles of other heights."""
+    import torch
+    rng = np.random.default_rng(9)
+    c = make(rng, 3001, 1000, 77, 5, 40, xb, yb, np.repeat(rng.integers(-1, 5, 30), 101)[:3001])
+    whole = run(c)
+    check(c, whole)
+    for n in (1, 130, 1000, 1024, 1025):
+        order = rng.permutation(3001)[:n]
+        d = dict(c, x=c["x"][order].contiguous(), adapter=c["adapter"][order].contiguous(), base=c["base"][order].contiguous())
+        assert torch.equal(run(d), whole[order])
+
+
 def test_what_is_no_number_stays_in_its_row():
     import torch
     rng = np.random.default_rng(10)

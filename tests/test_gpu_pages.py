@@ -134,9 +134,9 @@ def test_lengths_outside_the_lane():
 
 def test_large_pool_and_many_lanes():
     rng = np.random.default_rng(3)
-    pool = Pool(300001, 16384, 9, 16, 0.5, rng)
-    pool.update(rng.integers(0, 60, 16384), max_rows=600000)
-    pool.update(rng.integers(0, 9, 16384), keep=rng.integers(0, 80, 16384), max_rows=140000)
+    pool = Pool(300001, 8192, 9, 16, 0.5, rng)
+    pool.update(rng.integers(0, 60, 8192), max_rows=600000)
+    pool.update(rng.integers(0, 9, 8192), keep=rng.integers(0, 80, 8192), max_rows=140000)
 
 
 def test_long_lane_retired():

@@ -68,7 +68,7 @@ def test_the_calls_that_are_varied_are_refused_for_their_addresses_alone():
 
 @pytest.mark.parametrize("bad", [
     dict(holders=None), dict(table=None), dict(lengths=None), dict(grow=None), dict(start=None),
-    dict(status=None), dict(n_pages=0), dict(n_lanes=0), dict(n_lanes=16385), dict(max_pages=0),
+    dict(status=None), dict(n_pages=0), dict(n_lanes=0), dict(n_lanes=8193), dict(max_pages=0),
     dict(page=0), dict(page=-1), dict(rows=-1), dict(max_pages=1 << 16, page=(1 << 14) + 1),
     dict(holders=MB + 2), dict(keep=4 * MB + 1), dict(pos=8 * MB + 2), dict(slot=10 * MB + 4),
     dict(lengths=3 * MB, keep=3 * MB), dict(grow=3 * MB), dict(lane=8 * MB + 4), dict(status=2 * MB + 8),
