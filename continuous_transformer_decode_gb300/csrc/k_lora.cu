@@ -86,6 +86,17 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = x[i];
       }
+      parts(v);
+    }
+  }
+  // from shared memory, its halves swapped if `odd`
+  __device__ __forceinline__ void load2(const unsigned char* p, bool odd) {
+    const float4 a = *reinterpret_cast<const float4*>(p + (odd ? 16 : 0)), b = *reinterpret_cast<const float4*>(p + (odd ? 0 : 16));
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    parts(v);
+  }
+  __device__ __forceinline__ void parts(const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
       __nv_bfloat16* out[3] = {reinterpret_cast<__nv_bfloat16*>(&p[0]), reinterpret_cast<__nv_bfloat16*>(&p[1]),
                                reinterpret_cast<__nv_bfloat16*>(&p[2])};
 #pragma unroll
@@ -106,47 +117,53 @@ __device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint
   attn::mma16816(d, a1, b.z, b.w);
 }
 
+// 8 consecutive values as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, int n, float (&v)[8]) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Raw8 {
+  static constexpr int kV = sizeof(T) / 2;
+  uint4 v[kV];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  // the first n of p (whole: all 8, 16-byte aligned)
+  __device__ __forceinline__ void load(const T* p, bool whole, int n) {
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(&u);
+      clear();
+      T* t = reinterpret_cast<T*>(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(h[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (sizeof(T) == 4) v[i] = i < n ? p[i] : 0.0f;
-      else v[i] = i < n ? __bfloat162float(p[i]) : 0.0f;
+      for (int i = 0; i < 8; ++i)
+        if (i < n) t[i] = p[i];
     }
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, bool vec, int n, const float (&v)[8]) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint4 u;
-      u.x = attn::pack_bf16(v[0], v[1]), u.y = attn::pack_bf16(v[2], v[3]);
-      u.z = attn::pack_bf16(v[4], v[5]), u.w = attn::pack_bf16(v[6], v[7]);
-      *reinterpret_cast<uint4*>(p) = u;
-    }
-  } else {
+  __device__ __forceinline__ void store(T* p, bool whole, int n) const {
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        if constexpr (sizeof(T) == 4) p[i] = v[i];
-        else p[i] = __float2bfloat16_rn(v[i]);
-      }
+      for (int i = 0; i < kV; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    } else {
+      const T* t = reinterpret_cast<const T*>(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = t[i];
+    }
   }
+  // values 2 i and 2 i + 1 plus (a, b)
+  __device__ __forceinline__ void add2(int i, float a, float b) {
+    if constexpr (sizeof(T) == 4) {
+      float* f = reinterpret_cast<float*>(v);
+      f[2 * i] += a, f[2 * i + 1] += b;
+    } else {
+      uint32_t* u = reinterpret_cast<uint32_t*>(v);
+      u[i] = attn::pack_bf16(__uint_as_float(u[i] << 16) + a, __uint_as_float(u[i] & 0xffff0000u) + b);
+    }
+  }
+};
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 struct Gather {
@@ -159,28 +176,37 @@ struct Gather {
   int firsts[kW], bare[kW];
 };
 
-// Shared memory behind Gather: the parts of A x, [part][row] of `pitch` values, and f32
-// sums: a tile a warp and a tile a block of the cluster (kMT 1), or the block's own.
+// Shared memory behind Gather. kMT 1: the parts of A x, [part][row] of `pitch` values, and
+// f32 tiles of sums, a warp's and a block's each. kMT 4: the block's own sums, and stages of
+// the first product (64 of K, of the rows and of A), where the parts of A x lie afterwards.
+constexpr int kStages = 4;
 struct Sizes {
-  int pitch;
+  int pitch, stage;
   int64_t low, sums, bytes;
-  __host__ __device__ Sizes(int mt, int parts, int rank) {
+  __host__ __device__ Sizes(int mt, int parts, int rank, int x_bytes) {
     const int blocks = (rank + 31) / 32;
     pitch = 32 * blocks + (blocks % 2 ? 0 : 32);  // rows 64 bytes apart modulo 128: no conflicts
     low = (int64_t)parts * mt * 16 * pitch * 2;
     sums = (int64_t)(mt == 1 ? kW + kC : 1) * mt * 16 * rank * 4;
+    stage = mt * 16 * 64 * x_bytes + rank * 128;
+    if (mt > 1 && low < kStages * stage) low = kStages * stage;
     bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + sums;
   }
 };
 
+// 16 bytes to shared memory, zeros without `in`.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
 template <typename TX, typename TY, int kMT>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
-  constexpr int kMP = kMT == 1 ? 1 : 2;         // row tiles that share a load of B
+  constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   extern __shared__ __align__(16) unsigned char dyn[];
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
-  const Sizes sz(kMT, kParts, a.rank);
+  const Sizes sz(kMT, kParts, a.rank, sizeof(TX));
   __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
   float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
@@ -247,9 +273,11 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       if (i % per_window != item0) continue;
       const int64_t row = first + warp * 32 + __ffs(m) - 1;
       for (int j = 32 * chunk0 + 8 * lane; j < min(a.N, 32 * chunk1); j += 256) {
-        float v[8] = {};
-        if (base) load8(base + row * a.base_stride + j, y_vec, a.N - j, v);
-        store8(out + row * a.out_stride + j, y_vec, a.N - j, v);
+        const bool whole = y_vec && j + 8 <= a.N;
+        Raw8<TY> v;
+        v.clear();
+        if (base) v.load(base + row * a.base_stride + j, whole, a.N - j);
+        v.store(out + row * a.out_stride + j, whole, a.N - j);
       }
     }
   }
@@ -260,8 +288,24 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   const int tiles = a.rank / 8, rblocks = (a.rank + 31) / 32;
   auto piece = [&](int s) { return kb0 + (kb1 - kb0) * s / kW; };  // the s-th of eight starts here
 
+  // What an item reads is asked into L2 ahead of its use: A (this block's K) and B (its
+  // columns) of all items at once, base with the item.
+  __syncthreads();  // sh.lead
   for (int item = item0; item < items; item += per_window) {
-    __syncthreads();  // also: sh.lead
+    const int64_t id = sh.id[sh.lead[item]];
+    const int line = 64 * (kb1 - kb0);  // bytes of a rank
+    const char* const pa = reinterpret_cast<const char*>(a.A + id * a.rank * a.K + 32 * kb0);
+    for (int i = tid; i < a.rank * ((line + 127) / 128); i += kT) {
+      const int r = i % a.rank, o = i / a.rank * 128;
+      if (32 * kb0 + o / 2 < a.K) prefetch_l2(pa + (int64_t)r * a.K * 2 + o);
+    }
+    const char* const pb = reinterpret_cast<const char*>(a.B + (id * a.N + 32 * chunk0) * a.rank);
+    const int64_t bytes = (int64_t)(min(a.N, 32 * chunk1) - 32 * chunk0) * a.rank * 2;
+    for (int64_t o = 128 * tid; o < bytes; o += 128 * kT) prefetch_l2(pb + o);
+  }
+
+  for (int item = item0; item < items; item += per_window) {
+    __syncthreads();
     const int lead = sh.lead[item], id = sh.id[lead], part = sh.nth[lead] / kR;
     const bool mine = has && my_id == id && nth / kR == part;
     if (mine) sh.row[nth % kR] = my_row;
@@ -272,43 +316,37 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
     if (kMT == 1 && item != item0) cluster.sync();  // the last item's sums have been read
 
-    // sums += x A^T of row tile mt and rank tiles nt0 .. nt0 + 3 over blocks b0 .. b1 - 1
-    auto shrink = [&](int mt, int nt0, int b0, int b1, float (&d)[4][4]) {
-      const int64_t r0 = row_of(16 * mt + g), r1 = row_of(16 * mt + g + 8);
-#pragma unroll 2
-      for (int b = b0; b < b1; ++b) {
-        const int k = 32 * b + 8 * tig;
-        const bool in = k < a.K;
-        Eight<TX> lo, hi;
-        lo.clear(), hi.clear();
-        if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
-        if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
-        uint4 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
-                                       : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(d[j], lo.p[p], hi.p[p], w[j]);
-      }
-    };
-    auto put = [&](float* to, int mt, int nt0, const float (&d)[4][4]) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (nt0 + j < tiles) {
-          float* p = to + (16 * mt + g) * a.rank + 8 * (nt0 + j) + 2 * tig;
-          *reinterpret_cast<float2*>(p) = make_float2(d[j][0], d[j][1]);
-          *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[j][2], d[j][3]);
-        }
+    auto put = [&](float* to, int mt, int nt, const float (&d)[4]) {
+      float* p = to + (16 * mt + g) * a.rank + 8 * nt + 2 * tig;
+      *reinterpret_cast<float2*>(p) = make_float2(d[0], d[1]);
+      *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[2], d[3]);
     };
     const int tile = 16 * a.rank;
     if constexpr (kMT == 1) {
-      for (int nt0 = 0; nt0 < tiles; nt0 += 4) {
+      const int64_t r0 = row_of(g), r1 = row_of(g + 8);
+      for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks, a warp its piece of K
         float d[4][4] = {};
-        shrink(0, nt0, piece(warp), piece(warp + 1), d);
-        put(sums + warp * tile, 0, nt0, d);
+#pragma unroll 2
+        for (int b = piece(warp); b < piece(warp + 1); ++b) {
+          const int k = 32 * b + 8 * tig;
+          const bool in = k < a.K;
+          Eight<TX> lo, hi;
+          lo.clear(), hi.clear();
+          if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
+          if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
+          uint4 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
+                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(d[j], lo.p[p], hi.p[p], w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (nt0 + j < tiles) put(sums + warp * tile, 0, nt0 + j, d[j]);
       }
       __syncthreads();
       for (int i = tid; i < tile; i += kT) {
@@ -336,20 +374,104 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       __syncthreads();
     } else {
       static_assert(kMT == 4, "eight warps are four row tiles and two halves of the ranks");
-      const int mt = warp & 3;
-      for (int nt0 = 4 * (warp >> 2); nt0 < tiles; nt0 += 8) {
-        float d[4][4] = {};
-        if (16 * mt < rows)
-          for (int s = 0; s < kW; ++s) {
-            float e[4][4] = {};
-            shrink(mt, nt0, piece(s), piece(s + 1), e);
+      const int mt = warp & 3, half = warp >> 2;  // tiles half, half + 2, .. of the ranks
+      // Steps of up to two blocks of K inside a piece, kStages - 1 of them on their way. A
+      // row of a stage is 128 bytes (f32 x: 256), its 16-byte parts swapped in odd rows so
+      // that a quarter of a warp reads all banks.
+      constexpr int kXC = 4 * (int)sizeof(TX);  // 16-byte parts of a row of x
+      unsigned char* const stages = reinterpret_cast<unsigned char*>(low);
+      struct Step {
+        int s, b;
+      };
+      auto settle = [&](Step t) {  // past pieces that are done
+        while (t.s < kW && t.b >= piece(t.s + 1)) ++t.s;
+        return t;
+      };
+      auto after = [&](Step t) {
+        t.b = min(t.b + 2, piece(t.s + 1));
+        return settle(t);
+      };
+      auto fetch = [&](Step t, int slot) {
+        if (t.s < kW) {
+          unsigned char* const sx = stages + slot * sz.stage;
+          unsigned char* const sa = sx + kR * 16 * kXC;
+          for (int i = tid; i < kR * kXC; i += kT) {
+            const int r = i / kXC, q = i % kXC, k = 32 * t.b + q * 16 / (int)sizeof(TX);
+            const bool in = r < rows && k < a.K;
+            const int64_t o = in ? sh.row[r] * a.x_stride + k : 0;
+            unsigned char* const to = sx + r * 16 * kXC + 16 * (q ^ (r & 1) * (sizeof(TX) == 2 ? 4 : 1));
+            if (x_vec) {
+              copy16(attn::smem_u32(to), x + o, in);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) d[j][q] = s == 0 ? e[j][q] : d[j][q] + e[j][q];
+              for (int e = 0; e < 16 / (int)sizeof(TX); ++e) reinterpret_cast<TX*>(to)[e] = in ? x[o + e] : TX(0.0f);
+            }
           }
-        put(sums, mt, nt0, d);
+          for (int i = tid; i < a.rank * 8; i += kT) {
+            const int r = i / 8, q = i % 8, k = 32 * t.b + 8 * q;
+            copy16(attn::smem_u32(sa + r * 128 + 16 * (q ^ (r & 1) * 4)), A + (k < a.K ? (int64_t)r * a.K + k : 0), k < a.K);
+          }
+        }
+        attn::cp_commit();
+      };
+      float d[8][4] = {}, e[8][4] = {};
+      Step now = settle({0, kb0}), ahead = now;
+      int slot = 0, last = -1;
+      for (int i = 0; i < kStages - 1; ++i) {
+        fetch(ahead, i);
+        ahead = after(ahead);
       }
+      auto add_piece = [&](int s) {  // the first piece's sums are the start
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            d[j][q] = s == 0 ? e[j][q] : d[j][q] + e[j][q];
+            e[j][q] = 0.0f;
+          }
+      };
+      while (now.s < kW) {
+        attn::cp_wait<kStages - 2>();
+        __syncthreads();
+        fetch(ahead, (slot + kStages - 1) % kStages);
+        ahead = after(ahead);
+        if (last >= 0 && last != now.s) add_piece(last);
+        last = now.s;
+        const unsigned char* const sx = stages + slot * sz.stage;
+        const unsigned char* const sa = sx + kR * 16 * kXC;
+        if (16 * mt < rows) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (now.b + b >= piece(now.s + 1)) break;
+            Eight<TX> lo, hi;
+            const unsigned char* const px = sx + (16 * mt + g) * 16 * kXC;
+            if constexpr (sizeof(TX) == 2) {
+              const int q = 16 * ((4 * b + tig) ^ ((g & 1) * 4));
+              lo.load(reinterpret_cast<const TX*>(px + q), true);
+              hi.load(reinterpret_cast<const TX*>(px + 8 * 16 * kXC + q), true);
+            } else {
+              const int q = 16 * (8 * b + 2 * tig);
+              lo.load2(px + q, g & 1);
+              hi.load2(px + 8 * 16 * kXC + q, g & 1);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int nt = half + 2 * j;
+              if (nt >= tiles) break;
+              const uint4 w = *reinterpret_cast<const uint4*>(sa + (8 * nt + g) * 128 + 16 * ((4 * b + tig) ^ ((g & 1) * 4)));
+#pragma unroll
+              for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(e[j], lo.p[p], hi.p[p], w);
+            }
+          }
+        }
+        now = after(now);
+        slot = (slot + 1) % kStages;
+      }
+      attn::cp_wait<0>();
+      if (last >= 0) add_piece(last);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (half + 2 * j < tiles) put(sums, mt, half + 2 * j, d[j]);
       cluster.sync();
       // this block adds up kR / kC of the rows and gives them to all
       constexpr int kOwn = kR / kC;
@@ -380,58 +502,63 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     }
 
     // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles
+    uint4 w[2][4];
+    auto load_b = [&](int chunk, int b0) {  // tile j's column g over two blocks of ranks
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int r = 32 * (b0 + b) + 8 * tig;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = 32 * chunk + 8 * (g >> 1) + 2 * j + (g & 1);
+          w[b][j] = r < a.rank && n < a.N ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.rank + r)
+                                          : make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
     for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW) {
-      const int col = 32 * chunk + 8 * tig, left = a.N - col;
+      const int col = 32 * chunk + 8 * tig;
+      const bool whole = y_vec && 32 * chunk + 32 <= a.N;
+      if (rblocks <= 2) load_b(chunk, 0);
 #pragma unroll 1
       for (int m0 = 0; m0 < kMT; m0 += kMP) {
         if (16 * m0 >= rows) break;
-        float y[kMP][2][8];
+        Raw8<TY> y[kMP][2];
+        int row[kMP][2];
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int64_t r = row_of(16 * (m0 + m) + g + 8 * h);
-            if (base && r >= 0) {
-              load8(base + r * a.base_stride + col, y_vec, left, y[m][h]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[m][h][i] = 0.0f;
-            }
+            row[m][h] = row_of(16 * (m0 + m) + g + 8 * h);
+            if (base && row[m][h] >= 0) y[m][h].load(base + row[m][h] * a.base_stride + col, whole, a.N - col);
+            else y[m][h].clear();
           }
         float d[kMP][4][4] = {};
 #pragma unroll 1
-        for (int b = 0; b < rblocks; ++b) {
-          const int r = 32 * b + 8 * tig;
-          uint4 w[4];
+        for (int b0 = 0; b0 < rblocks; b0 += 2) {
+          if (rblocks > 2) load_b(chunk, b0);
+          const __nv_bfloat16* const t = low + (16 * m0 + g) * sz.pitch + 32 * b0 + 8 * tig;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // tile j's column g
-            const int n = 32 * chunk + 8 * (g >> 1) + 2 * j + (g & 1);
-            w[j] = r < a.rank && n < a.N ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.rank + r)
-                                         : make_uint4(0, 0, 0, 0);
+          for (int b = 0; b < 2; ++b) {
+            if (b0 + b >= rblocks) break;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int m = 0; m < kMP; ++m) {
+                const __nv_bfloat16* const u = t + (p * kR + 16 * m) * sz.pitch + 32 * b;
+                const uint4 lo = *reinterpret_cast<const uint4*>(u), hi = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma32(d[m][j], lo, hi, w[b][j]);
+              }
           }
-#pragma unroll
-          for (int m = 0; m < kMP; ++m)
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-              const __nv_bfloat16* t = low + (p * kR + 16 * (m0 + m) + g) * sz.pitch + r;
-              const uint4 lo = *reinterpret_cast<const uint4*>(t), hi = *reinterpret_cast<const uint4*>(t + 8 * sz.pitch);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma32(d[m][j], lo, hi, w[j]);
-            }
         }
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int64_t r = row_of(16 * (m0 + m) + g + 8 * h);
-            if (r < 0 || left <= 0) continue;
-            float v[8];
+            if (row[m][h] < 0) continue;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[2 * j] = y[m][h][2 * j] + d[m][j][2 * h];
-              v[2 * j + 1] = y[m][h][2 * j + 1] + d[m][j][2 * h + 1];
-            }
-            store8(out + r * a.out_stride + col, y_vec, left, v);
+            for (int j = 0; j < 4; ++j) y[m][h].add2(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
+            y[m][h].store(out + row[m][h] * a.out_stride + col, whole, a.N - col);
           }
       }
     }
@@ -443,11 +570,11 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_lora<TX, TY, kMT>, (int)Sizes(kMT, kParts, 128).bytes, done);
+  l.error = allow_smem(k_lora<TX, TY, kMT>, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
   if (l.error != cudaSuccess) return l;
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
   l.add(launch_k_cluster(k_lora<TX, TY, kMT>, dim3((unsigned)(windows * per_window * kC)), kT,
-                         (size_t)Sizes(kMT, kParts, a.rank).bytes, s, kC, a, per_window));
+                         (size_t)Sizes(kMT, kParts, a.rank, sizeof(TX)).bytes, s, kC, a, per_window));
   return l;
 }
 template <typename TX, typename TY>
@@ -456,7 +583,7 @@ Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const bool wide = a.n > 1024;
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  if (wide) return launch_t<TX, TY, 4>(a, (int)std::min<int64_t>(4, std::max<int64_t>(2, fit)), s);
+  if (wide) return launch_t<TX, TY, 4>(a, 8, s);
   return launch_t<TX, TY, 1>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 

@@ -150,13 +150,16 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     const int p = 32 * w + lane;
     return __ballot_sync(kAll, p < a.n_pages && __ldcg(a.holders + p) == 0);
   };
-  // the first 1024 words, a warp 32 of them, stay with the threads
+  // the first 1024 words, shared evenly by the warps, stay with the threads
   unsigned word = 0;
-  const int mine0 = word0 + warp * 32;
-#pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
-    const unsigned m = mine0 + i < word1 ? free_word(mine0 + i) : 0;
-    if (i == lane) word = m;
+  const int share = min(32, (word1 - word0 + kW - 1) / kW), mine0 = word0 + warp * share;
+#pragma unroll 1
+  for (int i0 = 0; i0 < share; i0 += 8) {
+#pragma unroll
+    for (int i = i0; i < i0 + 8; ++i) {
+      const unsigned m = i < share && mine0 + i < word1 ? free_word(mine0 + i) : 0;
+      if (i == lane) word = m;
+    }
   }
   int rest = 0;
   for (int w = word0 + kT + warp; w < word1; w += kW) rest += __popc(free_word(w));  // the same in all lanes
