@@ -8,14 +8,16 @@
 // and once few enough tokens are left they are ranked among themselves.
 //
 // Whole-number answers need more than f32 (a cut lies between tokens whose weights are
-// 1e-6 of the sum): weights are good to 2^-36 (draw.cuh) and are summed as whole numbers
-// of 2^-40 of their bin's largest weight, so that sums do not depend on their order; sums
-// of bins, and a draw's running sums, are pairs of f32 numbers.
+// 1e-6 of the sum): weights are whole numbers of 2^-39 of their bin's largest, good to
+// 2^-38, and their sums do not depend on the order; sums of bins, and a draw's running sums,
+// are pairs of f32 numbers. (f64 runs at 1/60 of f32's rate here.)
 //
 // One thread-block cluster serves a row and reads it once, into shared memory. A thread has
 // a run of consecutive tokens and a column of the bins' counts and masses for itself (no
 // atomics). What the draw needs, the kept mass of each run in order, is then the sum of a
 // column's bins ahead of the cut; only the tokens of the cut's own bin are weighed again.
+// They are gathered first (a tenth of the tokens, in lanes of their own), as the split and
+// the ranking want them as well.
 
 #include <cooperative_groups.h>
 
@@ -30,9 +32,9 @@ using namespace draw;
 namespace cg = cooperative_groups;
 
 constexpr int kBins = 24;   // of y: [b, b + 1), the last one also all above
-constexpr int kSub = 32;    // parts of a bin that is split
-constexpr int kList = 256;  // tokens that are ranked among themselves
-constexpr int kFrac = 40;   // a mass in bin b is a whole number of 2^-(b + kFrac)
+constexpr int kSub = 64;    // parts of a bin that is split
+constexpr int kList = 128;  // tokens that are ranked among themselves
+constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(b + kFrac)
 constexpr int kCount = 50;  // a column's entry: count << kCount | mass
 
 struct Bin {
@@ -47,24 +49,28 @@ struct Kept {
   Two mass;
   int count;
 };
+struct Power {  // 2^(k/256): times 2^kFrac, and as a pair
+  uint64_t whole;
+  float h, l;
+};
 
 template <int kC, int kW>
 struct Shared {
-  float2 tab[32];
+  Power tab[256];
   Best best[kC * kW];
   Kept kept[kC * kW];
   Bin bins[kC][kBins];
-  Bin sub[2][kC][kSub];
+  Bin sub[kC][kSub];
   unsigned long long sub_mass[kSub];
   uint32_t sub_count[kSub];
-  uint64_t range[2][kC][2];
+  uint64_t range[kC][2];
   unsigned long long lo, hi;
   uint64_t list[2][kList], sorted[kList];
   Two scan[kW];
   int hit, fill;
 };
 
-__device__ __forceinline__ Two to_two(uint64_t m, int e) {  // m * 2^e
+__device__ __forceinline__ Two to_two(uint64_t m, int e) {  // m * 2^e, e > -127
   const float h = __ull2float_rn(m);
   const float l = (float)(long long)(m - (uint64_t)h);
   const float s = __int_as_float((127 + e) << 23);
@@ -86,14 +92,43 @@ __device__ __forceinline__ float logit_of(uint64_t r) {
 // -0 as 0 and NaN as -inf.
 __device__ __forceinline__ float clean(float z) { return z == z ? z + 0.0f : -CUDART_INF_F; }
 
+// exp((z - M) / T) = m 2^(n - kFrac), m up to 2^(kFrac + 1); c = log2(e) / T. With y = (z -
+// M) c as a pair, k/256 its nearest multiple of 1/256 and f the rest, 2^f - 1 is its Taylor
+// series (the f^4 term is below 2^-42) and 2^(k/256) comes from the table: Tang's method
+// (ACM TOMS 1989). Below y = -125.5 it is 0, also for -inf.
+__device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* tab, int& n) {
+  const Two d = two_sum(z, -M);
+  const float p = __fmul_rn(d.h, c.h);
+  const float pe = fmaf(d.h, c.h, -p) + fmaf(d.h, c.l, __fmul_rn(d.l, c.h));
+  constexpr float kRound = 49152.0f;  // its last place is 1/256
+  const float t = __fadd_rn(fmaxf(p, -126.0f), kRound);
+  const int k = __float_as_int(t) - __float_as_int(kRound);
+  const float fh = __fsub_rn(p, __fsub_rn(t, kRound));  // exact
+  const float f = __fadd_rn(fh, pe);
+  constexpr float l1h = 0.6931471824645996f, l1l = -1.9046542e-09f;  // ln 2
+  const float a = __fmul_rn(fh, l1h);
+  float ae = fmaf(pe, l1h, fmaf(fh, l1l, fmaf(fh, l1h, -a)));
+  ae = fmaf(__fmul_rn(f, f), fmaf(f, 0.05550411f, 0.2402265f), ae);  // ln2^3 / 6, ln2^2 / 2
+  const Power w = tab[k & 255];
+  const float v = __fmul_rn(w.h, a);
+  const float ve = fmaf(w.l, a, fmaf(w.h, ae, fmaf(w.h, a, -v)));
+  constexpr float kOne = (float)(1ull << kFrac);
+  const uint64_t m = w.whole + (long long)__float2int_rn(v * kOne) + (long long)__float2int_rn(ve * kOne);
+  const bool one = z == M, in = p > -125.5f;  // not in: also -inf and NaN
+  n = one ? 0 : k >> 8;
+  return one ? 1ull << kFrac : in ? m : 0;
+}
+
 template <int kC, int kT>
-__global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held) {
+__global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastDiv by_each, int held) {
   constexpr int kW = kT / 32, kN = kC * kW;
   static_assert(kN <= 64, "two warps a lane");
+  static_assert(kT == 256, "a power of two of the table a thread");
   __shared__ Shared<kC, kW> sh;
   extern __shared__ __align__(16) unsigned char dyn[];
-  uint64_t* const column = reinterpret_cast<uint64_t*>(dyn) + threadIdx.x;  // [kBins] kT apart
-  float* const hold = reinterpret_cast<float*>(dyn + (size_t)kBins * kT * 8);
+  unsigned long long* const columns = reinterpret_cast<unsigned long long*>(dyn);  // [kBins][kT]
+  unsigned long long* const column = columns + threadIdx.x;
+  float* const hold = reinterpret_cast<float*>(columns + kBins * kT);
   cg::cluster_group cluster = cg::this_cluster();
   auto sync = [&] {
     if constexpr (kC == 1) __syncthreads();
@@ -105,22 +140,35 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
   };
   const int rank = kC == 1 ? 0 : (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < 32) sh.tab[tid] = kExp2[tid];
   // the other blocks' shared memory can be written once they have started
   if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  {  // 2^(k/256) = 2^(k/8 / 32) 2^(k%8 / 256)
+    constexpr float2 kFine[8] = {
+        {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.00b1b00000000p+0f, -0x1.6950d00000000p-26f},
+        {0x1.0163da0000000p+0f, 0x1.3f66660000000p-25f}, {0x1.0216820000000p+0f, -0x1.789fb00000000p-25f},
+        {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f}, {0x1.037d420000000p+0f, 0x1.c2377a0000000p-25f},
+        {0x1.04315e0000000p+0f, 0x1.0dcff00000000p-25f}, {0x1.04e5f80000000p+0f, -0x1.a1356a0000000p-25f}};
+    float2 fine = kFine[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if ((tid & 7) == i) fine = kFine[i];
+    const float2 e = kExp2[tid >> 3];
+    const Two w = mul({e.x, e.y}, {fine.x, fine.y});
+    sh.tab[tid] = {(uint64_t)(w.h * (float)(1ull << kFrac)) + (long long)rintf(w.l * (float)(1ull << kFrac)), w.h, w.l};
+  }
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x / kC, V = a.V;
-  const float temp = a.temps[row];
-  const float us = fminf(a.u[row], 1.0f);
-  const bool greedy = !(temp > 0.0f);
-  const Two c = log2e_over(greedy ? 1.0f : fminf(fmaxf(temp, 1e-30f), 1e30f));
+  const float temp = a.temps[row], u_row = a.u[row];
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   // a thread's run; odd, so that the threads of a warp read different banks
   const int each = ((V + kC * kT - 1) / (kC * kT)) | 1;
   const int base = (int)min((int64_t)V, (int64_t)rank * kT * each);
   const int count = (int)min((int64_t)V - base, (int64_t)kT * each);
   const int lo = min(count, tid * each), hi = min(count, lo + each);
   const float* const z_row = a.logits + row * a.ld + base;
+  uint16_t* const gathered = reinterpret_cast<uint16_t*>(hold + min(V, kT * each)) + warp * 32 * each;
   // ---- the row, its maximum (lowest index) and how many tokens it has
   Best best = {-CUDART_INF_F, V, 0};
   auto take = [&](float z, int i) {
@@ -128,7 +176,7 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
     if (z > best.max) best.max = z, best.at = base + i;
   };
   if ((reinterpret_cast<uintptr_t>(z_row) & 15) == 0) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 4 * tid; i < count; i += 4 * kT) {
       float4 v = load4(z_row, i, count, true);
       v.x = clean(v.x), v.y = clean(v.y), v.z = clean(v.z), v.w = clean(v.w);
@@ -143,38 +191,36 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
       take(v.x, i), take(v.y, i + 1), take(v.z, i + 2), take(v.w, i + 3);
     }
   } else {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = tid; i < count; i += kT) {
       const float z = clean(z_row[i]);
       if (held) hold[i] = z;
       take(z, i);
     }
   }
+  auto merge = [&](Best b) {
+    if (b.max > best.max || (b.max == best.max && b.at < best.at)) best.max = b.max, best.at = b.at;
+    best.tokens += b.tokens;
+  };
+  auto merge_lanes = [&] {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m = __shfl_xor_sync(kAll, best.max, o);
-    const int at = __shfl_xor_sync(kAll, best.at, o);
-    if (m > best.max || (m == best.max && at < best.at)) best.max = m, best.at = at;
-    best.tokens += __shfl_xor_sync(kAll, best.tokens, o);
-  }
+    for (int o = 16; o > 0; o >>= 1)
+      merge({__shfl_xor_sync(kAll, best.max, o), __shfl_xor_sync(kAll, best.at, o),
+             __shfl_xor_sync(kAll, best.tokens, o)});
+  };
+  merge_lanes();
+#pragma unroll
+  for (int b = 0; b < kBins; ++b) column[b * kT] = 0;
   if constexpr (kC > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (lane < kC) *remote(&sh.best[rank * kW + warp], lane) = best;
+  const bool greedy = !(temp > 0.0f);
+  const Two c = log2e_over(greedy ? 1.0f : fminf(fmaxf(temp, 1e-30f), 1e30f));
   sync();
   const int e0 = 2 * lane, e1 = 2 * lane + 1;  // a lane's warps of the cluster
-  {
-    const Best none = {-CUDART_INF_F, V, 0};
-    const Best b0 = e0 < kN ? sh.best[e0] : none, b1 = e1 < kN ? sh.best[e1] : none;
-    best = b0;
-    if (b1.max > best.max || (b1.max == best.max && b1.at < best.at)) best.max = b1.max, best.at = b1.at;
-    best.tokens += b1.tokens;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float m = __shfl_xor_sync(kAll, best.max, o);
-      const int at = __shfl_xor_sync(kAll, best.at, o);
-      if (m > best.max || (m == best.max && at < best.at)) best.max = m, best.at = at;
-      best.tokens += __shfl_xor_sync(kAll, best.tokens, o);
-    }
-  }
+  best = {-CUDART_INF_F, V, 0};
+  if (e0 < kN) merge(sh.best[e0]);
+  if (e1 < kN) merge(sh.best[e1]);
+  merge_lanes();
   const float M = best.max;
   if (greedy || best.tokens == 0) {
     if (rank == 0 && tid == 0) {
@@ -183,196 +229,229 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
     }
     return;
   }
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
   const bool by_k = top_k > 0 && top_k < best.tokens, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
 
   auto at = [&](int i) { return held ? hold[i] : clean(z_row[i]); };
   auto y_of = [&](float z) { return z == M ? 0.0f : (M - z) * c.h; };
   auto bin_of = [&](float y) { return min(kBins - 1, (int)y); };
   auto mass_of = [&](float z, int b) {  // the weight as a whole number of 2^-(b + kFrac)
-    const Two w = weight2(z, M, c, sh.tab);  // times 2^60
-    const float s = __int_as_float((127 + b - 60 + kFrac / 2) << 23);
-    const float h = w.h * s, t = rintf(h);
-    return (int64_t)(int)t * (1 << (kFrac / 2)) +
-           (int)rintf(((h - t) + w.l * s) * (float)(1 << (kFrac / 2)));
+    int n;
+    const uint64_t m = weigh(z, M, c, sh.tab, n);
+    return m >> min(63, max(0, -(n + b)));
+  };
+  auto weight = [&](float z) {  // times 2^60
+    int n;
+    const uint64_t m = weigh(z, M, c, sh.tab, n);
+    return to_two(m, n - kFrac + 60);
   };
   // ---- counts and masses of the bins
+  for (int i0 = lo; i0 < hi; i0 += 4) {
+    int b[4];
+    unsigned long long m[4];
 #pragma unroll
-  for (int b = 0; b < kBins; ++b) column[b * kT] = 0;
-#pragma unroll 2
-  for (int i = lo; i < hi; ++i) {
-    const float z = at(i);
-    if (z > -CUDART_INF_F) {
-      const int b = bin_of(y_of(z));
-      column[b * kT] += (uint64_t)mass_of(z, b) + (1ull << kCount);
+    for (int q = 0; q < 4; ++q) {
+      const float z = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
+      b[q] = bin_of(y_of(z));
+      m[q] = z > -CUDART_INF_F ? mass_of(z, b[q]) + (1ull << kCount) : 0;
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) column[b[q] * kT] += m[q];
   }
+  // The tokens of a bin, the warp's in its own part of shared memory; f(z, i) for each of
+  // them, every lane another.
+  int members_of = -1, gathered_n = 0;
+  auto gather = [&](int bin) {
+    if (members_of == bin) return;
+    members_of = bin;
+    if (!held) return;
+    __syncwarp();
+    gathered_n = 0;
+    for (int j = 0; j < each; ++j) {
+      const int i = lo + j;
+      const float z = i < hi ? hold[i] : -CUDART_INF_F;
+      const bool in = z > -CUDART_INF_F && bin_of(y_of(z)) == bin;
+      const unsigned m = __ballot_sync(kAll, in);
+      if (in) gathered[gathered_n + __popc(m & ((1u << lane) - 1))] = (uint16_t)i;
+      gathered_n += __popc(m);
+    }
+    __syncwarp();
+  };
+  auto members = [&](auto f) {
+    if (held) {
+      for (int j = lane; j < gathered_n; j += 32) {
+        const int i = gathered[j];
+        f(hold[i], i);
+      }
+    } else {
+      for (int i = lo; i < hi; ++i) {
+        const float z = at(i);
+        if (z > -CUDART_INF_F && bin_of(y_of(z)) == members_of) f(z, i);
+      }
+    }
+  };
   int cut_bin = kBins;               // all bins ahead of it stay whole
   uint64_t cut = ~0ull;              // the last rank that stays
   if (by_k || by_p) {
     __syncthreads();
     for (int b = warp; b < kBins; b += kW) {
-      uint64_t m = 0;
+      unsigned long long m = 0;
       uint32_t n = 0;
-      const uint64_t* e = reinterpret_cast<const uint64_t*>(dyn) + b * kT;
-      for (int j = lane; j < kT; j += 32) {
-        const uint64_t v = e[j];
+#pragma unroll
+      for (int j = 0; j < kT; j += 32) {
+        const unsigned long long v = columns[b * kT + j + lane];
         n += (uint32_t)(v >> kCount);
         m += v & ((1ull << kCount) - 1);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(kAll, m, o);
+      constexpr uint32_t kLimb = (1u << 24) - 1;
+      const unsigned long long sum = (unsigned long long)__reduce_add_sync(kAll, (uint32_t)m & kLimb) +
+                                     ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 24) & kLimb) << 24) +
+                                     ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 48)) << 48);
       n = __reduce_add_sync(kAll, n);
-      if (lane < kC) *remote(&sh.bins[rank][b], lane) = Bin{m, n, 0};
+      if (lane < kC) *remote(&sh.bins[rank][b], lane) = Bin{sum, n, 0};
     }
     sync();
-    int turn = 0;
     // The first rank whose running count reaches `need` (by_count) or whose running mass
-    // reaches `goal`; that running mass goes to `upto`.
+    // reaches `goal` (times 2^60); that running mass goes to `upto`.
     auto find = [&](bool by_count, uint32_t need, Two goal, int which, Two& upto) -> uint64_t {
       Two before = {0.0f, 0.0f};
-      uint32_t ahead = 0, members = 0;
-      // of the parts' counts and masses (lane's part over all blocks), the one with the target
-      auto choose = [&](uint32_t n, Two m) {
-        uint32_t n_in = n;
+      uint32_t ahead = 0, left = 0;
+      // of parts' counts and masses, two a lane, the one with the target
+      auto choose = [&](uint32_t n0, Two m0, uint32_t n1, Two m1) {
+        uint32_t n_in = n0 + n1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t up = __shfl_up_sync(kAll, n_in, o);
           if (lane >= o) n_in += up;
         }
-        const Two m_in = scan(m, lane);
-        const bool reach = by_count ? ahead + n_in >= need : !less(add(before, m_in), goal);
-        const unsigned has = __ballot_sync(kAll, n > 0);
-        const unsigned hit = __ballot_sync(kAll, n > 0 && reach);
+        const Two m_in = add(before, scan(add(m0, m1), lane));
+        const bool reach = by_count ? ahead + n_in >= need : !less(m_in, goal);
+        const unsigned has = __ballot_sync(kAll, n0 + n1 > 0);
+        const unsigned hit = __ballot_sync(kAll, n0 + n1 > 0 && reach);
         const int p = hit ? __ffs(hit) - 1 : 31 - __clz(has);
-        members = __shfl_sync(kAll, n, p);
         if (p > 0) {
-          before = add(before, shfl(m_in, p - 1));
+          before = shfl(m_in, p - 1);
           ahead += __shfl_sync(kAll, n_in, p - 1);
         }
-        return p;
+        n0 = __shfl_sync(kAll, n0, p), n1 = __shfl_sync(kAll, n1, p);
+        m0 = shfl(m0, p);
+        const Two half = add(before, m0);
+        if (n0 > 0 && (n1 == 0 || (hit && (by_count ? ahead + n0 >= need : !less(half, goal))))) {
+          left = n0;
+          return 2 * p;
+        }
+        before = half;
+        ahead += n0;
+        left = n1;
+        return 2 * p + 1;
       };
-      uint32_t n = 0;
-      uint64_t m = 0;
-      if (lane < kBins)
-        for (int r = 0; r < kC; ++r) n += sh.bins[r][lane].count, m += sh.bins[r][lane].mass;
-      const int bin = choose(n, to_two(m, -kFrac - min(lane, kBins - 1)));
+      auto part_sum = [&](const Bin* parts, int apart, int i, int n, uint32_t& cnt, uint64_t& m) {
+        cnt = 0, m = 0;
+        if (i < n)
+#pragma unroll
+          for (int r = 0; r < kC; ++r) cnt += parts[r * apart + i].count, m += parts[r * apart + i].mass;
+      };
+      uint32_t n0, n1;
+      uint64_t m0, m1;
+      part_sum(&sh.bins[0][0], kBins, e0, kBins, n0, m0);
+      part_sum(&sh.bins[0][0], kBins, e1, kBins, n1, m1);
+      const int bin = choose(n0, to_two(m0, 60 - kFrac - min(e0, kBins - 1)), n1,
+                             to_two(m1, 60 - kFrac - min(e1, kBins - 1)));
+      gather(bin);
       int part = -1;
       uint64_t from = 0, to = ~0ull;
       auto part_of = [&](float y) { return min(kSub - 1, (int)((y - (float)bin) * (float)kSub)); };
-      auto member = [&](float z, int i, float& y) {
-        if (!(z > -CUDART_INF_F)) return false;
-        y = y_of(z);
-        if (bin_of(y) != bin || (part >= 0 && part_of(y) != part)) return false;
-        const uint64_t r = rank_of(z, base + i);
-        return from <= r && r <= to;
+      auto each_left = [&](auto f) {
+        members([&](float z, int i) {
+          if (part >= 0 && part_of(y_of(z)) != part) return;
+          const uint64_t r = rank_of(z, base + i);
+          if (from <= r && r <= to) f(z, r);
+        });
       };
-      const Bin* from_blocks = nullptr;  // the chosen part's entry of block 0, the blocks' apart
+      const Bin* from_blocks = &sh.bins[0][bin];  // the chosen part's entry of block 0, the blocks' apart
       int apart = kBins;
-      from_blocks = &sh.bins[0][bin];
       bool ranged = false;
-      while (members > kList) {
+      for (int level = 0; left > kList; ++level) {
         const bool by_y = bin < kBins - 1 && part < 0;
         if (!by_y && !ranged) {  // the members' first and last rank
           if (tid == 0) sh.lo = ~0ull, sh.hi = 0;
           __syncthreads();
-          uint64_t l = ~0ull, h = 0;
-          for (int i = lo; i < hi; ++i) {
-            const float z = at(i);
-            float y;
-            if (member(z, i, y)) {
-              const uint64_t r = rank_of(z, base + i);
-              l = min(l, r), h = max(h, r);
-            }
-          }
+          unsigned long long l = ~0ull, h = 0;
+          each_left([&](float, uint64_t r) { l = min(l, (unsigned long long)r), h = max(h, (unsigned long long)r); });
           if (l <= h) atomicMin(&sh.lo, l), atomicMax(&sh.hi, h);
           __syncthreads();
           if (tid < kC) {
-            remote(&sh.range[turn][rank][0], tid)[0] = sh.lo;
-            remote(&sh.range[turn][rank][0], tid)[1] = sh.hi;
+            uint64_t* const to_block = remote(&sh.range[rank][0], tid);
+            to_block[0] = sh.lo, to_block[1] = sh.hi;
           }
           sync();
           from = ~0ull, to = 0;
           for (int r = 0; r < kC; ++r) {
-            from = min(from, sh.range[turn][r][0]);
-            to = max(to, sh.range[turn][r][1]);
+            from = min(from, sh.range[r][0]);
+            to = max(to, sh.range[r][1]);
           }
-          turn ^= 1;
           ranged = true;
         }
-        const int shift = max(0, 64 - __clzll((long long)(to - from)) - 5);
+        const int shift = max(0, 64 - __clzll((long long)(to - from)) - 6);
         if (tid < kSub) sh.sub_mass[tid] = 0, sh.sub_count[tid] = 0;
-        __syncthreads();
-        for (int i = lo; i < hi; ++i) {
-          const float z = at(i);
-          float y;
-          if (member(z, i, y)) {
-            const int p = by_y ? part_of(y) : (int)((rank_of(z, base + i) - from) >> shift);
-            atomicAdd(&sh.sub_mass[p], (unsigned long long)mass_of(z, bin));
-            atomicAdd(&sh.sub_count[p], 1u);
-          }
-        }
+        if (level) sync();  // the last level's parts have been read
+        else __syncthreads();
+        each_left([&](float z, uint64_t r) {
+          const int p = by_y ? part_of(y_of(z)) : (int)((r - from) >> shift);
+          atomicAdd(&sh.sub_mass[p], (unsigned long long)mass_of(z, bin));
+          atomicAdd(&sh.sub_count[p], 1u);
+        });
         __syncthreads();
         for (int t = tid; t < kC * kSub; t += kT)
-          *remote(&sh.sub[turn][rank][t % kSub], t / kSub) = Bin{sh.sub_mass[t % kSub], sh.sub_count[t % kSub], 0};
+          *remote(&sh.sub[rank][t % kSub], t / kSub) = Bin{sh.sub_mass[t % kSub], sh.sub_count[t % kSub], 0};
         sync();
-        n = 0, m = 0;
-        for (int r = 0; r < kC; ++r) n += sh.sub[turn][r][lane].count, m += sh.sub[turn][r][lane].mass;
-        const int p = choose(n, to_two(m, -kFrac - bin));
+        part_sum(&sh.sub[0][0], kSub, e0, kSub, n0, m0);
+        part_sum(&sh.sub[0][0], kSub, e1, kSub, n1, m1);
+        const int p = choose(n0, to_two(m0, 60 - kFrac - bin), n1, to_two(m1, 60 - kFrac - bin));
         if (by_y) {
           part = p;
         } else {
           from += (uint64_t)p << shift;
           to = min(to, from + ((uint64_t)1 << shift) - 1);
         }
-        from_blocks = &sh.sub[turn][0][p];
+        from_blocks = &sh.sub[0][p];
         apart = kSub;
-        turn ^= 1;
       }
       // the members, to every block
       int place = 0;
       for (int r = 0; r < rank; ++r) place += from_blocks[r * apart].count;
       if (tid == 0) sh.fill = place, sh.hit = kList;
       __syncthreads();
-      for (int i = lo; i < hi; ++i) {
-        const float z = at(i);
-        float y;
-        if (member(z, i, y)) {
-          const int p = atomicAdd(&sh.fill, 1);
-          for (int r = 0; r < kC; ++r) *remote(&sh.list[which][p], r) = rank_of(z, base + i);
-        }
-      }
+      each_left([&](float, uint64_t r) {
+        const int p = atomicAdd(&sh.fill, 1);
+#pragma unroll
+        for (int b = 0; b < kC; ++b) *remote(&sh.list[which][p], b) = r;
+      });
       sync();
-      const int m_n = (int)members;
-      for (int t = tid; t < m_n; t += kT) {
-        const uint64_t mine = sh.list[which][t];
+      const int n = (int)left;
+      static_assert(kList <= kT, "a thread a token");
+      if (tid < n) {
+        const uint64_t mine = sh.list[which][tid];
         int p = 0;
-        for (int j = 0; j < m_n; ++j) p += sh.list[which][j] < mine;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) p += sh.list[which][j] < mine;
         sh.sorted[p] = mine;
       }
       __syncthreads();
-      static_assert(kList <= kT, "a thread a token");
-      Two w = {0.0f, 0.0f};
-      if (tid < m_n) {
-        w = weight2(logit_of(sh.sorted[tid]), M, c, sh.tab);
-        w = {w.h * (1.0f / kUp), w.l * (1.0f / kUp)};
+      if (warp < kList / 32) {
+        Two in = scan(tid < n ? weight(logit_of(sh.sorted[tid])) : Two{0.0f, 0.0f}, lane);
+        if (lane == 31) sh.scan[warp] = in;
+        asm volatile("bar.sync 1, %0;" ::"n"(kList) : "memory");
+        for (int w = 0; w < warp; ++w) before = add(before, sh.scan[w]);
+        in = add(before, in);
+        if (tid < n && (by_count ? tid + 1 + ahead == need : !less(in, goal))) atomicMin(&sh.hit, tid);
+        asm volatile("bar.sync 1, %0;" ::"n"(kList) : "memory");
+        if (tid == min(sh.hit, n - 1)) sh.scan[kW - 1] = in;
       }
-      Two in = scan(w, lane);
-      if (lane == 31) sh.scan[warp] = in;
+      static_assert(kW > kList / 32, "a place of the sums' for the answer");
       __syncthreads();
-      const Two warps = scan(lane < kW ? sh.scan[lane] : Two{0.0f, 0.0f}, lane);
-      if (warp) in = add(shfl(warps, warp - 1), in);
-      in = add(before, in);
-      if (by_count ? tid + 1 + ahead == need : tid < m_n && !less(in, goal)) atomicMin(&sh.hit, tid);
-      __syncthreads();
-      const int pos = min(sh.hit, m_n - 1);
-      if (tid == pos) sh.scan[0] = in;
-      __syncthreads();
-      upto = sh.scan[0];
+      upto = sh.scan[kW - 1];
       cut_bin = min(cut_bin, bin);
-      __syncthreads();
-      return sh.sorted[pos];
+      return sh.sorted[min(sh.hit, n - 1)];
     };
     Two sum;
     if (by_k) {
@@ -381,47 +460,51 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
       uint64_t m = 0;
       if (lane < kBins)
         for (int r = 0; r < kC; ++r) m += sh.bins[r][lane].mass;
-      sum = to_two(m, -kFrac - min(lane, kBins - 1));
+      sum = to_two(m, 60 - kFrac - min(lane, kBins - 1));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     }
-    if (by_p) cut = min(cut, find(false, 0, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), 1, sum));
+    if (by_p) {
+      __syncthreads();  // sh.hit and sh.scan have been read
+      cut = min(cut, find(false, 0, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), 1, sum));
+    }
   }
-  // ---- min-p: bins that it keeps whole, and those that it may cut
-  int whole = cut_bin, last = cut_bin;  // bins whole .. last are looked at token by token
+  // ---- bins that stay whole, and those that are looked at token by token: the cut's, and
+  // the one or two where min-p may end
+  int whole = cut_bin, last = cut_bin;
   if (by_m) {
     const float y = -lg2(min_p);
     whole = min(whole, max(0, (int)(y - 0.001f)));
     last = min(last, max(0, (int)(y + 0.001f)));
     if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
   }
+  last = min(last, kBins - 1);
   const Two least = {min_p * kUp, 0.0f};
-  // ---- kept mass and count of the runs
-  auto stays = [&](float z, int i, Two w) {
-    return rank_of(z, base + i) <= cut && (!by_m || base + i == best.at || !less(w, least));
+  auto stays = [&](float z, int i) {
+    return rank_of(z, base + i) <= cut && (!by_m || base + i == best.at || !less(weight(z), least));
   };
+  for (int b = whole; b <= last; ++b) {
+    gather(b);
+    __syncwarp();
+    column[b * kT] = 0;
+    __syncwarp();
+    members([&](float z, int i) {
+      if (stays(z, i)) atomicAdd(columns + b * kT + by_each.div((uint32_t)i), mass_of(z, b) + (1ull << kCount));
+    });
+  }
+  __syncwarp();
+  // ---- kept mass and count of the runs
   Kept mine = {{0.0f, 0.0f}, 0};
   {
     uint64_t sum = 0;  // of 2^-54
-    for (int b = 0; b < min(whole, kBins); ++b) {
-      const uint64_t v = column[b * kT], m = v & ((1ull << kCount) - 1);
+#pragma unroll
+    for (int b = 0; b < kBins; ++b) {
+      const uint64_t v = b <= last ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
       mine.count += (int)(v >> kCount);
       const int s = 54 - kFrac - b;
-      sum += s >= 0 ? m << s : (m + (1ull << (-s - 1))) >> -s;
+      sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s - 1 : 0))) >> (s < 0 ? -s : 0);
     }
-    mine.mass = to_two(sum, -54);
-    if (whole < kBins) {
-      for (int i = lo; i < hi; ++i) {
-        const float z = at(i);
-        if (!(z > -CUDART_INF_F)) continue;
-        const int b = bin_of(y_of(z));
-        if (b < whole || b > last) continue;
-        Two w = weight2(z, M, c, sh.tab);
-        if (!stays(z, i, w)) continue;
-        ++mine.count;
-        mine.mass = add(mine.mass, {w.h * (1.0f / kUp), w.l * (1.0f / kUp)});
-      }
-    }
+    mine.mass = to_two(sum, 60 - 54);
   }
   const Two in = scan(mine.mass, lane);
   {
@@ -440,7 +523,7 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
   Two total = add(k0.mass, k1.mass);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total = add(total, shfl_xor(total, o));
-  const Two goal = mul({us, 0.0f}, total);
+  const Two goal = mul({fminf(u_row, 1.0f), 0.0f}, total);
   Two cum = {0.0f, 0.0f};
   const int chosen = pick(k0.mass, k1.mass, goal, cum, lane);
   if (chosen != rank * kW + warp) return;
@@ -455,10 +538,7 @@ __global__ void __launch_bounds__(kT) k_sample_filtered(FilteredArgs a, int held
     Two w = {0.0f, 0.0f};
     if (i < end) {
       const float z = at(i);
-      if (z > -CUDART_INF_F) {
-        w = weight2(z, M, c, sh.tab);
-        w = stays(z, i, w) ? Two{w.h * (1.0f / kUp), w.l * (1.0f / kUp)} : Two{0.0f, 0.0f};
-      }
+      if (z > -CUDART_INF_F && stays(z, i)) w = weight(z);
     }
     const Two s = add(cum, scan(w, lane));
     const unsigned h = __ballot_sync(kAll, w.h > 0.0f);
@@ -475,17 +555,19 @@ Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
   constexpr int kT = 256;
   constexpr int64_t kColumns = (int64_t)kBins * kT * 8, kMost = 200 * 1024;
   const int64_t each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
-  int64_t smem = kColumns + std::min<int64_t>(a.V, kT * each) * 4;
-  const int held = smem <= kMost;
+  // a row's part, and the gathered tokens' places in it
+  int64_t smem = kColumns + std::min<int64_t>(a.V, kT * each) * 4 + kT * each * 2;
+  const int held = smem <= kMost && kT * each <= 65536;
   if (!held) smem = kColumns;
   static std::atomic<uint64_t> done{0};
   Launched l;
   l.error = allow_smem(k_sample_filtered<kC, kT>, (int)kMost, done);
   if (l.error != cudaSuccess) return l;
+  const FastDiv by_each((uint32_t)each);
   if constexpr (kC == 1)
-    l.add(launch_k(k_sample_filtered<1, kT>, dim3((unsigned)a.n), kT, smem, s, a, held));
+    l.add(launch_k(k_sample_filtered<1, kT>, dim3((unsigned)a.n), kT, smem, s, a, by_each, held));
   else
-    l.add(launch_k_cluster(k_sample_filtered<kC, kT>, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, held));
+    l.add(launch_k_cluster(k_sample_filtered<kC, kT>, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each, held));
   return l;
 }
 
