@@ -17,9 +17,13 @@
 // atomics). What the draw needs, the kept mass of each run in order, is then the sum of a
 // column's bins ahead of the cut; only the tokens of the cut's own bin are weighed again.
 // They are gathered first (a tenth of the tokens, in lanes of their own), as the split and
-// the ranking want them as well.
+// the ranking want them as well. Where the tokens up to the cut are few, as with a small
+// top_k or a peaked row, they go to one block as a whole, which does the rest; a small top_k
+// asks for no weights but theirs.
 
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "draw.cuh"
 #include "fs_internal.h"
@@ -34,6 +38,7 @@ namespace cg = cooperative_groups;
 constexpr int kBins = 24;   // of y: [b, b + 1), the last one also all above
 constexpr int kSub = 64;    // parts of a bin that is split
 constexpr int kList = 128;  // tokens that are ranked among themselves
+constexpr int kFew = 64;    // a top_k that always ends in one list
 constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(b + kFrac)
 constexpr int kCount = 50;  // a column's entry: count << kCount | mass
 
@@ -67,14 +72,20 @@ struct Shared {
   unsigned long long lo, hi;
   uint64_t list[2][kList], sorted[kList];
   Two scan[kW];
-  int hit, fill;
+  int hit, fill, taken;
+  struct {  // what one warp found for all
+    Two before;
+    uint32_t ahead, left;
+    int at;
+  } found;
 };
 
-__device__ __forceinline__ Two to_two(uint64_t m, int e) {  // m * 2^e, e > -127
-  const float h = __ull2float_rn(m);
-  const float l = (float)(long long)(m - (uint64_t)h);
+__device__ __forceinline__ Two to_two(uint64_t m, int e) {  // m * 2^e, -127 < e < 87
   const float s = __int_as_float((127 + e) << 23);
-  return {h * s, l * s};
+  const float h = (float)(uint32_t)(m >> 40) * 0x1p40f, i = (float)((uint32_t)(m >> 20) & 0xfffffu) * 0x1p20f;
+  const Two t = fast_two_sum(h, i);
+  const Two u = fast_two_sum(t.h, __fadd_rn(t.l, (float)((uint32_t)m & 0xfffffu)));
+  return {u.h * s, u.l * s};
 }
 
 // The rank of a token, the first the smallest: its logit's bits in falling order, then
@@ -119,8 +130,14 @@ __device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* 
   return one ? 1ull << kFrac : in ? m : 0;
 }
 
-template <int kC, int kT>
-__global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastDiv by_each, int held) {
+// What all lanes hold anyway, told to the compiler: a branch on it then needs no
+// reconvergence before each of the shuffles inside (256 rows: 188 us without, 1xx with).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
+__device__ __forceinline__ float uniform(float v) { return __shfl_sync(kAll, v, 0); }
+
+// held: the row's parts fit the blocks' shared memory; else they are read again from global.
+template <int kC, int kT, bool held>
+__global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastDiv by_each) {
   constexpr int kW = kT / 32, kN = kC * kW;
   static_assert(kN <= 64, "two warps a lane");
   static_assert(kT == 256, "a power of two of the table a thread");
@@ -139,8 +156,9 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     else return cluster.map_shared_rank(p, r);
   };
   const int rank = kC == 1 ? 0 : (int)cluster.block_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   // the other blocks' shared memory can be written once they have started
+  if (tid == 0) sh.taken = 0;
   if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   {  // 2^(k/256) = 2^(k/8 / 32) 2^(k%8 / 256)
     constexpr float2 kFine[8] = {
@@ -159,9 +177,9 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x / kC, V = a.V;
-  const float temp = a.temps[row], u_row = a.u[row];
-  const int top_k = a.top_k ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
+  const float temp = uniform(a.temps[row]), u_row = a.u[row];
+  const int top_k = uniform(a.top_k ? a.top_k[row] : 0);
+  const float top_p = uniform(a.top_p ? a.top_p[row] : 1.0f), min_p = uniform(a.min_p ? a.min_p[row] : 0.0f);
   // a thread's run; odd, so that the threads of a warp read different banks
   const int each = ((V + kC * kT - 1) / (kC * kT)) | 1;
   const int base = (int)min((int64_t)V, (int64_t)rank * kT * each);
@@ -221,6 +239,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   if (e0 < kN) merge(sh.best[e0]);
   if (e1 < kN) merge(sh.best[e1]);
   merge_lanes();
+  best = {uniform(best.max), uniform(best.at), uniform(best.tokens)};
   const float M = best.max;
   if (greedy || best.tokens == 0) {
     if (rank == 0 && tid == 0) {
@@ -245,18 +264,26 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     return to_two(m, n - kFrac + 60);
   };
   // ---- counts and masses of the bins
-  for (int i0 = lo; i0 < hi; i0 += 4) {
-    int b[4];
-    unsigned long long m[4];
+  // Four tokens in step, without branches, so that their chains of dependent operations
+  // overlap; past the run's end and for -inf nothing is added.
+  const bool few = by_k && top_k <= kFew;  // no weights are wanted
+  auto count_bins = [&](auto weighed) {
+    for (int i0 = lo; i0 < hi; i0 += 4) {
+      int b[4];
+      unsigned long long m[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float z = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
-      b[q] = bin_of(y_of(z));
-      m[q] = z > -CUDART_INF_F ? mass_of(z, b[q]) + (1ull << kCount) : 0;
+      for (int q = 0; q < 4; ++q) {
+        const float z = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
+        b[q] = bin_of(y_of(z));
+        m[q] = z > -CUDART_INF_F ? 1ull << kCount : 0;
+        if constexpr (decltype(weighed)::value) m[q] += mass_of(z, b[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) column[b[q] * kT] += m[q];
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) column[b[q] * kT] += m[q];
-  }
+  };
+  if (few) count_bins(std::false_type{});
+  else count_bins(std::true_type{});
   // The tokens of a bin, the warp's in its own part of shared memory; f(z, i) for each of
   // them, every lane another.
   int members_of = -1, gathered_n = 0;
@@ -266,14 +293,18 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (!held) return;
     __syncwarp();
     gathered_n = 0;
+    const float y0 = (float)bin, y1 = bin < kBins - 1 ? y0 + 1.0f : CUDART_NAN_F;
+#pragma unroll 4
     for (int j = 0; j < each; ++j) {
       const int i = lo + j;
       const float z = i < hi ? hold[i] : -CUDART_INF_F;
-      const bool in = z > -CUDART_INF_F && bin_of(y_of(z)) == bin;
+      const float y = y_of(z);
+      const bool in = z > -CUDART_INF_F && y >= y0 && !(y >= y1);
       const unsigned m = __ballot_sync(kAll, in);
       if (in) gathered[gathered_n + __popc(m & ((1u << lane) - 1))] = (uint16_t)i;
       gathered_n += __popc(m);
     }
+    gathered_n = uniform(gathered_n);
     __syncwarp();
   };
   auto members = [&](auto f) {
@@ -291,6 +322,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   };
   int cut_bin = kBins;               // all bins ahead of it stay whole
   uint64_t cut = ~0ull;              // the last rank that stays
+  const Two least = {min_p * kUp, 0.0f};
   if (by_k || by_p) {
     __syncthreads();
     for (int b = warp; b < kBins; b += kW) {
@@ -310,57 +342,59 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       if (lane < kC) *remote(&sh.bins[rank][b], lane) = Bin{sum, n, 0};
     }
     sync();
-    // The first rank whose running count reaches `need` (by_count) or whose running mass
-    // reaches `goal` (times 2^60); that running mass goes to `upto`.
-    auto find = [&](bool by_count, uint32_t need, Two goal, int which, Two& upto) -> uint64_t {
-      Two before = {0.0f, 0.0f};
+    // Looks for the first rank whose running count reaches `need` (by_count) or whose running
+    // mass reaches `goal` (times 2^60). False: it is `cut`, and the running mass is `upto`.
+    // True: it is among the first `upto_n` ranks, which are in block 0's list `which`.
+    auto find = [&](bool by_count, uint32_t need, Two goal, int which, Two& upto, int& upto_n) {
       uint32_t ahead = 0, left = 0;
-      // of parts' counts and masses, two a lane, the one with the target
-      auto choose = [&](uint32_t n0, Two m0, uint32_t n1, Two m1) {
-        uint32_t n_in = n0 + n1;
+      Two before = {0.0f, 0.0f};
+      // of parts' counts and masses (of `n` parts, the blocks' `apart`), the one with the
+      // target: by the first warp, for all
+      auto choose = [&](const Bin* parts, int apart, int parts_n, int unit) {
+        if (warp == 0) {
+          uint32_t n[2] = {0, 0};
+          Two m[2];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t up = __shfl_up_sync(kAll, n_in, o);
-          if (lane >= o) n_in += up;
-        }
-        const Two m_in = add(before, scan(add(m0, m1), lane));
-        const bool reach = by_count ? ahead + n_in >= need : !less(m_in, goal);
-        const unsigned has = __ballot_sync(kAll, n0 + n1 > 0);
-        const unsigned hit = __ballot_sync(kAll, n0 + n1 > 0 && reach);
-        const int p = hit ? __ffs(hit) - 1 : 31 - __clz(has);
-        if (p > 0) {
-          before = shfl(m_in, p - 1);
-          ahead += __shfl_sync(kAll, n_in, p - 1);
-        }
-        n0 = __shfl_sync(kAll, n0, p), n1 = __shfl_sync(kAll, n1, p);
-        m0 = shfl(m0, p);
-        const Two half = add(before, m0);
-        if (n0 > 0 && (n1 == 0 || (hit && (by_count ? ahead + n0 >= need : !less(half, goal))))) {
-          left = n0;
-          return 2 * p;
-        }
-        before = half;
-        ahead += n0;
-        left = n1;
-        return 2 * p + 1;
-      };
-      auto part_sum = [&](const Bin* parts, int apart, int i, int n, uint32_t& cnt, uint64_t& m) {
-        cnt = 0, m = 0;
-        if (i < n)
+          for (int q = 0; q < 2; ++q) {
+            const int i = 2 * lane + q;
+            uint64_t sum = 0;
+            if (i < parts_n)
 #pragma unroll
-          for (int r = 0; r < kC; ++r) cnt += parts[r * apart + i].count, m += parts[r * apart + i].mass;
+              for (int r = 0; r < kC; ++r) n[q] += parts[r * apart + i].count, sum += parts[r * apart + i].mass;
+            m[q] = to_two(sum, 60 - kFrac - (unit < 0 ? min(i, kBins - 1) : unit));
+          }
+          uint32_t n_in = n[0] + n[1];
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(kAll, n_in, o);
+            if (lane >= o) n_in += up;
+          }
+          const Two m_in = add(before, scan(add(m[0], m[1]), lane));
+          const bool reach = by_count ? ahead + n_in >= need : !less(m_in, goal);
+          const unsigned has = __ballot_sync(kAll, n[0] + n[1] > 0);
+          const unsigned hit = __ballot_sync(kAll, n[0] + n[1] > 0 && reach);
+          const int p = hit ? __ffs(hit) - 1 : 31 - __clz(has);
+          if (p > 0) {
+            before = shfl(m_in, p - 1);
+            ahead += __shfl_sync(kAll, n_in, p - 1);
+          }
+          const uint32_t n0 = __shfl_sync(kAll, n[0], p), n1 = __shfl_sync(kAll, n[1], p);
+          const Two half = add(before, shfl(m[0], p));
+          const bool first = n0 > 0 && (n1 == 0 || (hit && (by_count ? ahead + n0 >= need : !less(half, goal))));
+          if (!first) before = half, ahead += n0;
+          if (lane == 0) sh.found = {before, ahead, first ? n0 : n1, 2 * p + !first};
+        }
+        __syncthreads();
+        before = sh.found.before;
+        ahead = (uint32_t)uniform((int)sh.found.ahead), left = (uint32_t)uniform((int)sh.found.left);
+        return uniform(sh.found.at);
       };
-      uint32_t n0, n1;
-      uint64_t m0, m1;
-      part_sum(&sh.bins[0][0], kBins, e0, kBins, n0, m0);
-      part_sum(&sh.bins[0][0], kBins, e1, kBins, n1, m1);
-      const int bin = choose(n0, to_two(m0, 60 - kFrac - min(e0, kBins - 1)), n1,
-                             to_two(m1, 60 - kFrac - min(e1, kBins - 1)));
-      gather(bin);
+      const int bin = choose(&sh.bins[0][0], kBins, kBins, -1);
       int part = -1;
       uint64_t from = 0, to = ~0ull;
       auto part_of = [&](float y) { return min(kSub - 1, (int)((y - (float)bin) * (float)kSub)); };
       auto each_left = [&](auto f) {
+        gather(bin);
         members([&](float z, int i) {
           if (part >= 0 && part_of(y_of(z)) != part) return;
           const uint64_t r = rank_of(z, base + i);
@@ -370,7 +404,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       const Bin* from_blocks = &sh.bins[0][bin];  // the chosen part's entry of block 0, the blocks' apart
       int apart = kBins;
       bool ranged = false;
-      for (int level = 0; left > kList; ++level) {
+      for (int level = 0; left > kList || (by_count && need <= kFew && ahead + left > kList); ++level) {
         const bool by_y = bin < kBins - 1 && part < 0;
         if (!by_y && !ranged) {  // the members' first and last rank
           if (tid == 0) sh.lo = ~0ull, sh.hi = 0;
@@ -397,16 +431,14 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         else __syncthreads();
         each_left([&](float z, uint64_t r) {
           const int p = by_y ? part_of(y_of(z)) : (int)((r - from) >> shift);
-          atomicAdd(&sh.sub_mass[p], (unsigned long long)mass_of(z, bin));
+          if (!few) atomicAdd(&sh.sub_mass[p], (unsigned long long)mass_of(z, bin));
           atomicAdd(&sh.sub_count[p], 1u);
         });
         __syncthreads();
         for (int t = tid; t < kC * kSub; t += kT)
           *remote(&sh.sub[rank][t % kSub], t / kSub) = Bin{sh.sub_mass[t % kSub], sh.sub_count[t % kSub], 0};
         sync();
-        part_sum(&sh.sub[0][0], kSub, e0, kSub, n0, m0);
-        part_sum(&sh.sub[0][0], kSub, e1, kSub, n1, m1);
-        const int p = choose(n0, to_two(m0, 60 - kFrac - bin), n1, to_two(m1, 60 - kFrac - bin));
+        const int p = choose(&sh.sub[0][0], kSub, kSub, bin);
         if (by_y) {
           part = p;
         } else {
@@ -415,6 +447,19 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         }
         from_blocks = &sh.sub[0][p];
         apart = kSub;
+      }
+      if (ahead + left <= kList) {  // all ranks up to the part's last, to block 0
+        const float y1 = bin < kBins - 1 ? (float)(bin + 1) : CUDART_NAN_F;
+        for (int i = lo; i < hi; ++i) {
+          const float z = at(i), y = y_of(z);
+          if (!(z > -CUDART_INF_F) || y >= y1) continue;
+          const uint64_t r = rank_of(z, base + i);
+          if (y >= (float)bin && ((part >= 0 && part_of(y) > part) || r > to)) continue;
+          *remote(&sh.list[which][atomicAdd(remote(&sh.taken, 0), 1)], 0) = r;
+        }
+        upto_n = (int)(ahead + left);
+        sync();
+        return true;
       }
       // the members, to every block
       int place = 0;
@@ -451,11 +496,14 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       __syncthreads();
       upto = sh.scan[kW - 1];
       cut_bin = min(cut_bin, bin);
-      return sh.sorted[min(sh.hit, n - 1)];
+      cut = min(cut, sh.sorted[uniform(min(sh.hit, n - 1))]);
+      return false;
     };
-    Two sum;
+    Two sum = {0.0f, 0.0f};
+    int first_n = 0, which = 0;
+    bool listed = false, k_in = false;  // the first ranks are in a list; top-k's end too
     if (by_k) {
-      cut = find(true, (uint32_t)top_k, {0.0f, 0.0f}, 0, sum);
+      listed = k_in = find(true, (uint32_t)top_k, {0.0f, 0.0f}, 0, sum, first_n);
     } else {
       uint64_t m = 0;
       if (lane < kBins)
@@ -464,9 +512,78 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     }
-    if (by_p) {
+    if (by_p && !listed) {
       __syncthreads();  // sh.hit and sh.scan have been read
-      cut = min(cut, find(false, 0, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), 1, sum));
+      which = 1;
+      Two unused;
+      listed = find(false, 0, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), 1, unused, first_n);
+    }
+    if (listed) {
+      // ---- everything else in one block: a thread a rank, then a thread an index
+      if (rank != 0 || warp >= kList / 32) return;
+      auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kList) : "memory"); };
+      const int n = first_n;
+      if (tid < n) {
+        const uint64_t mine = sh.list[which][tid];
+        int p = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) p += sh.list[which][j] < mine;
+        sh.sorted[p] = mine;
+      }
+      if (tid == 0) sh.hit = kList, sh.fill = 0;
+      meet();
+      // running sums over the 128 threads
+      auto run_sum = [&](Two v) {
+        Two in = scan(v, lane);
+        meet();  // the last sums have been read
+        if (lane == 31) sh.scan[warp] = in;
+        meet();
+        Two ahead = {0.0f, 0.0f};
+        for (int w = 0; w < warp; ++w) ahead = add(ahead, sh.scan[w]);
+        return add(ahead, in);
+      };
+      const uint64_t mine = tid < n ? sh.sorted[tid] : ~0ull;
+      const Two w = tid < n ? weight(logit_of(mine)) : Two{0.0f, 0.0f};
+      int stay = k_in ? min(n, top_k) : n;
+      if (by_p) {
+        const Two in = run_sum(tid < stay ? w : Two{0.0f, 0.0f});
+        if (k_in) {
+          if (tid == stay - 1) sh.found.before = in;
+          meet();
+          sum = sh.found.before;
+        }
+        if (tid < stay && !less(in, mul({fmaxf(top_p, 0.0f), 0.0f}, sum))) atomicMin(&sh.hit, tid);
+        meet();
+        stay = min(stay, sh.hit + 1);
+      }
+      const bool kept = tid < stay && (!by_m || tid == 0 || !less(w, least));
+      if (kept) {
+        atomicAdd(&sh.fill, 1);
+      }
+      meet();
+      stay = sh.fill;  // a prefix: weights fall with the rank
+      if (tid == 0 && a.kept) a.kept[row] = stay;
+      // by index
+      if (tid < stay) {
+        int p = 0;
+#pragma unroll 4
+        for (int j = 0; j < stay; ++j) p += (uint32_t)sh.sorted[j] < (uint32_t)mine;
+        sh.list[which][p] = mine;
+      }
+      if (tid == 0) sh.hit = kList;
+      meet();
+      const uint64_t token = tid < stay ? sh.list[which][tid] : 0;
+      const Two v = tid < stay ? weight(logit_of(token)) : Two{0.0f, 0.0f};
+      const Two in = run_sum(v);
+      if (tid == stay - 1) sh.found.before = in;
+      meet();
+      if (v.h > 0.0f && !less(in, mul({fminf(u_row, 1.0f), 0.0f}, sh.found.before))) atomicMin(&sh.hit, tid);
+      if (tid == 0) sh.fill = -1;
+      meet();
+      if (v.h > 0.0f) atomicMax(&sh.fill, tid);
+      meet();
+      if (tid == 0) a.tokens[row] = (int)(uint32_t)sh.list[which][sh.hit < kList ? sh.hit : sh.fill];
+      return;
     }
   }
   // ---- bins that stay whole, and those that are looked at token by token: the cut's, and
@@ -479,7 +596,6 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
   }
   last = min(last, kBins - 1);
-  const Two least = {min_p * kUp, 0.0f};
   auto stays = [&](float z, int i) {
     return rank_of(z, base + i) <= cut && (!by_m || base + i == best.at || !less(weight(z), least));
   };
@@ -513,20 +629,24 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (lane < kC) *remote(&sh.kept[rank * kW + warp], lane) = Kept{m, n};
   }
   sync();
-  const Kept none = {{0.0f, 0.0f}, 0};
-  const Kept k0 = e0 < kN ? sh.kept[e0] : none, k1 = e1 < kN ? sh.kept[e1] : none;
-  if (rank == 0 && warp == 0 && a.kept) {
+  // ---- the draw: the warp (found by one of each block), the lane, the token
+  if (warp == 0) {
+    const Kept none = {{0.0f, 0.0f}, 0};
+    const Kept k0 = e0 < kN ? sh.kept[e0] : none, k1 = e1 < kN ? sh.kept[e1] : none;
     const int n = __reduce_add_sync(kAll, k0.count + k1.count);
-    if (lane == 0) a.kept[row] = n;
-  }
-  // ---- the draw: the warp, the lane, the token
-  Two total = add(k0.mass, k1.mass);
+    if (rank == 0 && lane == 0 && a.kept) a.kept[row] = n;
+    Two total = add(k0.mass, k1.mass);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total = add(total, shfl_xor(total, o));
-  const Two goal = mul({fminf(u_row, 1.0f), 0.0f}, total);
-  Two cum = {0.0f, 0.0f};
-  const int chosen = pick(k0.mass, k1.mass, goal, cum, lane);
-  if (chosen != rank * kW + warp) return;
+    for (int o = 16; o > 0; o >>= 1) total = add(total, shfl_xor(total, o));
+    const Two goal = mul({fminf(u_row, 1.0f), 0.0f}, total);
+    Two cum = {0.0f, 0.0f};
+    const int chosen = pick(k0.mass, k1.mass, goal, cum, lane);
+    if (lane == 0) sh.found.before = cum, sh.found.at = chosen, sh.scan[0] = goal;
+  }
+  __syncthreads();
+  Two cum = sh.found.before;
+  const Two goal = sh.scan[0];
+  if (uniform(sh.found.at) != rank * kW + warp) return;
   const unsigned reach = __ballot_sync(kAll, mine.mass.h > 0.0f && !less(add(cum, in), goal));
   const unsigned has = __ballot_sync(kAll, mine.mass.h > 0.0f);
   const int who = reach ? __ffs(reach) - 1 : 31 - __clz(has);
@@ -550,25 +670,29 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   if (lane == 0) a.tokens[row] = found >= 0 ? base + found : last_in >= 0 ? base + last_in : best.at;
 }
 
-template <int kC>
-Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
+template <int kC, bool kHeld>
+Launched launch_h(const FilteredArgs& a, int64_t each, int64_t smem, cudaStream_t s) {
   constexpr int kT = 256;
-  constexpr int64_t kColumns = (int64_t)kBins * kT * 8, kMost = 200 * 1024;
-  const int64_t each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
-  // a row's part, and the gathered tokens' places in it
-  int64_t smem = kColumns + std::min<int64_t>(a.V, kT * each) * 4 + kT * each * 2;
-  const int held = smem <= kMost && kT * each <= 65536;
-  if (!held) smem = kColumns;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_sample_filtered<kC, kT>, (int)kMost, done);
+  l.error = allow_smem(k_sample_filtered<kC, kT, kHeld>, 200 * 1024, done);
   if (l.error != cudaSuccess) return l;
   const FastDiv by_each((uint32_t)each);
   if constexpr (kC == 1)
-    l.add(launch_k(k_sample_filtered<1, kT>, dim3((unsigned)a.n), kT, smem, s, a, by_each, held));
+    l.add(launch_k(k_sample_filtered<1, kT, kHeld>, dim3((unsigned)a.n), kT, smem, s, a, by_each));
   else
-    l.add(launch_k_cluster(k_sample_filtered<kC, kT>, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each, held));
+    l.add(launch_k_cluster(k_sample_filtered<kC, kT, kHeld>, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each));
   return l;
+}
+template <int kC>
+Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
+  constexpr int kT = 256;
+  const int64_t columns = (int64_t)kBins * kT * 8, each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
+  // a row's part, and the gathered tokens' places in it
+  const int64_t smem = columns + std::min<int64_t>(a.V, kT * each) * 4 + kT * each * 2;
+  if constexpr (kC == 8)
+    if (smem > 200 * 1024 || kT * each > 65536) return launch_h<kC, false>(a, each, columns, s);
+  return launch_h<kC, true>(a, each, smem, s);
 }
 
 }  // namespace
