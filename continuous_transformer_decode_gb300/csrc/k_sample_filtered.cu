@@ -4,7 +4,7 @@
 // With tokens ranked by (logit descending, index ascending), what top-k and top-p keep is a
 // prefix of the ranking: all that is wanted is its last token, the cut. Nothing is sorted.
 // A cut is found by counting: tokens fall into bins of y = (max - z) log2(e) / T (a weight
-// is 2^-y), the bin in which the running count or mass passes the target is split again,
+// is 2^-y), 4/3 wide, the bin in which the running count or mass passes the target is split again,
 // and once few enough tokens are left they are ranked among themselves.
 //
 // Whole-number answers need more than f32 (a cut lies between tokens whose weights are
@@ -35,12 +35,15 @@ using namespace draw;
 
 namespace cg = cooperative_groups;
 
-constexpr int kBins = 24;   // of y: [b, b + 1), the last one also all above
+constexpr int kBins = 16;   // of 3/4 y: [b, b + 1), the last one also all above
 constexpr int kSub = 64;    // parts of a bin that is split
 constexpr int kList = 128;  // tokens that are ranked among themselves
 constexpr int kFew = 64;    // a top_k that always ends in one list
-constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(b + kFrac)
+constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(exponent(b) + kFrac)
 constexpr int kCount = 50;  // a column's entry: count << kCount | mass
+
+// A weight in bin b is at most 2^-exponent(b).
+__device__ __forceinline__ constexpr int exponent(int b) { return 4 * b / 3; }
 
 struct Bin {
   uint64_t mass;
@@ -186,7 +189,6 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const int count = (int)min((int64_t)V - base, (int64_t)kT * each);
   const int lo = min(count, tid * each), hi = min(count, lo + each);
   const float* const z_row = a.logits + row * a.ld + base;
-  uint16_t* const gathered = reinterpret_cast<uint16_t*>(hold + min(V, kT * each)) + warp * 32 * each;
   // ---- the row, its maximum (lowest index) and how many tokens it has
   Best best = {-CUDART_INF_F, V, 0};
   auto take = [&](float z, int i) {
@@ -251,12 +253,13 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const bool by_k = top_k > 0 && top_k < best.tokens, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
 
   auto at = [&](int i) { return held ? hold[i] : clean(z_row[i]); };
-  auto y_of = [&](float z) { return z == M ? 0.0f : (M - z) * c.h; };
+  const float c_bins = c.h * 0.75f;
+  auto y_of = [&](float z) { return z == M ? 0.0f : (M - z) * c_bins; };  // in bins
   auto bin_of = [&](float y) { return min(kBins - 1, (int)y); };
-  auto mass_of = [&](float z, int b) {  // the weight as a whole number of 2^-(b + kFrac)
+  auto mass_of = [&](float z, int b) {  // the weight as a whole number of 2^-(exponent(b) + kFrac)
     int n;
     const uint64_t m = weigh(z, M, c, sh.tab, n);
-    return m >> min(63, max(0, -(n + b)));
+    return m >> min(63, max(0, -(n + exponent(b))));
   };
   auto weight = [&](float z) {  // times 2^60
     int n;
@@ -284,15 +287,21 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   };
   if (few) count_bins(std::false_type{});
   else count_bins(std::true_type{});
-  // The tokens of a bin, the warp's in its own part of shared memory; f(z, i) for each of
-  // them, every lane another.
+  // The tokens of a bin, each warp's own; f(z, i) for each of them, every lane another.
+  // Their places lie in the warp's columns of the bins behind, which no one wants any more,
+  // 128 a bin; a warp that has more of them, or whose row is not held, looks at its runs.
   int members_of = -1, gathered_n = 0;
+  bool in_columns = false;
+  auto place_of = [&](int k) {
+    return reinterpret_cast<uint16_t*>(columns + (members_of + 1 + (k >> 7)) * kT + warp * 32) + (k & 127);
+  };
   auto gather = [&](int bin) {
     if (members_of == bin) return;
     members_of = bin;
     if (!held) return;
     __syncwarp();
-    gathered_n = 0;
+    const int room = (kBins - 1 - bin) * 128;
+    int n = 0;
     const float y0 = (float)bin, y1 = bin < kBins - 1 ? y0 + 1.0f : CUDART_NAN_F;
 #pragma unroll 4
     for (int j = 0; j < each; ++j) {
@@ -301,16 +310,18 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       const float y = y_of(z);
       const bool in = z > -CUDART_INF_F && y >= y0 && !(y >= y1);
       const unsigned m = __ballot_sync(kAll, in);
-      if (in) gathered[gathered_n + __popc(m & ((1u << lane) - 1))] = (uint16_t)i;
-      gathered_n += __popc(m);
+      const int k = n + __popc(m & ((1u << lane) - 1));
+      if (in && k < room) *place_of(k) = (uint16_t)i;
+      n += __popc(m);
     }
-    gathered_n = uniform(gathered_n);
+    gathered_n = uniform(n);
+    in_columns = gathered_n <= room;
     __syncwarp();
   };
   auto members = [&](auto f) {
-    if (held) {
+    if (held && in_columns) {
       for (int j = lane; j < gathered_n; j += 32) {
-        const int i = gathered[j];
+        const int i = *place_of(j);
         f(hold[i], i);
       }
     } else {
@@ -361,7 +372,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
             if (i < parts_n)
 #pragma unroll
               for (int r = 0; r < kC; ++r) n[q] += parts[r * apart + i].count, sum += parts[r * apart + i].mass;
-            m[q] = to_two(sum, 60 - kFrac - (unit < 0 ? min(i, kBins - 1) : unit));
+            m[q] = to_two(sum, 60 - kFrac - exponent(unit < 0 ? min(i, kBins - 1) : unit));
           }
           uint32_t n_in = n[0] + n[1];
 #pragma unroll
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       uint64_t m = 0;
       if (lane < kBins)
         for (int r = 0; r < kC; ++r) m += sh.bins[r][lane].mass;
-      sum = to_two(m, 60 - kFrac - min(lane, kBins - 1));
+      sum = to_two(m, 60 - kFrac - exponent(min(lane, kBins - 1)));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     }
@@ -590,7 +601,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // the one or two where min-p may end
   int whole = cut_bin, last = cut_bin;
   if (by_m) {
-    const float y = -lg2(min_p);
+    const float y = -0.75f * lg2(min_p);  // in bins
     whole = min(whole, max(0, (int)(y - 0.001f)));
     last = min(last, max(0, (int)(y + 0.001f)));
     if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     for (int b = 0; b < kBins; ++b) {
       const uint64_t v = b <= last ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
       mine.count += (int)(v >> kCount);
-      const int s = 54 - kFrac - b;
+      const int s = 54 - kFrac - exponent(b);
       sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s - 1 : 0))) >> (s < 0 ? -s : 0);
     }
     mine.mass = to_two(sum, 60 - 54);
@@ -688,8 +699,7 @@ template <int kC>
 Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
   constexpr int kT = 256;
   const int64_t columns = (int64_t)kBins * kT * 8, each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
-  // a row's part, and the gathered tokens' places in it
-  const int64_t smem = columns + std::min<int64_t>(a.V, kT * each) * 4 + kT * each * 2;
+  const int64_t smem = columns + std::min<int64_t>(a.V, kT * each) * 4;  // and a row's part
   if constexpr (kC == 8)
     if (smem > 200 * 1024 || kT * each > 65536) return launch_h<kC, false>(a, each, columns, s);
   return launch_h<kC, true>(a, each, smem, s);
@@ -698,7 +708,7 @@ Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
 }  // namespace
 
 Launched launch_sample_filtered(const FilteredArgs& a, int sms, cudaStream_t s) {
-  if (a.V > 4096) return launch_c<8>(a, s);
+  if (a.V > 4096 && ((int64_t)a.n * 8 <= 2 * sms || a.V > 131072)) return launch_c<8>(a, s);
   return a.V > 2048 ? launch_c<4>(a, s) : launch_c<1>(a, s);
 }
 
