@@ -49,10 +49,6 @@ struct Bin {
   uint64_t mass;
   uint32_t count, pad;
 };
-struct Best {
-  float max;
-  int at, tokens;
-};
 struct Kept {
   Two mass;
   int count;
@@ -65,12 +61,12 @@ struct Power {  // 2^(k/256): times 2^kFrac, and as a pair
 template <int kC, int kW>
 struct Shared {
   Power tab[256];
-  Best best[kC * kW];
+  float max[kC * kW];
+  int at[kC * kW];
   Kept kept[kC * kW];
   Bin bins[kC][kBins];
   Bin sub[kC][kSub];
-  unsigned long long sub_mass[kSub];
-  uint32_t sub_count[kSub];
+  uint32_t own[3 + 1][kSub];  // of this block: a mass in three, and the count
   uint64_t range[kC][2];
   unsigned long long lo, hi;
   uint64_t list[2][kList], sorted[kList];
@@ -104,7 +100,14 @@ __device__ __forceinline__ float logit_of(uint64_t r) {
 }
 
 // -0 as 0 and NaN as -inf.
-__device__ __forceinline__ float clean(float z) { return z == z ? z + 0.0f : -CUDART_INF_F; }
+__device__ __forceinline__ float clean(float z) { return fmaxf(z, -CUDART_INF_F) + 0.0f; }
+
+// The largest of the lanes' values (no NaN, no -0).
+__device__ __forceinline__ float warp_max(float v) {
+  const int i = __float_as_int(v);
+  const int m = __reduce_max_sync(kAll, i ^ ((i >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
 
 // exp((z - M) / T) = m 2^(n - kFrac), m up to 2^(kFrac + 1); c = log2(e) / T. With y = (z -
 // M) c as a pair, k/256 its nearest multiple of 1/256 and f the rest, 2^f - 1 is its Taylor
@@ -189,12 +192,8 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const int count = (int)min((int64_t)V - base, (int64_t)kT * each);
   const int lo = min(count, tid * each), hi = min(count, lo + each);
   const float* const z_row = a.logits + row * a.ld + base;
-  // ---- the row, its maximum (lowest index) and how many tokens it has
-  Best best = {-CUDART_INF_F, V, 0};
-  auto take = [&](float z, int i) {
-    best.tokens += z > -CUDART_INF_F;
-    if (z > best.max) best.max = z, best.at = base + i;
-  };
+  // ---- the row and its maximum
+  float M = -CUDART_INF_F;
   if ((reinterpret_cast<uintptr_t>(z_row) & 15) == 0) {
 #pragma unroll 8
     for (int i = 4 * tid; i < count; i += 4 * kT) {
@@ -208,51 +207,45 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
           if (i + 2 < count) hold[i + 2] = v.z;
         }
       }
-      take(v.x, i), take(v.y, i + 1), take(v.z, i + 2), take(v.w, i + 3);
+      M = fmaxf(M, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
     }
   } else {
 #pragma unroll 8
     for (int i = tid; i < count; i += kT) {
       const float z = clean(z_row[i]);
       if (held) hold[i] = z;
-      take(z, i);
+      M = fmaxf(M, z);
     }
   }
-  auto merge = [&](Best b) {
-    if (b.max > best.max || (b.max == best.max && b.at < best.at)) best.max = b.max, best.at = b.at;
-    best.tokens += b.tokens;
-  };
-  auto merge_lanes = [&] {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      merge({__shfl_xor_sync(kAll, best.max, o), __shfl_xor_sync(kAll, best.at, o),
-             __shfl_xor_sync(kAll, best.tokens, o)});
-  };
-  merge_lanes();
+  M = warp_max(M);
 #pragma unroll
   for (int b = 0; b < kBins; ++b) column[b * kT] = 0;
   if constexpr (kC > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (lane < kC) *remote(&sh.best[rank * kW + warp], lane) = best;
-  const bool greedy = !(temp > 0.0f);
-  const Two c = log2e_over(greedy ? 1.0f : fminf(fmaxf(temp, 1e-30f), 1e30f));
+  if (lane < kC) *remote(&sh.max[rank * kW + warp], lane) = M;
+  // only the first in rank stays: of the largest logits the lowest index
+  const bool only = !(temp > 0.0f) || min_p > 1.0f;
+  const Two c = log2e_over(only ? 1.0f : fminf(fmaxf(temp, 1e-30f), 1e30f));
   sync();
   const int e0 = 2 * lane, e1 = 2 * lane + 1;  // a lane's warps of the cluster
-  best = {-CUDART_INF_F, V, 0};
-  if (e0 < kN) merge(sh.best[e0]);
-  if (e1 < kN) merge(sh.best[e1]);
-  merge_lanes();
-  best = {uniform(best.max), uniform(best.at), uniform(best.tokens)};
-  const float M = best.max;
-  if (greedy || best.tokens == 0) {
-    if (rank == 0 && tid == 0) {
-      a.tokens[row] = best.tokens ? best.at : 0;
-      if (a.kept) a.kept[row] = best.tokens ? 1 : 0;
+  M = uniform(warp_max(fmaxf(e0 < kN ? sh.max[e0] : -CUDART_INF_F, e1 < kN ? sh.max[e1] : -CUDART_INF_F)));
+  auto at = [&](int i) { return held ? hold[i] : clean(z_row[i]); };
+  if (only || M == -CUDART_INF_F) {
+    int first = V;
+    for (int i = tid; i < count; i += kT)
+      if (at(i) == M && first == V) first = base + i;
+    first = __reduce_min_sync(kAll, first);
+    if (lane == 0) *remote(&sh.at[rank * kW + warp], 0) = first;
+    sync();
+    if (rank != 0 || warp != 0) return;
+    first = __reduce_min_sync(kAll, min(e0 < kN ? sh.at[e0] : V, e1 < kN ? sh.at[e1] : V));
+    if (lane == 0) {
+      a.tokens[row] = M > -CUDART_INF_F ? first : 0;
+      if (a.kept) a.kept[row] = M > -CUDART_INF_F ? 1 : 0;
     }
     return;
   }
-  const bool by_k = top_k > 0 && top_k < best.tokens, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
+  const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
 
-  auto at = [&](int i) { return held ? hold[i] : clean(z_row[i]); };
   const float c_bins = c.h * 0.75f;
   auto y_of = [&](float z) { return z == M ? 0.0f : (M - z) * c_bins; };  // in bins
   auto bin_of = [&](float y) { return min(kBins - 1, (int)y); };
@@ -271,16 +264,23 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // overlap; past the run's end and for -inf nothing is added.
   const bool few = by_k && top_k <= kFew;  // no weights are wanted
   auto count_bins = [&](auto weighed) {
+    float next[4];
+    auto ask = [&](int i0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) next[q] = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
+    };
+    ask(lo);
     for (int i0 = lo; i0 < hi; i0 += 4) {
       int b[4];
       unsigned long long m[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float z = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
+        const float z = next[q];
         b[q] = bin_of(y_of(z));
         m[q] = z > -CUDART_INF_F ? 1ull << kCount : 0;
         if constexpr (decltype(weighed)::value) m[q] += mass_of(z, b[q]);
       }
+      ask(i0 + 4);
 #pragma unroll
       for (int q = 0; q < 4; ++q) column[b[q] * kT] += m[q];
     }
@@ -303,31 +303,53 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     const int room = (kBins - 1 - bin) * 128;
     int n = 0;
     const float y0 = (float)bin, y1 = bin < kBins - 1 ? y0 + 1.0f : CUDART_NAN_F;
-#pragma unroll 4
-    for (int j = 0; j < each; ++j) {
-      const int i = lo + j;
-      const float z = i < hi ? hold[i] : -CUDART_INF_F;
-      const float y = y_of(z);
-      const bool in = z > -CUDART_INF_F && y >= y0 && !(y >= y1);
-      const unsigned m = __ballot_sync(kAll, in);
-      const int k = n + __popc(m & ((1u << lane) - 1));
-      if (in && k < room) *place_of(k) = (uint16_t)i;
-      n += __popc(m);
+    for (int j = 0; j < each; j += 4) {
+      float z[4];
+      bool in[4];
+      unsigned m[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[q] = lo + j + q < hi ? hold[lo + j + q] : -CUDART_INF_F;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float y = y_of(z[q]);
+        in[q] = z[q] > -CUDART_INF_F && y >= y0 && !(y >= y1);
+        m[q] = __ballot_sync(kAll, in[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = n + __popc(m[q] & ((1u << lane) - 1));
+        if (in[q] && k < room) *place_of(k) = (uint16_t)(lo + j + q);
+        n += __popc(m[q]);
+      }
     }
     gathered_n = uniform(n);
     in_columns = gathered_n <= room;
     __syncwarp();
   };
-  auto members = [&](auto f) {
+  auto members = [&](auto f) {  // f(z[4], i[4], in[4])
+    float z[4];
+    int i[4];
+    bool in[4];
     if (held && in_columns) {
-      for (int j = lane; j < gathered_n; j += 32) {
-        const int i = *place_of(j);
-        f(hold[i], i);
+      for (int j = lane; j < gathered_n; j += 128) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          in[q] = j + 32 * q < gathered_n;
+          i[q] = *place_of(in[q] ? j + 32 * q : lane);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] = hold[i[q]];
+        f(z, i, in);
       }
     } else {
-      for (int i = lo; i < hi; ++i) {
-        const float z = at(i);
-        if (z > -CUDART_INF_F && bin_of(y_of(z)) == members_of) f(z, i);
+      for (int j = lo; j < hi; j += 4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          i[q] = min(j + q, hi - 1);
+          z[q] = at(i[q]);
+          in[q] = j + q < hi && z[q] > -CUDART_INF_F && bin_of(y_of(z[q])) == members_of;
+        }
+        f(z, i, in);
       }
     }
   };
@@ -404,12 +426,16 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       int part = -1;
       uint64_t from = 0, to = ~0ull;
       auto part_of = [&](float y) { return min(kSub - 1, (int)((y - (float)bin) * (float)kSub)); };
-      auto each_left = [&](auto f) {
+      auto each_left = [&](auto f) {  // f(z[4], rank[4], in[4])
         gather(bin);
-        members([&](float z, int i) {
-          if (part >= 0 && part_of(y_of(z)) != part) return;
-          const uint64_t r = rank_of(z, base + i);
-          if (from <= r && r <= to) f(z, r);
+        members([&](const float (&z)[4], const int (&i)[4], bool (&in)[4]) {
+          uint64_t r[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            r[q] = rank_of(z[q], base + i[q]);
+            in[q] = in[q] && (part < 0 || part_of(y_of(z[q])) == part) && from <= r[q] && r[q] <= to;
+          }
+          f(z, r, in);
         });
       };
       const Bin* from_blocks = &sh.bins[0][bin];  // the chosen part's entry of block 0, the blocks' apart
@@ -421,7 +447,11 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
           if (tid == 0) sh.lo = ~0ull, sh.hi = 0;
           __syncthreads();
           unsigned long long l = ~0ull, h = 0;
-          each_left([&](float, uint64_t r) { l = min(l, (unsigned long long)r), h = max(h, (unsigned long long)r); });
+          each_left([&](const float (&)[4], const uint64_t (&r)[4], const bool (&in)[4]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (in[q]) l = min(l, (unsigned long long)r[q]), h = max(h, (unsigned long long)r[q]);
+          });
           if (l <= h) atomicMin(&sh.lo, l), atomicMax(&sh.hi, h);
           __syncthreads();
           if (tid < kC) {
@@ -437,17 +467,33 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
           ranged = true;
         }
         const int shift = max(0, 64 - __clzll((long long)(to - from)) - 6);
-        if (tid < kSub) sh.sub_mass[tid] = 0, sh.sub_count[tid] = 0;
+        for (int t = tid; t < 4 * kSub; t += kT) sh.own[t / kSub][t % kSub] = 0;
         if (level) sync();  // the last level's parts have been read
         else __syncthreads();
-        each_left([&](float z, uint64_t r) {
-          const int p = by_y ? part_of(y_of(z)) : (int)((r - from) >> shift);
-          if (!few) atomicAdd(&sh.sub_mass[p], (unsigned long long)mass_of(z, bin));
-          atomicAdd(&sh.sub_count[p], 1u);
+        // a mass in three parts of 13 and 14 bits: 2^17 of them fit 32 bits
+        each_left([&](const float (&z)[4], const uint64_t (&r)[4], const bool (&in)[4]) {
+          uint64_t m[4] = {};
+          if (!few)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m[q] = mass_of(z[q], bin);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (in[q]) {
+              const int p = by_y ? part_of(y_of(z[q])) : (int)((r[q] - from) >> shift);
+              if (!few) {
+                atomicAdd(&sh.own[0][p], (uint32_t)m[q] & 0x1fff);
+                atomicAdd(&sh.own[1][p], (uint32_t)(m[q] >> 13) & 0x1fff);
+                atomicAdd(&sh.own[2][p], (uint32_t)(m[q] >> 26));
+              }
+              atomicAdd(&sh.own[3][p], 1u);
+            }
         });
         __syncthreads();
-        for (int t = tid; t < kC * kSub; t += kT)
-          *remote(&sh.sub[rank][t % kSub], t / kSub) = Bin{sh.sub_mass[t % kSub], sh.sub_count[t % kSub], 0};
+        for (int t = tid; t < kC * kSub; t += kT) {
+          const int p = t % kSub;
+          const uint64_t m = sh.own[0][p] + ((uint64_t)sh.own[1][p] << 13) + ((uint64_t)sh.own[2][p] << 26);
+          *remote(&sh.sub[rank][p], t / kSub) = Bin{m, sh.own[3][p], 0};
+        }
         sync();
         const int p = choose(&sh.sub[0][0], kSub, kSub, bin);
         if (by_y) {
@@ -477,10 +523,14 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       for (int r = 0; r < rank; ++r) place += from_blocks[r * apart].count;
       if (tid == 0) sh.fill = place, sh.hit = kList;
       __syncthreads();
-      each_left([&](float, uint64_t r) {
-        const int p = atomicAdd(&sh.fill, 1);
+      each_left([&](const float (&)[4], const uint64_t (&r)[4], const bool (&in)[4]) {
 #pragma unroll
-        for (int b = 0; b < kC; ++b) *remote(&sh.list[which][p], b) = r;
+        for (int q = 0; q < 4; ++q)
+          if (in[q]) {
+            const int p = atomicAdd(&sh.fill, 1);
+#pragma unroll
+            for (int b = 0; b < kC; ++b) *remote(&sh.list[which][p], b) = r[q];
+          }
       });
       sync();
       const int n = (int)left;
@@ -567,7 +617,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         meet();
         stay = min(stay, sh.hit + 1);
       }
-      const bool kept = tid < stay && (!by_m || tid == 0 || !less(w, least));
+      const bool kept = tid < stay && (!by_m || !less(w, least));
       if (kept) {
         atomicAdd(&sh.fill, 1);
       }
@@ -607,16 +657,20 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
   }
   last = min(last, kBins - 1);
-  auto stays = [&](float z, int i) {
-    return rank_of(z, base + i) <= cut && (!by_m || base + i == best.at || !less(weight(z), least));
-  };
+  auto stays = [&](float z, int i) { return rank_of(z, base + i) <= cut && (!by_m || !less(weight(z), least)); };
   for (int b = whole; b <= last; ++b) {
     gather(b);
     __syncwarp();
     column[b * kT] = 0;
     __syncwarp();
-    members([&](float z, int i) {
-      if (stays(z, i)) atomicAdd(columns + b * kT + by_each.div((uint32_t)i), mass_of(z, b) + (1ull << kCount));
+    members([&](const float (&z)[4], const int (&i)[4], const bool (&in)[4]) {
+      uint64_t m[4];
+      bool stay[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m[q] = mass_of(z[q], b), stay[q] = stays(z[q], i[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (in[q] && stay[q]) atomicAdd(columns + b * kT + by_each.div((uint32_t)i[q]), m[q] + (1ull << kCount));
     });
   }
   __syncwarp();
@@ -678,7 +732,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (r) found = i0 + __ffs(r) - 1;
     if (h) last_in = i0 + 31 - __clz(h);
   }
-  if (lane == 0) a.tokens[row] = found >= 0 ? base + found : last_in >= 0 ? base + last_in : best.at;
+  if (lane == 0) a.tokens[row] = base + (found >= 0 ? found : last_in);
 }
 
 template <int kC, bool kHeld>
