@@ -4,7 +4,7 @@
 // With tokens ranked by (logit descending, index ascending), what top-k and top-p keep is a
 // prefix of the ranking: all that is wanted is its last token, the cut. Nothing is sorted.
 // A cut is found by counting: tokens fall into bins of y = (max - z) log2(e) / T (a weight
-// is 2^-y), 4/3 wide, the bin in which the running count or mass passes the target is split again,
+// is 2^-y), the bin in which the running count or mass passes the target is split again,
 // and once few enough tokens are left they are ranked among themselves.
 //
 // Whole-number answers need more than f32 (a cut lies between tokens whose weights are
@@ -35,15 +35,12 @@ using namespace draw;
 
 namespace cg = cooperative_groups;
 
-constexpr int kBins = 16;   // of 3/4 y: [b, b + 1), the last one also all above
+constexpr int kBins = 20;   // of y: (b - 1, b], the last one also all above
 constexpr int kSub = 64;    // parts of a bin that is split
 constexpr int kList = 128;  // tokens that are ranked among themselves
 constexpr int kFew = 64;    // a top_k that always ends in one list
-constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(exponent(b) + kFrac)
+constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(b + kFrac)
 constexpr int kCount = 50;  // a column's entry: count << kCount | mass
-
-// A weight in bin b is at most 2^-exponent(b).
-__device__ __forceinline__ constexpr int exponent(int b) { return 4 * b / 3; }
 
 struct Bin {
   uint64_t mass;
@@ -109,17 +106,29 @@ __device__ __forceinline__ float warp_max(float v) {
   return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
-// exp((z - M) / T) = m 2^(n - kFrac), m up to 2^(kFrac + 1); c = log2(e) / T. With y = (z -
-// M) c as a pair, k/256 its nearest multiple of 1/256 and f the rest, 2^f - 1 is its Taylor
-// series (the f^4 term is below 2^-42) and 2^(k/256) comes from the table: Tang's method
-// (ACM TOMS 1989). Below y = -125.5 it is 0, also for -inf.
-__device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* tab, int& n) {
+// -256 y of a logit, rounded to a whole number: 0 for M (also an infinite one), at least
+// -126 * 256. It falls with the logit; bins and their parts are ranges of it.
+constexpr float kRound = 49152.0f;  // numbers of its size have 1/256 as their last place
+__device__ __forceinline__ float to_grid(float p) { return __fadd_rn(fmaxf(fminf(p, 0.0f), -126.0f), kRound); }
+__device__ __forceinline__ int steps_of(float t) { return __float_as_int(t) - __float_as_int(kRound); }
+__device__ __forceinline__ int place(float z, float M, Two c) {
+  return steps_of(to_grid(__fmul_rn(__fadd_rn(z, -M), c.h)));
+}
+__device__ __forceinline__ int bin_of(int k) { return min(kBins - 1, -(k >> 8)); }
+// Of kSub parts of a bin, the last one apart.
+__device__ __forceinline__ int part_of(int k, int bin) { return (255 - k - 256 * bin) >> 2; }
+static_assert(kSub == 64, "four of 256 steps");
+
+// exp((z - M) / T) = m 2^(n - kFrac), 2^kFrac <= m <= 2^(kFrac + 1); c = log2(e) / T. With y
+// as a pair, k = place(z) and f the rest, 2^f - 1 is its Taylor series (the f^4 term is below
+// 2^-42) and 2^(k/256) comes from the table: Tang's method (ACM TOMS 1989). Far below (y >
+// 126) n is -126.
+__device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* tab, int& k) {
   const Two d = two_sum(z, -M);
   const float p = __fmul_rn(d.h, c.h);
   const float pe = fmaf(d.h, c.h, -p) + fmaf(d.h, c.l, __fmul_rn(d.l, c.h));
-  constexpr float kRound = 49152.0f;  // its last place is 1/256
-  const float t = __fadd_rn(fmaxf(p, -126.0f), kRound);
-  const int k = __float_as_int(t) - __float_as_int(kRound);
+  const float t = to_grid(p);
+  k = steps_of(t);
   const float fh = __fsub_rn(p, __fsub_rn(t, kRound));  // exact
   const float f = __fadd_rn(fh, pe);
   constexpr float l1h = 0.6931471824645996f, l1l = -1.9046542e-09f;  // ln 2
@@ -130,10 +139,8 @@ __device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* 
   const float v = __fmul_rn(w.h, a);
   const float ve = fmaf(w.l, a, fmaf(w.h, ae, fmaf(w.h, a, -v)));
   constexpr float kOne = (float)(1ull << kFrac);
-  const uint64_t m = w.whole + (long long)__float2int_rn(v * kOne) + (long long)__float2int_rn(ve * kOne);
-  const bool one = z == M, in = p > -125.5f;  // not in: also -inf and NaN
-  n = one ? 0 : k >> 8;
-  return one ? 1ull << kFrac : in ? m : 0;
+  const int more = __float2int_rn(v * kOne) + __float2int_rn(ve * kOne);  // within 2^31
+  return z == M ? 1ull << kFrac : w.whole + (long long)more;
 }
 
 // What all lanes hold anyway, told to the compiler: a branch on it then needs no
@@ -190,7 +197,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const int each = ((V + kC * kT - 1) / (kC * kT)) | 1;
   const int base = (int)min((int64_t)V, (int64_t)rank * kT * each);
   const int count = (int)min((int64_t)V - base, (int64_t)kT * each);
-  const int lo = min(count, tid * each), hi = min(count, lo + each);
+  const int run = tid * each, hi = min(count, run + each);
   const float* const z_row = a.logits + row * a.ld + base;
   // ---- the row and its maximum
   float M = -CUDART_INF_F;
@@ -217,6 +224,8 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       M = fmaxf(M, z);
     }
   }
+  if (held)
+    for (int i = count + tid; i < kT * each; i += kT) hold[i] = -CUDART_INF_F;
   M = warp_max(M);
 #pragma unroll
   for (int b = 0; b < kBins; ++b) column[b * kT] = 0;
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   sync();
   const int e0 = 2 * lane, e1 = 2 * lane + 1;  // a lane's warps of the cluster
   M = uniform(warp_max(fmaxf(e0 < kN ? sh.max[e0] : -CUDART_INF_F, e1 < kN ? sh.max[e1] : -CUDART_INF_F)));
-  auto at = [&](int i) { return held ? hold[i] : clean(z_row[i]); };
+  auto at = [&](int i) { return held ? hold[i] : i < count ? clean(z_row[i]) : -CUDART_INF_F; };
   if (only || M == -CUDART_INF_F) {
     int first = V;
     for (int i = tid; i < count; i += kT)
@@ -246,44 +255,45 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   }
   const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
 
-  const float c_bins = c.h * 0.75f;
-  auto y_of = [&](float z) { return z == M ? 0.0f : (M - z) * c_bins; };  // in bins
-  auto bin_of = [&](float y) { return min(kBins - 1, (int)y); };
-  auto mass_of = [&](float z, int b) {  // the weight as a whole number of 2^-(exponent(b) + kFrac)
-    int n;
-    const uint64_t m = weigh(z, M, c, sh.tab, n);
-    return m >> min(63, max(0, -(n + exponent(b))));
+  // A weight as a whole number of 2^-(bin + kFrac): in the last bin, and for tokens that far
+  // below that they end there, what is left of it.
+  auto mass_of = [&](float z, int& bin) {
+    int k;
+    const uint64_t m = weigh(z, M, c, sh.tab, k);
+    const int b = -(k >> 8);
+    bin = min(kBins - 1, b);
+    return m >> min(63, b - bin);
+  };
+  auto mass = [&](float z) {
+    int bin;
+    return mass_of(z, bin);
   };
   auto weight = [&](float z) {  // times 2^60
-    int n;
-    const uint64_t m = weigh(z, M, c, sh.tab, n);
-    return to_two(m, n - kFrac + 60);
+    int k;
+    const uint64_t m = weigh(z, M, c, sh.tab, k);
+    return to_two(k > -125 * 256 ? m : 0, (k >> 8) - kFrac + 60);
   };
   // ---- counts and masses of the bins
   // Four tokens in step, without branches, so that their chains of dependent operations
-  // overlap; past the run's end and for -inf nothing is added.
+  // overlap; for -inf, which also stands behind the row's end, nothing is added.
   const bool few = by_k && top_k <= kFew;  // no weights are wanted
   auto count_bins = [&](auto weighed) {
-    float next[4];
-    auto ask = [&](int i0) {
+    auto step = [&](auto n, int j) {
+      int b[n];
+      unsigned long long m[n];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) next[q] = i0 + q < hi ? at(i0 + q) : -CUDART_INF_F;
-    };
-    ask(lo);
-    for (int i0 = lo; i0 < hi; i0 += 4) {
-      int b[4];
-      unsigned long long m[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float z = next[q];
-        b[q] = bin_of(y_of(z));
-        m[q] = z > -CUDART_INF_F ? 1ull << kCount : 0;
-        if constexpr (decltype(weighed)::value) m[q] += mass_of(z, b[q]);
+      for (int q = 0; q < n; ++q) {
+        const float z = at(run + j + q);
+        if constexpr (decltype(weighed)::value) m[q] = mass_of(z, b[q]);
+        else m[q] = 0, b[q] = bin_of(place(z, M, c));
+        m[q] = z > -CUDART_INF_F ? m[q] + (1ull << kCount) : 0;
       }
-      ask(i0 + 4);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) column[b[q] * kT] += m[q];
-    }
+      for (int q = 0; q < n; ++q) column[b[q] * kT] += m[q];
+    };
+    int j = 0;
+    for (; j + 4 <= each; j += 4) step(std::integral_constant<int, 4>{}, j);
+    for (; j < each; ++j) step(std::integral_constant<int, 1>{}, j);
   };
   if (few) count_bins(std::false_type{});
   else count_bins(std::true_type{});
@@ -301,26 +311,37 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     if (!held) return;
     __syncwarp();
     const int room = (kBins - 1 - bin) * 128;
+    // the bin's places, on the grid: from the last token's to the first's
+    const float t0 = bin < kBins - 1 ? kRound - (float)bin : 0.0f, t1 = kRound - (float)bin + 255.0f / 256.0f;
     int n = 0;
-    const float y0 = (float)bin, y1 = bin < kBins - 1 ? y0 + 1.0f : CUDART_NAN_F;
-    for (int j = 0; j < each; j += 4) {
-      float z[4];
-      bool in[4];
-      unsigned m[4];
+    for (int j0 = 0; j0 < each; j0 += 32) {  // 32 tokens of each lane: which, how many, where to
+      unsigned in = 0;
+      const int some = min(32, each - j0);
+      auto look = [&](auto n, int j) {
+        float z[n];
+        unsigned m = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) z[q] = lo + j + q < hi ? hold[lo + j + q] : -CUDART_INF_F;
+        for (int q = 0; q < n; ++q) z[q] = hold[run + j0 + j + q];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float y = y_of(z[q]);
-        in[q] = z[q] > -CUDART_INF_F && y >= y0 && !(y >= y1);
-        m[q] = __ballot_sync(kAll, in[q]);
+        for (int q = 0; q < n; ++q) {
+          const float t = to_grid(__fmul_rn(__fadd_rn(z[q], -M), c.h));
+          if (t >= t0 && t <= t1 && z[q] > -CUDART_INF_F) m |= 1u << q;
+        }
+        in |= m << j;
+      };
+      int j = 0;
+      for (; j + 8 <= some; j += 8) look(std::integral_constant<int, 8>{}, j);
+      for (; j < some; ++j) look(std::integral_constant<int, 1>{}, j);
+      int k = __popc(in), upto = k;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += up;
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = n + __popc(m[q] & ((1u << lane) - 1));
-        if (in[q] && k < room) *place_of(k) = (uint16_t)(lo + j + q);
-        n += __popc(m[q]);
-      }
+      k = n + upto - k;
+      n += __shfl_sync(kAll, upto, 31);
+      for (; in; in &= in - 1, ++k)
+        if (k < room) *place_of(k) = (uint16_t)(run + j0 + __ffs(in) - 1);
     }
     gathered_n = uniform(n);
     in_columns = gathered_n <= room;
@@ -342,12 +363,12 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         f(z, i, in);
       }
     } else {
-      for (int j = lo; j < hi; j += 4) {
+      for (int j = run; j < hi; j += 4) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           i[q] = min(j + q, hi - 1);
           z[q] = at(i[q]);
-          in[q] = j + q < hi && z[q] > -CUDART_INF_F && bin_of(y_of(z[q])) == members_of;
+          in[q] = j + q < hi && z[q] > -CUDART_INF_F && bin_of(place(z[q], M, c)) == members_of;
         }
         f(z, i, in);
       }
@@ -394,7 +415,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
             if (i < parts_n)
 #pragma unroll
               for (int r = 0; r < kC; ++r) n[q] += parts[r * apart + i].count, sum += parts[r * apart + i].mass;
-            m[q] = to_two(sum, 60 - kFrac - exponent(unit < 0 ? min(i, kBins - 1) : unit));
+            m[q] = to_two(sum, 60 - kFrac - (unit < 0 ? min(i, kBins - 1) : unit));
           }
           uint32_t n_in = n[0] + n[1];
 #pragma unroll
@@ -425,7 +446,6 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       const int bin = choose(&sh.bins[0][0], kBins, kBins, -1);
       int part = -1;
       uint64_t from = 0, to = ~0ull;
-      auto part_of = [&](float y) { return min(kSub - 1, (int)((y - (float)bin) * (float)kSub)); };
       auto each_left = [&](auto f) {  // f(z[4], rank[4], in[4])
         gather(bin);
         members([&](const float (&z)[4], const int (&i)[4], bool (&in)[4]) {
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             r[q] = rank_of(z[q], base + i[q]);
-            in[q] = in[q] && (part < 0 || part_of(y_of(z[q])) == part) && from <= r[q] && r[q] <= to;
+            in[q] = in[q] && (part < 0 || part_of(place(z[q], M, c), bin) == part) && from <= r[q] && r[q] <= to;
           }
           f(z, r, in);
         });
@@ -475,11 +495,11 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
           uint64_t m[4] = {};
           if (!few)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m[q] = mass_of(z[q], bin);
+            for (int q = 0; q < 4; ++q) m[q] = mass(z[q]);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (in[q]) {
-              const int p = by_y ? part_of(y_of(z[q])) : (int)((r[q] - from) >> shift);
+              const int p = by_y ? part_of(place(z[q], M, c), bin) : (int)((r[q] - from) >> shift);
               if (!few) {
                 atomicAdd(&sh.own[0][p], (uint32_t)m[q] & 0x1fff);
                 atomicAdd(&sh.own[1][p], (uint32_t)(m[q] >> 13) & 0x1fff);
@@ -506,12 +526,12 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         apart = kSub;
       }
       if (ahead + left <= kList) {  // all ranks up to the part's last, to block 0
-        const float y1 = bin < kBins - 1 ? (float)(bin + 1) : CUDART_NAN_F;
-        for (int i = lo; i < hi; ++i) {
-          const float z = at(i), y = y_of(z);
-          if (!(z > -CUDART_INF_F) || y >= y1) continue;
+        for (int i = run; i < hi; ++i) {
+          const float z = at(i);
+          const int k = place(z, M, c), b = bin_of(k);
+          if (!(z > -CUDART_INF_F) || b > bin) continue;
           const uint64_t r = rank_of(z, base + i);
-          if (y >= (float)bin && ((part >= 0 && part_of(y) > part) || r > to)) continue;
+          if (b == bin && ((part >= 0 && part_of(k, bin) > part) || r > to)) continue;
           *remote(&sh.list[which][atomicAdd(remote(&sh.taken, 0), 1)], 0) = r;
         }
         upto_n = (int)(ahead + left);
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       uint64_t m = 0;
       if (lane < kBins)
         for (int r = 0; r < kC; ++r) m += sh.bins[r][lane].mass;
-      sum = to_two(m, 60 - kFrac - exponent(min(lane, kBins - 1)));
+      sum = to_two(m, 60 - kFrac - min(lane, kBins - 1));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     }
@@ -651,9 +671,9 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // the one or two where min-p may end
   int whole = cut_bin, last = cut_bin;
   if (by_m) {
-    const float y = -0.75f * lg2(min_p);  // in bins
-    whole = min(whole, max(0, (int)(y - 0.001f)));
-    last = min(last, max(0, (int)(y + 0.001f)));
+    const float y = fminf(-lg2(min_p), 200.0f);  // bin b has y from b - 1 to b, 1/512 less or more
+    whole = min(whole, (int)floorf(y - 0.01f) + 1);
+    last = min(last, (int)(y + 1.02f));
     if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
   }
   last = min(last, kBins - 1);
@@ -667,7 +687,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       uint64_t m[4];
       bool stay[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) m[q] = mass_of(z[q], b), stay[q] = stays(z[q], i[q]);
+      for (int q = 0; q < 4; ++q) m[q] = mass(z[q]), stay[q] = stays(z[q], i[q]);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (in[q] && stay[q]) atomicAdd(columns + b * kT + by_each.div((uint32_t)i[q]), m[q] + (1ull << kCount));
@@ -682,7 +702,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     for (int b = 0; b < kBins; ++b) {
       const uint64_t v = b <= last ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
       mine.count += (int)(v >> kCount);
-      const int s = 54 - kFrac - exponent(b);
+      const int s = 54 - kFrac - b;
       sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s - 1 : 0))) >> (s < 0 ? -s : 0);
     }
     mine.mass = to_two(sum, 60 - 54);
@@ -716,7 +736,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const unsigned has = __ballot_sync(kAll, mine.mass.h > 0.0f);
   const int who = reach ? __ffs(reach) - 1 : 31 - __clz(has);
   if (who > 0) cum = add(cum, shfl(in, who - 1));
-  const int start = __shfl_sync(kAll, lo, who), end = __shfl_sync(kAll, hi, who);
+  const int start = __shfl_sync(kAll, run, who), end = __shfl_sync(kAll, hi, who);
   int found = -1, last_in = -1;
   for (int i0 = start; i0 < end && found < 0; i0 += 32) {
     const int i = i0 + lane;
@@ -753,7 +773,7 @@ template <int kC>
 Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
   constexpr int kT = 256;
   const int64_t columns = (int64_t)kBins * kT * 8, each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
-  const int64_t smem = columns + std::min<int64_t>(a.V, kT * each) * 4;  // and a row's part
+  const int64_t smem = columns + kT * each * 4;  // and a row's part
   if constexpr (kC == 8)
     if (smem > 200 * 1024 || kT * each > 65536) return launch_h<kC, false>(a, each, columns, s);
   return launch_h<kC, true>(a, each, smem, s);
