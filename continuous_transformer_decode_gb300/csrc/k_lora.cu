@@ -199,6 +199,10 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
 }
 
+// What all lanes hold anyway, told to the compiler: inside a branch or loop on it MMAs and
+// shuffles then need no reconvergence before each of them.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
+
 template <typename TX, typename TY, int kMT>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.block_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2, tig = lane & 3;
   // the other blocks' shared memory can be written once they have started
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   for (int i = tid; i < kSlots; i += kT) sh.key[i] = -1;
@@ -255,6 +259,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     items += sh.firsts[w];
     bares += sh.bare[w];
   }
+  items = uniform(items);
   if (has && nth % kR == 0) sh.lead[at + __popc(leads & below)] = (int16_t)tid;
 
   // this block's columns, in chunks of 32
@@ -306,10 +311,10 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 
   for (int item = item0; item < items; item += per_window) {
     __syncthreads();
-    const int lead = sh.lead[item], id = sh.id[lead], part = sh.nth[lead] / kR;
+    const int lead = uniform(sh.lead[item]), id = uniform(sh.id[lead]), part = sh.nth[lead] / kR;
     const bool mine = has && my_id == id && nth / kR == part;
     if (mine) sh.row[nth % kR] = my_row;
-    const int rows = __syncthreads_count(mine);
+    const int rows = uniform(__syncthreads_count(mine));
     const float scale = a.scale[id];
     const __nv_bfloat16* const A = a.A + (int64_t)id * a.rank * a.K;
     const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
