@@ -109,12 +109,12 @@ struct Eight {
   }
 };
 
-// d += a b over 32 values of the summed index: rows g (lo) and g + 8 (hi) of a, column g
-// of b, a lane's 8 values each.
-__device__ __forceinline__ void mma32(float (&d)[4], const uint4& lo, const uint4& hi, const uint4& b) {
-  const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-  attn::mma16816(d, a0, b.x, b.y);
-  attn::mma16816(d, a1, b.z, b.w);
+// d += a b over 16 of 32 values of the summed index (half 0, then 1): rows g (lo) and g + 8
+// (hi) of a, column g of b, a lane's 8 values each. Products that do not add to the same sums
+// go between the halves: an MMA waits for the last one's sums.
+__device__ __forceinline__ void mma_half(float (&d)[4], const uint4& lo, const uint4& hi, const uint4& b, int half) {
+  const uint32_t a[4] = {half ? lo.z : lo.x, half ? hi.z : hi.x, half ? lo.w : lo.y, half ? hi.w : hi.y};
+  attn::mma16816(d, a, half ? b.z : b.x, half ? b.w : b.y);
 }
 
 // 8 consecutive values as they lie in memory.
@@ -203,7 +203,8 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
 // shuffles then need no reconvergence before each of them.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
-template <typename TX, typename TY, int kMT>
+// kMT: row tiles of an item; kNT: tiles of ranks of half a block's warps (kMT 4).
+template <typename TX, typename TY, int kMT, int kNT>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
   constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
@@ -345,9 +346,9 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
             w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
                                          : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
 #pragma unroll
-            for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(d[j], lo.p[p], hi.p[p], w[j]);
+            for (int j = 0; j < 4; ++j) mma_half(d[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -396,30 +397,49 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         t.b = min(t.b + 2, piece(t.s + 1));
         return settle(t);
       };
+      // a thread's 16-byte parts of a stage: the same rows and columns in every step
+      constexpr int kXN = kR * kXC / kT, kAN = kNT / 2;
+      const TX* x_from[kXN];
+      uint32_t x_to[kXN], a_to[kAN];
+      const __nv_bfloat16* a_from[kAN];
+      const int x_k = tid % kXC * 16 / (int)sizeof(TX), a_k = tid % 8 * 8;
+#pragma unroll
+      for (int i = 0; i < kXN; ++i) {
+        const int r = (tid + i * kT) / kXC, q = tid % kXC;
+        x_from[i] = r < rows ? x + sh.row[r] * a.x_stride + x_k : nullptr;
+        x_to[i] = r * 16 * kXC + 16 * (q ^ (r & 1) * (sizeof(TX) == 2 ? 4 : 1));
+      }
+#pragma unroll
+      for (int i = 0; i < kAN; ++i) {
+        const int r = (tid + i * kT) / 8, q = tid % 8;
+        a_from[i] = r < a.rank ? A + (int64_t)r * a.K + a_k : nullptr;
+        a_to[i] = kR * 16 * kXC + r * 128 + 16 * (q ^ (r & 1) * 4);
+      }
       auto fetch = [&](Step t, int slot) {
         if (t.s < kW) {
-          unsigned char* const sx = stages + slot * sz.stage;
-          unsigned char* const sa = sx + kR * 16 * kXC;
-          for (int i = tid; i < kR * kXC; i += kT) {
-            const int r = i / kXC, q = i % kXC, k = 32 * t.b + q * 16 / (int)sizeof(TX);
-            const bool in = r < rows && k < a.K;
-            const int64_t o = in ? sh.row[r] * a.x_stride + k : 0;
-            unsigned char* const to = sx + r * 16 * kXC + 16 * (q ^ (r & 1) * (sizeof(TX) == 2 ? 4 : 1));
+          unsigned char* const to = stages + slot * sz.stage;
+          const uint32_t to32 = attn::smem_u32(to);
+          const int k = 32 * t.b;
+#pragma unroll
+          for (int i = 0; i < kXN; ++i) {
+            const bool in = x_from[i] && k + x_k < a.K;
             if (x_vec) {
-              copy16(attn::smem_u32(to), x + o, in);
+              copy16(to32 + x_to[i], in ? x_from[i] + k : x, in);
             } else {
 #pragma unroll
-              for (int e = 0; e < 16 / (int)sizeof(TX); ++e) reinterpret_cast<TX*>(to)[e] = in ? x[o + e] : TX(0.0f);
+              for (int e = 0; e < 16 / (int)sizeof(TX); ++e)
+                reinterpret_cast<TX*>(to + x_to[i])[e] = in ? x_from[i][k + e] : TX(0.0f);
             }
           }
-          for (int i = tid; i < a.rank * 8; i += kT) {
-            const int r = i / 8, q = i % 8, k = 32 * t.b + 8 * q;
-            copy16(attn::smem_u32(sa + r * 128 + 16 * (q ^ (r & 1) * 4)), A + (k < a.K ? (int64_t)r * a.K + k : 0), k < a.K);
+#pragma unroll
+          for (int i = 0; i < kAN; ++i) {
+            const bool in = k + a_k < a.K;
+            if (a_from[i]) copy16(to32 + a_to[i], in ? a_from[i] + k : A, in);
           }
         }
         attn::cp_commit();
       };
-      float d[8][4] = {}, e[8][4] = {};
+      float d[kNT][4] = {}, e[kNT][4] = {};
       Step now = settle({0, kb0}), ahead = now;
       int slot = 0, last = -1;
       for (int i = 0; i < kStages - 1; ++i) {
@@ -428,7 +448,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       }
       auto add_piece = [&](int s) {  // the first piece's sums are the start
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < kNT; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             d[j][q] = s == 0 ? e[j][q] : d[j][q] + e[j][q];
@@ -459,14 +479,16 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
               lo.load2(px + q, g & 1);
               hi.load2(px + 8 * 16 * kXC + q, g & 1);
             }
+            uint4 w[kNT];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int nt = half + 2 * j;
-              if (nt >= tiles) break;
-              const uint4 w = *reinterpret_cast<const uint4*>(sa + (8 * nt + g) * 128 + 16 * ((4 * b + tig) ^ ((g & 1) * 4)));
+            for (int j = 0; j < kNT; ++j)
+              w[j] = half + 2 * j < tiles
+                         ? *reinterpret_cast<const uint4*>(sa + (8 * (half + 2 * j) + g) * 128 + 16 * ((4 * b + tig) ^ ((g & 1) * 4)))
+                         : make_uint4(0, 0, 0, 0);
 #pragma unroll
-              for (int p = 0; p < Eight<TX>::kParts; ++p) mma32(e[j], lo.p[p], hi.p[p], w);
-            }
+            for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
+#pragma unroll
+              for (int j = 0; j < kNT; ++j) mma_half(e[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
           }
         }
         now = after(now);
@@ -475,7 +497,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       attn::cp_wait<0>();
       if (last >= 0) add_piece(last);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kNT; ++j)
         if (half + 2 * j < tiles) put(sums, mt, half + 2 * j, d[j]);
       cluster.sync();
       // this block adds up kR / kC of the rows and gives them to all
@@ -507,10 +529,11 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     }
 
     // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles
-    uint4 w[2][4];
-    auto load_b = [&](int chunk, int b0) {  // tile j's column g over two blocks of ranks
+    constexpr int kHold = 2;  // blocks of ranks of B in registers
+    uint4 w[kHold][4];
+    auto load_b = [&](int chunk, int b0) {  // tile j's column g
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < kHold; ++b) {
         const int r = 32 * (b0 + b) + 8 * tig;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -523,10 +546,9 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW) {
       const int col = 32 * chunk + 8 * tig;
       const bool whole = y_vec && 32 * chunk + 32 <= a.N;
-      if (rblocks <= 2) load_b(chunk, 0);
+      if (rblocks <= kHold) load_b(chunk, 0);
 #pragma unroll 1
-      for (int m0 = 0; m0 < kMT; m0 += kMP) {
-        if (16 * m0 >= rows) break;
+      for (int m0 = 0; 16 * m0 < rows; m0 += kMP) {
         Raw8<TY> y[kMP][2];
         int row[kMP][2];
 #pragma unroll
@@ -538,23 +560,30 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
             else y[m][h].clear();
           }
         float d[kMP][4][4] = {};
+        const __nv_bfloat16* t = low + (16 * m0 + g) * sz.pitch + 8 * tig;
 #pragma unroll 1
-        for (int b0 = 0; b0 < rblocks; b0 += 2) {
-          if (rblocks > 2) load_b(chunk, b0);
-          const __nv_bfloat16* const t = low + (16 * m0 + g) * sz.pitch + 32 * b0 + 8 * tig;
+        for (int b0 = 0; b0 < rblocks; b0 += kHold) {
+          if (rblocks > kHold) load_b(chunk, b0);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
+          for (int b = 0; b < kHold; ++b) {
             if (b0 + b >= rblocks) break;
 #pragma unroll
-            for (int p = 0; p < kParts; ++p)
+            for (int p = 0; p < kParts; ++p) {
+              uint4 lo[kMP], hi[kMP];
 #pragma unroll
               for (int m = 0; m < kMP; ++m) {
                 const __nv_bfloat16* const u = t + (p * kR + 16 * m) * sz.pitch + 32 * b;
-                const uint4 lo = *reinterpret_cast<const uint4*>(u), hi = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma32(d[m][j], lo, hi, w[b][j]);
+                lo[m] = *reinterpret_cast<const uint4*>(u), hi[m] = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
               }
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int m = 0; m < kMP; ++m)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m], hi[m], w[b][j], i);
+            }
           }
+          t += 32 * kHold;
         }
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
@@ -570,15 +599,15 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   }
 }
 
-template <typename TX, typename TY, int kMT>
+template <typename TX, typename TY, int kMT, int kNT>
 Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_lora<TX, TY, kMT>, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
+  l.error = allow_smem(k_lora<TX, TY, kMT, kNT>, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
   if (l.error != cudaSuccess) return l;
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  l.add(launch_k_cluster(k_lora<TX, TY, kMT>, dim3((unsigned)(windows * per_window * kC)), kT,
+  l.add(launch_k_cluster(k_lora<TX, TY, kMT, kNT>, dim3((unsigned)(windows * per_window * kC)), kT,
                          (size_t)Sizes(kMT, kParts, a.rank, sizeof(TX)).bytes, s, kC, a, per_window));
   return l;
 }
@@ -588,8 +617,8 @@ Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const bool wide = a.n > 1024;
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  if (wide) return launch_t<TX, TY, 4>(a, 8, s);
-  return launch_t<TX, TY, 1>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
+  if (wide) return a.rank <= 64 ? launch_t<TX, TY, 4, 4>(a, 8, s) : launch_t<TX, TY, 4, 8>(a, 8, s);
+  return launch_t<TX, TY, 1, 0>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 
 }  // namespace
