@@ -162,10 +162,6 @@ struct Raw8 {
   }
 };
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 struct Gather {
   int key[kSlots];
   uint16_t count[kW][kSlots];  // rows of a warp
@@ -272,21 +268,6 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   const bool x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && a.x_stride * sizeof(TX) % 16 == 0;
   const bool y_vec = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
                      (a.base_stride | a.out_stride) * sizeof(TY) % 16 == 0;
-  // ---- rows without an adapter, shared by the window's clusters
-  if (a.base != a.out && bares) {
-    unsigned m = bare;
-    for (int i = bare_at; m; ++i, m &= m - 1) {  // a warp its own rows
-      if (i % per_window != item0) continue;
-      const int64_t row = first + warp * 32 + __ffs(m) - 1;
-      for (int j = 32 * chunk0 + 8 * lane; j < min(a.N, 32 * chunk1); j += 256) {
-        const bool whole = y_vec && j + 8 <= a.N;
-        Raw8<TY> v;
-        v.clear();
-        if (base) v.load(base + row * a.base_stride + j, whole, a.N - j);
-        v.store(out + row * a.out_stride + j, whole, a.N - j);
-      }
-    }
-  }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   // ---- this block's part of K, in blocks of 32
   const int kbs = (a.K + 31) / 32;
@@ -294,24 +275,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   const int tiles = a.rank / 8, rblocks = (a.rank + 31) / 32;
   auto piece = [&](int s) { return kb0 + (kb1 - kb0) * s / kW; };  // the s-th of eight starts here
 
-  // What an item reads is asked into L2 ahead of its use: A (this block's K) and B (its
-  // columns) of all items at once, base with the item.
-  __syncthreads();  // sh.lead
   for (int item = item0; item < items; item += per_window) {
-    const int64_t id = sh.id[sh.lead[item]];
-    const int line = 64 * (kb1 - kb0);  // bytes of a rank
-    const char* const pa = reinterpret_cast<const char*>(a.A + id * a.rank * a.K + 32 * kb0);
-    for (int i = tid; i < a.rank * ((line + 127) / 128); i += kT) {
-      const int r = i % a.rank, o = i / a.rank * 128;
-      if (32 * kb0 + o / 2 < a.K) prefetch_l2(pa + (int64_t)r * a.K * 2 + o);
-    }
-    const char* const pb = reinterpret_cast<const char*>(a.B + (id * a.N + 32 * chunk0) * a.rank);
-    const int64_t bytes = (int64_t)(min(a.N, 32 * chunk1) - 32 * chunk0) * a.rank * 2;
-    for (int64_t o = 128 * tid; o < bytes; o += 128 * kT) prefetch_l2(pb + o);
-  }
-
-  for (int item = item0; item < items; item += per_window) {
-    __syncthreads();
+    __syncthreads();  // also: sh.lead
     const int lead = uniform(sh.lead[item]), id = uniform(sh.id[lead]), part = sh.nth[lead] / kR;
     const bool mine = has && my_id == id && nth / kR == part;
     if (mine) sh.row[nth % kR] = my_row;
@@ -597,6 +562,21 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       }
     }
   }
+  // ---- rows without an adapter, shared by the window's clusters
+  if (a.base != a.out && bares) {
+    unsigned m = bare;
+    for (int i = bare_at; m; ++i, m &= m - 1) {  // a warp its own rows
+      if (i % per_window != item0) continue;
+      const int64_t row = first + warp * 32 + __ffs(m) - 1;
+      for (int j = 32 * chunk0 + 8 * lane; j < min(a.N, 32 * chunk1); j += 256) {
+        const bool whole = y_vec && j + 8 <= a.N;
+        Raw8<TY> v;
+        v.clear();
+        if (base) v.load(base + row * a.base_stride + j, whole, a.N - j);
+        v.store(out + row * a.out_stride + j, whole, a.N - j);
+      }
+    }
+  }
 }
 
 template <typename TX, typename TY, int kMT, int kNT>
@@ -617,7 +597,7 @@ Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const bool wide = a.n > 1024;
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  if (wide) return a.rank <= 64 ? launch_t<TX, TY, 4, 4>(a, 8, s) : launch_t<TX, TY, 4, 8>(a, 8, s);
+  if (wide) return a.rank <= 64 ? launch_t<TX, TY, 4, 4>(a, 6, s) : launch_t<TX, TY, 4, 8>(a, 6, s);
   return launch_t<TX, TY, 1, 0>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 
