@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
   const Sizes sz(kMT, kParts, a.rank, sizeof(TX));
   __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
-  float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
+  float* const block_sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
   const int c = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2, tig = lane & 3;
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     const __nv_bfloat16* const A = a.A + (int64_t)id * a.rank * a.K;
     const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
     auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
-    if (kMT == 1 && item != item0) cluster.sync();  // the last item's sums have been read
+    const bool few = kMT == 1 || rows <= 16;
+    if (few && item != item0) cluster.sync();  // the last item's sums have been read
 
     auto put = [&](float* to, int mt, int nt, const float (&d)[4]) {
       float* p = to + (16 * mt + g) * a.rank + 8 * nt + 2 * tig;
@@ -293,7 +294,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[2], d[3]);
     };
     const int tile = 16 * a.rank;
-    if constexpr (kMT == 1) {
+    if (few) {
+      float* const sums = kMT == 1 ? block_sums : reinterpret_cast<float*>(low);
       const int64_t r0 = row_of(g), r1 = row_of(g + 8);
       for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks, a warp its piece of K
         float d[4][4] = {};
@@ -327,23 +329,37 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         for (int r = 0; r < kC; ++r) *cluster.map_shared_rank(sums + (kW + c) * tile + i, r) = s;
       }
       cluster.sync();
-      for (int i = tid; i < 16 * sz.pitch; i += kT) {
+      auto total = [&](int i) {  // of place i of the parts' rows
         const int m = i / sz.pitch, r = i - m * sz.pitch;
-        float s = 0.0f;
-        if (r < a.rank) {
-          const float* p = sums + kW * tile + m * a.rank + r;
-          s = p[0];
+        if (m >= 16 || r >= a.rank) return 0.0f;
+        const float* p = sums + kW * tile + m * a.rank + r;
+        float v = p[0];
 #pragma unroll
-          for (int b = 1; b < kC; ++b) s += p[b * tile];
-          s *= scale;
-        }
-        __nv_bfloat16 v[kParts];
-        split(s, v);
+        for (int b = 1; b < kC; ++b) v += p[b * tile];
+        return v * scale;
+      };
+      auto keep = [&](int i, float v) {
+        __nv_bfloat16 u[kParts];
+        split(v, u);
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = v[p];
+        for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = u[p];
+      };
+      if constexpr (kMT == 1) {
+        for (int i = tid; i < 16 * sz.pitch; i += kT) keep(i, total(i));
+      } else {  // the sums lie where the parts go
+        constexpr int kMost = 16 * (128 + 32) / kT;  // of the longest pitch
+        float v[kMost];
+#pragma unroll
+        for (int q = 0; q < kMost; ++q) v[q] = total(tid + q * kT);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kMost; ++q)
+          if (tid + q * kT < 16 * sz.pitch) keep(tid + q * kT, v[q]);
       }
       __syncthreads();
-    } else {
+    }
+    if constexpr (kMT > 1) if (!few) {
+      float* const sums = block_sums;
       static_assert(kMT == 4, "eight warps are four row tiles and two halves of the ranks");
       const int mt = warp & 3, half = warp >> 2;  // tiles half, half + 2, .. of the ranks
       // Steps of up to two blocks of K inside a piece, kStages - 1 of them on their way. A
@@ -594,7 +610,7 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  const bool wide = a.n > 1024;
+  const bool wide = a.n > 2048;
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
   if (wide) return a.rank <= 64 ? launch_t<TX, TY, 4, 4>(a, 6, s) : launch_t<TX, TY, 4, 8>(a, 6, s);
