@@ -57,16 +57,18 @@ __device__ __forceinline__ T block_scan(T v, T* tmp, T& total) {
   return before + ahead;
 }
 
-// The last i < n with first[i] <= x (first[0] = 0 <= x).
-__device__ __forceinline__ int owner(const int* first, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= x) lo = mid;
-    else hi = mid;
-  }
+// The last i < n with first[i] <= x (first[0] = 0 <= x), in steps of `top` (the largest
+// power of two below n) and halves of it: the same number of steps for every thread.
+__device__ __forceinline__ int owner(const int* first, int n, int top, int x) {
+  int lo = 0;
+  for (int d = top; d > 0; d >>= 1)
+    if (lo + d < n && first[lo + d] <= x) lo += d;
   return lo;
 }
+
+// What all lanes hold anyway, told to the compiler: a ballot or shuffle in a branch on it
+// needs no reconvergence first.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
 template <int kC>
 __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
@@ -81,11 +83,13 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     else cluster.sync();
   };
   const int c = kC == 1 ? 0 : (int)cluster.block_rank();
-  const int n = a.n_lanes, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = a.n_lanes, tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const int top = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
   int* const held = sh;           // tokens kept
   int* const pages0 = sh + n;     // running sum of the pages wanted
   int* const rows0 = pages0 + n;  // of the rows
   int* const gone0 = rows0 + n;   // of the pages let go
+  uint16_t* const found = reinterpret_cast<uint16_t*>(gone0 + n);  // this block's free pages
   if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     };
     if (total.a <= INT32_MAX) {
       for (int64_t t = c * kT + tid; t < total.a; t += kC * kT) {
-        const int l = owner(gone0, n, (int)t);
+        const int l = owner(gone0, n, top, (int)t);
         let_go(l, pages_of(held[l]) + ((int)t - gone0[l]));
       }
     } else {
@@ -186,25 +190,30 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   if (ok) {
     const int want = (int)total.b;
     auto take = [&](int p, int rank) {
-      const int l = owner(pages0, n, rank);
+      const int l = owner(pages0, n, top, rank);
       a.table[(int64_t)l * a.max_pages + pages_of(held[l]) + (rank - pages0[l])] = p;
       a.holders[p] = 1;
     };
-    int rank = before + rank_in;
-    for (unsigned m = word; m && rank < want; m &= m - 1, ++rank) take(32 * (mine0 + lane) + __ffs(m) - 1, rank);
+    // those of the first words in a list first, for all threads to share
+    int rank = rank_in;
+    for (unsigned m = before + rank < want ? word : 0; m; m &= m - 1)
+      found[rank++] = (uint16_t)(32 * (mine0 - word0 + lane) + __ffs(m) - 1);
+    __syncthreads();
+#pragma unroll 2
+    for (int i = tid; i < min(first_n, want - before); i += kT) take(32 * word0 + found[i], before + i);
     rank = before + first_n;
     for (int w0 = word0 + kT; w0 < word1 && rank < want; w0 += kW) {
       const int w = w0 + warp;
       const unsigned m = w < word1 ? free_word(w) : 0;
-      int found;
+      int some;
       __syncthreads();
-      const int ahead = block_scan(lane == 0 ? __popc(m) : 0, tmp[0], found);
+      const int ahead = block_scan(lane == 0 ? __popc(m) : 0, tmp[0], some);
       const int first = rank + at(ahead, 0);
       if ((m >> lane) & 1) {
         const int r = first + __popc(m & ((1u << lane) - 1));
         if (r < want) take(32 * w + lane, r);
       }
-      rank += found;
+      rank += some;
     }
   }
   // ---- 3. lanes and rows
@@ -221,22 +230,54 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     a.status[2] = (int)min(total.b, most);
     a.status[3] = free_n;
   }
+  // four consecutive rows a thread: their lanes are looked for once, their numbers written
+  // in vectors
   const int rows = ok ? (int)total.c : 0;
-  for (int64_t r64 = c * kT + tid; r64 < a.max_rows; r64 += kC * kT) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.row_lane) | reinterpret_cast<uintptr_t>(a.row_position) |
+                     reinterpret_cast<uintptr_t>(a.row_length) | reinterpret_cast<uintptr_t>(a.row_slot)) & 15) == 0;
+  for (int64_t r64 = 4 * (int64_t)(c * kT + tid); r64 < a.max_rows; r64 += 4 * kC * kT) {
     const int r = (int)r64;
-    int l = -1, pos = -1;
-    int64_t slot = -1;
-    if (r < rows) {
-      l = owner(rows0, n, r);
-      pos = held[l] + (r - rows0[l]);
-      const int j = a.by_page.div((uint32_t)pos);
-      if (a.row_slot)
-        slot = (int64_t)__ldcg(a.table + (int64_t)l * a.max_pages + j) * a.page_size + (pos - j * a.page_size);
+    int l[4], pos[4];
+    int64_t slot[4];
+    int own = r < rows ? owner(rows0, n, top, r) : 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = r64 + q < rows;
+      if (q > 0 && in)
+        while (own + 1 < n && rows0[own + 1] <= r + q) ++own;
+      l[q] = in ? own : -1;
+      pos[q] = in ? held[own] + (r + q - rows0[own]) : -1;
     }
-    if (a.row_lane) a.row_lane[r] = l;
-    if (a.row_position) a.row_position[r] = pos;
-    if (a.row_length) a.row_length[r] = pos + 1;
-    if (a.row_slot) a.row_slot[r] = slot;
+    if (a.row_slot) {
+      int page[4], j[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        j[q] = a.by_page.div((uint32_t)max(pos[q], 0));
+        page[q] = l[q] >= 0 ? __ldcg(a.table + (int64_t)l[q] * a.max_pages + j[q]) : 0;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        slot[q] = l[q] >= 0 ? (int64_t)page[q] * a.page_size + (pos[q] - j[q] * a.page_size) : -1;
+    }
+    if (vec && r64 + 4 <= a.max_rows) {
+      if (a.row_lane) *reinterpret_cast<int4*>(a.row_lane + r) = make_int4(l[0], l[1], l[2], l[3]);
+      if (a.row_position) *reinterpret_cast<int4*>(a.row_position + r) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (a.row_length)
+        *reinterpret_cast<int4*>(a.row_length + r) = make_int4(pos[0] + 1, pos[1] + 1, pos[2] + 1, pos[3] + 1);
+      if (a.row_slot) {
+        reinterpret_cast<longlong2*>(a.row_slot + r)[0] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2*>(a.row_slot + r)[1] = make_longlong2(slot[2], slot[3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r64 + q >= a.max_rows) break;
+        if (a.row_lane) a.row_lane[r + q] = l[q];
+        if (a.row_position) a.row_position[r + q] = pos[q];
+        if (a.row_length) a.row_length[r + q] = pos[q] + 1;
+        if (a.row_slot) a.row_slot[r + q] = slot[q];
+      }
+    }
   }
 }
 
@@ -244,9 +285,11 @@ template <int kC>
 Launched launch_c(const PagesArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_pages<kC>, kMaxPageLanes * 16, done);
+  l.error = allow_smem(k_pages<kC>, kMaxPageLanes * 16 + 65536, done);
   if (l.error != cudaSuccess) return l;
-  const size_t smem = (size_t)a.n_lanes * 16;
+  // four numbers a lane, and the places of a block's first 32768 pages
+  const int64_t own = 32 * ((a.n_pages + 31) / 32 / kC + 1);
+  const size_t smem = (size_t)a.n_lanes * 16 + (size_t)std::min<int64_t>(own, 32768) * 2;
   if constexpr (kC == 1) l.add(launch_k(k_pages<1>, dim3(1), kT, smem, s, a));
   else l.add(launch_k_cluster(k_pages<kC>, dim3(kC), kT, smem, s, kC, a));
   return l;
