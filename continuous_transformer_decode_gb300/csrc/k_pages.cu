@@ -70,7 +70,61 @@ __device__ __forceinline__ int owner(const int* first, int n, int top, int x) {
 // needs no reconvergence first.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
-template <int kC>
+// Rows from r0 on, four consecutive ones a thread: their lanes are looked for once, their
+// numbers written in vectors. to_pos(l) takes a row of lane l to its token's place.
+template <typename F>
+__device__ __forceinline__ void write_rows(const PagesArgs& a, const int* rows0, int n, int top, int rows, int64_t r0,
+                                           int64_t step, F to_pos) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.row_lane) | reinterpret_cast<uintptr_t>(a.row_position) |
+                     reinterpret_cast<uintptr_t>(a.row_length) | reinterpret_cast<uintptr_t>(a.row_slot)) & 15) == 0;
+  for (int64_t r64 = r0; r64 < a.max_rows; r64 += step) {
+    const int r = (int)r64;
+    int l[4], pos[4];
+    int64_t slot[4];
+    int own = r < rows ? owner(rows0, n, top, r) : 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = r64 + q < rows;
+      if (q > 0 && in)
+        while (own + 1 < n && rows0[own + 1] <= r + q) ++own;
+      l[q] = in ? own : -1;
+      pos[q] = in ? r + q + to_pos(own) : -1;
+    }
+    if (a.row_slot) {
+      int page[4], j[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        j[q] = a.by_page.div((uint32_t)max(pos[q], 0));
+        page[q] = l[q] >= 0 ? __ldcg(a.table + (int64_t)l[q] * a.max_pages + j[q]) : 0;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        slot[q] = l[q] >= 0 ? (int64_t)page[q] * a.page_size + (pos[q] - j[q] * a.page_size) : -1;
+    }
+    if (vec && r64 + 4 <= a.max_rows) {
+      if (a.row_lane) *reinterpret_cast<int4*>(a.row_lane + r) = make_int4(l[0], l[1], l[2], l[3]);
+      if (a.row_position) *reinterpret_cast<int4*>(a.row_position + r) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (a.row_length)
+        *reinterpret_cast<int4*>(a.row_length + r) = make_int4(pos[0] + 1, pos[1] + 1, pos[2] + 1, pos[3] + 1);
+      if (a.row_slot) {
+        reinterpret_cast<longlong2*>(a.row_slot + r)[0] = make_longlong2(slot[0], slot[1]);
+        reinterpret_cast<longlong2*>(a.row_slot + r)[1] = make_longlong2(slot[2], slot[3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r64 + q >= a.max_rows) break;
+        if (a.row_lane) a.row_lane[r + q] = l[q];
+        if (a.row_position) a.row_position[r + q] = pos[q];
+        if (a.row_length) a.row_length[r + q] = pos[q] + 1;
+        if (a.row_slot) a.row_slot[r + q] = slot[q];
+      }
+    }
+  }
+}
+
+// kRows: with the rows; else another kernel writes them.
+template <int kC, bool kRows>
 __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   extern __shared__ int sh[];
   __shared__ Three tmp3[kW];
@@ -150,29 +204,32 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   // ---- free pages: this block's are page0 .. page1 - 1, 32 a warp's word
   const int words = (a.n_pages + 31) / 32;
   const int word0 = (int)((int64_t)words * c / kC), word1 = (int)((int64_t)words * (c + 1) / kC);
-  auto free_word = [&](int w) {  // by the whole warp
+  auto holders_of = [&](int w, int end) {  // of the lane's page of a word
     const int p = 32 * w + lane;
-    return __ballot_sync(kAll, p < a.n_pages && __ldcg(a.holders + p) == 0);
+    return w < end && p < a.n_pages ? __ldcg(a.holders + p) : 1;
   };
+  auto free_word = [&](int w, int end) { return __ballot_sync(kAll, holders_of(w, end) == 0); };
   // the first 1024 words, shared evenly by the warps, stay with the threads
   unsigned word = 0;
   const int share = min(32, (word1 - word0 + kW - 1) / kW), mine0 = word0 + warp * share;
-#pragma unroll 1
   for (int i0 = 0; i0 < share; i0 += 8) {
+    int h[8];
 #pragma unroll
-    for (int i = i0; i < i0 + 8; ++i) {
-      const unsigned m = i < share && mine0 + i < word1 ? free_word(mine0 + i) : 0;
-      if (i == lane) word = m;
+    for (int i = 0; i < 8; ++i) h[i] = holders_of(mine0 + i0 + i, min(word1, mine0 + share));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned m = __ballot_sync(kAll, h[i] == 0);
+      if (i0 + i == lane) word = m;
     }
   }
-  int rest = 0;
-  for (int w = word0 + kT + warp; w < word1; w += kW) rest += __popc(free_word(w));  // the same in all lanes
-  int here, first_n;
-  const int rank_in = block_scan(__popc(word), tmp[0], first_n);
-  {
-    int rest_n;
+  int here;
+  const int rank_in = block_scan(__popc(word), tmp[0], here);
+  const int first_n = here;
+  if (word1 - word0 > kT) {  // the same for the whole block
+    int rest = 0, rest_n;
+    for (int w = word0 + kT + warp; w < word1; w += kW) rest += __popc(free_word(w, word1));  // the same in all lanes
     block_scan(lane == 0 ? rest : 0, tmp[1], rest_n);
-    here = first_n + rest_n;
+    here += rest_n;
   }
   int before = 0, free_n = here;
   if constexpr (kC > 1) {
@@ -204,7 +261,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     rank = before + first_n;
     for (int w0 = word0 + kT; w0 < word1 && rank < want; w0 += kW) {
       const int w = w0 + warp;
-      const unsigned m = w < word1 ? free_word(w) : 0;
+      const unsigned m = free_word(w, word1);
       int some;
       __syncthreads();
       const int ahead = block_scan(lane == 0 ? __popc(m) : 0, tmp[0], some);
@@ -230,76 +287,51 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     a.status[2] = (int)min(total.b, most);
     a.status[3] = free_n;
   }
-  // four consecutive rows a thread: their lanes are looked for once, their numbers written
-  // in vectors
-  const int rows = ok ? (int)total.c : 0;
-  const bool vec = ((reinterpret_cast<uintptr_t>(a.row_lane) | reinterpret_cast<uintptr_t>(a.row_position) |
-                     reinterpret_cast<uintptr_t>(a.row_length) | reinterpret_cast<uintptr_t>(a.row_slot)) & 15) == 0;
-  for (int64_t r64 = 4 * (int64_t)(c * kT + tid); r64 < a.max_rows; r64 += 4 * kC * kT) {
-    const int r = (int)r64;
-    int l[4], pos[4];
-    int64_t slot[4];
-    int own = r < rows ? owner(rows0, n, top, r) : 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool in = r64 + q < rows;
-      if (q > 0 && in)
-        while (own + 1 < n && rows0[own + 1] <= r + q) ++own;
-      l[q] = in ? own : -1;
-      pos[q] = in ? held[own] + (r + q - rows0[own]) : -1;
-    }
-    if (a.row_slot) {
-      int page[4], j[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        j[q] = a.by_page.div((uint32_t)max(pos[q], 0));
-        page[q] = l[q] >= 0 ? __ldcg(a.table + (int64_t)l[q] * a.max_pages + j[q]) : 0;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        slot[q] = l[q] >= 0 ? (int64_t)page[q] * a.page_size + (pos[q] - j[q] * a.page_size) : -1;
-    }
-    if (vec && r64 + 4 <= a.max_rows) {
-      if (a.row_lane) *reinterpret_cast<int4*>(a.row_lane + r) = make_int4(l[0], l[1], l[2], l[3]);
-      if (a.row_position) *reinterpret_cast<int4*>(a.row_position + r) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      if (a.row_length)
-        *reinterpret_cast<int4*>(a.row_length + r) = make_int4(pos[0] + 1, pos[1] + 1, pos[2] + 1, pos[3] + 1);
-      if (a.row_slot) {
-        reinterpret_cast<longlong2*>(a.row_slot + r)[0] = make_longlong2(slot[0], slot[1]);
-        reinterpret_cast<longlong2*>(a.row_slot + r)[1] = make_longlong2(slot[2], slot[3]);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (r64 + q >= a.max_rows) break;
-        if (a.row_lane) a.row_lane[r + q] = l[q];
-        if (a.row_position) a.row_position[r + q] = pos[q];
-        if (a.row_length) a.row_length[r + q] = pos[q] + 1;
-        if (a.row_slot) a.row_slot[r + q] = slot[q];
-      }
-    }
-  }
+  if constexpr (kRows)
+    write_rows(a, rows0, n, top, ok ? (int)total.c : 0, 4 * (int64_t)(c * kT + tid), 4 * kC * kT,
+               [&](int l) { return held[l] - rows0[l]; });
 }
 
-template <int kC>
+// The rows alone, by many blocks, behind a call of the kernel above without them.
+constexpr int kRowT = 256;
+__global__ void __launch_bounds__(kRowT) k_page_rows(const PagesArgs a) {
+  extern __shared__ int sh[];
+  const int n = a.n_lanes, top = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
+  pdl_wait();
+  pdl_trigger();
+  for (int l = threadIdx.x; l < n; l += kRowT) sh[l] = a.row_start[l];
+  const int rows = a.row_start[n];
+  __syncthreads();
+  // lengths are the new ones: a lane's first token is its length less its rows
+  write_rows(a, sh, n, top, rows, 4 * ((int64_t)blockIdx.x * kRowT + threadIdx.x), 4 * (int64_t)gridDim.x * kRowT,
+             [&](int l) { return a.lengths[l] - (l + 1 < n ? sh[l + 1] : rows); });
+}
+
+template <int kC, bool kRows>
 Launched launch_c(const PagesArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_pages<kC>, kMaxPageLanes * 16 + 65536, done);
+  l.error = allow_smem(k_pages<kC, kRows>, kMaxPageLanes * 16 + 65536, done);
   if (l.error != cudaSuccess) return l;
   // four numbers a lane, and the places of a block's first 32768 pages
   const int64_t own = 32 * ((a.n_pages + 31) / 32 / kC + 1);
   const size_t smem = (size_t)a.n_lanes * 16 + (size_t)std::min<int64_t>(own, 32768) * 2;
-  if constexpr (kC == 1) l.add(launch_k(k_pages<1>, dim3(1), kT, smem, s, a));
-  else l.add(launch_k_cluster(k_pages<kC>, dim3(kC), kT, smem, s, kC, a));
+  const bool fine = kC == 1 ? l.add(launch_k(k_pages<kC, kRows>, dim3(1), kT, smem, s, a))
+                            : l.add(launch_k_cluster(k_pages<kC, kRows>, dim3(kC), kT, smem, s, kC, a));
+  if (!kRows && fine) {
+    const int64_t blocks = ((int64_t)a.max_rows + 4 * kRowT - 1) / (4 * kRowT);
+    l.add(launch_k(k_page_rows, dim3((unsigned)std::min<int64_t>(blocks, 2048)), kRowT, (size_t)a.n_lanes * 4, s, a));
+  }
   return l;
 }
 
 }  // namespace
 
-// One block for small pools and batches, which saves the cluster's barriers.
+// One block for small pools and batches, which saves the cluster's barriers; a kernel of its
+// own for many rows.
 Launched launch_pages(const PagesArgs& a, cudaStream_t s) {
-  return a.n_pages <= 32768 && a.max_rows <= 4096 && a.n_lanes <= 1024 ? launch_c<1>(a, s) : launch_c<8>(a, s);
+  if (a.n_pages <= 32768 && a.max_rows <= 4096 && a.n_lanes <= 1024) return launch_c<1, true>(a, s);
+  return a.max_rows <= 16384 ? launch_c<8, true>(a, s) : launch_c<8, false>(a, s);
 }
 
 }  // namespace fsk
