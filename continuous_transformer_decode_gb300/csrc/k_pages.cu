@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   extern __shared__ int sh[];
   __shared__ Three tmp3[kW];
   __shared__ int tmp[2][kW];
-  __shared__ int free_of[8];
+  __shared__ int2 free_of[8];  // the blocks' free pages, and how many of them are listed
   static_assert(kC <= 8, "free_of");
   cg::cluster_group cluster = cg::this_cluster();
   auto sync = [&] {
@@ -231,15 +231,14 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     block_scan(lane == 0 ? rest : 0, tmp[1], rest_n);
     here += rest_n;
   }
-  int before = 0, free_n = here;
-  if constexpr (kC > 1) {
-    if (tid < kC) *cluster.map_shared_rank(&free_of[c], tid) = here;
-    sync();
-    free_n = 0;
-    for (int b = 0; b < kC; ++b) {
-      if (b == c) before = free_n;
-      free_n += free_of[b];
-    }
+  for (int rank = rank_in; word; word &= word - 1)
+    found[rank++] = (uint16_t)(32 * (mine0 - word0 + lane) + __ffs(word) - 1);
+  if (tid < kC) *(kC == 1 ? &free_of[0] : cluster.map_shared_rank(&free_of[c], tid)) = make_int2(here, first_n);
+  sync();
+  int before = 0, free_n = 0;
+  for (int b = 0; b < kC; ++b) {
+    if (b == c) before = free_n;
+    free_n += free_of[b].x;
   }
   const int code = past || total.b > free_n ? a.code_full : total.c > a.max_rows ? a.code_rows : 0;
   const bool ok = code == 0;
@@ -251,14 +250,17 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
       a.table[(int64_t)l * a.max_pages + pages_of(held[l]) + (rank - pages0[l])] = p;
       a.holders[p] = 1;
     };
-    // those of the first words in a list first, for all threads to share
-    int rank = rank_in;
-    for (unsigned m = before + rank < want ? word : 0; m; m &= m - 1)
-      found[rank++] = (uint16_t)(32 * (mine0 - word0 + lane) + __ffs(m) - 1);
-    __syncthreads();
+    // the listed ones, shared by all threads of all blocks
 #pragma unroll 2
-    for (int i = tid; i < min(first_n, want - before); i += kT) take(32 * word0 + found[i], before + i);
-    rank = before + first_n;
+    for (int r = c * kT + tid; r < want; r += kC * kT) {
+      int b = 0, i = r;
+      while (b + 1 < kC && i >= free_of[b].x) i -= free_of[b++].x;
+      if (i >= free_of[b].y) continue;
+      const int at0 = (int)((int64_t)words * b / kC);
+      take(32 * at0 + *(kC == 1 ? found + i : cluster.map_shared_rank(found + i, b)), r);
+    }
+    // and a block's own behind them
+    int rank = before + first_n;
     for (int w0 = word0 + kT; w0 < word1 && rank < want; w0 += kW) {
       const int w = w0 + warp;
       const unsigned m = free_word(w, word1);
