@@ -24,19 +24,27 @@ struct VecOf<4> { using T = uint32_t; };
 template <>
 struct VecOf<2> { using T = uint16_t; };
 
-// kN consecutive values of T in vectors of kBytes.
-template <typename T, int kN, int kBytes>
+// kN consecutive values of T in vectors of kBytes; kStream: the caches keep them no longer
+// than others.
+template <typename T, int kN, int kBytes, bool kStream>
 struct Vals {
   using V = typename VecOf<kBytes>::T;
   static constexpr int kV = kN * (int)sizeof(T) / kBytes;
   V v[kV];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = reinterpret_cast<const V*>(p)[i];
+    for (int i = 0; i < kV; ++i) {
+      const V* q = reinterpret_cast<const V*>(p) + i;
+      v[i] = kStream ? __ldcs(q) : *q;
+    }
   }
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) reinterpret_cast<V*>(p)[i] = v[i];
+    for (int i = 0; i < kV; ++i) {
+      V* q = reinterpret_cast<V*>(p) + i;
+      if (kStream) __stcs(q, v[i]);
+      else *q = v[i];
+    }
   }
   __device__ __forceinline__ float get(int i) const {
     const T x = reinterpret_cast<const T*>(v)[i];
@@ -64,7 +72,7 @@ __device__ __forceinline__ float2 turn(uint32_t pos, uint64_t F, float m, bool i
 
 // kNear: pairs of neighbours, else of halves. A unit is kP pairs of a head, or 2 kP
 // values behind the turned ones, which are copied.
-template <typename T, int kBytes, bool kNear>
+template <typename T, int kBytes, bool kNear, bool kStream>
 __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
   constexpr int kP = kNear ? (kBytes / (2 * (int)sizeof(T)) > 0 ? kBytes / (2 * (int)sizeof(T)) : 1)
                            : kBytes / (int)sizeof(T);
@@ -88,19 +96,20 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
     return h < a.H ? static_cast<T*>(a.q_out) + row * a.qo_stride + (int64_t)h * a.hd
                    : static_cast<T*>(a.k_out) + row * a.ko_stride + (int64_t)(h - a.H) * a.hd;
   };
-  // kH heads at a time: their loads are asked for before the first store
-  constexpr int kH = 4;
+  // kH heads at a time: their loads, eight, are asked for before the first store (4099 rows
+  // of neighbours: 27 us, with four loads 30; 65536 rows of halves: 207 us, with sixteen 236)
+  constexpr int kH = kNear ? 8 : 4;
   if (unit >= turned) {  // behind the turned values (out of place)
     constexpr int kE = kBytes / (int)sizeof(T);
     const int at = a.rot + (unit - turned) * kE;
 #pragma unroll 1
-    for (int h = h0; h < h1; h += kH) {
-      Vals<T, kE, kBytes> x[kH];
+    for (int h = h0; h < h1; h += 8) {
+      Vals<T, kE, kBytes, kStream> x[8];
 #pragma unroll
-      for (int u = 0; u < kH; ++u)
+      for (int u = 0; u < 8; ++u)
         if (h + u < h1) x[u].load(in(h + u) + at);
 #pragma unroll
-      for (int u = 0; u < kH; ++u)
+      for (int u = 0; u < 8; ++u)
         if (h + u < h1) x[u].store(out(h + u) + at);
     }
     return;
@@ -111,7 +120,7 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
 #pragma unroll 1
   for (int h = h0; h < h1; h += kH) {
     if constexpr (kNear) {
-      Vals<T, 2 * kP, kBytes> x[kH];
+      Vals<T, 2 * kP, kBytes, kStream> x[kH];
 #pragma unroll
       for (int u = 0; u < kH; ++u)
         if (h + u < h1) x[u].load(in(h + u) + unit * 2 * kP);
@@ -127,7 +136,7 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
         x[u].store(out(h + u) + unit * 2 * kP);
       }
     } else {
-      Vals<T, kP, kBytes> x[kH], y[kH];
+      Vals<T, kP, kBytes, kStream> x[kH], y[kH];
 #pragma unroll
       for (int u = 0; u < kH; ++u)
         if (h + u < h1) {
@@ -163,9 +172,14 @@ Launched launch_t(RopeArgs a, bool near, int sms, cudaStream_t s) {
   a.per = (heads + a.groups - 1) / a.groups;
   a.groups = (heads + a.per - 1) / a.per;
   const int64_t threads = (int64_t)a.n * a.groups * a.units;
+  // what is more than the L2 may keep passes through it first to go (65536 rows, 537 MB and as
+  // much out: 207 us, without 232; 4099 rows, 75 MB: 27 and 28)
+  constexpr bool kWide = kBytes == 16;
+  const bool stream = kWide && (int64_t)a.n * heads * a.hd * (int64_t)sizeof(T) > (64 << 20);
+  auto kernel = stream ? (near ? k_rope<T, kBytes, true, kWide> : k_rope<T, kBytes, false, kWide>)
+                       : (near ? k_rope<T, kBytes, true, false> : k_rope<T, kBytes, false, false>);
   Launched l;
-  l.add(launch_k(near ? k_rope<T, kBytes, true> : k_rope<T, kBytes, false>,
-                 dim3((unsigned)((threads + 255) / 256)), 256, 0, s, a));
+  l.add(launch_k(kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, a));
   return l;
 }
 
