@@ -444,8 +444,7 @@ int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int
   const double ih = 0.15915494309189535, il = -9.839338337591243e-18;  // 1 / (2 pi)
   for (int j = 0; j < rotary_dim / 2; ++j) {
     const double f = inv_freq[j], p = f * ih, pe = std::fma(f, ih, -p) + f * il;
-    double whole;
-    const double part = std::modf(p, &whole);  // exact
+    const double part = p - std::trunc(p);  // exact
     // the top 32 bits of the fraction, then what is left of it and pe
     const double top = std::floor(part * 0x1p32);
     const double rest = (part * 0x1p32 - top) * 0x1p32 + pe * 0x1p64;

@@ -797,6 +797,17 @@ def fs_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: dict |
     return f, m.value
 
 
+def _host_f64(x):
+    """(array, address) of a vector of f64 in host memory."""
+    f = np.ascontiguousarray(x, np.float64)
+    if f.ndim != 1:
+        _refuse("inv_freq: a vector of f64 is needed")
+    try:
+        return f, C.addressof(C.c_char.from_buffer(f))  # a fifth of the time of .ctypes.data
+    except (TypeError, ValueError):  # read-only or empty
+        return f, f.ctypes.data
+
+
 def fs_rope(q, positions, inv_freq, k=None, q_out=None, k_out=None, interleaved: bool = False,
             factor: float = 1.0, inverse: bool = False, stream=None) -> None:
     """Turns the first 2 * len(inv_freq) values of each head of q [n, H, hd] and k
@@ -819,11 +830,9 @@ def fs_rope(q, positions, inv_freq, k=None, q_out=None, k_out=None, interleaved:
         _refuse("k_out without k")
     if not dt == do == dk == dko:
         _refuse("q, k and their outputs have different types")
-    f = np.ascontiguousarray(inv_freq, np.float64)
-    if f.ndim != 1:
-        _refuse("inv_freq: a vector of f64 is needed")
+    f, fp = _host_f64(inv_freq)
     _op_check(lib().fs_rope(qp, qs, H, kp, ks, Hkv, n, hd, dt, _vec(positions, n, ty.i32, "positions"),
-                            f.ctypes.data, 2 * f.size, factor, bool(interleaved) | bool(inverse) << 1,
+                            fp, 2 * f.size, factor, bool(interleaved) | bool(inverse) << 1,
                             op, os_, okp, oks, _raw(stream, positions)))
 
 
