@@ -199,8 +199,10 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
 // shuffles then need no reconvergence before each of them.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
-// kMT: row tiles of an item; kNT: tiles of ranks of half a block's warps (kMT 4).
-template <typename TX, typename TY, int kMT, int kNT>
+// kMT: row tiles of an item; kNT: tiles of ranks of half a block's warps (kMT 4); kSolo: a
+// block takes an item for itself (kMT 1), its warps the shares of K that a cluster's blocks
+// have.
+template <typename TX, typename TY, int kMT, int kNT, bool kSolo>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
   constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
@@ -211,16 +213,18 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
   float* const block_sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
-  const int c = (int)cluster.block_rank();
+  static_assert(kW == kC, "a warp a share of K");
+  constexpr int kBlocks = kSolo ? 1 : kC;  // of an item
+  const int c = kSolo ? 0 : (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2, tig = lane & 3;
   // the other blocks' shared memory can be written once they have started
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (!kSolo) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   for (int i = tid; i < kSlots; i += kT) sh.key[i] = -1;
   for (int i = tid; i < kW * kSlots / 8; i += kT) reinterpret_cast<uint4*>(sh.count)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   pdl_trigger();
-  const int item0 = blockIdx.x / kC % per_window;
-  const int first = (int)(blockIdx.x / kC / per_window) * kWindow;
+  const int item0 = blockIdx.x / kBlocks % per_window;
+  const int first = (int)(blockIdx.x / kBlocks / per_window) * kWindow;
   // ---- the window's rows by adapter
   const int my_row = first + tid;
   const int my_id = my_row < a.n ? a.adapter[my_row] : -1;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   if (has && nth % kR == 0) sh.lead[at + __popc(leads & below)] = (int16_t)tid;
 
   // this block's columns, in chunks of 32
-  const int chunks = (a.N + 31) / 32, per = (chunks + kC - 1) / kC;
+  const int chunks = (a.N + 31) / 32, per = (chunks + kBlocks - 1) / kBlocks;
   const int chunk0 = min(chunks, c * per), chunk1 = min(chunks, chunk0 + per);
   const TX* const x = static_cast<const TX*>(a.x);
   const TY* const base = static_cast<const TY*>(a.base);
@@ -268,10 +272,11 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   const bool x_vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && a.x_stride * sizeof(TX) % 16 == 0;
   const bool y_vec = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
                      (a.base_stride | a.out_stride) * sizeof(TY) % 16 == 0;
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  // ---- this block's part of K, in blocks of 32
+  if constexpr (!kSolo) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // ---- this block's share of K (kSolo: this warp's), in blocks of 32
   const int kbs = (a.K + 31) / 32;
-  const int kb0 = (int)((int64_t)kbs * c / kC), kb1 = (int)((int64_t)kbs * (c + 1) / kC);
+  const int share = kSolo ? warp : c;
+  const int kb0 = (int)((int64_t)kbs * share / kC), kb1 = (int)((int64_t)kbs * (share + 1) / kC);
   const int tiles = a.rank / 8, rblocks = (a.rank + 31) / 32;
   auto piece = [&](int s) { return kb0 + (kb1 - kb0) * s / kW; };  // the s-th of eight starts here
 
@@ -286,7 +291,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
     auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
     const bool few = kMT == 1 || rows <= 16;
-    if (few && item != item0) cluster.sync();  // the last item's sums have been read
+    if constexpr (!kSolo)
+      if (few && item != item0) cluster.sync();  // the last item's sums have been read
 
     auto put = [&](float* to, int mt, int nt, const float (&d)[4]) {
       float* p = to + (16 * mt + g) * a.rank + 8 * nt + 2 * tig;
@@ -297,42 +303,60 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     if (few) {
       float* const sums = kMT == 1 ? block_sums : reinterpret_cast<float*>(low);
       const int64_t r0 = row_of(g), r1 = row_of(g + 8);
-      for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks, a warp its piece of K
-        float d[4][4] = {};
+      for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks
+        // d += x A^T over blocks b0 .. b1 - 1 of K
+        auto product = [&](int b0, int b1, float (&d)[4][4]) {
 #pragma unroll 2
-        for (int b = piece(warp); b < piece(warp + 1); ++b) {
-          const int k = 32 * b + 8 * tig;
-          const bool in = k < a.K;
-          Eight<TX> lo, hi;
-          lo.clear(), hi.clear();
-          if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
-          if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
-          uint4 w[4];
+          for (int b = b0; b < b1; ++b) {
+            const int k = 32 * b + 8 * tig;
+            const bool in = k < a.K;
+            Eight<TX> lo, hi;
+            lo.clear(), hi.clear();
+            if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
+            if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
+            uint4 w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
-                                         : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < 4; ++j)
+              w[j] = in && nt0 + j < tiles ? *reinterpret_cast<const uint4*>(A + (int64_t)(8 * (nt0 + j) + g) * a.K + k)
+                                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
+            for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_half(d[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
+              for (int j = 0; j < 4; ++j) mma_half(d[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
+          }
+        };
+        float d[4][4] = {};
+        if constexpr (kSolo) {  // the warp's share, piece by piece
+          product(piece(0), piece(1), d);
+          for (int p = 1; p < kW; ++p) {
+            float e[4][4] = {};
+            product(piece(p), piece(p + 1), e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) d[j][q] += e[j][q];
+          }
+        } else {  // the warp's piece of the block's share
+          product(piece(warp), piece(warp + 1), d);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (nt0 + j < tiles) put(sums + warp * tile, 0, nt0 + j, d[j]);
       }
       __syncthreads();
-      for (int i = tid; i < tile; i += kT) {
-        float s = sums[i];
+      if constexpr (!kSolo) {
+        for (int i = tid; i < tile; i += kT) {
+          float s = sums[i];
 #pragma unroll
-        for (int w = 1; w < kW; ++w) s += sums[w * tile + i];
-        for (int r = 0; r < kC; ++r) *cluster.map_shared_rank(sums + (kW + c) * tile + i, r) = s;
+          for (int w = 1; w < kW; ++w) s += sums[w * tile + i];
+          for (int r = 0; r < kC; ++r) *cluster.map_shared_rank(sums + (kW + c) * tile + i, r) = s;
+        }
+        cluster.sync();
       }
-      cluster.sync();
       auto total = [&](int i) {  // of place i of the parts' rows
         const int m = i / sz.pitch, r = i - m * sz.pitch;
         if (m >= 16 || r >= a.rank) return 0.0f;
-        const float* p = sums + kW * tile + m * a.rank + r;
+        const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
         float v = p[0];
 #pragma unroll
         for (int b = 1; b < kC; ++b) v += p[b * tile];
@@ -595,26 +619,28 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   }
 }
 
-template <typename TX, typename TY, int kMT, int kNT>
+template <typename TX, typename TY, int kMT, int kNT, bool kSolo>
 Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
+  auto kernel = k_lora<TX, TY, kMT, kNT, kSolo>;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_lora<TX, TY, kMT, kNT>, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
+  l.error = allow_smem(kernel, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
   if (l.error != cudaSuccess) return l;
-  const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  l.add(launch_k_cluster(k_lora<TX, TY, kMT, kNT>, dim3((unsigned)(windows * per_window * kC)), kT,
-                         (size_t)Sizes(kMT, kParts, a.rank, sizeof(TX)).bytes, s, kC, a, per_window));
+  const int64_t blocks = (a.n + kWindow - 1) / (int64_t)kWindow * per_window * (kSolo ? 1 : kC);
+  const size_t smem = (size_t)Sizes(kMT, kParts, a.rank, sizeof(TX)).bytes;
+  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window));
+  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
   return l;
 }
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  const bool wide = a.n > 2048;
+  if (a.n > 2048) return a.rank <= 64 ? launch_t<TX, TY, 4, 4, false>(a, 6, s) : launch_t<TX, TY, 4, 8, false>(a, 6, s);
+  if (a.n > kWindow) return launch_t<TX, TY, 1, 0, true>(a, (int)std::min<int64_t>(kWindow, 4 * sms / windows), s);
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  if (wide) return a.rank <= 64 ? launch_t<TX, TY, 4, 4>(a, 6, s) : launch_t<TX, TY, 4, 8>(a, 6, s);
-  return launch_t<TX, TY, 1, 0>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
+  return launch_t<TX, TY, 1, 0, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 
 }  // namespace
