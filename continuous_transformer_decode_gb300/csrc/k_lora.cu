@@ -179,13 +179,13 @@ constexpr int kStages = 4;
 struct Sizes {
   int pitch, stage;
   int64_t low, sums, bytes;
-  __host__ __device__ Sizes(int mt, int parts, int rank, int x_bytes) {
+  __host__ __device__ Sizes(int mt, bool solo, int parts, int rank, int x_bytes) {
     const int blocks = (rank + 31) / 32;
     pitch = 32 * blocks + (blocks % 2 ? 0 : 32);  // rows 64 bytes apart modulo 128: no conflicts
     low = (int64_t)parts * mt * 16 * pitch * 2;
-    sums = (int64_t)(mt == 1 ? kW + kC : 1) * mt * 16 * rank * 4;
+    sums = (int64_t)(solo ? kW : mt == 1 ? kW + kC : 1) * mt * 16 * rank * 4;
     stage = mt * 16 * 64 * x_bytes + rank * 128;
-    if (mt > 1 && low < kStages * stage) low = kStages * stage;
+    if (mt == 4 && low < kStages * stage) low = kStages * stage;
     bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + sums;
   }
 };
@@ -200,7 +200,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
 // kMT: row tiles of an item; kNT: tiles of ranks of half a block's warps (kMT 4); kSolo: a
-// block takes an item for itself (kMT 1), its warps the shares of K that a cluster's blocks
+// block takes an item for itself (kMT 1 or 2), its warps the shares of K that a cluster's blocks
 // have.
 template <typename TX, typename TY, int kMT, int kNT, bool kSolo>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   extern __shared__ __align__(16) unsigned char dyn[];
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
-  const Sizes sz(kMT, kParts, a.rank, sizeof(TX));
+  const Sizes sz(kMT, kSolo, kParts, a.rank, sizeof(TX));
   __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
   float* const block_sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     const __nv_bfloat16* const A = a.A + (int64_t)id * a.rank * a.K;
     const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
     auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
-    const bool few = kMT == 1 || rows <= 16;
+    const bool few = kMT < 4 || rows <= 16;
     if constexpr (!kSolo)
       if (few && item != item0) cluster.sync();  // the last item's sums have been read
 
@@ -299,21 +299,27 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       *reinterpret_cast<float2*>(p) = make_float2(d[0], d[1]);
       *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[2], d[3]);
     };
-    const int tile = 16 * a.rank;
+    constexpr int kF = kSolo ? kMT : 1;  // row tiles of an item of few rows
+    const int tile = kF * 16 * a.rank;
     if (few) {
-      float* const sums = kMT == 1 ? block_sums : reinterpret_cast<float*>(low);
-      const int64_t r0 = row_of(g), r1 = row_of(g + 8);
+      float* const sums = kMT == 4 ? reinterpret_cast<float*>(low) : block_sums;
+      int64_t r0[kF], r1[kF];
+#pragma unroll
+      for (int m = 0; m < kF; ++m) r0[m] = row_of(16 * m + g), r1[m] = row_of(16 * m + g + 8);
       for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks
         // d += x A^T over blocks b0 .. b1 - 1 of K
-        auto product = [&](int b0, int b1, float (&d)[4][4]) {
+        auto product = [&](int b0, int b1, float (&d)[kF][4][4]) {
 #pragma unroll 2
           for (int b = b0; b < b1; ++b) {
             const int k = 32 * b + 8 * tig;
             const bool in = k < a.K;
-            Eight<TX> lo, hi;
-            lo.clear(), hi.clear();
-            if (in && r0 >= 0) lo.load(x + r0 * a.x_stride + k, x_vec);
-            if (in && r1 >= 0) hi.load(x + r1 * a.x_stride + k, x_vec);
+            Eight<TX> lo[kF], hi[kF];
+#pragma unroll
+            for (int m = 0; m < kF; ++m) {
+              lo[m].clear(), hi[m].clear();
+              if (in && r0[m] >= 0) lo[m].load(x + r0[m] * a.x_stride + k, x_vec);
+              if (in && r1[m] >= 0) hi[m].load(x + r1[m] * a.x_stride + k, x_vec);
+            }
             uint4 w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -322,26 +328,32 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
             for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) mma_half(d[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
+              for (int m = 0; m < kF; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m].p[i / 2], hi[m].p[i / 2], w[j], i % 2);
           }
         };
-        float d[4][4] = {};
+        float d[kF][4][4] = {};
         if constexpr (kSolo) {  // the warp's share, piece by piece
           product(piece(0), piece(1), d);
           for (int p = 1; p < kW; ++p) {
-            float e[4][4] = {};
+            float e[kF][4][4] = {};
             product(piece(p), piece(p + 1), e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int m = 0; m < kF; ++m)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) d[j][q] += e[j][q];
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) d[m][j][q] += e[m][j][q];
           }
         } else {  // the warp's piece of the block's share
           product(piece(warp), piece(warp + 1), d);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (nt0 + j < tiles) put(sums + warp * tile, 0, nt0 + j, d[j]);
+        for (int m = 0; m < kF; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (nt0 + j < tiles) put(sums + warp * tile, m, nt0 + j, d[m][j]);
       }
       __syncthreads();
       if constexpr (!kSolo) {
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       }
       auto total = [&](int i) {  // of place i of the parts' rows
         const int m = i / sz.pitch, r = i - m * sz.pitch;
-        if (m >= 16 || r >= a.rank) return 0.0f;
+        if (m >= kF * 16 || r >= a.rank) return 0.0f;
         const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
         float v = p[0];
 #pragma unroll
@@ -368,8 +380,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
         for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = u[p];
       };
-      if constexpr (kMT == 1) {
-        for (int i = tid; i < 16 * sz.pitch; i += kT) keep(i, total(i));
+      if constexpr (kMT < 4) {
+        for (int i = tid; i < kF * 16 * sz.pitch; i += kT) keep(i, total(i));
       } else {  // the sums lie where the parts go
         constexpr int kMost = 16 * (128 + 32) / kT;  // of the longest pitch
         float v[kMost];
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       }
       __syncthreads();
     }
-    if constexpr (kMT > 1) if (!few) {
+    if constexpr (kMT == 4) if (!few) {
       float* const sums = block_sums;
       static_assert(kMT == 4, "eight warps are four row tiles and two halves of the ranks");
       const int mt = warp & 3, half = warp >> 2;  // tiles half, half + 2, .. of the ranks
@@ -625,10 +637,10 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   auto kernel = k_lora<TX, TY, kMT, kNT, kSolo>;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(kernel, (int)Sizes(kMT, kParts, 128, sizeof(TX)).bytes, done);
+  l.error = allow_smem(kernel, (int)Sizes(kMT, kSolo, kParts, 128, sizeof(TX)).bytes, done);
   if (l.error != cudaSuccess) return l;
   const int64_t blocks = (a.n + kWindow - 1) / (int64_t)kWindow * per_window * (kSolo ? 1 : kC);
-  const size_t smem = (size_t)Sizes(kMT, kParts, a.rank, sizeof(TX)).bytes;
+  const size_t smem = (size_t)Sizes(kMT, kSolo, kParts, a.rank, sizeof(TX)).bytes;
   if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window));
   else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
   return l;
@@ -637,7 +649,9 @@ template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
   if (a.n > 2048) return a.rank <= 64 ? launch_t<TX, TY, 4, 4, false>(a, 6, s) : launch_t<TX, TY, 4, 8, false>(a, 6, s);
-  if (a.n > kWindow) return launch_t<TX, TY, 1, 0, true>(a, (int)std::min<int64_t>(kWindow, 4 * sms / windows), s);
+  const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * sms / windows));
+  if (a.n > 4096) return launch_t<TX, TY, 2, 0, true>(a, each, s);
+  if (a.n > kWindow) return launch_t<TX, TY, 1, 0, true>(a, each, s);
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
   return launch_t<TX, TY, 1, 0, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
