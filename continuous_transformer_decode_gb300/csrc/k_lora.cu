@@ -168,25 +168,22 @@ struct Gather {
   int id[kWindow];
   int16_t nth[kWindow];   // of its adapter's rows in the window
   int16_t lead[kWindow];  // first rows of the items
-  int row[64];            // of an item
+  int row[32];            // of an item
   int firsts[kW], bare[kW];
 };
 
-// Shared memory behind Gather. kMT 1: the parts of A x, [part][row] of `pitch` values, and
-// f32 tiles of sums, a warp's and a block's each. kMT 4: the block's own sums, and stages of
-// the first product (64 of K, of the rows and of A), where the parts of A x lie afterwards.
-constexpr int kStages = 4;
+// Shared memory behind Gather: the parts of A x, [part][row] of `pitch` values, and f32 tiles
+// of sums, a warp's each and, of a cluster's blocks, a block's each; the warps' buffers of B
+// lie where the sums were.
 struct Sizes {
-  int pitch, stage;
-  int64_t low, sums, bytes;
-  __host__ __device__ Sizes(int mt, bool solo, int parts, int rank, int x_bytes) {
+  int pitch;
+  int64_t low, bytes;
+  __host__ __device__ Sizes(int mt, bool solo, int parts, int rank) {
     const int blocks = (rank + 31) / 32;
     pitch = 32 * blocks + (blocks % 2 ? 0 : 32);  // rows 64 bytes apart modulo 128: no conflicts
     low = (int64_t)parts * mt * 16 * pitch * 2;
-    sums = (int64_t)(solo ? kW : mt == 1 ? kW + kC : 1) * mt * 16 * rank * 4;
-    stage = mt * 16 * 64 * x_bytes + rank * 128;
-    if (mt == 4 && low < kStages * stage) low = kStages * stage;
-    bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + sums;
+    const int64_t sums = (int64_t)(solo ? kW : kW + kC) * mt * 16 * rank * 4, buffers = (int64_t)kW * 128 * rank;
+    bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + (sums > buffers ? sums : buffers);
   }
 };
 
@@ -199,19 +196,18 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
 // shuffles then need no reconvergence before each of them.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
-// kMT: row tiles of an item; kNT: tiles of ranks of half a block's warps (kMT 4); kSolo: a
-// block takes an item for itself (kMT 1 or 2), its warps the shares of K that a cluster's blocks
-// have.
-template <typename TX, typename TY, int kMT, int kNT, bool kSolo>
-__global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
+// kMT: row tiles of an item; kSolo: a block takes an item for itself, its warps the shares of
+// K that a cluster's blocks have.
+template <typename TX, typename TY, int kMT, bool kSolo>
+__global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window, FastDiv by_tiles) {
   constexpr int kR = 16 * kMT;                  // rows of an item
   constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   extern __shared__ __align__(16) unsigned char dyn[];
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
-  const Sizes sz(kMT, kSolo, kParts, a.rank, sizeof(TX));
+  const Sizes sz(kMT, kSolo, kParts, a.rank);
   __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
-  float* const block_sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
+  float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
   static_assert(kW == kC, "a warp a share of K");
   constexpr int kBlocks = kSolo ? 1 : kC;  // of an item
@@ -290,32 +286,29 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     const __nv_bfloat16* const A = a.A + (int64_t)id * a.rank * a.K;
     const __nv_bfloat16* const B = a.B + (int64_t)id * a.N * a.rank;
     auto row_of = [&](int i) { return i < rows ? sh.row[i] : -1; };
-    const bool few = kMT < 4 || rows <= 16;
     if constexpr (!kSolo)
-      if (few && item != item0) cluster.sync();  // the last item's sums have been read
+      if (item != item0) cluster.sync();  // the last item's sums and columns are done with
 
     auto put = [&](float* to, int mt, int nt, const float (&d)[4]) {
       float* p = to + (16 * mt + g) * a.rank + 8 * nt + 2 * tig;
       *reinterpret_cast<float2*>(p) = make_float2(d[0], d[1]);
       *reinterpret_cast<float2*>(p + 8 * a.rank) = make_float2(d[2], d[3]);
     };
-    constexpr int kF = kSolo ? kMT : 1;  // row tiles of an item of few rows
-    const int tile = kF * 16 * a.rank;
-    if (few) {
-      float* const sums = kMT == 4 ? reinterpret_cast<float*>(low) : block_sums;
-      int64_t r0[kF], r1[kF];
+    const int tile = kMT * 16 * a.rank;
+    {
+      int64_t r0[kMT], r1[kMT];
 #pragma unroll
-      for (int m = 0; m < kF; ++m) r0[m] = row_of(16 * m + g), r1[m] = row_of(16 * m + g + 8);
+      for (int m = 0; m < kMT; ++m) r0[m] = row_of(16 * m + g), r1[m] = row_of(16 * m + g + 8);
       for (int nt0 = 0; nt0 < tiles; nt0 += 4) {  // four tiles of ranks
         // d += x A^T over blocks b0 .. b1 - 1 of K
-        auto product = [&](int b0, int b1, float (&d)[kF][4][4]) {
+        auto product = [&](int b0, int b1, float (&d)[kMT][4][4]) {
 #pragma unroll 2
           for (int b = b0; b < b1; ++b) {
             const int k = 32 * b + 8 * tig;
             const bool in = k < a.K;
-            Eight<TX> lo[kF], hi[kF];
+            Eight<TX> lo[kMT], hi[kMT];
 #pragma unroll
-            for (int m = 0; m < kF; ++m) {
+            for (int m = 0; m < kMT; ++m) {
               lo[m].clear(), hi[m].clear();
               if (in && r0[m] >= 0) lo[m].load(x + r0[m] * a.x_stride + k, x_vec);
               if (in && r1[m] >= 0) hi[m].load(x + r1[m] * a.x_stride + k, x_vec);
@@ -328,19 +321,19 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
             for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
 #pragma unroll
-              for (int m = 0; m < kF; ++m)
+              for (int m = 0; m < kMT; ++m)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m].p[i / 2], hi[m].p[i / 2], w[j], i % 2);
           }
         };
-        float d[kF][4][4] = {};
+        float d[kMT][4][4] = {};
         if constexpr (kSolo) {  // the warp's share, piece by piece
           product(piece(0), piece(1), d);
           for (int p = 1; p < kW; ++p) {
-            float e[kF][4][4] = {};
+            float e[kMT][4][4] = {};
             product(piece(p), piece(p + 1), e);
 #pragma unroll
-            for (int m = 0; m < kF; ++m)
+            for (int m = 0; m < kMT; ++m)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -350,7 +343,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
           product(piece(warp), piece(warp + 1), d);
         }
 #pragma unroll
-        for (int m = 0; m < kF; ++m)
+        for (int m = 0; m < kMT; ++m)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (nt0 + j < tiles) put(sums + warp * tile, m, nt0 + j, d[m][j]);
@@ -367,7 +360,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       }
       auto total = [&](int i) {  // of place i of the parts' rows
         const int m = i / sz.pitch, r = i - m * sz.pitch;
-        if (m >= kF * 16 || r >= a.rank) return 0.0f;
+        if (m >= kMT * 16 || r >= a.rank) return 0.0f;
         const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
         float v = p[0];
 #pragma unroll
@@ -380,190 +373,52 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
         for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = u[p];
       };
-      if constexpr (kMT < 4) {
-        for (int i = tid; i < kF * 16 * sz.pitch; i += kT) keep(i, total(i));
-      } else {  // the sums lie where the parts go
-        constexpr int kMost = 16 * (128 + 32) / kT;  // of the longest pitch
-        float v[kMost];
-#pragma unroll
-        for (int q = 0; q < kMost; ++q) v[q] = total(tid + q * kT);
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kMost; ++q)
-          if (tid + q * kT < 16 * sz.pitch) keep(tid + q * kT, v[q]);
-      }
+      for (int i = tid; i < kMT * 16 * sz.pitch; i += kT) keep(i, total(i));
       __syncthreads();
     }
-    if constexpr (kMT == 4) if (!few) {
-      float* const sums = block_sums;
-      static_assert(kMT == 4, "eight warps are four row tiles and two halves of the ranks");
-      const int mt = warp & 3, half = warp >> 2;  // tiles half, half + 2, .. of the ranks
-      // Steps of up to two blocks of K inside a piece, kStages - 1 of them on their way. A
-      // row of a stage is 128 bytes (f32 x: 256), its 16-byte parts swapped in odd rows so
-      // that a quarter of a warp reads all banks.
-      constexpr int kXC = 4 * (int)sizeof(TX);  // 16-byte parts of a row of x
-      unsigned char* const stages = reinterpret_cast<unsigned char*>(low);
-      struct Step {
-        int s, b;
-      };
-      auto settle = [&](Step t) {  // past pieces that are done
-        while (t.s < kW && t.b >= piece(t.s + 1)) ++t.s;
-        return t;
-      };
-      auto after = [&](Step t) {
-        t.b = min(t.b + 2, piece(t.s + 1));
-        return settle(t);
-      };
-      // a thread's 16-byte parts of a stage: the same rows and columns in every step
-      constexpr int kXN = kR * kXC / kT, kAN = kNT / 2;
-      const TX* x_from[kXN];
-      uint32_t x_to[kXN], a_to[kAN];
-      const __nv_bfloat16* a_from[kAN];
-      const int x_k = tid % kXC * 16 / (int)sizeof(TX), a_k = tid % 8 * 8;
-#pragma unroll
-      for (int i = 0; i < kXN; ++i) {
-        const int r = (tid + i * kT) / kXC, q = tid % kXC;
-        x_from[i] = r < rows ? x + sh.row[r] * a.x_stride + x_k : nullptr;
-        x_to[i] = r * 16 * kXC + 16 * (q ^ (r & 1) * (sizeof(TX) == 2 ? 4 : 1));
-      }
-#pragma unroll
-      for (int i = 0; i < kAN; ++i) {
-        const int r = (tid + i * kT) / 8, q = tid % 8;
-        a_from[i] = r < a.rank ? A + (int64_t)r * a.K + a_k : nullptr;
-        a_to[i] = kR * 16 * kXC + r * 128 + 16 * (q ^ (r & 1) * 4);
-      }
-      auto fetch = [&](Step t, int slot) {
-        if (t.s < kW) {
-          unsigned char* const to = stages + slot * sz.stage;
-          const uint32_t to32 = attn::smem_u32(to);
-          const int k = 32 * t.b;
-#pragma unroll
-          for (int i = 0; i < kXN; ++i) {
-            const bool in = x_from[i] && k + x_k < a.K;
-            if (x_vec) {
-              copy16(to32 + x_to[i], in ? x_from[i] + k : x, in);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16 / (int)sizeof(TX); ++e)
-                reinterpret_cast<TX*>(to + x_to[i])[e] = in ? x_from[i][k + e] : TX(0.0f);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kAN; ++i) {
-            const bool in = k + a_k < a.K;
-            if (a_from[i]) copy16(to32 + a_to[i], in ? a_from[i] + k : A, in);
-          }
-        }
-        attn::cp_commit();
-      };
-      float d[kNT][4] = {}, e[kNT][4] = {};
-      Step now = settle({0, kb0}), ahead = now;
-      int slot = 0, last = -1;
-      for (int i = 0; i < kStages - 1; ++i) {
-        fetch(ahead, i);
-        ahead = after(ahead);
-      }
-      auto add_piece = [&](int s) {  // the first piece's sums are the start
-#pragma unroll
-        for (int j = 0; j < kNT; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            d[j][q] = s == 0 ? e[j][q] : d[j][q] + e[j][q];
-            e[j][q] = 0.0f;
-          }
-      };
-      while (now.s < kW) {
-        attn::cp_wait<kStages - 2>();
-        __syncthreads();
-        fetch(ahead, (slot + kStages - 1) % kStages);
-        ahead = after(ahead);
-        if (last >= 0 && last != now.s) add_piece(last);
-        last = now.s;
-        const unsigned char* const sx = stages + slot * sz.stage;
-        const unsigned char* const sa = sx + kR * 16 * kXC;
-        if (16 * mt < rows) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (now.b + b >= piece(now.s + 1)) break;
-            Eight<TX> lo, hi;
-            const unsigned char* const px = sx + (16 * mt + g) * 16 * kXC;
-            if constexpr (sizeof(TX) == 2) {
-              const int q = 16 * ((4 * b + tig) ^ ((g & 1) * 4));
-              lo.load(reinterpret_cast<const TX*>(px + q), true);
-              hi.load(reinterpret_cast<const TX*>(px + 8 * 16 * kXC + q), true);
-            } else {
-              const int q = 16 * (8 * b + 2 * tig);
-              lo.load2(px + q, g & 1);
-              hi.load2(px + 8 * 16 * kXC + q, g & 1);
-            }
-            uint4 w[kNT];
-#pragma unroll
-            for (int j = 0; j < kNT; ++j)
-              w[j] = half + 2 * j < tiles
-                         ? *reinterpret_cast<const uint4*>(sa + (8 * (half + 2 * j) + g) * 128 + 16 * ((4 * b + tig) ^ ((g & 1) * 4)))
-                         : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 2 * Eight<TX>::kParts; ++i)
-#pragma unroll
-              for (int j = 0; j < kNT; ++j) mma_half(e[j], lo.p[i / 2], hi.p[i / 2], w[j], i % 2);
-          }
-        }
-        now = after(now);
-        slot = (slot + 1) % kStages;
-      }
-      attn::cp_wait<0>();
-      if (last >= 0) add_piece(last);
-#pragma unroll
-      for (int j = 0; j < kNT; ++j)
-        if (half + 2 * j < tiles) put(sums, mt, half + 2 * j, d[j]);
-      cluster.sync();
-      // this block adds up kR / kC of the rows and gives them to all
-      constexpr int kOwn = kR / kC;
-      for (int i = tid; i < kOwn * sz.pitch / 2; i += kT) {
-        const int m = i / (sz.pitch / 2), r = 2 * (i - m * (sz.pitch / 2));
-        float2 s = make_float2(0.0f, 0.0f);
-        if (r < a.rank) {
-          const int o = (c * kOwn + m) * a.rank + r;
-          s = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sums + o, 0));
-#pragma unroll
-          for (int b = 1; b < kC; ++b) {
-            const float2 t = *reinterpret_cast<const float2*>(cluster.map_shared_rank(sums + o, b));
-            s.x += t.x, s.y += t.y;
-          }
-          s.x *= scale, s.y *= scale;
-        }
-        __nv_bfloat16 u[kParts], v[kParts];
-        split(s.x, u);
-        split(s.y, v);
-#pragma unroll
-        for (int p = 0; p < kParts; ++p) {
-          const uint32_t w = (uint32_t)__bfloat16_as_ushort(u[p]) | ((uint32_t)__bfloat16_as_ushort(v[p]) << 16);
-          uint32_t* to = reinterpret_cast<uint32_t*>(low + (p * kR + c * kOwn + m) * sz.pitch + r);
-          for (int b = 0; b < kC; ++b) *cluster.map_shared_rank(to, b) = w;
+    // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles. B comes
+    // by two buffers of the warp's own, base of the next tiles is asked for before the
+    // products of these. 16-byte parts of odd columns are swapped where a column is 128 bytes
+    // long or twice that, so that a quarter of a warp reads all banks.
+    unsigned char* const buffers = reinterpret_cast<unsigned char*>(sums) + warp * 128 * a.rank;
+    const int swap = a.rank % 64 ? 0 : 4;
+    auto fetch = [&](int chunk, int slot) {
+      if (chunk < chunk1) {
+        const uint32_t to = attn::smem_u32(buffers + slot * 64 * a.rank);
+        const __nv_bfloat16* const from = B + (int64_t)32 * chunk * a.rank;
+        for (int i = lane; i < 32 * tiles; i += 32) {
+          const int n = (int)by_tiles.div((uint32_t)i), q = i - n * tiles;
+          const bool in = 32 * chunk + n < a.N;
+          copy16(to + (n * tiles + (q ^ (n & 1) * swap)) * 16, in ? from + 8 * i : B, in);
         }
       }
-      cluster.sync();
-    }
-
-    // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles
-    constexpr int kHold = 2;  // blocks of ranks of B in registers
-    uint4 w[kHold][4];
-    auto load_b = [&](int chunk, int b0) {  // tile j's column g
-#pragma unroll
-      for (int b = 0; b < kHold; ++b) {
-        const int r = 32 * (b0 + b) + 8 * tig;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 32 * chunk + 8 * (g >> 1) + 2 * j + (g & 1);
-          w[b][j] = r < a.rank && n < a.N ? *reinterpret_cast<const uint4*>(B + (int64_t)n * a.rank + r)
-                                          : make_uint4(0, 0, 0, 0);
-        }
-      }
+      attn::cp_commit();
     };
-    for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW) {
+    Raw8<TY> next[kMP][2];
+    int next_row[kMP][2];
+    auto ask = [&](int chunk, int m0) {
+      if (chunk >= chunk1) return;
       const int col = 32 * chunk + 8 * tig;
       const bool whole = y_vec && 32 * chunk + 32 <= a.N;
-      if (rblocks <= kHold) load_b(chunk, 0);
+#pragma unroll
+      for (int m = 0; m < kMP; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          next_row[m][h] = row_of(16 * (m0 + m) + g + 8 * h);
+          if (base && next_row[m][h] >= 0) next[m][h].load(base + next_row[m][h] * a.base_stride + col, whole, a.N - col);
+          else next[m][h].clear();
+        }
+    };
+    fetch(chunk0 + warp, 0);
+    ask(chunk0 + warp, 0);
+    int slot = 0;
+    for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW, slot ^= 1) {
+      fetch(chunk + kW, slot ^ 1);
+      attn::cp_wait<1>();
+      __syncwarp();
+      const int col = 32 * chunk + 8 * tig;
+      const bool whole = y_vec && 32 * chunk + 32 <= a.N;
+      const unsigned char* const buffer = buffers + slot * 64 * a.rank;
 #pragma unroll 1
       for (int m0 = 0; 16 * m0 < rows; m0 += kMP) {
         Raw8<TY> y[kMP][2];
@@ -571,36 +426,35 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            row[m][h] = row_of(16 * (m0 + m) + g + 8 * h);
-            if (base && row[m][h] >= 0) y[m][h].load(base + row[m][h] * a.base_stride + col, whole, a.N - col);
-            else y[m][h].clear();
-          }
+          for (int h = 0; h < 2; ++h) y[m][h] = next[m][h], row[m][h] = next_row[m][h];
+        const bool more = 16 * (m0 + kMP) < rows;
+        ask(more ? chunk : chunk + kW, more ? m0 + kMP : 0);
         float d[kMP][4][4] = {};
         const __nv_bfloat16* t = low + (16 * m0 + g) * sz.pitch + 8 * tig;
-#pragma unroll 1
-        for (int b0 = 0; b0 < rblocks; b0 += kHold) {
-          if (rblocks > kHold) load_b(chunk, b0);
+        for (int b = 0; b < rblocks; ++b, t += 32) {
+          uint4 w[4];  // tile j's column g
+          const int q = 4 * b + tig;
 #pragma unroll
-          for (int b = 0; b < kHold; ++b) {
-            if (b0 + b >= rblocks) break;
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-              uint4 lo[kMP], hi[kMP];
-#pragma unroll
-              for (int m = 0; m < kMP; ++m) {
-                const __nv_bfloat16* const u = t + (p * kR + 16 * m) * sz.pitch + 32 * b;
-                lo[m] = *reinterpret_cast<const uint4*>(u), hi[m] = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
-              }
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int m = 0; m < kMP; ++m)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m], hi[m], w[b][j], i);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const int n = 8 * (g >> 1) + 2 * j + (g & 1);
+            w[j] = q < tiles ? *reinterpret_cast<const uint4*>(buffer + (n * tiles + (q ^ (n & 1) * swap)) * 16)
+                             : make_uint4(0, 0, 0, 0);
           }
-          t += 32 * kHold;
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) {
+            uint4 lo[kMP], hi[kMP];
+#pragma unroll
+            for (int m = 0; m < kMP; ++m) {
+              const __nv_bfloat16* const u = t + (p * kR + 16 * m) * sz.pitch;
+              lo[m] = *reinterpret_cast<const uint4*>(u), hi[m] = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int m = 0; m < kMP; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m], hi[m], w[j], i);
+          }
         }
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
@@ -612,7 +466,9 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
             y[m][h].store(out + row[m][h] * a.out_stride + col, whole, a.N - col);
           }
       }
+      __syncwarp();  // before the buffer is filled again
     }
+    attn::cp_wait<0>();
   }
   // ---- rows without an adapter, shared by the window's clusters
   if (a.base != a.out && bares) {
@@ -631,30 +487,30 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   }
 }
 
-template <typename TX, typename TY, int kMT, int kNT, bool kSolo>
+template <typename TX, typename TY, int kMT, bool kSolo>
 Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
-  auto kernel = k_lora<TX, TY, kMT, kNT, kSolo>;
+  auto kernel = k_lora<TX, TY, kMT, kSolo>;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(kernel, (int)Sizes(kMT, kSolo, kParts, 128, sizeof(TX)).bytes, done);
+  l.error = allow_smem(kernel, (int)Sizes(kMT, kSolo, kParts, 128).bytes, done);
   if (l.error != cudaSuccess) return l;
   const int64_t blocks = (a.n + kWindow - 1) / (int64_t)kWindow * per_window * (kSolo ? 1 : kC);
-  const size_t smem = (size_t)Sizes(kMT, kSolo, kParts, a.rank, sizeof(TX)).bytes;
-  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window));
-  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
+  const size_t smem = (size_t)Sizes(kMT, kSolo, kParts, a.rank).bytes;
+  const FastDiv by_tiles((uint32_t)a.rank / 8);
+  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window, by_tiles));
+  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window, by_tiles));
   return l;
 }
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  if (a.n > 2048) return a.rank <= 64 ? launch_t<TX, TY, 4, 4, false>(a, 6, s) : launch_t<TX, TY, 4, 8, false>(a, 6, s);
   const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * sms / windows));
-  if (a.n > 4096) return launch_t<TX, TY, 2, 0, true>(a, each, s);
-  if (a.n > kWindow) return launch_t<TX, TY, 1, 0, true>(a, each, s);
+  if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, true>(a, each, s);
+  if (a.n > kWindow) return launch_t<TX, TY, 1, true>(a, each, s);
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most
   const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  return launch_t<TX, TY, 1, 0, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
+  return launch_t<TX, TY, 1, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
 }
 
 }  // namespace
