@@ -21,6 +21,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "attn_mma.cuh"
 #include "fs_internal.h"
 
@@ -187,6 +189,11 @@ struct Sizes {
   }
 };
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
 // 16 bytes to shared memory, zeros without `in`.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
@@ -199,7 +206,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); 
 // kMT: row tiles of an item; kSolo: a block takes an item for itself, its warps the shares of
 // K that a cluster's blocks have.
 template <typename TX, typename TY, int kMT, bool kSolo>
-__global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window, FastDiv by_tiles) {
+__global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
   constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
@@ -380,37 +387,52 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     // by two buffers of the warp's own, base of the next tiles is asked for before the
     // products of these. 16-byte parts of odd columns are swapped where a column is 128 bytes
     // long or twice that, so that a quarter of a warp reads all banks.
-    unsigned char* const buffers = reinterpret_cast<unsigned char*>(sums) + warp * 128 * a.rank;
+    // What does not change from chunk to chunk is formed once (in all, a chunk of two row tiles at
+    // rank 64 took 1150 instructions without that; its MMAs are 64).
     const int swap = a.rank % 64 ? 0 : 4;
+    const uint32_t buffers = attn::smem_u32(sums) + warp * 128 * a.rank;
+    const uint32_t b_to = buffers + 16 * (lane ^ ((lane / tiles) & 1) * swap);  // 32 / tiles is even or swap 0
+    const int b_end = a.N * tiles;                                              // 16-byte parts of B
+    const uint32_t b_at = buffers + (8 * (g >> 1) + (g & 1)) * 16 * tiles;      // column g of MMA tile 0
+    const uint32_t t_at = attn::smem_u32(low) + (g * sz.pitch + 8 * tig) * 2;
+    int row[kMT][2];
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) row[m][h] = row_of(16 * m + g + 8 * h);
+    const int some_row = sh.row[0];  // read in place of none
     auto fetch = [&](int chunk, int slot) {
       if (chunk < chunk1) {
-        const uint32_t to = attn::smem_u32(buffers + slot * 64 * a.rank);
-        const __nv_bfloat16* const from = B + (int64_t)32 * chunk * a.rank;
-        for (int i = lane; i < 32 * tiles; i += 32) {
-          const int n = (int)by_tiles.div((uint32_t)i), q = i - n * tiles;
-          const bool in = 32 * chunk + n < a.N;
-          copy16(to + (n * tiles + (q ^ (n & 1) * swap)) * 16, in ? from + 8 * i : B, in);
+        const int i0 = 32 * chunk * tiles + lane;
+        const uint32_t to = b_to + slot * 64 * a.rank;
+        const __nv_bfloat16* const from = B + (int64_t)8 * i0;
+#pragma unroll 4
+        for (int k = 0; k < tiles; ++k) {
+          const bool in = i0 + 32 * k < b_end;
+          copy16(to + 512 * k, in ? from + 256 * k : B, in);
         }
       }
       attn::cp_commit();
     };
     Raw8<TY> next[kMP][2];
-    int next_row[kMP][2];
-    auto ask = [&](int chunk, int m0) {
-      if (chunk >= chunk1) return;
+    auto ask = [&](int chunk, auto m0) {
+      if (!base || chunk >= chunk1) return;
       const int col = 32 * chunk + 8 * tig;
       const bool whole = y_vec && 32 * chunk + 32 <= a.N;
 #pragma unroll
       for (int m = 0; m < kMP; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          next_row[m][h] = row_of(16 * (m0 + m) + g + 8 * h);
-          if (base && next_row[m][h] >= 0) next[m][h].load(base + next_row[m][h] * a.base_stride + col, whole, a.N - col);
-          else next[m][h].clear();
+          const int r = row[decltype(m0)::value + m][h];
+          next[m][h].load(base + (r >= 0 ? r : some_row) * a.base_stride + col, whole, a.N - col);
         }
     };
+#pragma unroll
+    for (int m = 0; m < kMP; ++m) next[m][0].clear(), next[m][1].clear();  // without base
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, kMT - kMP>;
     fetch(chunk0 + warp, 0);
-    ask(chunk0 + warp, 0);
+    ask(chunk0 + warp, First{});
     int slot = 0;
     for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW, slot ^= 1) {
       fetch(chunk + kW, slot ^ 1);
@@ -418,35 +440,29 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       __syncwarp();
       const int col = 32 * chunk + 8 * tig;
       const bool whole = y_vec && 32 * chunk + 32 <= a.N;
-      const unsigned char* const buffer = buffers + slot * 64 * a.rank;
-#pragma unroll 1
-      for (int m0 = 0; 16 * m0 < rows; m0 += kMP) {
+      auto columns = [&](auto m0, auto then) {
+        constexpr int kM = decltype(m0)::value;
         Raw8<TY> y[kMP][2];
-        int row[kMP][2];
 #pragma unroll
-        for (int m = 0; m < kMP; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) y[m][h] = next[m][h], row[m][h] = next_row[m][h];
-        const bool more = 16 * (m0 + kMP) < rows;
-        ask(more ? chunk : chunk + kW, more ? m0 + kMP : 0);
+        for (int m = 0; m < kMP; ++m) y[m][0] = next[m][0], y[m][1] = next[m][1];
+        then();
         float d[kMP][4][4] = {};
-        const __nv_bfloat16* t = low + (16 * m0 + g) * sz.pitch + 8 * tig;
-        for (int b = 0; b < rblocks; ++b, t += 32) {
+        uint32_t t = t_at + kM * 16 * sz.pitch * 2;
+        const uint32_t w_at = b_at + slot * 64 * a.rank;
+#pragma unroll 1
+        for (int b = 0; b < rblocks; ++b, t += 64) {
           uint4 w[4];  // tile j's column g
           const int q = 4 * b + tig;
+          const uint32_t at = w_at + 16 * (q ^ (g & 1) * swap);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = 8 * (g >> 1) + 2 * j + (g & 1);
-            w[j] = q < tiles ? *reinterpret_cast<const uint4*>(buffer + (n * tiles + (q ^ (n & 1) * swap)) * 16)
-                             : make_uint4(0, 0, 0, 0);
-          }
+          for (int j = 0; j < 4; ++j) w[j] = q < tiles ? lds128(at + 32 * j * tiles) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int p = 0; p < kParts; ++p) {
             uint4 lo[kMP], hi[kMP];
 #pragma unroll
             for (int m = 0; m < kMP; ++m) {
-              const __nv_bfloat16* const u = t + (p * kR + 16 * m) * sz.pitch;
-              lo[m] = *reinterpret_cast<const uint4*>(u), hi[m] = *reinterpret_cast<const uint4*>(u + 8 * sz.pitch);
+              const uint32_t u = t + (p * kR + 16 * m) * sz.pitch * 2;
+              lo[m] = lds128(u), hi[m] = lds128(u + 16 * sz.pitch);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -460,11 +476,16 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         for (int m = 0; m < kMP; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (row[m][h] < 0) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[m][h].add2(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
-            y[m][h].store(out + row[m][h] * a.out_stride + col, whole, a.N - col);
+            if (row[kM + m][h] >= 0) y[m][h].store(out + row[kM + m][h] * a.out_stride + col, whole, a.N - col);
           }
+      };
+      if (kMT == kMP || rows <= 16 * kMP) {
+        columns(First{}, [&] { ask(chunk + kW, First{}); });
+      } else {
+        columns(First{}, [&] { ask(chunk, Second{}); });
+        columns(Second{}, [&] { ask(chunk + kW, First{}); });
       }
       __syncwarp();  // before the buffer is filled again
     }
@@ -497,9 +518,8 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   if (l.error != cudaSuccess) return l;
   const int64_t blocks = (a.n + kWindow - 1) / (int64_t)kWindow * per_window * (kSolo ? 1 : kC);
   const size_t smem = (size_t)Sizes(kMT, kSolo, kParts, a.rank).bytes;
-  const FastDiv by_tiles((uint32_t)a.rank / 8);
-  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window, by_tiles));
-  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window, by_tiles));
+  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window));
+  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
   return l;
 }
 template <typename TX, typename TY>
