@@ -1,23 +1,31 @@
 // Low-rank adapters of many requests (fs_lora_add): out = base + scale B (A x) with the
 // row's own A [rank][K] and B [N][rank].
 //
-// The bytes bound it: base and out once, x once, an adapter once for all its rows. One
-// launch does both products. A cluster of eight blocks takes up to kR rows of one adapter
-// out of a window of 256 rows (rows of any order are gathered by a hash of their adapters
-// in shared memory, in each block alike); its blocks share K, exchange their parts of A x
-// through distributed shared memory, and then share N.
+// The least it can do is to read base and x once, an adapter once for all its rows, and to
+// write out. One launch does both products. Rows of any order are gathered out of windows of
+// 256 by a hash of their adapters in shared memory; an item is up to kR rows of one adapter.
+// Up to 256 rows a cluster of eight blocks takes an item: its blocks share K, exchange their
+// parts of A x through distributed shared memory, and then share N (256 rows of 64 adapters,
+// rank 16, 4096 to 4096: 16.5 us, a block an item 31). Beyond, a block takes an item for itself,
+// without barriers between blocks (1000 rows of 200 adapters, 576 to 960: 20 us, clusters
+// 104; of 64 adapters, 4096 to 4096: 33 and 61). Items have one row tile of 16, or two where
+// adapters have many rows (8192 rows of 8 adapters, rank 64, 4096 to 14336: 195 us, one tile
+// 223; of 64 adapters, rank 16, 4096 to 4096: 143 and 135).
 //
 // Both products run on bf16 warp MMAs (m16n8k16, rows of x as M): a decode step has one to
-// a few rows an adapter, so that most of a 128-row tcgen05 tile would be empty, and a
-// prompt's products are a few percent of the bytes' time. Fragments come straight from
-// global memory, 16 bytes a lane: the order of the summed index is free as long as both
-// operands have the same, so a lane's 8 values of 32 feed two MMAs.
+// a few rows an adapter, so that most of a 128-row tcgen05 tile would be empty. Their rate here
+// is 600 TFLOP/s (measured), so 16 rows a tile and two parts of A x cost the 8192 rows 57 us
+// of MMAs, next to 79 us of bytes; what bounds that case now is the warps' chains of shared
+// loads, MMAs and stores (of 4700 cycles a warp and chunk of two tiles, 2600 are the MMAs'
+// loop). Fragments of x and A come straight from global memory, 16 bytes a lane: the order of
+// the summed index is free as long as both operands have the same, so a lane's 8 values of 32
+// feed two MMAs.
 //
 // A x is held in f32 and enters the second product as two bf16 parts (16 bits) for bf16
-// results and three (24 bits) for f32 ones; an f32 x enters the first as three. Products of
-// parts are exact, sums f32. Sums run over the same pieces in the same order whatever kR:
-// K in eight blocks' shares, each in eight pieces, so that a row's bits depend on the row
-// alone.
+// results, whose own rounding is 2^-9, and three (24 bits) for f32 ones; an f32 x enters the
+// first as three. Products of parts are exact, sums f32. Sums run over the same pieces in the
+// same order however rows are tiled and shared: K in eight shares, each in eight pieces, so
+// that a row's bits depend on the row alone.
 
 #include <cooperative_groups.h>
 
@@ -90,12 +98,6 @@ struct Eight {
       }
       parts(v);
     }
-  }
-  // from shared memory, its halves swapped if `odd`
-  __device__ __forceinline__ void load2(const unsigned char* p, bool odd) {
-    const float4 a = *reinterpret_cast<const float4*>(p + (odd ? 16 : 0)), b = *reinterpret_cast<const float4*>(p + (odd ? 0 : 16));
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    parts(v);
   }
   __device__ __forceinline__ void parts(const float (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
@@ -525,7 +527,9 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
+  // blocks a window: four an SM's worth (two run at a time), at least eight
   const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * sms / windows));
+  // two row tiles an item where there are 256 rows an adapter and more
   if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, true>(a, each, s);
   if (a.n > kWindow) return launch_t<TX, TY, 1, true>(a, each, s);
   // clusters a window: what fits the SMs at once (two blocks each), a row each at most

@@ -134,6 +134,22 @@ def test_a_rows_bits_are_the_same_in_large_batches(xb, yb):
         assert torch.equal(run(d), whole[order])
 
 
+@pytest.mark.parametrize("xb,yb", [(True, False), (True, True), (False, False), (False, True)])
+@pytest.mark.parametrize("rank", [8, 64, 104])
+def test_a_rows_bits_are_the_same_in_batches_of_two_tiles(xb, yb, rank):
+    """More than 4096 rows of few adapters: items of two row tiles."""
+    import torch
+    rng = np.random.default_rng(rank)
+    c = make(rng, 5003, 264, 69, 4, rank, xb, yb, np.repeat(rng.integers(-1, 4, 51), 99)[:5003])
+    whole = run(c)
+    check(c, whole)
+    assert torch.equal(run(c, base=None)[c["adapter"] < 0], torch.zeros_like(whole[c["adapter"] < 0]))
+    for n in (3, 200, 700):
+        order = rng.permutation(5003)[:n]
+        d = dict(c, x=c["x"][order].contiguous(), adapter=c["adapter"][order].contiguous(), base=c["base"][order].contiguous())
+        assert torch.equal(run(d), whole[order])
+
+
 def test_what_is_no_number_stays_in_its_row():
     import torch
     rng = np.random.default_rng(10)
