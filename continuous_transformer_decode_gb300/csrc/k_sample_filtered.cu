@@ -40,6 +40,7 @@ constexpr int kSub = 64;    // parts of a bin that is split
 constexpr int kList = 128;  // tokens that are ranked among themselves
 constexpr int kFew = 64;    // a top_k that always ends in one list
 constexpr int kFrac = 39;   // a mass in bin b is a whole number of 2^-(b + kFrac)
+constexpr int kLeast = -125 * 256;  // weights at this place and behind are 0
 constexpr int kCount = 50;  // a column's entry: count << kCount | mass
 
 struct Bin {
@@ -255,14 +256,16 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   }
   const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
 
-  // A weight as a whole number of 2^-(bin + kFrac): in the last bin, and for tokens that far
-  // below that they end there, what is left of it.
+  // A weight as a whole number of 2^-(bin + kFrac): in the last bin what is left of it, and 1
+  // where nothing is, so that the first of them can be drawn (by u = 0). 2^20 such ones are
+  // 2^-38 of the sum.
   auto mass_of = [&](float z, int& bin) {
     int k;
     const uint64_t m = weigh(z, M, c, sh.tab, k);
     const int b = -(k >> 8);
     bin = min(kBins - 1, b);
-    return m >> min(63, b - bin);
+    const uint64_t left = m >> min(63, b - bin);
+    return left ? left : (uint64_t)(k > kLeast);
   };
   auto mass = [&](float z) {
     int bin;
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   auto weight = [&](float z) {  // times 2^60
     int k;
     const uint64_t m = weigh(z, M, c, sh.tab, k);
-    return to_two(k > -125 * 256 ? m : 0, (k >> 8) - kFrac + 60);
+    return to_two(k > kLeast ? m : 0, (k >> 8) - kFrac + 60);
   };
   // ---- counts and masses of the bins
   // Four tokens in step, without branches, so that their chains of dependent operations
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       const uint64_t v = b <= last ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
       mine.count += (int)(v >> kCount);
       const int s = 54 - kFrac - b;
-      sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s - 1 : 0))) >> (s < 0 ? -s : 0);
+      sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s : 0)) - 1) >> (s < 0 ? -s : 0);  // rounded up: none is lost
     }
     mine.mass = to_two(sum, 60 - 54);
   }

@@ -728,9 +728,10 @@ int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t*
  * temps[i] = 0. top_k, top_p and min_p may each be NULL: all stay. Logits of -inf or NaN never stay; equal +inf
  * logits share all of the weight; a row without a token gives token 0 and kept 0. temps is
  * held in [1e-30, 1e30]; a NaN in top_p or min_p turns it off. Weights are good to a
- * relative 2^-36 and summed in pairs of f32 numbers, so that a cut or a draw is that of
- * the real numbers but next to a border. A weight below 2^-125 of the largest is 0. vocab
- * is at most 2^20. */
+ * relative 2^-37 and summed as whole numbers and as pairs of f32 numbers, so that a cut or a
+ * draw is that of the real numbers but next to a border. A weight below 2^-125 of the
+ * largest is 0, and one below 2^-58 of it counts as that much in the sums over runs of
+ * tokens. vocab is at most 2^20. */
 int fs_sample_filtered(const float* logits, int64_t logits_stride, int32_t n, int32_t vocab,
                        const float* temps, const int32_t* top_k, const float* top_p,
                        const float* min_p, const float* u, int32_t* tokens, int32_t* kept,

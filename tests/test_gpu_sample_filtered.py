@@ -161,6 +161,25 @@ def test_random_numbers_at_their_ends():
     check(z, 1.0, u, k=9, p=np.float32(0.8))
 
 
+@pytest.mark.parametrize("V", [600, 5000, 50000])
+def test_the_smallest_weights_can_be_drawn(V):
+    """u = 0 takes the first token whose weight is not 0, however small (2^-60 to 2^-120 of
+    the largest here), also behind tokens without any."""
+    rng = np.random.default_rng(V)
+    z = np.full((6, V), -np.inf, np.float32)
+    for i, bits in enumerate((45, 57, 59, 80, 100, 120)):
+        z[i, 3 * i + 2:] = -bits * np.log(2)
+        z[i, 3 * i] = -200.0  # a weight of 0
+        z[i, rng.integers(V // 2, V)] = 0.0
+    u = np.zeros(6, np.float32)
+    z[:, 0] = -np.inf
+    for T in (1.0, 0.98):
+        for p, m in ((None, None), (np.float32(0.9999999), None), (None, np.float32(1e-30))):
+            got = run(z, T, u, p=p, m=m)
+            want = [R.sample(np.where(r == -200.0, -np.inf, r), T, 0.0, 0, 1.0 if p is None else p, 0.0 if m is None else m) for r in z]
+            assert list(got[0]) == [w[0] for w in want]
+
+
 @pytest.mark.parametrize("V,k", [(500, None), (4099, None), (49152, None), (49152, 100)])
 def test_draws_next_to_borders(V, k):
     """Random numbers that are the nearest f32, and its neighbours, to borders of the
