@@ -176,16 +176,16 @@ struct Gather {
   int firsts[kW], bare[kW];
 };
 
-// Shared memory behind Gather: the parts of A x, [part][row] of `pitch` values, and f32 tiles
-// of sums, a warp's each and, of a cluster's blocks, a block's each; the warps' buffers of B
-// lie where the sums were.
+// Shared memory behind Gather: the parts of A x, and f32 tiles of sums, a warp's each and, of a
+// cluster's blocks, a block's each; the warps' buffers of B lie where the sums were. A part of
+// a row tile is a run of MMA fragments, [block of 32 ranks][half][lane] of 16 bytes, so that one
+// load gives a lane the four registers of an operand, side by side.
 struct Sizes {
-  int pitch;
+  int tile;  // bytes of a part of a row tile
   int64_t low, bytes;
   __host__ __device__ Sizes(int mt, bool solo, int parts, int rank) {
-    const int blocks = (rank + 31) / 32;
-    pitch = 32 * blocks + (blocks % 2 ? 0 : 32);  // rows 64 bytes apart modulo 128: no conflicts
-    low = (int64_t)parts * mt * 16 * pitch * 2;
+    tile = (rank + 31) / 32 * 1024;
+    low = (int64_t)parts * mt * tile;
     const int64_t sums = (int64_t)(solo ? kW : kW + kC) * mt * 16 * rank * 4, buffers = (int64_t)kW * 128 * rank;
     bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + (sums > buffers ? sums : buffers);
   }
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   extern __shared__ __align__(16) unsigned char dyn[];
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
   const Sizes sz(kMT, kSolo, kParts, a.rank);
-  __nv_bfloat16* const low = reinterpret_cast<__nv_bfloat16*>(dyn + (sizeof(Gather) + 15) / 16 * 16);
-  float* const sums = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(low) + sz.low);
+  unsigned char* const low = dyn + (sizeof(Gather) + 15) / 16 * 16;
+  float* const sums = reinterpret_cast<float*>(low + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
   static_assert(kW == kC, "a warp a share of K");
   constexpr int kBlocks = kSolo ? 1 : kC;  // of an item
@@ -367,22 +367,25 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         }
         cluster.sync();
       }
-      auto total = [&](int i) {  // of place i of the parts' rows
-        const int m = i / sz.pitch, r = i - m * sz.pitch;
-        if (m >= kMT * 16 || r >= a.rank) return 0.0f;
-        const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
-        float v = p[0];
+      // a value of A x a thread and step: its fragment's lane and half, two ranks a register
+      for (int i = tid; i < kMT * 16 * 32 * rblocks; i += kT) {
+        const int m = i / (32 * rblocks), r = i - m * 32 * rblocks;
+        float v = 0.0f;
+        if (r < a.rank) {
+          const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
+          v = p[0];
 #pragma unroll
-        for (int b = 1; b < kC; ++b) v += p[b * tile];
-        return v * scale;
-      };
-      auto keep = [&](int i, float v) {
+          for (int b = 1; b < kC; ++b) v += p[b * tile];
+          v *= scale;
+        }
         __nv_bfloat16 u[kParts];
         split(v, u);
+        const int unit = ((r >> 5) * 2 + ((r >> 2) & 1)) * 32 + (m & 7) * 4 + ((r >> 3) & 3);
+        const int reg = ((r >> 1) & 1) * 2 + ((m >> 3) & 1);
+        unsigned char* const to = low + (m >> 4) * sz.tile + unit * 16 + reg * 4 + (r & 1) * 2;
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) low[p * kR * sz.pitch + i] = u[p];
-      };
-      for (int i = tid; i < kMT * 16 * sz.pitch; i += kT) keep(i, total(i));
+        for (int p = 0; p < kParts; ++p) *reinterpret_cast<__nv_bfloat16*>(to + p * kMT * sz.tile) = u[p];
+      }
       __syncthreads();
     }
     // ---- the columns: chunks of 32, a lane's 8 consecutive ones from four MMA tiles. B comes
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     const uint32_t b_to = buffers + 16 * (lane ^ ((lane / tiles) & 1) * swap);  // 32 / tiles is even or swap 0
     const int b_end = a.N * tiles;                                              // 16-byte parts of B
     const uint32_t b_at = buffers + (8 * (g >> 1) + (g & 1)) * 16 * tiles;      // column g of MMA tile 0
-    const uint32_t t_at = attn::smem_u32(low) + (g * sz.pitch + 8 * tig) * 2;
+    const uint32_t t_at = attn::smem_u32(low) + 16 * lane;
     int row[kMT][2];
 #pragma unroll
     for (int m = 0; m < kMT; ++m)
@@ -449,10 +452,10 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         for (int m = 0; m < kMP; ++m) y[m][0] = next[m][0], y[m][1] = next[m][1];
         then();
         float d[kMP][4][4] = {};
-        uint32_t t = t_at + kM * 16 * sz.pitch * 2;
+        uint32_t t = t_at + kM * sz.tile;
         const uint32_t w_at = b_at + slot * 64 * a.rank;
 #pragma unroll 1
-        for (int b = 0; b < rblocks; ++b, t += 64) {
+        for (int b = 0; b < rblocks; ++b, t += 1024) {
           uint4 w[4];  // tile j's column g
           const int q = 4 * b + tig;
           const uint32_t at = w_at + 16 * (q ^ (g & 1) * swap);
@@ -460,18 +463,20 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
           for (int j = 0; j < 4; ++j) w[j] = q < tiles ? lds128(at + 32 * j * tiles) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int p = 0; p < kParts; ++p) {
-            uint4 lo[kMP], hi[kMP];
+            uint4 f[kMP][2];
 #pragma unroll
-            for (int m = 0; m < kMP; ++m) {
-              const uint32_t u = t + (p * kR + 16 * m) * sz.pitch * 2;
-              lo[m] = lds128(u), hi[m] = lds128(u + 16 * sz.pitch);
-            }
+            for (int m = 0; m < kMP; ++m)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) f[m][i] = lds128(t + (p * kMT + m) * sz.tile + 512 * i);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int m = 0; m < kMP; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m], hi[m], w[j], i);
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t x[4] = {f[m][i].x, f[m][i].y, f[m][i].z, f[m][i].w};
+                  attn::mma16816(d[m][j], x, i ? w[j].z : w[j].x, i ? w[j].w : w[j].y);
+                }
           }
         }
 #pragma unroll
