@@ -154,14 +154,23 @@ struct Raw8 {
         if (i < n) p[i] = t[i];
     }
   }
-  // values 2 i and 2 i + 1 plus (a, b)
-  __device__ __forceinline__ void add2(int i, float a, float b) {
+  // What the sums of values 2 i and 2 i + 1 start with, and their end. f32 values are added
+  // last, so that the sums of products do not round at the size of base; bf16 ones, which round
+  // to 8 bits themselves, first.
+  __device__ __forceinline__ void start(int i, float& a, float& b) const {
+    if constexpr (sizeof(T) == 4) {
+      a = b = 0.0f;
+    } else {
+      const uint32_t u = reinterpret_cast<const uint32_t*>(v)[i];
+      a = __uint_as_float(u << 16), b = __uint_as_float(u & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void end(int i, float a, float b) {
     if constexpr (sizeof(T) == 4) {
       float* f = reinterpret_cast<float*>(v);
       f[2 * i] += a, f[2 * i + 1] += b;
     } else {
-      uint32_t* u = reinterpret_cast<uint32_t*>(v);
-      u[i] = attn::pack_bf16(__uint_as_float(u[i] << 16) + a, __uint_as_float(u[i] & 0xffff0000u) + b);
+      reinterpret_cast<uint32_t*>(v)[i] = attn::pack_bf16(a, b);
     }
   }
 };
@@ -448,10 +457,16 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
       auto columns = [&](auto m0, auto then) {
         constexpr int kM = decltype(m0)::value;
         Raw8<TY> y[kMP][2];
+        float d[kMP][4][4];
 #pragma unroll
-        for (int m = 0; m < kMP; ++m) y[m][0] = next[m][0], y[m][1] = next[m][1];
+        for (int m = 0; m < kMP; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (sizeof(TY) == 4) y[m][h] = next[m][h];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) next[m][h].start(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
+          }
         then();
-        float d[kMP][4][4] = {};
         uint32_t t = t_at + kM * sz.tile;
         const uint32_t w_at = b_at + slot * 64 * a.rank;
 #pragma unroll 1
@@ -484,7 +499,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[m][h].add2(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
+            for (int j = 0; j < 4; ++j) y[m][h].end(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
             if (row[kM + m][h] >= 0) y[m][h].store(out + row[kM + m][h] * a.out_stride + col, whole, a.N - col);
           }
       };
