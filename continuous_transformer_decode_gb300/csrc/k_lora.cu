@@ -4,25 +4,22 @@
 // The least it can do is to read base and x once, an adapter once for all its rows, and to
 // write out. One launch does both products. Rows of any order are gathered out of windows of
 // 256 by a hash of their adapters in shared memory; an item is up to kR rows of one adapter.
-// Up to 256 rows a cluster of eight blocks takes an item: its blocks share K, exchange their
-// parts of A x through distributed shared memory, and then share N (256 rows of 64 adapters,
-// rank 16, 4096 to 4096: 16.5 us, a block an item 31). Beyond, a block takes an item for itself,
-// without barriers between blocks (1000 rows of 200 adapters, 576 to 960: 20 us, clusters
-// 104; of 64 adapters, 4096 to 4096: 33 and 61). Items have one row tile of 16, or two where
-// adapters have many rows (8192 rows of 8 adapters, rank 64, 4096 to 14336: 195 us, one tile
-// 223; of 64 adapters, rank 16, 4096 to 4096: 143 and 135).
+// Where items are few and large a cluster of eight blocks takes each: its blocks share K,
+// exchange their parts of A x through distributed shared memory, and then share N. Else a block
+// takes an item for itself, without barriers between blocks (the choice and both sides'
+// times are at launch_xy).
 //
 // Both products run on bf16 warp MMAs (m16n8k16, rows of x as M): a decode step has one to
 // a few rows an adapter, so that most of a 128-row tcgen05 tile would be empty. Their rate here
-// is 600 TFLOP/s (measured), so 16 rows a tile and two parts of A x cost the 8192 rows 57 us
-// of MMAs, next to 79 us of bytes; what bounds that case now is the warps' chains of shared
-// loads, MMAs and stores (of 4700 cycles a warp and chunk of two tiles, 2600 are the MMAs'
-// loop). Fragments of x and A come straight from global memory, 16 bytes a lane: the order of
-// the summed index is free as long as both operands have the same, so a lane's 8 values of 32
-// feed two MMAs.
+// is 600 TFLOP/s (measured), so two parts of A x cost 8192 rows of 8 adapters, rank 64, 4096 to
+// 14336, 57 us of MMAs, next to 79 us of bytes; they take 161 us. What bounds them is the
+// warps' issue slots and their chains of shared loads, MMAs and stores (3.3 TB/s; MMAs active
+// 0.4 of the time; one round of blocks, two an SM by their registers). Fragments of x and A
+// come straight from global memory, 16 bytes a lane: the order of the summed index is free as
+// long as both operands have the same, so a lane's 8 values of 32 feed two MMAs.
 //
 // A x is held in f32 and enters the second product as two bf16 parts (16 bits) for bf16
-// results, whose own rounding is 2^-9, and three (24 bits) for f32 ones; an f32 x enters the
+// results, which round by 2^-8 themselves, and three (24 bits) for f32 ones; an f32 x enters the
 // first as three. Products of parts are exact, sums f32. Sums run over the same pieces in the
 // same order however rows are tiled and shared: K in eight shares, each in eight pieces, so
 // that a row's bits depend on the row alone.
@@ -544,17 +541,29 @@ Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
   else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
   return l;
 }
+// Which blocks take an item, from how long it would take at most, as the adapters' mix is not
+// known here: a window of 256 rows has up to n_adapters items and one more for every 16
+// rows. A block alone takes 6 us and `alone`, a cluster 4 us and an eighth of it; 2 blocks an SM
+// run at a time. Measured, us, a block alone | a cluster (rows, adapters, rank, K, N):
+//   256, 8, 16, 4096, 4096: 22 | 8.5     256, 64, 16, 4096, 4096: 27 | 16
+//   256, 200, 16, 576, 960: 10 | 29      1000, 8, 64, 4096, 14336: 91 | 57
+//   1000, 64, 16, 4096, 4096: 32 | 60    2500, 8, 64, 4096, 14336: 97 | 118
+// Two row tiles an item where adapters have 256 rows and more (8192 rows, two | one):
+//   8, 16, 4096, 4096: 52 | 65    8, 64, 4096, 14336: 161 | 190    64, 16, 4096, 4096: 142 | 132
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + kWindow - 1) / kWindow;
-  // blocks a window: four an SM's worth (two run at a time), at least eight
-  const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * sms / windows));
-  // two row tiles an item where there are 256 rows an adapter and more
+  const int64_t items = std::min<int64_t>(a.n, windows * std::min<int64_t>(kWindow, (int64_t)a.n_adapters + kWindow / 16));
+  const double alone = a.N / 256.0 * (0.5 + 0.007 * a.rank) + a.K / 1024.0;
+  const int64_t clusters = std::max(1, 2 * sms / kC), blocks = 2 * (int64_t)sms;
+  const double by_clusters = (double)((items + clusters - 1) / clusters) * (4 + alone / 8);
+  const double by_blocks = (double)((items + blocks - 1) / blocks) * (6 + alone);
+  if (by_clusters <= by_blocks)
+    return launch_t<TX, TY, 1, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), std::max<int64_t>(1, clusters / windows)), s);
+  // blocks a window: four an SM's worth, at least eight
+  const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * (int64_t)sms / windows));
   if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, true>(a, each, s);
-  if (a.n > kWindow) return launch_t<TX, TY, 1, true>(a, each, s);
-  // clusters a window: what fits the SMs at once (two blocks each), a row each at most
-  const int64_t fit = std::max<int64_t>(1, 2 * (int64_t)sms / kC / windows);
-  return launch_t<TX, TY, 1, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), fit), s);
+  return launch_t<TX, TY, 1, true>(a, each, s);
 }
 
 }  // namespace

@@ -3,9 +3,14 @@
 // Which pages a lane takes follows from two running sums: of the pages that the lanes
 // want, in lane order, and of the free pages, in page order; the j-th wanted page is the
 // j-th free one. The lanes' sums are formed by every block for itself, in its shared
-// memory, from the lanes' numbers, which are few; the pages and the rows are shared among
-// the blocks of one cluster, which exchange their counts of free pages. A page's or a
-// row's lane is found by bisection in the running sums.
+// memory, from the lanes' numbers, which are few; the pages are shared among the blocks of
+// one cluster, which list their free ones and exchange the counts, and the wanted ones among
+// all their threads. A page's or a row's lane is found by bisection in the running sums.
+//
+// The bytes are nothing (3 MB for 1021 lanes, 102282 pages and 131198 rows: 0.5 us); it is a
+// chain of a few loads, sums and barriers: 4.5 us for one lane, 10 us for 256 lanes and 47955
+// pages, 16 us for the 1021 lanes, 5 of them in the rows' kernel (by the cluster's eight SMs
+// alone the rows took 11).
 #include <cooperative_groups.h>
 
 #include "fs_internal.h"

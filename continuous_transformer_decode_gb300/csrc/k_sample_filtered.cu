@@ -20,6 +20,13 @@
 // the ranking want them as well. Where the tokens up to the cut are few, as with a small
 // top_k or a peaked row, they go to one block as a whole, which does the rest; a small top_k
 // asks for no weights but theirs.
+//
+// The logits' bytes are a few percent of the time (256 rows of 49152: 7 us at the copy's rate).
+// A row's chain bounds it: of 55 thousand cycles a block of four takes (256 rows, two blocks an
+// SM by their shared memory, top-p: 107 to 140 us by the inputs), 14 go to the weights of its 12288
+// tokens, which are bound by issue (66 instructions each), 6 to the loads, 11 to five barriers
+// of the cluster and what they wait for, the rest to choosing, gathering and ranking. 64 mixed
+// rows: 34 us; one row of 32000 with top-k 50 and top-p: 10 us.
 
 #include <cooperative_groups.h>
 
@@ -145,7 +152,8 @@ __device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* 
 }
 
 // What all lanes hold anyway, told to the compiler: a branch on it then needs no
-// reconvergence before each of the shuffles inside (256 rows: 188 us without, 1xx with).
+// reconvergence before each of the shuffles inside (the draw's sums and choice by one warp:
+// 1450 cycles, 9100 without).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 __device__ __forceinline__ float uniform(float v) { return __shfl_sync(kAll, v, 0); }
 
