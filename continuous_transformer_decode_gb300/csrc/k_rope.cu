@@ -8,8 +8,10 @@
 // f32's.) The signed top 24 bits give sine and cosine by sincospi, the next 24 turn them
 // by a first-order step, as their angle is below 2^-22.
 //
-// One pass over the bytes: a thread has one vector of pairs of a row, computes their sines
-// and cosines once and takes several heads by them.
+// One pass over the bytes, which bound it: a thread has one vector of pairs of a row, computes
+// their sines and cosines once and takes several heads by them. 65536 rows of 40 heads of 128
+// in bf16: 207 us, 6.5 TB/s, 0.96 of the measured copy; 4099 rows of 18 heads of 256 in f32, a
+// quarter turned: 25 us, 0.88; one row: 2 us, the launch.
 #include "fs_internal.h"
 
 namespace fsk {
