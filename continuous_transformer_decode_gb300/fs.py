@@ -535,7 +535,7 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
 
 
 # ------------------------------------------------------- 8-bit paged KV cache
-# The calls of this section and the next take CUDA tensors and a stream (a
+# The calls of this section and the next two take CUDA tensors and a stream (a
 # torch.cuda.Stream or an address; None: torch's current stream) and return once
 # their work is enqueued there. As with any kernel on a stream of the caller's,
 # tensors that were made or are freed on another stream are the caller's to order.

@@ -611,7 +611,8 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
  * are aligned to their element type.
  * Errors, with nothing enqueued: FS_ERR_ARG (a NULL pointer, a size, a type, an
  * alignment, overlapping buffers, memory of another device or of the host);
- * FS_ERR_CUDA (a launch failed). */
+ * FS_ERR_CUDA (a launch failed: of fs_pages_update's two, for many rows, the first may
+ * have run). */
 
 /* Page tables and slot maps, kept on the GPU: one call lets lanes give up tokens
  * and take new ones. The pool is holders[n_pages] (how many lanes hold a page, 0:
