@@ -4,15 +4,15 @@
 // The least it can do is to read base and x once, an adapter once for all its rows, and to
 // write out. One launch does both products. Rows of any order are gathered out of windows of
 // 256 by a hash of their adapters in shared memory; an item is up to kR rows of one adapter.
-// Where items are few and large a cluster of eight blocks takes each: its blocks share K,
+// Where items are few and large a cluster of eight or four blocks takes each: its blocks share K,
 // exchange their parts of A x through distributed shared memory, and then share N. Else a block
-// takes an item for itself, without barriers between blocks (the choice and both sides'
-// times are at launch_xy).
+// takes an item for itself, without barriers between blocks (the choice and its times are at
+// launch_xy).
 //
 // Both products run on bf16 warp MMAs (m16n8k16, rows of x as M): a decode step has one to
 // a few rows an adapter, so that most of a 128-row tcgen05 tile would be empty. Their rate here
 // is 600 TFLOP/s (measured), so two parts of A x cost 8192 rows of 8 adapters, rank 64, 4096 to
-// 14336, 57 us of MMAs, next to 79 us of bytes; they take 161 us. What bounds them is the
+// 14336, 57 us of MMAs, next to 79 us of bytes; they take 160 us. What bounds them is the
 // warps' issue slots and their chains of shared loads, MMAs and stores (3.3 TB/s; MMAs active
 // 0.4 of the time; one round of blocks, two an SM by their registers). Fragments of x and A
 // come straight from global memory, 16 bytes a lane: the order of the summed index is free as
@@ -37,8 +37,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kC = 8, kT = 256, kW = kT / 32;  // blocks of a cluster, threads, warps
-constexpr int kWindow = kT;                    // rows that are gathered, one a thread
+constexpr int kShares = 8, kT = 256, kW = kT / 32;  // shares of K, threads, warps
+constexpr int kWindow = kT;                         // rows that are gathered, one a thread
 constexpr int kSlots = 2 * kWindow;
 
 // Three bf16 parts of f32 values that hold their 24 bits (two: 16). A value past bf16's
@@ -182,17 +182,18 @@ struct Gather {
   int firsts[kW], bare[kW];
 };
 
-// Shared memory behind Gather: the parts of A x, and f32 tiles of sums, a warp's each and, of a
-// cluster's blocks, a block's each; the warps' buffers of B lie where the sums were. A part of
+// Shared memory behind Gather: the parts of A x, and f32 tiles of sums, a warp's for each of
+// the block's shares and, in a cluster, a share's each; the warps' buffers of B lie where the sums were. A part of
 // a row tile is a run of MMA fragments, [block of 32 ranks][half][lane] of 16 bytes, so that one
 // load gives a lane the four registers of an operand, side by side.
 struct Sizes {
   int tile;  // bytes of a part of a row tile
   int64_t low, bytes;
-  __host__ __device__ Sizes(int mt, bool solo, int parts, int rank) {
+  __host__ __device__ Sizes(int mt, int item_blocks, int parts, int rank) {
     tile = (rank + 31) / 32 * 1024;
     low = (int64_t)parts * mt * tile;
-    const int64_t sums = (int64_t)(solo ? kW : kW + kC) * mt * 16 * rank * 4, buffers = (int64_t)kW * 128 * rank;
+    const int tiles = item_blocks == 1 ? kW : kShares / item_blocks * kW + kShares;
+    const int64_t sums = (int64_t)tiles * mt * 16 * rank * 4, buffers = (int64_t)kW * 128 * rank;
     bytes = (int64_t)((sizeof(Gather) + 15) / 16 * 16) + low + (sums > buffers ? sums : buffers);
   }
 };
@@ -211,21 +212,21 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
 // shuffles then need no reconvergence before each of them.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 
-// kMT: row tiles of an item; kSolo: a block takes an item for itself, its warps the shares of
-// K that a cluster's blocks have.
-template <typename TX, typename TY, int kMT, bool kSolo>
+// kMT: row tiles of an item; kBlocks: blocks that take one together, 8 or 4 (a cluster) or 1,
+// whose warps have a share of K each.
+template <typename TX, typename TY, int kMT, int kBlocks>
 __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window) {
   constexpr int kR = 16 * kMT;                  // rows of an item
   constexpr int kMP = kMT == 1 || sizeof(TY) == 4 ? 1 : 2;  // row tiles at a time
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
   extern __shared__ __align__(16) unsigned char dyn[];
   Gather& sh = *reinterpret_cast<Gather*>(dyn);
-  const Sizes sz(kMT, kSolo, kParts, a.rank);
+  constexpr bool kSolo = kBlocks == 1;
+  const Sizes sz(kMT, kBlocks, kParts, a.rank);
   unsigned char* const low = dyn + (sizeof(Gather) + 15) / 16 * 16;
   float* const sums = reinterpret_cast<float*>(low + sz.low);
   cg::cluster_group cluster = cg::this_cluster();
-  static_assert(kW == kC, "a warp a share of K");
-  constexpr int kBlocks = kSolo ? 1 : kC;  // of an item
+  static_assert(kW == kShares, "a warp a share of K");
   const int c = kSolo ? 0 : (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, g = lane >> 2, tig = lane & 3;
   // the other blocks' shared memory can be written once they have started
@@ -284,12 +285,14 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   const bool y_vec = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
                      (a.base_stride | a.out_stride) * sizeof(TY) % 16 == 0;
   if constexpr (!kSolo) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  // ---- this block's share of K (kSolo: this warp's), in blocks of 32
-  const int kbs = (a.K + 31) / 32;
-  const int share = kSolo ? warp : c;
-  const int kb0 = (int)((int64_t)kbs * share / kC), kb1 = (int)((int64_t)kbs * (share + 1) / kC);
+  // ---- K, in blocks of 32: eight shares of eight pieces each
+  constexpr int kOwn = kSolo ? 1 : kShares / kBlocks;  // shares of a block (kSolo: of a warp)
+  const int kbs = (a.K + 31) / 32, share0 = kSolo ? warp : c * kOwn;
   const int tiles = a.rank / 8, rblocks = (a.rank + 31) / 32;
-  auto piece = [&](int s) { return kb0 + (kb1 - kb0) * s / kW; };  // the s-th of eight starts here
+  auto piece = [&](int q, int s) {  // the s-th of own share q starts here
+    const int kb0 = (int)((int64_t)kbs * (share0 + q) / kShares), kb1 = (int)((int64_t)kbs * (share0 + q + 1) / kShares);
+    return kb0 + (kb1 - kb0) * s / kW;
+  };
 
   for (int item = item0; item < items; item += per_window) {
     __syncthreads();  // also: sh.lead
@@ -341,35 +344,41 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
                 for (int j = 0; j < 4; ++j) mma_half(d[m][j], lo[m].p[i / 2], hi[m].p[i / 2], w[j], i % 2);
           }
         };
-        float d[kMT][4][4] = {};
+        float d[kOwn][kMT][4][4] = {};
         if constexpr (kSolo) {  // the warp's share, piece by piece
-          product(piece(0), piece(1), d);
+          product(piece(0, 0), piece(0, 1), d[0]);
           for (int p = 1; p < kW; ++p) {
             float e[kMT][4][4] = {};
-            product(piece(p), piece(p + 1), e);
+            product(piece(0, p), piece(0, p + 1), e);
 #pragma unroll
             for (int m = 0; m < kMT; ++m)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) d[m][j][q] += e[m][j][q];
+                for (int q = 0; q < 4; ++q) d[0][m][j][q] += e[m][j][q];
           }
-        } else {  // the warp's piece of the block's share
-          product(piece(warp), piece(warp + 1), d);
+        } else {  // the warp's piece of the block's shares
+#pragma unroll
+          for (int q = 0; q < kOwn; ++q) product(piece(q, warp), piece(q, warp + 1), d[q]);
         }
 #pragma unroll
-        for (int m = 0; m < kMT; ++m)
+        for (int q = 0; q < kOwn; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (nt0 + j < tiles) put(sums + warp * tile, m, nt0 + j, d[m][j]);
+          for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (nt0 + j < tiles) put(sums + (q * kW + warp) * tile, m, nt0 + j, d[q][m][j]);
       }
       __syncthreads();
       if constexpr (!kSolo) {
-        for (int i = tid; i < tile; i += kT) {
-          float s = sums[i];
+        for (int i = tid; i < kOwn * tile; i += kT) {
+          const int q = kOwn == 1 ? 0 : i / tile, at = i - q * tile;
+          const float* const p = sums + q * kW * tile + at;
+          float s = p[0];
 #pragma unroll
-          for (int w = 1; w < kW; ++w) s += sums[w * tile + i];
-          for (int r = 0; r < kC; ++r) *cluster.map_shared_rank(sums + (kW + c) * tile + i, r) = s;
+          for (int w = 1; w < kW; ++w) s += p[w * tile];
+          for (int r = 0; r < kBlocks; ++r)
+            *cluster.map_shared_rank(sums + (kOwn * kW + share0 + q) * tile + at, r) = s;
         }
         cluster.sync();
       }
@@ -378,10 +387,10 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         const int m = i / (32 * rblocks), r = i - m * 32 * rblocks;
         float v = 0.0f;
         if (r < a.rank) {
-          const float* p = sums + (kSolo ? 0 : kW) * tile + m * a.rank + r;
+          const float* p = sums + (kSolo ? 0 : kOwn * kW) * tile + m * a.rank + r;
           v = p[0];
 #pragma unroll
-          for (int b = 1; b < kC; ++b) v += p[b * tile];
+          for (int b = 1; b < kShares; ++b) v += p[b * tile];
           v *= scale;
         }
         __nv_bfloat16 u[kParts];
@@ -527,43 +536,50 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
   }
 }
 
-template <typename TX, typename TY, int kMT, bool kSolo>
-Launched launch_t(const LoraArgs& a, int per_window, cudaStream_t s) {
+template <typename TX, typename TY, int kMT, int kBlocks>
+Launched launch_t(const LoraArgs& a, int64_t per_window, cudaStream_t s) {
   constexpr int kParts = sizeof(TY) == 4 ? 3 : 2;
-  auto kernel = k_lora<TX, TY, kMT, kSolo>;
+  auto kernel = k_lora<TX, TY, kMT, kBlocks>;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(kernel, (int)Sizes(kMT, kSolo, kParts, 128).bytes, done);
+  l.error = allow_smem(kernel, (int)Sizes(kMT, kBlocks, kParts, 128).bytes, done);
   if (l.error != cudaSuccess) return l;
-  const int64_t blocks = (a.n + kWindow - 1) / (int64_t)kWindow * per_window * (kSolo ? 1 : kC);
-  const size_t smem = (size_t)Sizes(kMT, kSolo, kParts, a.rank).bytes;
-  if constexpr (kSolo) l.add(launch_k(kernel, dim3((unsigned)blocks), kT, smem, s, a, per_window));
-  else l.add(launch_k_cluster(kernel, dim3((unsigned)blocks), kT, smem, s, kC, a, per_window));
+  const int per = (int)std::min<int64_t>(std::min(a.n, kWindow), std::max<int64_t>(1, per_window));
+  const dim3 grid((unsigned)((a.n + (int64_t)kWindow - 1) / kWindow * per * kBlocks));
+  const size_t smem = (size_t)Sizes(kMT, kBlocks, kParts, a.rank).bytes;
+  if constexpr (kBlocks == 1) l.add(launch_k(kernel, grid, kT, smem, s, a, per));
+  else l.add(launch_k_cluster(kernel, grid, kT, smem, s, kBlocks, a, per));
   return l;
 }
-// Which blocks take an item, from how long it would take at most, as the adapters' mix is not
-// known here: a window of 256 rows has up to n_adapters items and one more for every 16
-// rows. A block alone takes 6 us and `alone`, a cluster 4 us and an eighth of it; 2 blocks an SM
-// run at a time. Measured, us, a block alone | a cluster (rows, adapters, rank, K, N):
-//   256, 8, 16, 4096, 4096: 22 | 8.5     256, 64, 16, 4096, 4096: 27 | 16
-//   256, 200, 16, 576, 960: 10 | 29      1000, 8, 64, 4096, 14336: 91 | 57
-//   1000, 64, 16, 4096, 4096: 32 | 60    2500, 8, 64, 4096, 14336: 97 | 118
+
+// How many blocks take an item, from how long it would take at most, as the adapters' mix is
+// not known here: a window of 256 rows has up to n_adapters items and one more for every 16
+// rows. A block by itself takes 6 us and `alone`, four together 4.7 us and a quarter of it, eight
+// 4 us and an eighth; 2 blocks an SM run at a time. Measured, us, by 1 | 4 | 8 blocks (rows,
+// adapters, rank, K, N):
+//   30, 8, 64, 4096, 14336: 59 | 22 | 17      100, 64, 16, 4096, 4096: 21 | 12 | 15
+//   100, 200, 16, 576, 960: 8.4 | 13 | 19     256, 8, 16, 4096, 4096: 22 | 11 | 8.2
+//   256, 64, 16, 4096, 4096: 27 | 13 | 17     256, 200, 16, 576, 960: 10 | 14 | 29
+//   1000, 8, 64, 4096, 14336: 92 | 55 | 57    1000, 64, 16, 4096, 4096: 31 | 46 | 56
+//   2500, 8, 64, 4096, 14336: 96 | 99 | 119   8192, 64, 16, 4096, 4096: 133 | 161 | 208
 // Two row tiles an item where adapters have 256 rows and more (8192 rows, two | one):
 //   8, 16, 4096, 4096: 52 | 65    8, 64, 4096, 14336: 161 | 190    64, 16, 4096, 4096: 142 | 132
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
-  const int64_t windows = (a.n + kWindow - 1) / kWindow;
+  const int64_t windows = (a.n + (int64_t)kWindow - 1) / kWindow;
   const int64_t items = std::min<int64_t>(a.n, windows * std::min<int64_t>(kWindow, (int64_t)a.n_adapters + kWindow / 16));
   const double alone = a.N / 256.0 * (0.5 + 0.007 * a.rank) + a.K / 1024.0;
-  const int64_t clusters = std::max(1, 2 * sms / kC), blocks = 2 * (int64_t)sms;
-  const double by_clusters = (double)((items + clusters - 1) / clusters) * (4 + alone / 8);
-  const double by_blocks = (double)((items + blocks - 1) / blocks) * (6 + alone);
-  if (by_clusters <= by_blocks)
-    return launch_t<TX, TY, 1, false>(a, (int)std::min<int64_t>(std::min(a.n, kWindow), std::max<int64_t>(1, clusters / windows)), s);
-  // blocks a window: four an SM's worth, at least eight
-  const int each = (int)std::min<int64_t>(kWindow, std::max<int64_t>(8, 4 * (int64_t)sms / windows));
-  if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, true>(a, each, s);
-  return launch_t<TX, TY, 1, true>(a, each, s);
+  auto estimate = [&](int blocks, double start) {
+    const int64_t at_once = std::max(1, 2 * sms / blocks);
+    return (double)((items + at_once - 1) / at_once) * (start + alone / blocks);
+  };
+  const double by_8 = estimate(8, 4), by_4 = estimate(4, 4.7), by_1 = estimate(1, 6);
+  if (by_8 <= by_4 && by_8 <= by_1) return launch_t<TX, TY, 1, 8>(a, 2 * sms / 8 / windows, s);
+  if (by_4 <= by_1) return launch_t<TX, TY, 1, 4>(a, 2 * sms / 4 / windows, s);
+  // four blocks an SM in all, at least eight a window
+  const int64_t each = std::max<int64_t>(8, 4 * sms / windows);
+  if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, 1>(a, each, s);
+  return launch_t<TX, TY, 1, 1>(a, each, s);
 }
 
 }  // namespace

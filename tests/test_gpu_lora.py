@@ -150,6 +150,22 @@ def test_a_rows_bits_are_the_same_in_batches_of_two_tiles(xb, yb, rank):
         assert torch.equal(run(d), whole[order])
 
 
+@pytest.mark.parametrize("xb,yb", [(True, False), (False, True)])
+def test_a_rows_bits_are_the_same_however_many_blocks_take_it(xb, yb):
+    """300 adapters of one row each (a block an item), 64 (four blocks), three (eight), with K
+    that the shares and pieces do not divide."""
+    import torch
+    rng = np.random.default_rng(21)
+    for rank, K, N in ((16, 1096, 333), (104, 328, 1001), (8, 8, 5)):
+        c = make(rng, 300, K, N, 300, rank, xb, yb, rng.permutation(300))
+        whole = run(c)
+        check(c, whole)
+        for n in (1, 3, 40, 64, 76):
+            order = rng.permutation(300)[:n]
+            d = dict(c, x=c["x"][order].contiguous(), adapter=c["adapter"][order].contiguous(), base=c["base"][order].contiguous())
+            assert torch.equal(run(d), whole[order]), (rank, n)
+
+
 def test_what_is_no_number_stays_in_its_row():
     import torch
     rng = np.random.default_rng(10)
