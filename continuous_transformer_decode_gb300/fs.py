@@ -542,6 +542,7 @@ def fs_gemm_bf16_noalloc(W, X, Y, splits: int = 1, stream=None) -> None:
 class _Types:
     """torch and its types, once torch is there (this module does not import it)."""
     torch = f32 = bf16 = i32 = i64 = u8 = None
+    rows = {}  # of rows: FS_DTYPE
 
 
 def _types():
@@ -551,6 +552,7 @@ def _types():
         _Types.bf16, _Types.i32, _Types.u8 = torch.bfloat16, torch.int32, torch.uint8
         _Types.i64 = torch.int64
         _Types.f32 = torch.float32
+        _Types.rows = {torch.float32: FS_DTYPE_F32, torch.bfloat16: FS_DTYPE_BF16}
     return _Types
 
 
@@ -568,9 +570,10 @@ def _raw(stream, x):
     torch's own calls take it."""
     if stream is not None:
         return getattr(stream, "cuda_stream", stream)
-    if not x.is_cuda:  # refused by the C call
+    device = x.get_device()
+    if device < 0:  # host memory, refused by the C call
         return None
-    return _types().torch._C._cuda_getCurrentRawStream(x.get_device())
+    return _types().torch._C._cuda_getCurrentRawStream(device)
 
 
 def _vec(x, n: int, dtype, what: str):
@@ -583,8 +586,10 @@ def _vec(x, n: int, dtype, what: str):
 
 def _rows(x, n: int, heads: int, hd: int, what: str):
     """(address, row stride, dtype) of n rows [heads, hd], each contiguous."""
-    dt = FS_DTYPE_F32 if x.dtype is _Types.f32 else FS_DTYPE_BF16
-    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.shape == (n, heads, hd):
+    dt = _Types.rows.get(x.dtype)
+    if dt is not None and x.shape == (n, heads, hd):
+        if x.is_contiguous():
+            return x.data_ptr(), heads * hd, dt
         s0, s1, s2 = x.stride()
         if n == 0 or (s2 == 1 and (heads == 1 or s1 == hd)):
             return x.data_ptr(), s0 if n > 1 else heads * hd, dt
@@ -751,13 +756,16 @@ def fs_pages_update(holders, page_table, lengths, grow, page_size: int, status, 
     row_length int32 and row_slot int64 [max_rows], each or None. max_rows: the rows'
     length where none of the four is given."""
     ty = _types()
-    if page_table.dim() != 2:
+    shape = page_table.shape
+    if len(shape) != 2:
         _refuse("the page table is [n_lanes, max_pages]")
-    n, wide = page_table.shape
+    n, wide = shape
     if row_start is None:
         _refuse(f"row_start: a contiguous CUDA tensor of {n + 1} values is needed")
-    rows = [t.numel() for t in (row_lane, row_position, row_length, row_slot) if t is not None]
-    m = max_rows if max_rows is not None else rows[0] if rows else 0
+    m = max_rows
+    if m is None:
+        rows = [t for t in (row_lane, row_position, row_length, row_slot) if t is not None]
+        m = rows[0].numel() if rows else 0
     n_pages = holders.numel()
     _op_check(lib().fs_pages_update(
         _vec(holders, n_pages, ty.i32, "holders"), n_pages,
@@ -797,17 +805,6 @@ def fs_rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: dict |
     return f, m.value
 
 
-def _host_f64(x):
-    """(array, address) of a vector of f64 in host memory."""
-    f = np.ascontiguousarray(x, np.float64)
-    if f.ndim != 1:
-        _refuse("inv_freq: a vector of f64 is needed")
-    try:
-        return f, C.addressof(C.c_char.from_buffer(f))  # a fifth of the time of .ctypes.data
-    except (TypeError, ValueError):  # read-only or empty
-        return f, f.ctypes.data
-
-
 def fs_rope(q, positions, inv_freq, k=None, q_out=None, k_out=None, interleaved: bool = False,
             factor: float = 1.0, inverse: bool = False, stream=None) -> None:
     """Turns the first 2 * len(inv_freq) values of each head of q [n, H, hd] and k
@@ -816,32 +813,38 @@ def fs_rope(q, positions, inv_freq, k=None, q_out=None, k_out=None, interleaved:
     host array of f64). Without q_out / k_out in place."""
     ty = _types()
     n = positions.numel()
-    if q.dim() != 3 or (k is not None and k.dim() != 3):
+    shape, k_shape = q.shape, (0, 0, 0) if k is None else k.shape
+    if len(shape) != 3 or len(k_shape) != 3:
         _refuse("q and k are [n, heads, head_dim]")
-    H, hd = q.shape[1:]
+    _, H, hd = shape
     qp, qs, dt = _rows(q, n, H, hd, "q")
     op, os_, do = (qp, qs, dt) if q_out is None else _rows(q_out, n, H, hd, "q_out")
     kp, ks, dk, Hkv, okp, oks, dko = None, 0, dt, 0, None, 0, dt
     if k is not None:
-        Hkv = k.shape[1]
+        Hkv = k_shape[1]
         kp, ks, dk = _rows(k, n, Hkv, hd, "k")
         okp, oks, dko = (kp, ks, dk) if k_out is None else _rows(k_out, n, Hkv, hd, "k_out")
     elif k_out is not None:
         _refuse("k_out without k")
     if not dt == do == dk == dko:
         _refuse("q, k and their outputs have different types")
-    f, fp = _host_f64(inv_freq)
+    f = np.asarray(inv_freq, np.float64)
+    if f.ndim != 1:
+        _refuse("inv_freq: a vector of f64 is needed")
     _op_check(lib().fs_rope(qp, qs, H, kp, ks, Hkv, n, hd, dt, _vec(positions, n, ty.i32, "positions"),
-                            fp, 2 * f.size, factor, bool(interleaved) | bool(inverse) << 1,
+                            f.tobytes(), 2 * f.size, factor, bool(interleaved) | bool(inverse) << 1,
                             op, os_, okp, oks, _raw(stream, positions)))
 
 
 def _panel(x, n: int, width: int, what: str):
     """(address, row stride, dtype) of n contiguous rows of `width` f32 or bf16 values."""
-    dt = FS_DTYPE_F32 if x.dtype is _Types.f32 else FS_DTYPE_BF16
-    if (dt == FS_DTYPE_F32 or x.dtype is _Types.bf16) and x.shape == (n, width) and (
-            width == 1 or n == 0 or x.stride(1) == 1):
-        return x.data_ptr(), x.stride(0) if n > 1 else width, dt
+    dt = _Types.rows.get(x.dtype)
+    if dt is not None and x.shape == (n, width):
+        if x.is_contiguous():
+            return x.data_ptr(), width, dt
+        s0, s1 = x.stride()
+        if width == 1 or s1 == 1:
+            return x.data_ptr(), s0 if n > 1 else width, dt
     _refuse(f"{what}: a CUDA tensor [{n}, {width}] of f32 or bf16 whose rows are contiguous is needed")
 
 
@@ -851,10 +854,11 @@ def fs_lora_add(x, adapter, A, B, scale, out, base=None, stream=None) -> None:
     any row stride; base may be out, None is 0), A bf16 [adapters, rank, K], B bf16
     [adapters, N, rank], contiguous, scale f32 [adapters]. All CUDA tensors."""
     ty = _types()
-    if A.dim() != 3 or B.dim() != 3:
+    a, b = A.shape, B.shape
+    if len(a) != 3 or len(b) != 3:
         _refuse("A is [adapters, rank, K], B [adapters, N, rank]")
-    n, (ad, r, K), N = adapter.numel(), A.shape, B.shape[1]
-    if B.shape != (ad, N, r):
+    n, (ad, r, K), N = adapter.numel(), a, b[1]
+    if b != (ad, N, r):
         _refuse(f"B: [{ad}, N, {r}] is needed")
     xp, xs, dx = _panel(x, n, K, "x")
     op, os_, do = _panel(out, n, N, "out")
@@ -875,13 +879,17 @@ def fs_sample_filtered(logits, temps, u, tokens, top_k=None, top_p=None, min_p=N
     stayed) if given. top_k, top_p, min_p: None for all tokens. All CUDA tensors."""
     ty = _types()
     n = temps.numel()
-    if logits.dim() != 2 or logits.dtype is not ty.f32 or logits.shape[0] != n:
+    shape = logits.shape
+    if len(shape) != 2 or logits.dtype is not ty.f32 or shape[0] != n:
         _refuse(f"logits: a CUDA tensor [{n}, vocab] of f32 is needed")
-    V = logits.shape[1]
-    if V > 1 and n and logits.stride(1) != 1:
-        _refuse("rows of logits must be contiguous")
+    V = ld = shape[1]
+    if not logits.is_contiguous():
+        s0, s1 = logits.stride()
+        if V > 1 and s1 != 1:
+            _refuse("rows of logits must be contiguous")
+        ld = s0 if n > 1 else V
     _op_check(lib().fs_sample_filtered(
-        logits.data_ptr(), logits.stride(0) if n > 1 else V, n, V, _vec(temps, n, ty.f32, "temps"),
+        logits.data_ptr(), ld, n, V, _vec(temps, n, ty.f32, "temps"),
         _or_none(top_k, n, ty.i32, "top_k"), _or_none(top_p, n, ty.f32, "top_p"),
         _or_none(min_p, n, ty.f32, "min_p"), _vec(u, n, ty.f32, "u"),
         _vec(tokens, n, ty.i32, "tokens"), _or_none(kept, n, ty.i32, "kept"), _raw(stream, temps)))
