@@ -12,24 +12,26 @@
 // 2^-38, and their sums do not depend on the order; sums of bins, and a draw's running sums,
 // are pairs of f32 numbers. (f64 runs at 1/60 of f32's rate here.)
 //
-// One thread-block cluster serves a row and reads it once, into shared memory. A thread has
-// a run of consecutive tokens and a column of the bins' counts and masses for itself (no
-// atomics). What the draw needs, the kept mass of each run in order, is then the sum of a
-// column's bins ahead of the cut; only the tokens of the cut's own bin are weighed again.
-// They are gathered first (a tenth of the tokens, in lanes of their own), as the split and
-// the ranking want them as well. Where the tokens up to the cut are few, as with a small
-// top_k or a peaked row, they go to one block as a whole, which does the rest; a small top_k
-// asks for no weights but theirs.
+// A block or a cluster of two, four or eight serves a row and reads it once, into shared memory
+// (the choice and its times are at launch_sample_filtered). A thread has a run of consecutive
+// tokens and a column of the bins' counts and masses for itself (no atomics). What the draw
+// needs, the kept mass of each run in order, is then the sum of a column's bins ahead of the
+// cut; only the tokens of the cut's own bin are weighed again. They are gathered first (a tenth
+// of the tokens, in lanes of their own), as the split and the ranking want them as well. Where
+// the tokens up to the cut are few, as with a small top_k or a peaked row, they go to one block
+// as a whole, which does the rest; a small top_k asks for no weights but theirs. Where min-p
+// certainly ends ahead of the cut's bin, the cut is not looked for.
 //
 // The logits' bytes are a few percent of the time (256 rows of 49152: 7 us at the copy's rate).
-// A row's chain bounds it: of 55 thousand cycles a block of four takes (256 rows, two blocks an
-// SM by their shared memory, top-p: 107 to 140 us by the inputs), 14 go to the weights of its 12288
-// tokens, which are bound by issue (66 instructions each), 6 to the loads, 11 to five barriers
-// of the cluster and what they wait for, the rest to choosing, gathering and ranking. 64 mixed
-// rows: 34 us; one row of 32000 with top-k 50 and top-p: 10 us.
+// A row's chain bounds it, and the issue slots, half of them used: 256 rows with top-p take
+// four waves of two blocks a row, 102 us, 47 of them the issue of 56 million instructions (66 for
+// each token's weight); the rest is what 16 warps an SM wait for, barriers, shared memory and
+// each other. 64 mixed rows: 32 us; one row of 32000 with top-k 50 and top-p: 10 us.
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "draw.cuh"
@@ -122,9 +124,10 @@ __device__ __forceinline__ int steps_of(float t) { return __float_as_int(t) - __
 __device__ __forceinline__ int place(float z, float M, Two c) {
   return steps_of(to_grid(__fmul_rn(__fadd_rn(z, -M), c.h)));
 }
-__device__ __forceinline__ int bin_of(int k) { return min(kBins - 1, -(k >> 8)); }
+// The bin, of those from y = off on: below 0 for what lies ahead of them.
+__device__ __forceinline__ int bin_of(int k, int off) { return min(kBins - 1, -(k >> 8) - off); }
 // Of kSub parts of a bin, the last one apart.
-__device__ __forceinline__ int part_of(int k, int bin) { return (255 - k - 256 * bin) >> 2; }
+__device__ __forceinline__ int part_of(int k, int y) { return (255 - k - 256 * y) >> 2; }
 static_assert(kSub == 64, "four of 256 steps");
 
 // exp((z - M) / T) = m 2^(n - kFrac), 2^kFrac <= m <= 2^(kFrac + 1); c = log2(e) / T. With y
@@ -157,12 +160,18 @@ __device__ __forceinline__ uint64_t weigh(float z, float M, Two c, const Power* 
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kAll, v, 0); }
 __device__ __forceinline__ float uniform(float v) { return __shfl_sync(kAll, v, 0); }
 
+// Tokens of a thread's run; odd, so that the threads of a warp read different banks.
+template <int kC, int kT>
+__host__ __device__ __forceinline__ int each_of(int V) {
+  return ((V + kC * kT - 1) / (kC * kT)) | 1;
+}
+
 // held: the row's parts fit the blocks' shared memory; else they are read again from global.
 template <int kC, int kT, bool held>
-__global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastDiv by_each) {
+__global__ void __launch_bounds__(kT, 512 / kT) k_sample_filtered(FilteredArgs a, FastDiv by_each) {
   constexpr int kW = kT / 32, kN = kC * kW;
   static_assert(kN <= 64, "two warps a lane");
-  static_assert(kT == 256, "a power of two of the table a thread");
+  static_assert(kT >= 256, "a power of two of the table a thread");
   __shared__ Shared<kC, kW> sh;
   extern __shared__ __align__(16) unsigned char dyn[];
   unsigned long long* const columns = reinterpret_cast<unsigned long long*>(dyn);  // [kBins][kT]
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // the other blocks' shared memory can be written once they have started
   if (tid == 0) sh.taken = 0;
   if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  {  // 2^(k/256) = 2^(k/8 / 32) 2^(k%8 / 256)
+  if (tid < 256) {  // 2^(k/256) = 2^(k/8 / 32) 2^(k%8 / 256)
     constexpr float2 kFine[8] = {
         {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.00b1b00000000p+0f, -0x1.6950d00000000p-26f},
         {0x1.0163da0000000p+0f, 0x1.3f66660000000p-25f}, {0x1.0216820000000p+0f, -0x1.789fb00000000p-25f},
@@ -202,37 +211,42 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   const float temp = uniform(a.temps[row]), u_row = a.u[row];
   const int top_k = uniform(a.top_k ? a.top_k[row] : 0);
   const float top_p = uniform(a.top_p ? a.top_p[row] : 1.0f), min_p = uniform(a.min_p ? a.min_p[row] : 0.0f);
-  // a thread's run; odd, so that the threads of a warp read different banks
-  const int each = ((V + kC * kT - 1) / (kC * kT)) | 1;
+  const int each = each_of<kC, kT>(V);
   const int base = (int)min((int64_t)V, (int64_t)rank * kT * each);
   const int count = (int)min((int64_t)V - base, (int64_t)kT * each);
   const int run = tid * each, hi = min(count, run + each);
   const float* const z_row = a.logits + row * a.ld + base;
   // ---- the row and its maximum
   float M = -CUDART_INF_F;
-  if ((reinterpret_cast<uintptr_t>(z_row) & 15) == 0) {
-#pragma unroll 8
-    for (int i = 4 * tid; i < count; i += 4 * kT) {
-      float4 v = load4(z_row, i, count, true);
-      v.x = clean(v.x), v.y = clean(v.y), v.z = clean(v.z), v.w = clean(v.w);
-      if (held) {
-        if (i + 4 <= count) *reinterpret_cast<float4*>(hold + i) = v;
-        else {
-          hold[i] = v.x;
-          if (i + 1 < count) hold[i + 1] = v.y;
-          if (i + 2 < count) hold[i + 2] = v.z;
-        }
+  // eight vectors asked for at once: the blocks of a wave start together, and wait for these
+  // (256 rows of 49152 from HBM, top-p: 100 us, 114 with a bound to check between them)
+  auto look = [&](auto n, auto one, int i0) {
+    constexpr int kOne = decltype(one)::value;  // tokens of a load
+    using Raw = std::conditional_t<kOne == 4, float4, float>;
+    Raw v[n];
+#pragma unroll
+    for (int q = 0; q < n; ++q) v[q] = *reinterpret_cast<const Raw*>(z_row + i0 + q * kOne * kT);
+#pragma unroll
+    for (int q = 0; q < n; ++q) {
+      if constexpr (kOne == 4) {
+        v[q].x = clean(v[q].x), v[q].y = clean(v[q].y), v[q].z = clean(v[q].z), v[q].w = clean(v[q].w);
+        M = fmaxf(M, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
+      } else {
+        v[q] = clean(v[q]);
+        M = fmaxf(M, v[q]);
       }
-      M = fmaxf(M, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+      if (held) *reinterpret_cast<Raw*>(hold + i0 + q * kOne * kT) = v[q];
     }
-  } else {
-#pragma unroll 8
-    for (int i = tid; i < count; i += kT) {
-      const float z = clean(z_row[i]);
-      if (held) hold[i] = z;
-      M = fmaxf(M, z);
-    }
-  }
+  };
+  auto look_from = [&](auto one, int from, int to) {  // to - from: whole loads
+    constexpr int kOne = decltype(one)::value;
+    int i = from + kOne * tid;
+    for (; i + 7 * kOne * kT < to; i += 8 * kOne * kT) look(std::integral_constant<int, 8>{}, one, i);
+    for (; i < to; i += kOne * kT) look(std::integral_constant<int, 1>{}, one, i);
+  };
+  const int vectors = (reinterpret_cast<uintptr_t>(z_row) & 15) == 0 ? count & ~3 : 0;
+  look_from(std::integral_constant<int, 4>{}, 0, vectors);
+  look_from(std::integral_constant<int, 1>{}, vectors, count);
   if (held)
     for (int i = count + tid; i < kT * each; i += kT) hold[i] = -CUDART_INF_F;
   M = warp_max(M);
@@ -263,21 +277,33 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     return;
   }
   const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
+  // min-p ends in y's bins m_first to m_last (of kNone bins)
+  constexpr int kNone = 1 << 20;
+  int m_first = kNone, m_last = kNone;
+  if (by_m) {
+    const float y = fminf(-lg2(min_p), 200.0f);  // bin b has y from b - 1 to b, 1/512 less or more
+    m_first = (int)floorf(y - 0.01f) + 1;
+    m_last = (int)(y + 1.02f);
+  }
 
-  // A weight as a whole number of 2^-(bin + kFrac): in the last bin what is left of it, and 1
-  // where nothing is, so that the first of them can be drawn (by u = 0). 2^20 such ones are
+  // The columns' bins are those from y = off on, of which a thread has ahead_sum (of 2^-54) and
+  // ahead_n in front.
+  int off = 0, ahead_n = 0;
+  uint64_t ahead_sum = 0;
+  // A weight as a whole number of 2^-(off + bin + kFrac): in the last bin what is left of it, and
+  // 1 where nothing is, so that the first of them can be drawn (by u = 0). 2^20 such ones are
   // 2^-38 of the sum.
-  auto mass_of = [&](float z, int& bin) {
+  auto mass_of = [&](float z, int from, int& bin) {
     int k;
     const uint64_t m = weigh(z, M, c, sh.tab, k);
-    const int b = -(k >> 8);
+    const int b = -(k >> 8) - from;
     bin = min(kBins - 1, b);
     const uint64_t left = m >> min(63, b - bin);
-    return left ? left : (uint64_t)(k > kLeast);
+    return k > kLeast ? left | (left == 0) : 0;
   };
   auto mass = [&](float z) {
     int bin;
-    return mass_of(z, bin);
+    return mass_of(z, off, bin);
   };
   auto weight = [&](float z) {  // times 2^60
     int k;
@@ -288,16 +314,19 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // Four tokens in step, without branches, so that their chains of dependent operations
   // overlap; for -inf, which also stands behind the row's end, nothing is added.
   const bool few = by_k && top_k <= kFew;  // no weights are wanted
-  auto count_bins = [&](auto weighed) {
+  auto count_bins = [&](auto weighed, auto all) {
+    const int from = decltype(all)::value ? 0 : off;
     auto step = [&](auto n, int j) {
       int b[n];
       unsigned long long m[n];
 #pragma unroll
       for (int q = 0; q < n; ++q) {
         const float z = at(run + j + q);
-        if constexpr (decltype(weighed)::value) m[q] = mass_of(z, b[q]);
-        else m[q] = 0, b[q] = bin_of(place(z, M, c));
-        m[q] = z > -CUDART_INF_F ? m[q] + (1ull << kCount) : 0;
+        if constexpr (decltype(weighed)::value) m[q] = mass_of(z, from, b[q]);
+        else m[q] = 0, b[q] = bin_of(place(z, M, c), from);
+        bool in = z > -CUDART_INF_F;
+        if constexpr (!decltype(all)::value) in = in && b[q] >= 0, b[q] = max(b[q], 0);
+        m[q] = in ? m[q] + (1ull << kCount) : 0;
       }
 #pragma unroll
       for (int q = 0; q < n; ++q) column[b[q] * kT] += m[q];
@@ -306,8 +335,18 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     for (; j + 4 <= each; j += 4) step(std::integral_constant<int, 4>{}, j);
     for (; j < each; ++j) step(std::integral_constant<int, 1>{}, j);
   };
-  if (few) count_bins(std::false_type{});
-  else count_bins(std::true_type{});
+  if (few) count_bins(std::false_type{}, std::true_type{});
+  else count_bins(std::true_type{}, std::true_type{});
+  // a thread's mass (of 2^-54) and count in bins up to `to`
+  auto add_bins = [&](int to, uint64_t& sum, int& n) {
+#pragma unroll
+    for (int b = 0; b < kBins; ++b) {
+      const uint64_t v = b <= to ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
+      n += (int)(v >> kCount);
+      const int s = 54 - kFrac - b - off;
+      sum += s >= 0 ? m << s : (m + (1ull << min(-s, 62)) - 1) >> min(-s, 62);  // rounded up: none is lost
+    }
+  };
   // The tokens of a bin, each warp's own; f(z, i) for each of them, every lane another.
   // Their places lie in the warp's columns of the bins behind, which no one wants any more,
   // 128 a bin; a warp that has more of them, or whose row is not held, looks at its runs.
@@ -323,7 +362,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
     __syncwarp();
     const int room = (kBins - 1 - bin) * 128;
     // the bin's places, on the grid: from the last token's to the first's
-    const float t0 = bin < kBins - 1 ? kRound - (float)bin : 0.0f, t1 = kRound - (float)bin + 255.0f / 256.0f;
+    const float t0 = bin < kBins - 1 ? kRound - (float)(off + bin) : 0.0f, t1 = kRound - (float)(off + bin) + 255.0f / 256.0f;
     int n = 0;
     for (int j0 = 0; j0 < each; j0 += 32) {  // 32 tokens of each lane: which, how many, where to
       unsigned in = 0;
@@ -379,38 +418,59 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         for (int q = 0; q < 4; ++q) {
           i[q] = min(j + q, hi - 1);
           z[q] = at(i[q]);
-          in[q] = j + q < hi && z[q] > -CUDART_INF_F && bin_of(place(z[q], M, c)) == members_of;
+          in[q] = j + q < hi && z[q] > -CUDART_INF_F && bin_of(place(z[q], M, c), off) == members_of;
         }
         f(z, i, in);
       }
     }
   };
-  int cut_bin = kBins;               // all bins ahead of it stay whole
+  int cut_bin = kNone;               // of y's: all ahead of it stay whole
   uint64_t cut = ~0ull;              // the last rank that stays
   const Two least = {min_p * kUp, 0.0f};
   if (by_k || by_p) {
-    __syncthreads();
-    for (int b = warp; b < kBins; b += kW) {
-      unsigned long long m = 0;
-      uint32_t n = 0;
-#pragma unroll
-      for (int j = 0; j < kT; j += 32) {
-        const unsigned long long v = columns[b * kT + j + lane];
-        n += (uint32_t)(v >> kCount);
-        m += v & ((1ull << kCount) - 1);
+    auto exchange = [&] {  // the bins' counts and masses, to every block
+      for (int b = warp; b < kBins; b += kW) {
+        unsigned long long m = 0;
+        uint32_t n = 0;
+  #pragma unroll
+        for (int j = 0; j < kT; j += 32) {
+          const unsigned long long v = columns[b * kT + j + lane];
+          n += (uint32_t)(v >> kCount);
+          m += v & ((1ull << kCount) - 1);
+        }
+        constexpr uint32_t kLimb = (1u << 24) - 1;
+        const unsigned long long sum = (unsigned long long)__reduce_add_sync(kAll, (uint32_t)m & kLimb) +
+                                       ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 24) & kLimb) << 24) +
+                                       ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 48)) << 48);
+        n = __reduce_add_sync(kAll, n);
+        if (lane < kC) *remote(&sh.bins[rank][b], lane) = Bin{sum, n, 0};
       }
-      constexpr uint32_t kLimb = (1u << 24) - 1;
-      const unsigned long long sum = (unsigned long long)__reduce_add_sync(kAll, (uint32_t)m & kLimb) +
-                                     ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 24) & kLimb) << 24) +
-                                     ((unsigned long long)__reduce_add_sync(kAll, (uint32_t)(m >> 48)) << 48);
-      n = __reduce_add_sync(kAll, n);
-      if (lane < kC) *remote(&sh.bins[rank][b], lane) = Bin{sum, n, 0};
-    }
-    sync();
+      sync();
+    };
+    __syncthreads();
+    exchange();
+    // The columns with the bins from y = to on, 0 or a later one. The tokens of a cut far out
+    // (the tail of a peaked row) are in the last bin, with most others, or have no room behind
+    // theirs: another count takes less time than walks through all tokens (64 rows of 49152, T =
+    // 0.6, top-p 0.998: 38 us, 127 by walks).
+    auto move = [&](int to) {
+      if (to == 0) ahead_sum = 0, ahead_n = 0;
+      else add_bins(to - off - 1, ahead_sum, ahead_n);
+      off = to;
+      members_of = -1;
+      __syncwarp();
+#pragma unroll
+      for (int b = 0; b < kBins; ++b) column[b * kT] = 0;
+      if (few) count_bins(std::false_type{}, std::false_type{});
+      else count_bins(std::true_type{}, std::false_type{});
+      sync();  // also: the last bins have been read
+      exchange();
+    };
     // Looks for the first rank whose running count reaches `need` (by_count) or whose running
     // mass reaches `goal` (times 2^60). False: it is `cut`, and the running mass is `upto`.
     // True: it is among the first `upto_n` ranks, which are in block 0's list `which`.
     auto find = [&](bool by_count, uint32_t need, Two goal, int which, Two& upto, int& upto_n) {
+      upto = {0.0f, 0.0f};
       uint32_t ahead = 0, left = 0;
       Two before = {0.0f, 0.0f};
       // of parts' counts and masses (of `n` parts, the blocks' `apart`), the one with the
@@ -426,7 +486,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
             if (i < parts_n)
 #pragma unroll
               for (int r = 0; r < kC; ++r) n[q] += parts[r * apart + i].count, sum += parts[r * apart + i].mass;
-            m[q] = to_two(sum, 60 - kFrac - (unit < 0 ? min(i, kBins - 1) : unit));
+            m[q] = to_two(sum, 60 - kFrac - off - (unit < 0 ? min(i, kBins - 1) : unit));
           }
           uint32_t n_in = n[0] + n[1];
 #pragma unroll
@@ -454,7 +514,17 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
         ahead = (uint32_t)uniform((int)sh.found.ahead), left = (uint32_t)uniform((int)sh.found.left);
         return uniform(sh.found.at);
       };
-      const int bin = choose(&sh.bins[0][0], kBins, kBins, -1);
+      // a list, and top-p's sum, want the cut wherever it is, and no columns
+      const bool cut_only = few || (by_count && by_p);
+      int bin, next = off ? 0 : -1;  // top-k's cut was far out
+      for (;;) {
+        if (next >= 0) move(next);
+        bin = choose(&sh.bins[0][0], kBins, kBins, -1);
+        if (!cut_only && m_last < off + bin) return false;  // min-p ends ahead of it
+        const bool fits = left <= (uint32_t)((kBins - 1 - bin) * 112 * kN);  // 7/8 of the warps' room
+        if (fits || bin == 0 || off + bin > 126 || (!cut_only && m_first < off + bin)) break;
+        next = off + bin;
+      }
       int part = -1;
       uint64_t from = 0, to = ~0ull;
       auto each_left = [&](auto f) {  // f(z[4], rank[4], in[4])
@@ -464,7 +534,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             r[q] = rank_of(z[q], base + i[q]);
-            in[q] = in[q] && (part < 0 || part_of(place(z[q], M, c), bin) == part) && from <= r[q] && r[q] <= to;
+            in[q] = in[q] && (part < 0 || part_of(place(z[q], M, c), off + bin) == part) && from <= r[q] && r[q] <= to;
           }
           f(z, r, in);
         });
@@ -510,7 +580,7 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (in[q]) {
-              const int p = by_y ? part_of(place(z[q], M, c), bin) : (int)((r[q] - from) >> shift);
+              const int p = by_y ? part_of(place(z[q], M, c), off + bin) : (int)((r[q] - from) >> shift);
               if (!few) {
                 atomicAdd(&sh.own[0][p], (uint32_t)m[q] & 0x1fff);
                 atomicAdd(&sh.own[1][p], (uint32_t)(m[q] >> 13) & 0x1fff);
@@ -539,10 +609,10 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       if (ahead + left <= kList) {  // all ranks up to the part's last, to block 0
         for (int i = run; i < hi; ++i) {
           const float z = at(i);
-          const int k = place(z, M, c), b = bin_of(k);
+          const int k = place(z, M, c), b = bin_of(k, off);
           if (!(z > -CUDART_INF_F) || b > bin) continue;
           const uint64_t r = rank_of(z, base + i);
-          if (b == bin && ((part >= 0 && part_of(k, bin) > part) || r > to)) continue;
+          if (b == bin && ((part >= 0 && part_of(k, off + bin) > part) || r > to)) continue;
           *remote(&sh.list[which][atomicAdd(remote(&sh.taken, 0), 1)], 0) = r;
         }
         upto_n = (int)(ahead + left);
@@ -587,16 +657,12 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
       static_assert(kW > kList / 32, "a place of the sums' for the answer");
       __syncthreads();
       upto = sh.scan[kW - 1];
-      cut_bin = min(cut_bin, bin);
+      cut_bin = min(cut_bin, off + bin);
       cut = min(cut, sh.sorted[uniform(min(sh.hit, n - 1))]);
       return false;
     };
     Two sum = {0.0f, 0.0f};
-    int first_n = 0, which = 0;
-    bool listed = false, k_in = false;  // the first ranks are in a list; top-k's end too
-    if (by_k) {
-      listed = k_in = find(true, (uint32_t)top_k, {0.0f, 0.0f}, 0, sum, first_n);
-    } else {
+    if (!by_k) {
       uint64_t m = 0;
       if (lane < kBins)
         for (int r = 0; r < kC; ++r) m += sh.bins[r][lane].mass;
@@ -604,11 +670,15 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum = add(sum, shfl_xor(sum, o));
     }
-    if (by_p && !listed) {
-      __syncthreads();  // sh.hit and sh.scan have been read
-      which = 1;
-      Two unused;
-      listed = find(false, 0, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), 1, unused, first_n);
+    int first_n = 0, which = 0;
+    bool listed = false, k_in = false;  // the first ranks are in a list; top-k's end too
+#pragma unroll 1  // one copy of the search
+    for (int p = by_k ? 0 : 1; p < (by_p ? 2 : 1) && !listed; ++p) {
+      if (p) __syncthreads();  // sh.hit and sh.scan have been read
+      which = p;
+      Two upto;
+      listed = find(!p, (uint32_t)top_k, mul({fmaxf(top_p, 0.0f), 0.0f}, sum), p, upto, first_n);
+      if (!p) sum = upto, k_in = listed;
     }
     if (listed) {
       // ---- everything else in one block: a thread a rank, then a thread an index
@@ -680,14 +750,9 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   }
   // ---- bins that stay whole, and those that are looked at token by token: the cut's, and
   // the one or two where min-p may end
-  int whole = cut_bin, last = cut_bin;
-  if (by_m) {
-    const float y = fminf(-lg2(min_p), 200.0f);  // bin b has y from b - 1 to b, 1/512 less or more
-    whole = min(whole, (int)floorf(y - 0.01f) + 1);
-    last = min(last, (int)(y + 1.02f));
-    if (whole >= kBins - 1) whole = min(cut_bin, kBins - 1);
-  }
-  last = min(last, kBins - 1);
+  int whole = min(cut_bin, m_first) - off;
+  if (by_m || cut_bin < kNone) whole = min(whole, kBins - 1);
+  const int last = min(min(cut_bin, m_last) - off, kBins - 1);
   auto stays = [&](float z, int i) { return rank_of(z, base + i) <= cut && (!by_m || !less(weight(z), least)); };
   for (int b = whole; b <= last; ++b) {
     gather(b);
@@ -708,14 +773,9 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   // ---- kept mass and count of the runs
   Kept mine = {{0.0f, 0.0f}, 0};
   {
-    uint64_t sum = 0;  // of 2^-54
-#pragma unroll
-    for (int b = 0; b < kBins; ++b) {
-      const uint64_t v = b <= last ? column[b * kT] : 0, m = v & ((1ull << kCount) - 1);
-      mine.count += (int)(v >> kCount);
-      const int s = 54 - kFrac - b;
-      sum += s >= 0 ? m << (s >= 0 ? s : 0) : (m + (1ull << (s < 0 ? -s : 0)) - 1) >> (s < 0 ? -s : 0);  // rounded up: none is lost
-    }
+    uint64_t sum = ahead_sum;
+    mine.count = ahead_n;
+    add_bins(last, sum, mine.count);
     mine.mass = to_two(sum, 60 - 54);
   }
   const Two in = scan(mine.mass, lane);
@@ -766,35 +826,65 @@ __global__ void __launch_bounds__(kT, 2) k_sample_filtered(FilteredArgs a, FastD
   if (lane == 0) a.tokens[row] = base + (found >= 0 ? found : last_in);
 }
 
-template <int kC, bool kHeld>
-Launched launch_h(const FilteredArgs& a, int64_t each, int64_t smem, cudaStream_t s) {
-  constexpr int kT = 256;
+// Bytes of dynamic shared memory that a block can have.
+template <int kC, int kT>
+constexpr int kRoom = 227 * 1024 - (int)((sizeof(Shared<kC, kT / 32>) + 1023) / 1024 * 1024);
+
+template <int kC, int kT, bool kHeld>
+Launched launch_h(const FilteredArgs& a, cudaStream_t s) {
+  auto kernel = k_sample_filtered<kC, kT, kHeld>;
   static std::atomic<uint64_t> done{0};
   Launched l;
-  l.error = allow_smem(k_sample_filtered<kC, kT, kHeld>, 200 * 1024, done);
+  l.error = allow_smem(kernel, kRoom<kC, kT>, done);
   if (l.error != cudaSuccess) return l;
+  const int each = each_of<kC, kT>(a.V);
+  const int64_t smem = (int64_t)kBins * kT * 8 + (kHeld ? kT * (int64_t)each * 4 : 0);
   const FastDiv by_each((uint32_t)each);
-  if constexpr (kC == 1)
-    l.add(launch_k(k_sample_filtered<1, kT, kHeld>, dim3((unsigned)a.n), kT, smem, s, a, by_each));
-  else
-    l.add(launch_k_cluster(k_sample_filtered<kC, kT, kHeld>, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each));
+  if constexpr (kC == 1) l.add(launch_k(kernel, dim3((unsigned)a.n), kT, smem, s, a, by_each));
+  else l.add(launch_k_cluster(kernel, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each));
   return l;
 }
-template <int kC>
-Launched launch_c(const FilteredArgs& a, cudaStream_t s) {
-  constexpr int kT = 256;
-  const int64_t columns = (int64_t)kBins * kT * 8, each = ((a.V + kC * kT - 1) / (kC * kT)) | 1;
-  const int64_t smem = columns + kT * each * 4;  // and a row's part
-  if constexpr (kC == 8)
-    if (smem > 200 * 1024 || kT * each > 65536) return launch_h<kC, false>(a, each, columns, s);
-  return launch_h<kC, true>(a, each, smem, s);
+
+// About how long a call takes (us), or infinity where a row's parts do not fit the blocks' shared
+// memory or their places 16 bits.
+template <int kC, int kT>
+double estimate(const FilteredArgs& a, int sms) {
+  const int64_t mine = kT * (int64_t)each_of<kC, kT>(a.V), smem = (int64_t)kBins * kT * 8 + mine * 4;
+  if (smem > kRoom<kC, kT> || mine > 65536) return HUGE_VAL;
+  // blocks an SM; clusters of four and eight leave some of a GPC's SMs over
+  const int two = kT == 256 && smem <= kRoom<kC, kT> - 114 * 1024 ? 2 : 1;
+  const int usable = kC == 8 ? sms * 3 / 4 : kC == 4 ? sms * 7 / 8 : sms;
+  const int at_once = std::max(1, usable * two / kC);
+  const double row = 8.5 + (kC == 8 ? 2.4 : kC == 4 ? 1.6 : kC == 2 ? 0.8 : 0.0) + (kT == 512 ? 1.5 : 0.0) +
+                     (kT == 512 ? 0.56e-3 : 0.74e-3) * a.V / kC;
+  return (double)((a.n + at_once - 1) / at_once) * row * ((int64_t)a.n * kC > usable ? 1.25 : 1.0);
 }
 
 }  // namespace
 
+// More blocks a row make a row faster, and fewer rows at a time: the estimate of waves of rows
+// decides. Measured, us, top-p 0.95, by a block of 256 threads | a block of 512 | two of 512 |
+// four of 512 | eight of 256 (-: does not fit); what is taken in brackets:
+//   vocab   rows: 1                           64                          256
+//   2048    (8.4) | 8.3 | 8.2 | 7.5 | 7.2     (11) | 12 | 13 | 21 | 24    (12) | 20 | 39 | 62 | 66
+//   8192    14 | 13 | 11 | 10 | (9.4)         16 | 16 | (16) | 29 | 31    (19) | 30 | 55 | 96 | 106
+//   32000   29 | 28 | 21 | 18 | (17)          29 | 27 | (22) | 35 | 40    57 | (53) | 82 | 130 | 144
+//   49152   - | - | 25 | 20 | (18)            - | - | (25) | 39 | 44      - | - | (96) | 147 | 157
+//   131072  - | - | - | 29 | (23)             - | - | - | (58) | 110      - | - | - | (245) | 416
+// (16 rows of 131072: 30 by four blocks, 45 by eight.) A vocabulary that no variant holds is
+// read again from global memory for each pass.
 Launched launch_sample_filtered(const FilteredArgs& a, int sms, cudaStream_t s) {
-  if (a.V > 4096 && ((int64_t)a.n * 8 <= 2 * sms || a.V > 131072)) return launch_c<8>(a, s);
-  return a.V > 2048 ? launch_c<4>(a, s) : launch_c<1>(a, s);
+  double least = HUGE_VAL;
+  Launched (*launch)(const FilteredArgs&, cudaStream_t) = launch_h<8, 256, false>;
+  auto offer = [&](double us, Launched (*f)(const FilteredArgs&, cudaStream_t)) {
+    if (us < least) least = us, launch = f;
+  };
+  offer(estimate<1, 256>(a, sms), launch_h<1, 256, true>);
+  offer(estimate<1, 512>(a, sms), launch_h<1, 512, true>);
+  offer(estimate<2, 512>(a, sms), launch_h<2, 512, true>);
+  offer(estimate<4, 512>(a, sms), launch_h<4, 512, true>);
+  offer(estimate<8, 256>(a, sms), launch_h<8, 256, true>);
+  return launch(a, s);
 }
 
 }  // namespace fsk

@@ -255,3 +255,43 @@ def test_same_bits_whatever_the_batch_and_graphs():
         want = [R.sample(r, 0.8, a, 0, b) for r, a, b in zip(x, u, p)]
         for t, n in ((tok, kept), (tok2, kept2)):
             assert t.tolist() == [w[0] for w in want] and n.tolist() == [w[1] for w in want]
+
+
+@pytest.mark.parametrize("V,n", [(700, 12), (9000, 12), (9000, 300), (20000, 100), (32000, 40), (49152, 8), (49152, 30),
+                                 (140001, 4), (400003, 2)])
+def test_cuts_far_out(V, n):
+    """Peaked rows, whose top-k, top-p and min-p end far down the tail: among weights of 2^-19
+    and less, down to those that are 0."""
+    rng = np.random.default_rng(V + n)
+    z = (2.5 * rng.standard_normal((n, V))).astype(np.float32)
+    u = rng.random(n).astype(np.float32)
+    T = np.resize(np.array([0.5, 0.2, 0.06, 0.02], np.float32), n)
+    k = np.exp(rng.uniform(0.6, 1.0, n) * np.log(V)).astype(np.int32)
+    p = np.resize(np.array([0.998, 0.99, 0.9], np.float32), n)
+    m = np.exp2(-rng.uniform(10, 120, n)).astype(np.float32)
+    check(z, T, u, k=k)
+    check(z, T, u, p=p)
+    check(z, T, u, m=m)
+    check(z, T, u, k=k, p=p)
+    check(z, T, u, k=k, m=m)
+    check(z, T, u, k=k, p=p, m=m)
+    check(z, np.float32(0.6), u, p=np.float32(0.998), m=np.resize(np.array([0, 2.0**-18, 2.0**-19, 2.0**-17.5], np.float32), n))
+    check(z, T, u, k=np.resize(np.array([1, 5, 40, 64, 65]), n), m=m)
+
+
+@pytest.mark.parametrize("V", [5000, 49152])
+@pytest.mark.parametrize("y", [17.5, 18.0, 19.0, 40.0, 124.5, 126.5, 140.0])
+def test_one_token_and_a_plateau_far_below(V, y):
+    """All others in one bin, equal or nearly, with weights of 2^-y."""
+    rng = np.random.default_rng(5)
+    n = 6
+    z = np.full((n, V), -y * np.log(2), np.float32)
+    z[3:] += (1e-3 * rng.standard_normal((3, V))).astype(np.float32)
+    z[:, 1234] = 0.0
+    u = np.array([0, 0.5, 0.99, 0, 0.5, 1 - 2.0**-24], np.float32)
+    if y > 125:  # such weights may be 0, and u = 0 then draws another token
+        u = np.maximum(u, np.float32(0.25))
+    k = np.array([2, 100, V // 2, 40, 1000, V - 1])
+    check(z, 1.0, u, k=k)
+    check(z, 1.0, u, k=k, p=np.float32(0.9))
+    check(z, 1.0, u, k=k, m=np.float32(2.0**-18))
