@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kT, 512 / kT) k_sample_filtered(FilteredArgs a
         if (next >= 0) move(next);
         bin = choose(&sh.bins[0][0], kBins, kBins, -1);
         if (!cut_only && m_last < off + bin) return false;  // min-p ends ahead of it
-        const bool fits = left <= (uint32_t)((kBins - 1 - bin) * 112 * kN);  // 7/8 of the warps' room
+        // 7/8 of the warps' room for them
+        const bool fits = held ? left <= (uint32_t)((kBins - 1 - bin) * 112 * kN) : bin < kBins - 1;
         if (fits || bin == 0 || off + bin > 126 || (!cut_only && m_first < off + bin)) break;
         next = off + bin;
       }
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(kT, 512 / kT) k_sample_filtered(FilteredArgs a
   // ---- bins that stay whole, and those that are looked at token by token: the cut's, and
   // the one or two where min-p may end
   int whole = min(cut_bin, m_first) - off;
-  if (by_m || cut_bin < kNone) whole = min(whole, kBins - 1);
+  if (by_m || cut_bin < kNone) whole = max(0, min(whole, kBins - 1));
   const int last = min(min(cut_bin, m_last) - off, kBins - 1);
   auto stays = [&](float z, int i) { return rank_of(z, base + i) <= cut && (!by_m || !less(weight(z), least)); };
   for (int b = whole; b <= last; ++b) {

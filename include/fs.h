@@ -731,8 +731,8 @@ int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t*
  * held in [1e-30, 1e30]; a NaN in top_p or min_p turns it off. Weights are good to a
  * relative 2^-37 and summed as whole numbers and as pairs of f32 numbers, so that a cut or a
  * draw is that of the real numbers but next to a border. A weight below 2^-125 of the
- * largest is 0, and one below 2^-58 of it counts as that much in the sums over runs of
- * tokens. vocab is at most 2^20. */
+ * largest is 0; in the sums over runs of tokens one below 2^-54 of it may count as that
+ * much. vocab is at most 2^20. */
 int fs_sample_filtered(const float* logits, int64_t logits_stride, int32_t n, int32_t vocab,
                        const float* temps, const int32_t* top_k, const float* top_p,
                        const float* min_p, const float* u, int32_t* tokens, int32_t* kept,
