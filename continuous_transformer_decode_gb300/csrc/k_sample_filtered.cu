@@ -24,7 +24,7 @@
 //
 // The logits' bytes are a few percent of the time (256 rows of 49152: 7 us at the copy's rate).
 // A row's chain bounds it, and the issue slots, half of them used: 256 rows with top-p take
-// four waves of two blocks a row, 102 us, 47 of them the issue of 56 million instructions (66 for
+// four waves of two blocks a row, 104 us, 47 of them the issue of 56 million instructions (66 for
 // each token's weight); the rest is what 16 warps an SM wait for, barriers, shared memory and
 // each other. 64 mixed rows: 32 us; one row of 32000 with top-k 50 and top-p: 10 us.
 
@@ -44,7 +44,11 @@ using namespace draw;
 
 namespace cg = cooperative_groups;
 
-constexpr int kBins = 20;   // of y: (b - 1, b], the last one also all above
+// Bins of y: (b - 1, b], the last one also all above. Two more where a row has few blocks, whose
+// shared memory has room for them: more cuts have room for their tokens behind them (64 rows of
+// 49152, T = 1, top-p 0.998: 31 us, 42 with 20 bins; 0.95: 29.3 and 29.0).
+template <int kC>
+constexpr int kBinsOf = kC < 4 ? 22 : 20;
 constexpr int kSub = 64;    // parts of a bin that is split
 constexpr int kList = 128;  // tokens that are ranked among themselves
 constexpr int kFew = 64;    // a top_k that always ends in one list
@@ -71,7 +75,7 @@ struct Shared {
   float max[kC * kW];
   int at[kC * kW];
   Kept kept[kC * kW];
-  Bin bins[kC][kBins];
+  Bin bins[kC][kBinsOf<kC>];
   Bin sub[kC][kSub];
   uint32_t own[3 + 1][kSub];  // of this block: a mass in three, and the count
   uint64_t range[kC][2];
@@ -124,8 +128,6 @@ __device__ __forceinline__ int steps_of(float t) { return __float_as_int(t) - __
 __device__ __forceinline__ int place(float z, float M, Two c) {
   return steps_of(to_grid(__fmul_rn(__fadd_rn(z, -M), c.h)));
 }
-// The bin, of those from y = off on: below 0 for what lies ahead of them.
-__device__ __forceinline__ int bin_of(int k, int off) { return min(kBins - 1, -(k >> 8) - off); }
 // Of kSub parts of a bin, the last one apart.
 __device__ __forceinline__ int part_of(int k, int y) { return (255 - k - 256 * y) >> 2; }
 static_assert(kSub == 64, "four of 256 steps");
@@ -169,7 +171,7 @@ __host__ __device__ __forceinline__ int each_of(int V) {
 // held: the row's parts fit the blocks' shared memory; else they are read again from global.
 template <int kC, int kT, bool held>
 __global__ void __launch_bounds__(kT, 512 / kT) k_sample_filtered(FilteredArgs a, FastDiv by_each) {
-  constexpr int kW = kT / 32, kN = kC * kW;
+  constexpr int kW = kT / 32, kN = kC * kW, kBins = kBinsOf<kC>;
   static_assert(kN <= 64, "two warps a lane");
   static_assert(kT >= 256, "a power of two of the table a thread");
   __shared__ Shared<kC, kW> sh;
@@ -277,6 +279,8 @@ __global__ void __launch_bounds__(kT, 512 / kT) k_sample_filtered(FilteredArgs a
     return;
   }
   const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.0f, by_m = min_p > 0.0f;
+  // the bin, of those from y = from on: below 0 for what lies ahead of them
+  auto bin_of = [](int k, int from) { return min(kBins - 1, -(k >> 8) - from); };
   // min-p ends in y's bins m_first to m_last (of kNone bins)
   constexpr int kNone = 1 << 20;
   int m_first = kNone, m_last = kNone;
@@ -839,7 +843,7 @@ Launched launch_h(const FilteredArgs& a, cudaStream_t s) {
   l.error = allow_smem(kernel, kRoom<kC, kT>, done);
   if (l.error != cudaSuccess) return l;
   const int each = each_of<kC, kT>(a.V);
-  const int64_t smem = (int64_t)kBins * kT * 8 + (kHeld ? kT * (int64_t)each * 4 : 0);
+  const int64_t smem = (int64_t)kBinsOf<kC> * kT * 8 + (kHeld ? kT * (int64_t)each * 4 : 0);
   const FastDiv by_each((uint32_t)each);
   if constexpr (kC == 1) l.add(launch_k(kernel, dim3((unsigned)a.n), kT, smem, s, a, by_each));
   else l.add(launch_k_cluster(kernel, dim3((unsigned)a.n * kC), kT, smem, s, kC, a, by_each));
@@ -850,7 +854,7 @@ Launched launch_h(const FilteredArgs& a, cudaStream_t s) {
 // memory or their places 16 bits.
 template <int kC, int kT>
 double estimate(const FilteredArgs& a, int sms) {
-  const int64_t mine = kT * (int64_t)each_of<kC, kT>(a.V), smem = (int64_t)kBins * kT * 8 + mine * 4;
+  const int64_t mine = kT * (int64_t)each_of<kC, kT>(a.V), smem = (int64_t)kBinsOf<kC> * kT * 8 + mine * 4;
   if (smem > kRoom<kC, kT> || mine > 65536) return HUGE_VAL;
   // blocks an SM; clusters of four and eight leave some of a GPC's SMs over
   const int two = kT == 256 && smem <= kRoom<kC, kT> - 114 * 1024 ? 2 : 1;
@@ -869,8 +873,8 @@ double estimate(const FilteredArgs& a, int sms) {
 //   vocab   rows: 1                           64                          256
 //   2048    (8.4) | 8.3 | 8.2 | 7.5 | 7.2     (11) | 12 | 13 | 21 | 24    (12) | 20 | 39 | 62 | 66
 //   8192    14 | 13 | 11 | 10 | (9.4)         16 | 16 | (16) | 29 | 31    (19) | 30 | 55 | 96 | 106
-//   32000   29 | 28 | 21 | 18 | (17)          29 | 27 | (22) | 35 | 40    57 | (53) | 82 | 130 | 144
-//   49152   - | - | 25 | 20 | (18)            - | - | (25) | 39 | 44      - | - | (96) | 147 | 157
+//   32000   29 | 28 | 21 | 18 | (17)          29 | 27 | (22) | 35 | 40    57 | (54) | 83 | 130 | 144
+//   49152   - | - | 25 | 20 | (18)            - | - | (26) | 39 | 44      - | - | (98) | 147 | 157
 //   131072  - | - | - | 29 | (23)             - | - | - | (58) | 110      - | - | - | (245) | 416
 // (16 rows of 131072: 30 by four blocks, 45 by eight.) A vocabulary that no variant holds is
 // read again from global memory for each pass.
