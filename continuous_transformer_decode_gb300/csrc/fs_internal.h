@@ -610,7 +610,7 @@ struct PagesArgs {
   int64_t* row_slot;
   int max_rows;
   int32_t* status;
-  int code_full, code_rows;
+  int code_full, code_rows, code_shared;
 };
 Launched launch_pages(const PagesArgs& a, cudaStream_t s);
 

@@ -349,7 +349,7 @@ int fs_pages_update(int32_t* holders, int32_t n_pages, int32_t* page_table, int3
   a.by_page = FastDiv((uint32_t)page_size);
   a.row_start = row_start; a.row_lane = row_lane; a.row_position = row_position;
   a.row_length = row_length; a.row_slot = row_slot; a.max_rows = max_rows; a.status = status;
-  a.code_full = FS_ERR_KV_FULL; a.code_rows = FS_ERR_SCRATCH;
+  a.code_full = FS_ERR_KV_FULL; a.code_rows = FS_ERR_SCRATCH; a.code_shared = FS_ERR_STATE;
   return launched(launch_pages(a, (cudaStream_t)stream));
 }
 

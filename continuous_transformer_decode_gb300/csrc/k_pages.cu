@@ -22,6 +22,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kT = 1024, kW = kT / 32;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kNew = -2;  // in place of a page: a lane that starts a new one, or takes nothing
 
 struct Three {
   int64_t a, b, c;
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   __shared__ Three tmp3[kW];
   __shared__ int tmp[2][kW];
   __shared__ int2 free_of[8];  // the blocks' free pages, and how many of them are listed
+  __shared__ int shared;       // a lane would grow into a page that others hold too
   static_assert(kC <= 8, "free_of");
   cg::cluster_group cluster = cg::this_cluster();
   auto sync = [&] {
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   int* const rows0 = pages0 + n;  // of the rows
   int* const gone0 = rows0 + n;   // of the pages let go
   uint16_t* const found = reinterpret_cast<uint16_t*>(gone0 + n);  // this block's free pages
+  if (tid == 0) shared = 0;
   if constexpr (kC > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
@@ -163,13 +166,26 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     const int first = pages_of(keeps);
     return Three{pages_of(had) - first, end <= cap ? pages_of((int)end) - first : (end + add) / a.page_size - first, grow};
   };
+  // A lane grows into its last page, if that is not full, only where it alone holds it: a warp's
+  // lanes are one block's to look at (by every block 1021 lanes took 1 us). The entry is asked
+  // for here, its holders once pages have been let go, and both are looked at last.
+  const bool looks = warp % kC == c;
+  auto last_page = [&](int l, int keeps, int64_t grow) {  // -1: no page, or kNew
+    const int j = a.by_page.div((uint32_t)keeps);
+    return grow > 0 && keeps > j * a.page_size ? max(a.table[(int64_t)l * a.max_pages + j], -1) : kNew;
+  };
+  auto holders_or = [&](int p) {  // 1: the lane's own
+    return p == kNew ? 1 : p >= 0 && p < a.n_pages ? __ldcg(a.holders + p) : 0;
+  };
   bool past = false;
+  int last = kNew;
   Three mine = {}, total;
   for (int l = l0; l < l1; ++l) {
     int keeps;
     const Three t = of_lane(l, keeps);
     past |= keeps + t.c > cap;
     held[l] = keeps;
+    if (each == 1 && looks) last = last_page(l, keeps, t.c);
     mine = mine + t;
   }
   Three run = block_scan(mine, tmp3, total);
@@ -217,16 +233,21 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   // the first 1024 words, shared evenly by the warps, stay with the threads
   unsigned word = 0;
   const int share = min(32, (word1 - word0 + kW - 1) / kW), mine0 = word0 + warp * share;
-  for (int i0 = 0; i0 < share; i0 += 8) {
+  int alone = 1;
+  for (int i0 = 0; i0 < max(share, 1); i0 += 8) {
     int h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = holders_of(mine0 + i0 + i, min(word1, mine0 + share));
+    if (i0 == 0) alone = holders_or(last);  // the entry comes while these are on their way
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const unsigned m = __ballot_sync(kAll, h[i] == 0);
       if (i0 + i == lane) word = m;
     }
   }
+  if (each > 1 && looks)
+    for (int l = l0; l < l1; ++l)
+      if (holders_or(last_page(l, held[l], a.grow[l])) != 1) alone = 0;
   int here;
   const int rank_in = block_scan(__popc(word), tmp[0], here);
   const int first_n = here;
@@ -239,13 +260,16 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
   for (int rank = rank_in; word; word &= word - 1)
     found[rank++] = (uint16_t)(32 * (mine0 - word0 + lane) + __ffs(word) - 1);
   if (tid < kC) *(kC == 1 ? &free_of[0] : cluster.map_shared_rank(&free_of[c], tid)) = make_int2(here, first_n);
+  if (alone != 1)
+    for (int b = 0; b < kC; ++b) *(kC == 1 ? &shared : cluster.map_shared_rank(&shared, b)) = 1;
   sync();
   int before = 0, free_n = 0;
   for (int b = 0; b < kC; ++b) {
     if (b == c) before = free_n;
     free_n += free_of[b].x;
   }
-  const int code = past || total.b > free_n ? a.code_full : total.c > a.max_rows ? a.code_rows : 0;
+  const int code = past || total.b > free_n ? a.code_full : total.c > a.max_rows ? a.code_rows
+                   : shared ? a.code_shared : 0;
   const bool ok = code == 0;
   // ---- 2. the j-th free page is the j-th wanted
   if (ok) {

@@ -635,12 +635,15 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
  * status (int32 [4]): FS_OK or why no lane grew, rows wanted, pages wanted, pages
  * that were free for them (counts past 2^31 - 1 as that). FS_ERR_KV_FULL: too few
  * free pages, or a lane past max_pages * page_size tokens; FS_ERR_SCRATCH: more than
- * max_rows rows. 1. has happened then too, row_start is all 0 and every row padding.
+ * max_rows rows; FS_ERR_STATE: a lane would grow into a partial last page that it does not
+ * hold alone (one that another lane shares must be copied first; an entry outside the pool,
+ * or of a page without holders, is none). 1. has happened then too, row_start is all 0 and
+ * every row padding.
  * Lengths are taken as in [0, max_pages * page_size], negative keep and grow as 0. A
  * let go entry outside [0, n_pages) is only cleared, and a page that nobody holds
- * stays free. A page that several lanes hold is one that no lane will write: a lane
- * that shares its last, partial page must be given a copy before it grows. At most
- * 8192 lanes; max_pages * page_size at most 2^30. One call at a time on one pool. */
+ * stays free. A page that several lanes hold is one that no lane writes: a lane that
+ * shares its last, partial page must be given a copy before it grows. At most 8192
+ * lanes; max_pages * page_size at most 2^30. One call at a time on one pool. */
 int fs_pages_update(int32_t* holders, int32_t n_pages, int32_t* page_table, int32_t* lengths,
                     int32_t n_lanes, int32_t max_pages, int32_t page_size, const int32_t* keep,
                     const int32_t* grow, int32_t* row_start, int32_t* row_lane,
