@@ -608,11 +608,11 @@ struct PagesArgs {
   int32_t* row_position;
   int32_t* row_length;
   int64_t* row_slot;
-  int max_rows;
+  int max_rows, rows_end;  // rows that there may be; that are written (set by the launcher)
   int32_t* status;
   int code_full, code_rows, code_shared;
 };
-Launched launch_pages(const PagesArgs& a, cudaStream_t s);
+Launched launch_pages(PagesArgs a, cudaStream_t s);
 
 constexpr int kMaxRotary = 512;
 struct RopeArgs {

@@ -83,7 +83,7 @@ __device__ __forceinline__ void write_rows(const PagesArgs& a, const int* rows0,
                                            int64_t step, F to_pos) {
   const bool vec = ((reinterpret_cast<uintptr_t>(a.row_lane) | reinterpret_cast<uintptr_t>(a.row_position) |
                      reinterpret_cast<uintptr_t>(a.row_length) | reinterpret_cast<uintptr_t>(a.row_slot)) & 15) == 0;
-  for (int64_t r64 = r0; r64 < a.max_rows; r64 += step) {
+  for (int64_t r64 = r0; r64 < a.rows_end; r64 += step) {
     const int r = (int)r64;
     int l[4], pos[4];
     int64_t slot[4];
@@ -107,7 +107,7 @@ __device__ __forceinline__ void write_rows(const PagesArgs& a, const int* rows0,
       for (int q = 0; q < 4; ++q)
         slot[q] = l[q] >= 0 ? (int64_t)page[q] * a.page_size + (pos[q] - j[q] * a.page_size) : -1;
     }
-    if (vec && r64 + 4 <= a.max_rows) {
+    if (vec && r64 + 4 <= a.rows_end) {
       if (a.row_lane) *reinterpret_cast<int4*>(a.row_lane + r) = make_int4(l[0], l[1], l[2], l[3]);
       if (a.row_position) *reinterpret_cast<int4*>(a.row_position + r) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       if (a.row_length)
@@ -119,7 +119,7 @@ __device__ __forceinline__ void write_rows(const PagesArgs& a, const int* rows0,
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (r64 + q >= a.max_rows) break;
+        if (r64 + q >= a.rows_end) break;
         if (a.row_lane) a.row_lane[r + q] = l[q];
         if (a.row_position) a.row_position[r + q] = pos[q];
         if (a.row_length) a.row_length[r + q] = pos[q] + 1;
@@ -350,7 +350,7 @@ Launched launch_c(const PagesArgs& a, cudaStream_t s) {
   const bool fine = kC == 1 ? l.add(launch_k(k_pages<kC, kRows>, dim3(1), kT, smem, s, a))
                             : l.add(launch_k_cluster(k_pages<kC, kRows>, dim3(kC), kT, smem, s, kC, a));
   if (!kRows && fine) {
-    const int64_t blocks = ((int64_t)a.max_rows + 4 * kRowT - 1) / (4 * kRowT);
+    const int64_t blocks = ((int64_t)a.rows_end + 4 * kRowT - 1) / (4 * kRowT);
     l.add(launch_k(k_page_rows, dim3((unsigned)std::min<int64_t>(blocks, 2048)), kRowT, (size_t)a.n_lanes * 4, s, a));
   }
   return l;
@@ -359,10 +359,11 @@ Launched launch_c(const PagesArgs& a, cudaStream_t s) {
 }  // namespace
 
 // One block for small pools and batches, which saves the cluster's barriers; a kernel of its
-// own for many rows.
-Launched launch_pages(const PagesArgs& a, cudaStream_t s) {
-  if (a.n_pages <= 32768 && a.max_rows <= 4096 && a.n_lanes <= 1024) return launch_c<1, true>(a, s);
-  return a.max_rows <= 16384 ? launch_c<8, true>(a, s) : launch_c<8, false>(a, s);
+// own for many rows. Without an array for them there are no rows to write, whatever their limit.
+Launched launch_pages(PagesArgs a, cudaStream_t s) {
+  a.rows_end = a.row_lane || a.row_position || a.row_length || a.row_slot ? a.max_rows : 0;
+  if (a.n_pages <= 32768 && a.rows_end <= 4096 && a.n_lanes <= 1024) return launch_c<1, true>(a, s);
+  return a.rows_end <= 16384 ? launch_c<8, true>(a, s) : launch_c<8, false>(a, s);
 }
 
 }  // namespace fsk
