@@ -6,7 +6,8 @@
 // rounding (position * 2^-65 turns), whatever the position: whole turns drop out of the
 // integer product. (f64 would cost more than the rows' bytes do: its rate here is 1/60 of
 // f32's.) The signed top 24 bits give sine and cosine by sincospi, the next 24 turn them
-// by a first-order step, as their angle is below 2^-22.
+// by a first-order step, as their angle is below 2^-21 (2 pi 2^-24); the last 16, below 2^-48
+// turns, are left out.
 //
 // One pass over the bytes, which bound it: a thread has one vector of pairs of a row, computes
 // their sines and cosines once and takes several heads by them. 65536 rows of 40 heads of 128

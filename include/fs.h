@@ -630,8 +630,8 @@ int fs_verify_draft(const float* logits, int64_t logits_stride, int32_t n_rows, 
  *      plus 1) and row_slot (page * page_size + place in the page) are what
  *      fs_kv_q8_append, fs_rope and fs_kv_q8_attention take. Rows up to max_rows
  *      behind the last get lane, position and slot -1 and length 0, which pad a
- *      batch there. The five row arrays may each be NULL (max_rows limits the rows
- *      all the same).
+ *      batch there. row_lane, row_position, row_length and row_slot may each be NULL
+ *      (max_rows limits the rows all the same); row_start is always written.
  * status (int32 [4]): FS_OK or why no lane grew, rows wanted, pages wanted, pages
  * that were free for them (counts past 2^31 - 1 as that). FS_ERR_KV_FULL: too few
  * free pages, or a lane past max_pages * page_size tokens; FS_ERR_SCRATCH: more than
@@ -690,9 +690,10 @@ int fs_rope_frequencies(int32_t rotary_dim, double theta, const fs_rope_scaling*
  * sin a); the other values are copied. q_out may be q (in place, same stride), and k_out
  * k; buffers must not overlap otherwise. A negative position skips its row, which is
  * neither read nor written: -1 pads a batch. inv_freq is a HOST array of rotary_dim / 2
- * numbers within 2^20, read during the call. Angles are reduced exactly (as 64-bit fractions of
- * a turn: off by at most position * 2^-65 turns), sines and cosines are f32, and a result
- * is rounded once to dtype. head_dim at most 1024, rotary_dim even, at most 512. */
+ * numbers within 2^20, read during the call. Angles are reduced as 64-bit fractions of a turn,
+ * the first 48 bits of which are used (off by at most position * 2^-65 + 2^-48 turns), sines
+ * and cosines are f32, and a result is rounded once to dtype. head_dim at most 1024,
+ * rotary_dim even, at most 512, n_heads and n_kv_heads at most 65535. */
 int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int64_t k_stride,
             int32_t n_kv_heads, int32_t n, int32_t head_dim, int32_t dtype,
             const int32_t* positions, const double* inv_freq, int32_t rotary_dim, double factor,
@@ -707,8 +708,9 @@ int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int
  * gave; it may be out (in place, same stride: rows without an adapter are then not
  * touched), or NULL for 0; buffers must not overlap otherwise. A [n_adapters][rank][K] and
  * B [n_adapters][N][rank] are bf16, 16-byte aligned; rank is a multiple of 8, at most 128
- * (smaller ones padded with zeros), K a multiple of 8. scale is f32 [n_adapters]. Rows may
- * come in any order and mix; rows of one adapter within a block of rows share its reads.
+ * (smaller ones padded with zeros), K a multiple of 8; K and N at most 2^24. scale is f32
+ * [n_adapters]. Rows may come in any order and mix; rows of one adapter within a block of
+ * rows share its reads.
  * Products are exact, sums f32; A x is kept to 24 bits for f32 out and 16 for bf16; the
  * result is rounded once. A row's bits depend on its own inputs alone, not on the
  * batch. */
@@ -735,7 +737,7 @@ int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t*
  * relative 2^-37 and summed as whole numbers and as pairs of f32 numbers, so that a cut or a
  * draw is that of the real numbers but next to a border. A weight below 2^-125 of the
  * largest is 0; in the sums over runs of tokens one below 2^-54 of it may count as that
- * much. vocab is at most 2^20. */
+ * much. vocab is at most 2^20, n below 2^28. */
 int fs_sample_filtered(const float* logits, int64_t logits_stride, int32_t n, int32_t vocab,
                        const float* temps, const int32_t* top_k, const float* top_p,
                        const float* min_p, const float* u, int32_t* tokens, int32_t* kept,
