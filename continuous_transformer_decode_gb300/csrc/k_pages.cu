@@ -24,6 +24,9 @@ constexpr int kT = 1024, kW = kT / 32;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kNew = -2;  // in place of a page: a lane that starts a new one, or takes nothing
 
+// Words of 32 pages in a pool, which may have 2^31 - 1.
+__host__ __device__ inline int page_words(int n_pages) { return (n_pages - 1) / 32 + 1; }
+
 struct Three {
   int64_t a, b, c;
 };
@@ -223,11 +226,11 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     sync();
   }
   // ---- free pages: this block's are page0 .. page1 - 1, 32 a warp's word
-  const int words = (a.n_pages + 31) / 32;
+  const int words = page_words(a.n_pages);
   const int word0 = (int)((int64_t)words * c / kC), word1 = (int)((int64_t)words * (c + 1) / kC);
   auto holders_of = [&](int w, int end) {  // of the lane's page of a word
-    const int p = 32 * w + lane;
-    return w < end && p < a.n_pages ? __ldcg(a.holders + p) : 1;
+    const unsigned p = 32u * w + lane;
+    return w < end && p < (unsigned)a.n_pages ? __ldcg(a.holders + p) : 1;
   };
   auto free_word = [&](int w, int end) { return __ballot_sync(kAll, holders_of(w, end) == 0); };
   // the first 1024 words, shared evenly by the warps, stay with the threads
@@ -281,7 +284,8 @@ __global__ void __launch_bounds__(kT) k_pages(const PagesArgs a) {
     };
     // the listed ones, shared by all threads of all blocks
 #pragma unroll 2
-    for (int r = c * kT + tid; r < want; r += kC * kT) {
+    for (uint32_t at = c * kT + tid; at < (uint32_t)want; at += kC * kT) {  // want may be 2^31 - 1
+      const int r = (int)at;
       int b = 0, i = r;
       while (b + 1 < kC && i >= free_of[b].x) i -= free_of[b++].x;
       if (i >= free_of[b].y) continue;
@@ -345,7 +349,7 @@ Launched launch_c(const PagesArgs& a, cudaStream_t s) {
   l.error = allow_smem(k_pages<kC, kRows>, kMaxPageLanes * 16 + 65536, done);
   if (l.error != cudaSuccess) return l;
   // four numbers a lane, and the places of a block's first 32768 pages
-  const int64_t own = 32 * ((a.n_pages + 31) / 32 / kC + 1);
+  const int64_t own = 32 * ((int64_t)page_words(a.n_pages) / kC + 1);
   const size_t smem = (size_t)a.n_lanes * 16 + (size_t)std::min<int64_t>(own, 32768) * 2;
   const bool fine = kC == 1 ? l.add(launch_k(k_pages<kC, kRows>, dim3(1), kT, smem, s, a))
                             : l.add(launch_k_cluster(k_pages<kC, kRows>, dim3(kC), kT, smem, s, kC, a));
