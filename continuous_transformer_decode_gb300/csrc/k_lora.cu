@@ -18,6 +18,12 @@
 // come straight from global memory, 16 bytes a lane: the order of the summed index is free as
 // long as both operands have the same, so a lane's 8 values of 32 feed two MMAs.
 //
+// Infinite weights. The parts of a value behind the first are 0 or of the other sign, which makes
+// NaN of an infinite product. A sum that is NaN is therefore formed again: of A x (from f32 x)
+// as the sum of its terms that are no finite numbers, of the columns with finite weights for
+// the later parts. What finds them, a test of each chunk's results, takes 1 % of the 8192 rows'
+// time and up to 3 % of others.
+//
 // A x is held in f32 and enters the second product as two bf16 parts (16 bits) for bf16
 // results, which round by 2^-8 themselves, and three (24 bits) for f32 ones; an f32 x enters the
 // first as three. Products of parts are exact, sums f32. Sums run over the same pieces in the
@@ -162,6 +168,21 @@ struct Raw8 {
       a = __uint_as_float(u << 16), b = __uint_as_float(u & 0xffff0000u);
     }
   }
+  // NaN where m or one of the values is (and for some that are past half their type's range).
+  __device__ __forceinline__ uint32_t any_nan(uint32_t m) const {
+    if constexpr (sizeof(T) == 4) {
+      const float* f = reinterpret_cast<const float*>(v);
+      return __float_as_uint(fmaf(fmaf(f[0], f[1], f[2]), fmaf(f[3], f[4], f[5]), fmaf(f[6], f[7], __uint_as_float(m))));
+    } else {
+      const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(v);
+      __nv_bfloat162 r = __hfma2(__hfma2(f[0], f[1], f[2]), f[3], *reinterpret_cast<const __nv_bfloat162*>(&m));
+      return *reinterpret_cast<uint32_t*>(&r);
+    }
+  }
+  static __device__ __forceinline__ bool is_nan(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(m) != __uint_as_float(m);
+    else return !__hbeq2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&m));
+  }
   __device__ __forceinline__ void end(int i, float a, float b) {
     if constexpr (sizeof(T) == 4) {
       float* f = reinterpret_cast<float*>(v);
@@ -206,6 +227,25 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 // 16 bytes to shared memory, zeros without `in`.
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+}
+
+// The sum of n terms of which some are infinite or NaN (NaN where none is).
+template <typename F>
+__device__ __forceinline__ float sum_of(int n, F term) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < n && s == s; ++i) {
+    const float t = term(i);
+    if (!(fabsf(t) <= 3.4028235e38f)) s += t;
+  }
+  return s != 0.0f ? s : __int_as_float(0x7fffffff);
+}
+
+// Two weights without infinities and NaN (0 in their place), for the parts of a value behind the
+// first.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) { return w & __vcmpltu2(w & 0x7fff7fffu, 0x7f807f80u); }
+__device__ __forceinline__ uint4 finite8(const uint4& w) {
+  return make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
 }
 
 // What all lanes hold anyway, told to the compiler: inside a branch or loop on it MMAs and
@@ -391,6 +431,11 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
           v = p[0];
 #pragma unroll
           for (int b = 1; b < kShares; ++b) v += p[b * tile];
+          if (sizeof(TX) == 4 && v != v && m < rows) {  // of parts of x: an infinity of A?
+            const TX* const xr = x + sh.row[m] * a.x_stride;
+            const __nv_bfloat16* const Ar = A + (int64_t)r * a.K;
+            v = sum_of(a.K, [&](int k) { return (float)xr[k] * __bfloat162float(Ar[k]); });
+          }
           v *= scale;
         }
         __nv_bfloat16 u[kParts];
@@ -454,6 +499,44 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
     fetch(chunk0 + warp, 0);
     ask(chunk0 + warp, First{});
     int slot = 0;
+    // The same sums in the same order, with finite weights for the later parts of A x.
+    auto redo = [&](auto m0, int col, int slot, auto& y) {
+      constexpr int kM = decltype(m0)::value;
+      const bool whole = y_vec && (col & ~31) + 32 <= a.N;
+#pragma unroll
+      for (int m = 0; m < kMP; ++m) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = row[kM + m][h];
+          if (base) y[m][h].load(base + (r >= 0 ? r : some_row) * a.base_stride + col, whole, a.N - col);
+          else y[m][h].clear();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float d[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) y[m][h].start(j, d[2 * h], d[2 * h + 1]);
+#pragma unroll 1
+          for (int b = 0; b < rblocks; ++b) {
+            const int q = 4 * b + tig;
+            uint4 w = q < tiles ? lds128(b_at + slot * 64 * a.rank + 16 * (q ^ (g & 1) * swap) + 32 * j * tiles)
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+              if (p == 1) w = finite8(w);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 f = lds128(t_at + (p * kMT + kM + m) * sz.tile + 1024 * b + 512 * i);
+                const uint32_t x[4] = {f.x, f.y, f.z, f.w};
+                attn::mma16816(d, x, i ? w.z : w.x, i ? w.w : w.y);
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) y[m][h].end(j, d[2 * h], d[2 * h + 1]);
+        }
+      }
+    };
     for (int chunk = chunk0 + warp; chunk < chunk1; chunk += kW, slot ^= 1) {
       fetch(chunk + kW, slot ^ 1);
       attn::cp_wait<1>();
@@ -464,6 +547,7 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
         constexpr int kM = decltype(m0)::value;
         Raw8<TY> y[kMP][2];
         float d[kMP][4][4];
+        uint32_t nan = 0;
 #pragma unroll
         for (int m = 0; m < kMP; ++m)
 #pragma unroll
@@ -506,8 +590,14 @@ __global__ void __launch_bounds__(kT, 2) k_lora(const LoraArgs a, int per_window
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[m][h].end(j, d[m][j][2 * h], d[m][j][2 * h + 1]);
-            if (row[kM + m][h] >= 0) y[m][h].store(out + row[kM + m][h] * a.out_stride + col, whole, a.N - col);
+            nan = y[m][h].any_nan(nan);
           }
+        if (__any_sync(kAll, Raw8<TY>::is_nan(nan))) redo(m0, col, slot, y);
+#pragma unroll
+        for (int m = 0; m < kMP; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (row[kM + m][h] >= 0) y[m][h].store(out + row[kM + m][h] * a.out_stride + col, whole, a.N - col);
       };
       if (kMT == kMP || rows <= 16 * kMP) {
         columns(First{}, [&] { ask(chunk + kW, First{}); });

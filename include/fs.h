@@ -712,8 +712,9 @@ int fs_rope(const void* q, int64_t q_stride, int32_t n_heads, const void* k, int
  * [n_adapters]. Rows may come in any order and mix; rows of one adapter within a block of
  * rows share its reads.
  * Products are exact, sums f32; A x is kept to 24 bits for f32 out and 16 for bf16; the
- * result is rounded once. A row's bits depend on its own inputs alone, not on the
- * batch. */
+ * result is rounded once. scale multiplies A x; with infinities and NaN in x, A and B a
+ * result is what that gives, and other rows and columns are as without them. A row's bits
+ * depend on its own inputs alone, not on the batch. */
 int fs_lora_add(const void* x, int64_t x_stride, int32_t x_dtype, const int32_t* adapter,
                 int32_t n, int32_t K, int32_t N, const uint16_t* A, const uint16_t* B,
                 const float* scale, int32_t n_adapters, int32_t rank, const void* base,
