@@ -652,8 +652,11 @@ Launched launch_t(const LoraArgs& a, int64_t per_window, cudaStream_t s) {
 //   256, 64, 16, 4096, 4096: 27 | 13 | 17     256, 200, 16, 576, 960: 10 | 14 | 29
 //   1000, 8, 64, 4096, 14336: 92 | 55 | 57    1000, 64, 16, 4096, 4096: 31 | 46 | 56
 //   2500, 8, 64, 4096, 14336: 96 | 99 | 119   8192, 64, 16, 4096, 4096: 133 | 161 | 208
-// Two row tiles an item where adapters have 256 rows and more (8192 rows, two | one):
-//   8, 16, 4096, 4096: 52 | 65    8, 64, 4096, 14336: 161 | 190    64, 16, 4096, 4096: 142 | 132
+// An item takes two row tiles where adapters have 256 rows and more (64 adapters of 128 rows, rank
+// 16, 4096 to 4096: 142 | 132 by two | one) and items of one tile are more than run at a time,
+// which 8 adapters have from 4737 rows on. 8, 16, 4096, 4096 and 8, 64, 4096, 14336, blocks alone:
+//   4097 rows: 45 | 34, 157 | 101    4700: 46 | 39, 157 | 105    4864: 47 | 57, 158 | 163
+//   5300 rows: 47 | 60, 158 | 176    6000: 47 | 61, 158 | 187    8192: 50 | 64, 161 | 195
 template <typename TX, typename TY>
 Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   const int64_t windows = (a.n + (int64_t)kWindow - 1) / kWindow;
@@ -668,7 +671,7 @@ Launched launch_xy(const LoraArgs& a, int sms, cudaStream_t s) {
   if (by_4 <= by_1) return launch_t<TX, TY, 1, 4>(a, 2 * sms / 4 / windows, s);
   // four blocks an SM in all, at least eight a window
   const int64_t each = std::max<int64_t>(8, 4 * sms / windows);
-  if (a.n > 4096 && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, 1>(a, each, s);
+  if (((int64_t)a.n + 15) / 16 + a.n_adapters > 2 * sms && a.n / 256 >= a.n_adapters) return launch_t<TX, TY, 2, 1>(a, each, s);
   return launch_t<TX, TY, 1, 1>(a, each, s);
 }
 

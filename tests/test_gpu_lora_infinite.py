@@ -40,7 +40,7 @@ def check(c, got, clean, base=True):
 
 
 # rows and adapters: clusters of eight, of four, blocks alone, and items of two row tiles
-KINDS = {"eight": (30, 3), "four": (90, 70), "alone": (300, 300), "two tiles": (4500, 3)}
+KINDS = {"eight": (30, 3), "four": (90, 70), "alone": (300, 300), "two tiles": (4900, 3)}
 
 
 @pytest.mark.parametrize("xb,yb", [(True, False), (True, True), (False, False), (False, True)])
