@@ -8,8 +8,8 @@
 // all their threads. A page's or a row's lane is found by bisection in the running sums.
 //
 // The bytes are nothing (3 MB for 1021 lanes, 102282 pages and 131198 rows: 0.5 us); it is a
-// chain of a few loads, sums and barriers: 4.5 us for one lane, 10 us for 256 lanes and 47955
-// pages, 16 us for the 1021 lanes, 5 of them in the rows' kernel (by the cluster's eight SMs
+// chain of a few loads, sums and barriers: 5.2 us for one lane, 10 us for 256 lanes and 47955
+// pages, 15 us for the 1021 lanes, 5 of them in the rows' kernel (by the cluster's eight SMs
 // alone the rows took 11).
 #include <cooperative_groups.h>
 

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs a) {
                    : static_cast<T*>(a.k_out) + row * a.ko_stride + (int64_t)(h - a.H) * a.hd;
   };
   // kH heads at a time: their loads, eight, are asked for before the first store (4099 rows
-  // of neighbours: 27 us, with four loads 30; 65536 rows of halves: 207 us, with sixteen 236)
+  // of neighbours: 25 us, with four loads 27; 65536 rows of halves: 207 us, with sixteen 202)
   constexpr int kH = kNear ? 8 : 4;
   if (unit >= turned) {  // behind the turned values (out of place)
     constexpr int kE = kBytes / (int)sizeof(T);
@@ -176,7 +176,7 @@ Launched launch_t(RopeArgs a, bool near, int sms, cudaStream_t s) {
   a.groups = (heads + a.per - 1) / a.per;
   const int64_t threads = (int64_t)a.n * a.groups * a.units;
   // what is more than the L2 may keep passes through it first to go (65536 rows, 537 MB and as
-  // much out: 207 us, without 232; 4099 rows, 75 MB: 27 and 28)
+  // much out: 207 us, without 230; 4099 rows, 75 MB: 25 and 27)
   constexpr bool kWide = kBytes == 16;
   const bool stream = kWide && (int64_t)a.n * heads * a.hd * (int64_t)sizeof(T) > (64 << 20);
   auto kernel = stream ? (near ? k_rope<T, kBytes, true, kWide> : k_rope<T, kBytes, false, kWide>)
