@@ -645,16 +645,17 @@ Launched launch_t(const LoraArgs& a, int64_t per_window, cudaStream_t s) {
 // How many blocks take an item, from how long it would take at most, as the adapters' mix is
 // not known here: a window of 256 rows has up to n_adapters items and one more for every 16
 // rows. A block by itself takes 6 us and `alone`, four together 4.7 us and a quarter of it, eight
-// 4 us and an eighth; 2 blocks an SM run at a time. Measured, us, by 1 | 4 | 8 blocks (rows,
-// adapters, rank, K, N):
-//   30, 8, 64, 4096, 14336: 59 | 22 | 17      100, 64, 16, 4096, 4096: 21 | 12 | 15
-//   100, 200, 16, 576, 960: 8.4 | 13 | 19     256, 8, 16, 4096, 4096: 22 | 11 | 8.2
-//   256, 64, 16, 4096, 4096: 27 | 13 | 17     256, 200, 16, 576, 960: 10 | 14 | 29
-//   1000, 8, 64, 4096, 14336: 92 | 55 | 57    1000, 64, 16, 4096, 4096: 31 | 46 | 56
-//   2500, 8, 64, 4096, 14336: 96 | 99 | 119   8192, 64, 16, 4096, 4096: 133 | 161 | 208
-// An item takes two row tiles where adapters have 256 rows and more (64 adapters of 128 rows, rank
-// 16, 4096 to 4096: 142 | 132 by two | one) and items of one tile are more than run at a time,
-// which 8 adapters have from 4737 rows on. 8, 16, 4096, 4096 and 8, 64, 4096, 14336, blocks alone:
+// 4 us and an eighth; 2 blocks an SM run at a time. Measured, us, by 1 | 4 | 8 blocks (rows
+// in any order, adapters, rank, K, N; bf16):
+//   30, 8, 64, 4096, 14336: 60 | 21 | 16      100, 64, 16, 4096, 4096: 18 | 9.8 | 13
+//   100, 200, 16, 576, 960: 7.0 | 11 | 17     256, 8, 16, 4096, 4096: 21 | 9.0 | 7.2
+//   256, 64, 16, 4096, 4096: 24 | 11 | 14     256, 200, 16, 576, 960: 8.8 | 12 | 26
+//   1000, 8, 64, 4096, 14336: 93 | 55 | 53    1000, 64, 16, 4096, 4096: 26 | 49 | 52
+//   2500, 8, 64, 4096, 14336: 98 | 99 | 121   8192, 64, 16, 4096, 4096: 191 | 303 | 389
+// An item takes two row tiles where adapters have 256 rows and more (8192 rows of 64 in any order,
+// rank 16, 4096 to 4096: 279 | 191 by two | one) and items of one tile are more than run at a
+// time, which 8 adapters have from 4737 rows on. Rows in runs, blocks alone, 8, 16, 4096, 4096 and
+// 8, 64, 4096, 14336:
 //   4097 rows: 45 | 34, 157 | 101    4700: 46 | 39, 157 | 105    4864: 47 | 57, 158 | 163
 //   5300 rows: 47 | 60, 158 | 176    6000: 47 | 61, 158 | 187    8192: 50 | 64, 161 | 195
 template <typename TX, typename TY>
