@@ -45,7 +45,7 @@ KINDS = {"eight": (30, 3), "four": (90, 70), "alone": (300, 300), "two tiles": (
 
 @pytest.mark.parametrize("xb,yb", [(True, False), (True, True), (False, False), (False, True)])
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("rank", [8, 40, 64])
+@pytest.mark.parametrize("rank", [8, 40, 64, 128])
 def test_b(kind, rank, xb, yb):
     n, ads = KINDS[kind]
     rng = np.random.default_rng(rank + n)
@@ -65,7 +65,7 @@ def test_b(kind, rank, xb, yb):
 
 @pytest.mark.parametrize("xb,yb", [(True, False), (True, True), (False, False), (False, True)])
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("rank", [8, 40, 64])
+@pytest.mark.parametrize("rank", [8, 40, 64, 128])
 def test_a(kind, rank, xb, yb):
     """Infinities of A, alone and with ones of B and of x."""
     n, ads = KINDS[kind]
